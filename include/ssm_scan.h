@@ -2,7 +2,8 @@
  * ssm_scan.h — C ABI of the MI355X (gfx950) selective-scan library.
  *
  * The library computes the Mamba selective scan (S6) forward pass, its
- * backward, its one-token decode step and the Mamba-2 SSD layer with
+ * backward, its one-token decode step, the Mamba-2 SSD layer, the gated delta
+ * rule (forward, backward, decode step) and the norms around such a mixer with
  * hand-written HIP kernels. Every pointer that
  * names tensor data is a DEVICE pointer owned by the caller; the library
  * allocates and frees nothing. Work is enqueued asynchronously on the given
@@ -361,6 +362,207 @@ int ssm_ssd_fwd(const ssm_ssd_desc *desc, const void *x, const void *dt, const f
 int ssm_ssd_state_update(const ssm_ssd_desc *desc, const void *x, const void *dt, const float *A,
                          const void *B, const void *C, const float *D, const void *z, float *h,
                          void *y, hipStream_t stream);
+
+/*
+ * The gated delta rule: a linear-recurrence mixer whose (headdim x dstate)
+ * state per head is decayed like the SSD layer's and then corrected along the
+ * token's key instead of added to. Per batch row b and head h, with
+ * g = h / (nheads / ngroups):
+ *
+ *   step_t = dt[b,t,h] (+ dt_bias[h]), through softplus when dt_softplus
+ *   w_t    = beta[b,t,h], through the logistic sigmoid when beta_sigmoid
+ *   k_t, q_t = k[b,t,g,:], q[b,t,g,:]; with qk_norm each divided by
+ *            sqrt(its sum of squares + qk_eps)
+ *   H_t    = a_t H_{t-1} + w_t (v[b,t,h,:] - a_t H_{t-1} k_t) k_t^T,
+ *            a_t = exp(step_t A[h]),  H_{-1} = h0 (or 0)
+ *   y[b,t,h,:] = scale * H_t q_t
+ *
+ * The sequence is evaluated in chunks of 64 tokens on bf16 matrix cores. Every
+ * fp32 operand is split into three bf16 parts, so states and fp32 gradients
+ * are as exact as fp32 arithmetic makes them; y is formed from two parts and
+ * rounded once to bf16. The matrix inverse of a chunk is that of a unit lower
+ * triangular matrix, by substitution, and needs no bound on the keys; but the
+ * recurrence itself grows without bound unless w_t |k_t|^2 <= 2.
+ */
+typedef struct {
+    int64_t batch;     /* >= 0 */
+    int64_t seqlen;    /* >= 0 */
+    int32_t nheads;    /* H >= 1: heads of v, dt, beta, y */
+    int32_t headdim;   /* P: a multiple of 16 in 16..256 */
+    int32_t ngroups;   /* G >= 1, dividing nheads: heads of q and k */
+    int32_t dstate;    /* N: 64 or 128 */
+    int32_t dtype;     /* SSM_BF16 (SSM_F32 is reported as SSM_ERR_UNSUPPORTED) */
+    int32_t dt_softplus;    /* 0 or 1 */
+    int32_t beta_sigmoid;   /* 0 or 1 */
+    int32_t qk_norm;        /* 0 or 1 */
+    float scale;            /* of the readout; finite */
+    float qk_eps;           /* > 0 with qk_norm, else unused */
+    /* elements from one token's row to the next of q, k, v, dt, beta (of one
+     * batch row to the next: seqlen times that); 0 for densely packed rows. A
+     * row itself is dense. Strides of q, k, v are multiples of 8. */
+    int64_t q_stride, k_stride, v_stride, dt_stride, beta_stride;
+    const float *dt_bias;   /* (nheads) fp32 device pointer, or NULL */
+} ssm_gdr_desc;
+
+/* Bytes of device workspace of the forward, and of the backward and the
+ * training pair; 0 when there is nothing to compute and for an invalid
+ * descriptor. */
+size_t ssm_gdr_workspace_size(const ssm_gdr_desc *desc);
+size_t ssm_gdr_bwd_workspace_size(const ssm_gdr_desc *desc);
+
+/*
+ *   q, k      (batch, seqlen, ngroups, dstate)  bf16
+ *   v         (batch, seqlen, nheads, headdim)  bf16
+ *   dt, beta  (batch, seqlen, nheads)           bf16
+ *   A         (nheads) fp32 (negative for a decaying state)
+ *   h0        (batch, nheads, headdim, dstate)  fp32, or NULL for zeros
+ *   y         (batch, seqlen, nheads, headdim)  bf16, dense, written
+ *   h_last    (batch, nheads, headdim, dstate)  fp32, written, or NULL; may equal h0 exactly
+ *   workspace ssm_gdr_workspace_size(desc) bytes, 256-byte aligned; its
+ *             contents on entry do not matter and are clobbered
+ * q, k, v, y, h0 and h_last must be 16-byte aligned (dt, beta 2-byte, A,
+ * dt_bias 4-byte). Outputs must not overlap inputs, each other or the
+ * workspace. seqlen == 0 writes h_last = h0 (or zeros) and no y.
+ */
+int ssm_gdr_fwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
+                const void *beta, const float *A, const float *h0, void *y, float *h_last,
+                void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of  sum dy . y + sum dh_last . h_last  with respect to everything
+ * ssm_gdr_fwd reads (dt, beta, q and k as given, before softplus, sigmoid and
+ * the unit lengths).
+ *   dy        (batch, seqlen, nheads, headdim)  bf16, dense, 16-byte aligned
+ *   dh_last   (batch, nheads, headdim, dstate)  fp32, or NULL (0)
+ *   dq, dk    (batch, seqlen, ngroups, dstate)  bf16, dense, written (summed over a group's heads)
+ *   dv        (batch, seqlen, nheads, headdim)  bf16, dense, written
+ *   ddt, dbeta (batch, seqlen, nheads)          bf16, dense, written
+ *   dA        (nheads) fp32, written (summed over batch and time)
+ *   ddt_bias  (nheads) fp32, written; required when desc->dt_bias is given, unused otherwise
+ *   dh0       (batch, nheads, headdim, dstate)  fp32, written, or NULL (not wanted); may equal dh_last exactly
+ *   workspace ssm_gdr_bwd_workspace_size(desc) bytes, 256-byte aligned
+ * ssm_gdr_fwd_save is ssm_gdr_fwd (same results) that leaves in `workspace`
+ * (ssm_gdr_bwd_workspace_size bytes) what the backward would first recompute;
+ * ssm_gdr_bwd_saved is ssm_gdr_bwd reading it there. It must receive the
+ * workspace of an ssm_gdr_fwd_save call with the same descriptor and inputs,
+ * unmodified; nothing checks this. It clobbers the workspace's other parts
+ * only, so it may run again on the same saved contents.
+ * Every sum is taken in a fixed order: results do not depend on timing.
+ * seqlen == 0 writes dA = 0, ddt_bias = 0, dh0 = dh_last (or zeros).
+ */
+int ssm_gdr_bwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
+                const void *beta, const float *A, const float *h0, const void *dy, const float *dh_last,
+                void *dq, void *dk, void *dv, void *ddt, void *dbeta, float *dA, float *ddt_bias, float *dh0,
+                void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ssm_gdr_fwd_save(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
+                     const void *beta, const float *A, const float *h0, void *y, float *h_last,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ssm_gdr_bwd_saved(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
+                      const void *beta, const float *A, const float *h0, const void *dy, const float *dh_last,
+                      void *dq, void *dk, void *dv, void *ddt, void *dbeta, float *dA, float *ddt_bias,
+                      float *dh0, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One decode step of the gated delta rule: desc->seqlen must be 1 (the strides
+ * are then those from one batch row to the next).
+ *   q, k      (batch, ngroups, dstate)  bf16, 8-byte aligned, strides multiples of 4
+ *   v         (batch, nheads, headdim)  bf16;  dt, beta (batch, nheads) bf16
+ *   h         (batch, nheads, headdim, dstate) fp32, 16-byte aligned, read
+ *   h_out     the same shape, written; h itself for an update in place
+ *   y         (batch, nheads, headdim)  bf16, written
+ * Computed in fp32 without matrix cores. y must not overlap anything else,
+ * h_out nothing but h, and that exactly.
+ */
+int ssm_gdr_state_update(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
+                         const void *beta, const float *A, const float *h, float *h_out, void *y,
+                         hipStream_t stream);
+
+/*
+ * The residual add and RMS norm before a block. Per row (token) of `dim`
+ * channels, all arithmetic in fp32:
+ *
+ *   r = residual + scale * x      (scale (dim): a learned scale per channel; NULL: 1; residual NULL: 0)
+ *   y = r / sqrt(mean(r^2) + eps) * weight
+ *
+ * r is first rounded to residual_dtype, and y is that of the rounded r: what
+ * the next layer adds to is what was normed.
+ */
+typedef struct {
+    int64_t rows;            /* >= 0 */
+    int64_t dim;             /* 1..2^20 */
+    int32_t dtype;           /* of x, y, dy, dx */
+    int32_t residual_dtype;  /* of residual, r, dr, dresidual: dtype, or SSM_F32 */
+    float eps;               /* >= 0 */
+    int32_t reserved;        /* 0 */
+    int64_t x_stride;        /* elements from row to row of x; 0: dim */
+} ssm_prenorm_desc;
+
+/*
+ *   x         (rows, dim)  dtype
+ *   residual  (rows, dim)  residual_dtype, or NULL
+ *   scale     (dim) fp32, or NULL
+ *   weight    (dim) fp32
+ *   r         (rows, dim)  residual_dtype, written; may equal residual
+ *             exactly; or NULL (not wanted)
+ *   y         (rows, dim)  dtype, written
+ * Pointers need their element's alignment only (16-byte aligned rows move
+ * faster). Other overlaps of outputs are refused.
+ */
+int ssm_prenorm_fwd(const ssm_prenorm_desc *desc, const void *x, const void *residual, const float *scale,
+                    const float *weight, void *r, void *y, hipStream_t stream);
+
+/*
+ * Gradients of  sum dy . y + sum dr . r.
+ *   r         (rows, dim)  residual_dtype: what the forward wrote
+ *   dr        (rows, dim)  residual_dtype, or NULL (0)
+ *   x, scale  as the forward's; x is read only with a scale
+ *   dx        (rows, dim)  dtype, dense, written
+ *   dresidual (rows, dim)  residual_dtype, written, or NULL (not wanted); may equal dr exactly
+ *   dweight   (dim) fp32, written
+ *   dscale    (dim) fp32, written; required with a scale, unused otherwise
+ *   workspace ssm_prenorm_bwd_workspace_size(desc) bytes, 256-byte aligned
+ * Sums over rows are taken in a fixed order.
+ */
+size_t ssm_prenorm_bwd_workspace_size(const ssm_prenorm_desc *desc);
+int ssm_prenorm_bwd(const ssm_prenorm_desc *desc, const void *dy, const void *r, const void *dr, const void *x,
+                    const float *scale, const float *weight, void *dx, void *dresidual, float *dweight,
+                    float *dscale, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The gated RMS norm behind a mixer. Per row (token) and group of `dim`
+ * channels, in fp32:
+ *
+ *   gate_first 0:  y = x / sqrt(mean(x^2) + eps) * weight * silu(z)
+ *   gate_first 1:  f = x * silu(z),  y = f / sqrt(mean(f^2) + eps) * weight
+ *
+ * z NULL: no gate. weight is (groups, dim), or (dim) for every group with
+ * weight_shared (a norm per head with one weight for all heads).
+ */
+typedef struct {
+    int64_t rows;            /* >= 0 */
+    int64_t groups;          /* >= 1 */
+    int64_t dim;             /* channels of a group, 1..2^20 */
+    int32_t dtype;           /* of x, z, y and their gradients */
+    int32_t gate_first;      /* 0 or 1 */
+    int32_t weight_shared;   /* 0 or 1 */
+    float eps;               /* >= 0 */
+    int64_t x_stride, z_stride;   /* elements from row to row; 0: groups * dim */
+} ssm_gated_norm_desc;
+
+/*
+ *   x, z      (rows, groups, dim)  dtype; z may be NULL
+ *   y         (rows, groups, dim)  dtype, dense, written
+ * Backward: dy, dx, dz (rows, groups, dim) dtype, dense; dz is required with
+ * z, unused otherwise; dweight fp32 in weight's shape. Outputs must not
+ * overlap inputs, each other or the workspace (ssm_gated_norm_bwd_workspace_size
+ * bytes, 256-byte aligned).
+ */
+int ssm_gated_norm_fwd(const ssm_gated_norm_desc *desc, const void *x, const void *z, const float *weight,
+                       void *y, hipStream_t stream);
+size_t ssm_gated_norm_bwd_workspace_size(const ssm_gated_norm_desc *desc);
+int ssm_gated_norm_bwd(const ssm_gated_norm_desc *desc, const void *dy, const void *x, const void *z,
+                       const float *weight, void *dx, void *dz, float *dweight,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *ssm_status_string(int status);

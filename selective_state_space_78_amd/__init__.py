@@ -1,14 +1,15 @@
 """Python binding of the MI355X selective-scan library (libssm_scan.so).
 
-Argument marshalling only: every step of the scan and of the decode step runs
-in the library's HIP kernels. PyTorch supplies device memory and the current
+Argument marshalling only: every step of the scans, the delta rule, the norms
+and the decode steps runs in the library's HIP kernels. PyTorch supplies device memory and the current
 HIP stream; the library itself is a plain C ABI (include/ssm_scan.h) that
 links no torch. There is no fallback: if the library is missing, every call
 raises.
 
 Names follow the C ABI: ``ssm_scan_fwd``, ``ssm_scan_fwd_noalloc``, ``ssm_scan_workspace_size``,
 ``ssm_scan_plan``, ``ssm_scan_bwd``, ``ssm_state_update``, ``ssm_ssd_fwd``,
-``ssm_status_string``.
+``ssm_gdr_fwd``, ``ssm_gdr_bwd``, ``ssm_gdr_state_update``, ``ssm_prenorm_fwd``,
+``ssm_gated_norm_fwd``, ``ssm_status_string``.
 """
 from __future__ import annotations
 
@@ -27,7 +28,10 @@ _DISC = {"euler": SSM_DISC_EULER, "zoh": SSM_DISC_ZOH}
 EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_workspace_size_tuned",
            "ssm_scan_fwd_tuned", "ssm_scan_plan", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd",
            "ssm_scan_fwd_save", "ssm_scan_bwd_saved", "ssm_state_update", "ssm_ssd_fwd", "ssm_ssd_state_update",
-           "ssm_scan_fwd_noalloc", "ssm_status_string")
+           "ssm_scan_fwd_noalloc", "ssm_gdr_workspace_size", "ssm_gdr_bwd_workspace_size", "ssm_gdr_fwd",
+           "ssm_gdr_fwd_save", "ssm_gdr_bwd", "ssm_gdr_bwd_saved", "ssm_gdr_state_update", "ssm_prenorm_fwd",
+           "ssm_prenorm_bwd", "ssm_prenorm_bwd_workspace_size", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
+           "ssm_gated_norm_bwd_workspace_size", "ssm_status_string")
 
 # Fixed scratch of ssm_scan_fwd_noalloc per GPU (SSM_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -45,6 +49,27 @@ class SsdDesc(ctypes.Structure):
                 ("headdim", ctypes.c_int32), ("ngroups", ctypes.c_int32), ("dstate", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("disc", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("dt_bias", ctypes.c_void_p)]
+
+
+class GdrDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int32),
+                ("headdim", ctypes.c_int32), ("ngroups", ctypes.c_int32), ("dstate", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32), ("beta_sigmoid", ctypes.c_int32),
+                ("qk_norm", ctypes.c_int32), ("scale", ctypes.c_float), ("qk_eps", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64), ("dt_bias", ctypes.c_void_p)]
+
+
+class PrenormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64)]
+
+
+class GatedNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("gate_first", ctypes.c_int32), ("weight_shared", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64)]
 
 
 class ScanTuning(ctypes.Structure):
@@ -100,6 +125,22 @@ def lib() -> ctypes.CDLL:
             L.ssm_ssd_fwd.restype = ctypes.c_int
             L.ssm_ssd_state_update.argtypes = [ctypes.POINTER(SsdDesc)] + [vp] * 10
             L.ssm_ssd_state_update.restype = ctypes.c_int
+            pg, pp, pn = ctypes.POINTER(GdrDesc), ctypes.POINTER(PrenormDesc), ctypes.POINTER(GatedNormDesc)
+            for name, d in (("ssm_gdr_workspace_size", pg), ("ssm_gdr_bwd_workspace_size", pg),
+                            ("ssm_prenorm_bwd_workspace_size", pp), ("ssm_gated_norm_bwd_workspace_size", pn)):
+                getattr(L, name).argtypes = [d]
+                getattr(L, name).restype = sz
+            for name, args in (("ssm_gdr_fwd", [pg] + [vp] * 10 + [sz, vp]),
+                               ("ssm_gdr_fwd_save", [pg] + [vp] * 10 + [sz, vp]),
+                               ("ssm_gdr_bwd", [pg] + [vp] * 18 + [sz, vp]),
+                               ("ssm_gdr_bwd_saved", [pg] + [vp] * 18 + [sz, vp]),
+                               ("ssm_gdr_state_update", [pg] + [vp] * 10),
+                               ("ssm_prenorm_fwd", [pp] + [vp] * 7),
+                               ("ssm_prenorm_bwd", [pp] + [vp] * 11 + [sz, vp]),
+                               ("ssm_gated_norm_fwd", [pn] + [vp] * 5),
+                               ("ssm_gated_norm_bwd", [pn] + [vp] * 8 + [sz, vp])):
+                getattr(L, name).argtypes = args
+                getattr(L, name).restype = ctypes.c_int
             L.ssm_status_string.argtypes = [ctypes.c_int]
             L.ssm_status_string.restype = ctypes.c_char_p
             _lib = L
@@ -484,3 +525,358 @@ def ssm_ssd_state_update(x, dt, A, B, C, h, D=None, z=None, y=None, disc="euler"
     if rc != 0:
         raise SsmError(rc, "ssm_ssd_state_update")
     return y
+
+
+def _row_stride(t, name, lead, tail, dtype, device):
+    """Elements from one row of `t` (the `tail` dimensions, dense) to the next,
+    where the rows of the `lead` dimensions follow one another evenly; raises
+    for any other layout."""
+    shape = tuple(lead) + tuple(tail)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    width = 1
+    for n, st in zip(reversed(tail), reversed(t.stride()[len(lead):])):
+        if n != 1 and st != width and t.numel() > 0:
+            raise ValueError("the last %d dimension(s) of %s must be dense" % (len(tail), name))
+        width *= n
+    if t.numel() == 0:
+        return 0
+    # innermost leading dimension of more than one row gives the stride
+    row, rows = None, 1
+    for n, st in zip(reversed(lead), reversed(t.stride()[:len(lead)])):
+        if n == 1:
+            continue
+        if row is None:
+            row = st
+        elif st != row * rows:
+            raise ValueError("the rows of %s must be evenly spaced" % name)
+        rows *= n
+    if row is None or row == width:
+        return 0
+    if row < width:
+        raise ValueError("the rows of %s overlap" % name)
+    return row
+
+
+def _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm, qk_eps):
+    import torch
+    code = _dtype_code(v)
+    lead, (H, P), (G, N) = tuple(v.shape[:-2]), v.shape[-2:], q.shape[-2:]
+    dev, t = v.device, v.dtype
+    strides = [_row_stride(x, n, lead, tail, t, dev)
+               for x, n, tail in ((q, "q", (G, N)), (k, "k", (G, N)), (v, "v", (H, P)), (dt, "dt", (H,)),
+                                  (beta, "beta", (H,)))]
+    _check(A, "A", (H,), torch.float32, dev)
+    _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
+    batch, L = lead if len(lead) == 2 else (lead[0], 1)
+    return GdrDesc(batch, L, H, P, G, N, code, int(bool(dt_softplus)), int(bool(beta_sigmoid)), int(bool(qk_norm)),
+                   float(N ** -0.5 if scale is None else scale), float(qk_eps), *strides,
+                   None if dt_bias is None else dt_bias.data_ptr())
+
+
+def _workspace(workspace, need, device, name):
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None, need
+    _check(workspace, "workspace", device=device)
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError("workspace has %d bytes, %s needs %d" % (have, name, need))
+    return workspace, have
+
+
+def ssm_gdr_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate) -> int:
+    """Workspace bytes of ssm_gdr_fwd."""
+    desc = GdrDesc(batch, seqlen, nheads, headdim, ngroups, dstate, SSM_BF16, 0, 0, 0, 1.0)
+    return int(lib().ssm_gdr_workspace_size(ctypes.byref(desc)))
+
+
+def ssm_gdr_bwd_workspace_size(batch, seqlen, nheads, headdim, ngroups, dstate) -> int:
+    """Workspace bytes of ssm_gdr_bwd, ssm_gdr_fwd_save and ssm_gdr_bwd_saved."""
+    desc = GdrDesc(batch, seqlen, nheads, headdim, ngroups, dstate, SSM_BF16, 0, 0, 0, 1.0)
+    return int(lib().ssm_gdr_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def ssm_gdr_fwd(q, k, v, dt, beta, A, h0=None, y=None, h_last=None, scale=None, dt_bias=None, dt_softplus=False,
+                beta_sigmoid=False, qk_norm=False, qk_eps=1e-6, workspace=None, want_h_last=True, stream=None,
+                _save=False):
+    """The gated delta rule over a sequence, on device tensors.
+
+    q, k: (batch, L, G, N) bfloat16, N 64 or 128; v: (batch, L, H, P) bfloat16,
+    P a multiple of 16 up to 256; dt, beta: (batch, L, H) bfloat16; A, dt_bias:
+    (H,) float32; h0: (batch, H, P, N) float32. ``scale`` (of the readout)
+    defaults to N ** -0.5. ``dt_softplus`` passes dt + dt_bias through
+    softplus, ``beta_sigmoid`` beta through the sigmoid, ``qk_norm`` gives
+    queries and keys unit length (``qk_eps`` added to the sum of squares). q,
+    k, v, dt and beta may be cut out of wider rows (one projection's output).
+    Outputs y (batch, L, H, P) and h_last (batch, H, P, N) are allocated when
+    not given. Returns (y, h_last).
+    """
+    import torch
+    if v.dim() != 4:
+        raise ValueError("v must be (batch, L, H, P)")
+    desc = _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm, qk_eps)
+    batch, L, H, P = v.shape
+    N, dev = q.shape[-1], v.device
+    _check(h0, "h0", (batch, H, P, N), torch.float32, dev)
+    if y is None:
+        y = torch.empty((batch, L, H, P), dtype=v.dtype, device=dev)
+    if h_last is None and want_h_last:
+        h_last = torch.empty((batch, H, P, N), dtype=torch.float32, device=dev)
+    _check(y, "y", (batch, L, H, P), v.dtype, dev)
+    _check(h_last, "h_last", (batch, H, P, N), torch.float32, dev)
+    L_ = lib()
+    name = "ssm_gdr_fwd_save" if _save else "ssm_gdr_fwd"
+    size = L_.ssm_gdr_bwd_workspace_size if _save else L_.ssm_gdr_workspace_size
+    workspace, ws_bytes = _workspace(workspace, size(ctypes.byref(desc)), dev, name)
+    rc = getattr(L_, name)(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
+                           _ptr(y), _ptr(h_last), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, name)
+    return (y, h_last, workspace) if _save else (y, h_last)
+
+
+def ssm_gdr_fwd_save(q, k, v, dt, beta, A, h0=None, y=None, h_last=None, scale=None, dt_bias=None,
+                     dt_softplus=False, beta_sigmoid=False, qk_norm=False, qk_eps=1e-6, workspace=None,
+                     want_h_last=True, stream=None):
+    """ssm_gdr_fwd that also keeps what the backward would first recompute.
+    Returns (y, h_last, saved): ``saved`` is the workspace (uint8,
+    ssm_gdr_bwd_workspace_size bytes; ``workspace`` if given) to pass unchanged
+    to ssm_gdr_bwd_saved with the same inputs."""
+    return ssm_gdr_fwd(q, k, v, dt, beta, A, h0, y, h_last, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm,
+                       qk_eps, workspace, want_h_last, stream, _save=True)
+
+
+def ssm_gdr_bwd(q, k, v, dt, beta, A, dy, h0=None, dh_last=None, scale=None, dt_bias=None, dt_softplus=False,
+                beta_sigmoid=False, qk_norm=False, qk_eps=1e-6, workspace=None, want_dh0=True, out=None, stream=None,
+                _saved=False):
+    """Backward of ssm_gdr_fwd on device tensors.
+
+    Inputs as ssm_gdr_fwd, plus dy (batch, L, H, P) bfloat16 and an optional
+    dh_last (batch, H, P, N) float32. Returns a dict with dq, dk, dv, ddt, dbeta
+    (bfloat16, of the inputs' shapes), dA (H,), ddt_bias (H,) (with a
+    ``dt_bias``) and dh0 (batch, H, P, N) (when ``want_dh0``), float32. ``out``
+    may hold preallocated outputs.
+    """
+    import torch
+    if v.dim() != 4:
+        raise ValueError("v must be (batch, L, H, P)")
+    desc = _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm, qk_eps)
+    batch, L, H, P = v.shape
+    G, N = q.shape[-2:]
+    dev, t, f32 = v.device, v.dtype, torch.float32
+    _check(h0, "h0", (batch, H, P, N), f32, dev)
+    _check(dy, "dy", (batch, L, H, P), t, dev)
+    _check(dh_last, "dh_last", (batch, H, P, N), f32, dev)
+    o = dict(out or {})
+
+    def get(name, shape, dtype, wanted=True):
+        if not wanted:
+            return None
+        if o.get(name) is None:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        _check(o[name], name, shape, dtype, dev)
+        return o[name]
+    g = dict(dq=get("dq", (batch, L, G, N), t), dk=get("dk", (batch, L, G, N), t), dv=get("dv", (batch, L, H, P), t),
+             ddt=get("ddt", (batch, L, H), t), dbeta=get("dbeta", (batch, L, H), t), dA=get("dA", (H,), f32),
+             ddt_bias=get("ddt_bias", (H,), f32, dt_bias is not None),
+             dh0=get("dh0", (batch, H, P, N), f32, want_dh0))
+    L_ = lib()
+    name = "ssm_gdr_bwd_saved" if _saved else "ssm_gdr_bwd"
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_gdr_bwd_workspace_size(ctypes.byref(desc)), dev, name)
+    rc = getattr(L_, name)(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
+                           _ptr(dy), _ptr(dh_last), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]),
+                           _ptr(g["dbeta"]), _ptr(g["dA"]), _ptr(g["ddt_bias"]), _ptr(g["dh0"]), _ptr(workspace),
+                           ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, name)
+    return g
+
+
+def ssm_gdr_bwd_saved(q, k, v, dt, beta, A, dy, saved, h0=None, dh_last=None, scale=None, dt_bias=None,
+                      dt_softplus=False, beta_sigmoid=False, qk_norm=False, qk_eps=1e-6, want_dh0=True, out=None,
+                      stream=None):
+    """ssm_gdr_bwd that reads what an ssm_gdr_fwd_save call with the same inputs
+    left in ``saved`` (its returned workspace). Arguments and results as
+    ssm_gdr_bwd."""
+    if saved is None and v.numel() > 0:
+        raise ValueError("ssm_gdr_bwd_saved needs the workspace of an ssm_gdr_fwd_save call")
+    return ssm_gdr_bwd(q, k, v, dt, beta, A, dy, h0, dh_last, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm,
+                       qk_eps, saved, want_dh0, out, stream, _saved=True)
+
+
+def ssm_gdr_state_update(q, k, v, dt, beta, A, h, y=None, h_out=None, scale=None, dt_bias=None, dt_softplus=False,
+                         beta_sigmoid=False, qk_norm=False, qk_eps=1e-6, stream=None):
+    """One token of the gated delta rule: q, k (batch, G, N), v (batch, H, P),
+    dt, beta (batch, H) bfloat16; A, dt_bias (H,) float32; options as
+    ssm_gdr_fwd. h (batch, H, P, N) float32 is updated in place, or left and
+    the new state written to ``h_out``. Returns y (batch, H, P), allocated when
+    not given."""
+    import torch
+    if v.dim() != 3:
+        raise ValueError("v must be (batch, H, P)")
+    desc = _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm, qk_eps)
+    batch, H, P = v.shape
+    N, dev = q.shape[-1], v.device
+    _check(h, "h", (batch, H, P, N), torch.float32, dev)
+    if h_out is None:
+        h_out = h
+    _check(h_out, "h_out", (batch, H, P, N), torch.float32, dev)
+    if y is None:
+        y = torch.empty((batch, H, P), dtype=v.dtype, device=dev)
+    _check(y, "y", (batch, H, P), v.dtype, dev)
+    rc = lib().ssm_gdr_state_update(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A),
+                                    _ptr(h), _ptr(h_out), _ptr(y), _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gdr_state_update")
+    return y
+
+
+def ssm_prenorm_fwd(x, weight, residual=None, scale=None, eps=1e-5, y=None, r=None, want_r=True, stream=None):
+    """The residual add and RMS norm before a block, on device tensors:
+    r = residual + scale * x, y = r / sqrt(mean(r^2) + eps) * weight.
+
+    x: (..., dim) bfloat16 or float32 (rows evenly spaced); residual: the same
+    shape, of x's dtype or float32; weight, scale: (dim,) float32. r has
+    residual's dtype (x's without one) and y is the norm of r as stored.
+    ``r`` may be the residual itself. Returns (y, r); r is None with
+    ``want_r`` false.
+    """
+    import torch
+    dim, lead, dev = x.shape[-1], tuple(x.shape[:-1]), x.device
+    code = _dtype_code(x)
+    xs = _row_stride(x, "x", lead, (dim,), x.dtype, dev)
+    rt = x.dtype if residual is None else residual.dtype
+    if rt not in (x.dtype, torch.float32):
+        raise TypeError("residual must be float32 or of x's dtype, got %s" % rt)
+    _check(residual, "residual", x.shape, rt, dev)
+    _check(weight, "weight", (dim,), torch.float32, dev)
+    _check(scale, "scale", (dim,), torch.float32, dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if r is None and want_r:
+        r = torch.empty(x.shape, dtype=rt, device=dev)
+    _check(y, "y", x.shape, x.dtype, dev)
+    _check(r, "r", x.shape, rt, dev)
+    desc = PrenormDesc(x.numel() // dim if dim else 0, dim, code, SSM_F32 if rt == torch.float32 else SSM_BF16,
+                       float(eps), 0, xs)
+    rc = lib().ssm_prenorm_fwd(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), _ptr(r),
+                               _ptr(y), _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_prenorm_fwd")
+    return y, r
+
+
+def ssm_prenorm_bwd(dy, r, weight, dr=None, x=None, scale=None, eps=1e-5, want_dresidual=True, out=None,
+                    workspace=None, stream=None):
+    """Backward of ssm_prenorm_fwd. r: what the forward returned; dr: its
+    gradient (of r's dtype) or None; x (the forward's) is needed with a
+    ``scale``. Returns a dict with dx (dy's dtype), dresidual (r's dtype, when
+    wanted), dweight and dscale (with a scale), float32. ``out`` may hold
+    preallocated outputs (dresidual may be dr itself)."""
+    import torch
+    dim, dev = dy.shape[-1], dy.device
+    code = _dtype_code(dy)
+    rt = r.dtype
+    if rt not in (dy.dtype, torch.float32):
+        raise TypeError("r must be float32 or of dy's dtype, got %s" % rt)
+    _check(dy, "dy", device=dev)
+    _check(r, "r", dy.shape, rt, dev)
+    _check(dr, "dr", dy.shape, rt, dev)
+    _check(weight, "weight", (dim,), torch.float32, dev)
+    _check(scale, "scale", (dim,), torch.float32, dev)
+    if scale is not None and x is None:
+        raise ValueError("the gradient of scale needs x")
+    xs = 0 if scale is None else _row_stride(x, "x", tuple(dy.shape[:-1]), (dim,), dy.dtype, dev)
+    o = dict(out or {})
+
+    def get(name, shape, dtype, wanted=True):
+        if not wanted:
+            return None
+        if o.get(name) is None:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        _check(o[name], name, shape, dtype, dev)
+        return o[name]
+    g = dict(dx=get("dx", dy.shape, dy.dtype), dresidual=get("dresidual", dy.shape, rt, want_dresidual),
+             dweight=get("dweight", (dim,), torch.float32), dscale=get("dscale", (dim,), torch.float32, scale is not None))
+    desc = PrenormDesc(dy.numel() // dim if dim else 0, dim, code, SSM_F32 if rt == torch.float32 else SSM_BF16,
+                       float(eps), 0, xs)
+    L_ = lib()
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_prenorm_bwd_workspace_size(ctypes.byref(desc)), dev,
+                                     "ssm_prenorm_bwd")
+    rc = L_.ssm_prenorm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(r), _ptr(dr), _ptr(x if scale is not None else None),
+                            _ptr(scale), _ptr(weight), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
+                            _ptr(g["dscale"]), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_prenorm_bwd")
+    return g
+
+
+def _gated_desc(x, z, weight, eps, gate_first):
+    import torch
+    if x.dim() < 2:
+        raise ValueError("x must be (..., groups, dim)")
+    groups, dim = x.shape[-2:]
+    lead, dev = tuple(x.shape[:-2]), x.device
+    code = _dtype_code(x)
+    xs = _row_stride(x, "x", lead, (groups, dim), x.dtype, dev)
+    zs = 0 if z is None else _row_stride(z, "z", lead, (groups, dim), x.dtype, dev)
+    shared = weight.dim() == 1
+    _check(weight, "weight", (dim,) if shared else (groups, dim), torch.float32, dev)
+    width = groups * dim
+    return GatedNormDesc(x.numel() // width if width else 0, groups, dim, code, int(bool(gate_first)), int(shared),
+                         float(eps), xs, zs)
+
+
+def ssm_gated_norm_fwd(x, z, weight, eps=1e-5, gate_first=False, y=None, stream=None):
+    """The gated RMS norm behind a mixer, on device tensors. Per row and group:
+    y = x / sqrt(mean(x^2) + eps) * weight * silu(z), or with ``gate_first``
+    the norm of x * silu(z) times weight.
+
+    x, z: (..., groups, dim) bfloat16 or float32 (rows evenly spaced: z may be
+    cut out of a projection's output); z None: no gate. weight: (groups, dim)
+    or (dim,) for every group, float32. Returns y, allocated when not given.
+    """
+    desc = _gated_desc(x, z, weight, eps, gate_first)
+    import torch
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check(y, "y", x.shape, x.dtype, x.device)
+    rc = lib().ssm_gated_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(z), _ptr(weight), _ptr(y),
+                                  _stream(stream, x.device))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_norm_fwd")
+    return y
+
+
+def ssm_gated_norm_bwd(dy, x, z, weight, eps=1e-5, gate_first=False, out=None, workspace=None, stream=None):
+    """Backward of ssm_gated_norm_fwd. Returns a dict with dx, dz (x's dtype, dz
+    with a gate) and dweight (float32, of weight's shape). ``out`` may hold
+    preallocated outputs."""
+    import torch
+    desc = _gated_desc(x, z, weight, eps, gate_first)
+    dev = x.device
+    _check(dy, "dy", x.shape, x.dtype, dev)
+    o = dict(out or {})
+
+    def get(name, shape, dtype, wanted=True):
+        if not wanted:
+            return None
+        if o.get(name) is None:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+        _check(o[name], name, shape, dtype, dev)
+        return o[name]
+    g = dict(dx=get("dx", x.shape, x.dtype), dz=get("dz", x.shape, x.dtype, z is not None),
+             dweight=get("dweight", tuple(weight.shape), torch.float32))
+    L_ = lib()
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_gated_norm_bwd_workspace_size(ctypes.byref(desc)), dev,
+                                     "ssm_gated_norm_bwd")
+    rc = L_.ssm_gated_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(z), _ptr(weight), _ptr(g["dx"]),
+                               _ptr(g["dz"]), _ptr(g["dweight"]), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_norm_bwd")
+    return g

@@ -1,0 +1,974 @@
+// The gated delta rule on gfx950 matrix cores, chunk by chunk.
+//
+// Per batch row and head, with a (P x N) state S, keys k, queries q, values v,
+// the step's decay a_t = exp(dt_t A) and the write strength beta_t:
+//
+//   S_t = a_t S_{t-1} + beta_t (v_t - a_t S_{t-1} k_t) k_t^T,   y_t = S_t q_t
+//
+// For a chunk of C = 64 tokens that starts at state S, with G_i the running
+// sum of log a inside the chunk and Gam_ij = exp(G_i - G_j) for i >= j:
+//
+//   E = strictly lower part of (K K^T * Gam),   R = (I + diag(beta) E)^-1
+//   X = V - exp(G) K S^T,   U = R (beta X)             (C x P: what is written)
+//   Y = exp(G) Q S^T + lower part of (Q K^T * Gam) U
+//   S' = exp(G_C) S + (exp(G_C - G) U)^T K
+//
+// and backwards from dY and D' = dL/dS':
+//
+//   dU = (lower part of (Q K^T * Gam))^T dY + exp(G_C - G) K D'^T
+//   W = R^T dU,   dV = beta W
+//   D = exp(G_C) D' + (exp(G) dY)^T Q - (exp(G) beta W)^T K
+//   dq = exp(G) dY S + (dY U^T * Gam) K
+//   dk = [row] -exp(G) beta W S - (beta W U^T * Gam) K
+//      + [col] exp(G_C - G) U D' + (dY U^T * Gam)^T Q - (beta W U^T * Gam)^T K
+//   dbeta_i = W_i . V_i - exp(G_i) k_i . (W S)_i - sum_{j<i} E_ij W_i . U_j
+//   dG_i = q_i . dq_i + k_i . row_i - k_i . col_i
+//   d(log a_t) = <D', S'> + sum_{i >= t} dG_i
+//
+// Keys and queries of unit length are rows scaled by rk, rq: the scales (and
+// the query scale) ride on the fp32 tables, so that K and Q stay exact bf16
+// operands.
+//
+// What is fp32 stays fp32 through the matrix cores: a computed operand is
+// split into three bf16 parts (24 significant bits) and products of parts
+// below 2^-24 are left out, so a state or a parameter's gradient is as exact
+// as fp32 arithmetic gives it. Only y, a bf16 output, takes two parts.
+//
+// Kernels:
+//  * gdr_prep_kernel, one workgroup per chunk and head, every chunk at once:
+//    the tables, R (16 x 16 diagonal blocks by substitution, the blocks below
+//    by fp32 MFMA) and the decayed scores.
+//  * gdr_fwd_kernel / gdr_rev_kernel walk the chunks forwards / backwards. A
+//    column p of the state depends on no other, and a wave holds 16 columns of
+//    S^T as MFMA accumulators (lane = column, 4 consecutive n). Every product
+//    contracts over tokens or n, and an accumulator is the next product's
+//    operand in the same lane (the contraction index runs in the order in
+//    which a lane holds it), so a wave never exchanges data with another.
+//  * gdr_grad_kernel, one workgroup per chunk and group of heads, every chunk
+//    at once: dq, dk, dbeta and the decay's gradient from the stored S, D', U
+//    and W; gdr_reduce_kernel adds dA and ddt_bias in a fixed order.
+#pragma once
+
+#include "matrix_ops.hpp"
+#include "scan_kernels.hpp"
+
+namespace ssm_detail {
+
+constexpr int kGdrC = 64;         // tokens per chunk
+constexpr int kGdrTiles = 10;     // lower 16 x 16 tiles of a chunk's C x C matrices
+constexpr int kGdrTab = 13;       // fp32 tables per token and head
+enum GdrTable {
+    kTHk, kTHq, kTTk, kTBeta,     // exp(G) rk, exp(G) rq, exp(G_C - G) rk, beta
+    kTHead, kTGhi, kTGlo,         // exp(G); G / ln 2 as a sum of two floats
+    kTRk, kTRq, kTUq,             // rk, rq * scale, rq alone
+    kTStep, kTDstep, kTDbeta      // the step, d step / d dt, d strength / d beta
+};
+
+struct GdrParams {
+    const uint16_t *q, *k, *v, *dt, *beta, *dy;   // bf16 bit patterns
+    const float *A, *dt_bias, *h0, *dh_last;
+    uint16_t *y, *dq, *dk, *dv, *ddt, *dbeta;
+    float *h_last, *dA, *ddt_bias, *dh0;
+    // workspace
+    float *tab;            // (bh, chunk, table, token)
+    float *R, *score;      // (bh, chunk, tile, 16, 16)
+    float *S, *D;          // (bh, chunk, P, N): S at the chunk's start, D' at its end
+    float *U, *W;          // (bh, chunk, P, token)
+    float *part;           // (bh, chunk, 2): the chunk's dA and ddt_bias
+    int64_t qs, ks, vs, dts, bs;   // elements between tokens
+    int64_t L;
+    int nc, batch, H, G, hpg, P;
+    int dt_softplus, beta_sigmoid, qk_norm;
+    float scale, qk_eps;
+};
+
+#ifdef SSM_GDR_INSTANTIATE
+
+constexpr int kGdrPad = 8;                 // LDS row padding of K, Q (elements)
+constexpr int kGdrMS = kGdrC + 8;          // LDS row stride of C x C operands
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ ssd_f32x4 gdr_zero4() { return ssd_f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+
+// v as PARTS bf16 operands whose sum carries 8 PARTS significant bits
+template <int PARTS> struct GdrSplit { ssd_bf16x8 part[PARTS]; };
+
+template <int PARTS>
+__device__ __forceinline__ GdrSplit<PARTS> gdr_split(const float (&v)[8]) {
+    GdrSplit<PARTS> out;
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = v[e];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = ssd_pack(r[2 * e], r[2 * e + 1]);
+            if (k + 1 < PARTS) {
+                r[2 * e] -= __uint_as_float(w[e] << 16);
+                r[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+        out.part[k] = __builtin_bit_cast(ssd_bf16x8, uint4{w[0], w[1], w[2], w[3]});
+    }
+    return out;
+}
+
+template <int PARTS>
+__device__ __forceinline__ GdrSplit<PARTS> gdr_split(const ssd_f32x4 &a, const ssd_f32x4 &b) {
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return gdr_split<PARTS>(v);
+}
+
+// products of parts i, j with i + j < max(PA, PB): the others are below the
+// last bit that the parts carry. Small products first.
+template <int PA, int PB>
+__device__ __forceinline__ ssd_f32x4 gdr_mfma(const GdrSplit<PA> &a, const GdrSplit<PB> &b, ssd_f32x4 c) {
+    constexpr int M = PA > PB ? PA : PB;
+#pragma unroll
+    for (int s = M - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < PA; ++i)
+            if (s - i >= 0 && s - i < PB) c = ssd_mfma(a.part[i], b.part[s - i], c);
+    return c;
+}
+
+__device__ __forceinline__ GdrSplit<1> gdr_whole(const ssd_bf16x8 &v) {
+    GdrSplit<1> o;
+    o.part[0] = v;
+    return o;
+}
+
+// A row's operand whose contraction index runs as c = 32 s + 16 (e / 4) + 4 g4
+// + e % 4: two 8-byte reads 16 elements apart
+__device__ __forceinline__ ssd_bf16x8 gdr_ld_perm(const uint16_t *p) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    const uint2 b = *reinterpret_cast<const uint2 *>(p + 16);
+    return __builtin_bit_cast(ssd_bf16x8, uint4{a.x, a.y, b.x, b.y});
+}
+
+template <int PARTS>
+__device__ __forceinline__ GdrSplit<PARTS> gdr_ld_perm_parts(const uint16_t *p, int plane) {
+    GdrSplit<PARTS> o;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) o.part[k] = gdr_ld_perm(p + k * plane);
+    return o;
+}
+
+// A column's operand in the same order, from a row-major tile (r16: the lane's
+// place in its group of 16)
+__device__ __forceinline__ ssd_bf16x8 gdr_ld_col(const uint16_t *tile, int stride, int row0, int col0, int r16) {
+    const uint16_t *p = tile + (row0 + (r16 >> 2)) * stride + col0 + 4 * (r16 & 3);
+    return ssd_ld_tr2(p, p + 16 * stride);
+}
+
+template <int PARTS>
+__device__ __forceinline__ GdrSplit<PARTS> gdr_ld_col_parts(const uint16_t *tile, int stride, int row0, int col0,
+                                                           int r16, int plane) {
+    GdrSplit<PARTS> o;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) o.part[k] = gdr_ld_col(tile + k * plane, stride, row0, col0, r16);
+    return o;
+}
+
+// 4 floats as PARTS bf16 planes in LDS
+template <int PARTS>
+__device__ __forceinline__ void gdr_store_parts(uint16_t *dst, int plane, float4 v) {
+    float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        const uint2 w = {ssd_pack(r[0], r[1]), ssd_pack(r[2], r[3])};
+        *reinterpret_cast<uint2 *>(dst + k * plane) = w;
+        r[0] -= __uint_as_float(w.x << 16);
+        r[1] -= __uint_as_float(w.x & 0xffff0000u);
+        r[2] -= __uint_as_float(w.y << 16);
+        r[3] -= __uint_as_float(w.y & 0xffff0000u);
+    }
+}
+
+// tile (T, J), J <= T, of a C x C lower triangular matrix
+__device__ __forceinline__ constexpr int gdr_tile(int T, int J) { return T * (T + 1) / 2 + J; }
+
+__device__ __forceinline__ int gdr_valid(const GdrParams &p, int ci) {
+    return (int)min<int64_t>(kGdrC, p.L - (int64_t)ci * kGdrC);
+}
+
+// A chunk's token rows (width W elements) into LDS rows of stride `ls`; rows
+// past the sequence's end read zero by the buffer's range
+template <int W>
+__device__ __forceinline__ void gdr_stage_rows(uint16_t *dst, int ls, const uint16_t *src, int64_t stride, int nv,
+                                               int tid, int threads) {
+    const __amdgpu_buffer_rsrc_t r = ssd_buffer(src, 2u * ((uint32_t)(nv - 1) * (uint32_t)stride + W));
+    constexpr int PR = W / 8;
+    for (int q = tid; q < kGdrC * PR; q += threads) {
+        const int row = q / PR, c = 8 * (q % PR);
+        // rows past the last valid one have offsets past the range
+        const uint4 v = row < nv ? ssd_bload16(r, 2u * ((uint32_t)row * (uint32_t)stride + c)) : uint4{0, 0, 0, 0};
+        *reinterpret_cast<uint4 *>(dst + row * ls + c) = v;
+    }
+}
+
+// The step, its derivative by dt, the write strength and its derivative by beta
+struct GdrStep { float step, dstep, beta, dbeta; };
+__device__ __forceinline__ GdrStep gdr_step_of(float dt, float beta, float bias, int softplus, int sigmoid) {
+    GdrStep o;
+    const float raw = dt + bias;
+    o.step = raw;
+    o.dstep = 1.0f;
+    if (softplus) {
+        o.step = fmaxf(raw, 0.0f) + log1pf(expf(-fabsf(raw)));
+        o.dstep = 1.0f / (1.0f + expf(-raw));
+    }
+    o.beta = beta;
+    o.dbeta = 1.0f;
+    if (sigmoid) {
+        o.beta = 1.0f / (1.0f + expf(-beta));
+        o.dbeta = o.beta * (1.0f / (1.0f + expf(beta)));
+    }
+    return o;
+}
+
+// ---------------------------------------------------------------------------
+// Tables, R and scores of one chunk and head
+template <int N>
+__global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
+    constexpr int KS = N + kGdrPad;
+    constexpr int TS = kGdrC + 4;          // fp32 row stride of T and R
+    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
+    __shared__ __attribute__((aligned(16))) float sT[kGdrC * TS], sR[kGdrC * TS];
+    __shared__ float sGh[kGdrC], sGl[kGdrC], sB[kGdrC], sRk[kGdrC], sRq[kGdrC];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int64_t id = blockIdx.x;                // (b, h) major, chunk minor
+    const int ci = (int)(id % p.nc);
+    const int bh = (int)(id / p.nc);
+    const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
+    const int nv = gdr_valid(p, ci);
+    const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
+    gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, 256);
+    gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, 256);
+    float *tab = p.tab + id * (kGdrTab * kGdrC);
+    if (w == 0) {
+        GdrStep s = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (lane < nv)
+            s = gdr_step_of(ssd_bf(p.dt[(row0 + lane) * p.dts + h]), ssd_bf(p.beta[(row0 + lane) * p.bs + h]),
+                            p.dt_bias ? p.dt_bias[h] : 0.0f, p.dt_softplus, p.beta_sigmoid);
+        // the running sum in 64 bits: differences of it are exponents, and a
+        // rounding of the sum would be an error relative to the product
+        double G = (double)s.step * (double)p.A[h] * 1.4426950408889634074;
+        for (int o = 1; o < kGdrC; o <<= 1) {
+            const double up = __shfl_up(G, o);
+            if (lane >= o) G += up;
+        }
+        const double Gc = __shfl(G, kGdrC - 1);
+        const float hi = (float)G;
+        sGh[lane] = hi;
+        sGl[lane] = (float)(G - (double)hi);
+        sB[lane] = s.beta;
+        tab[kTBeta * kGdrC + lane] = s.beta;
+        tab[kTHead * kGdrC + lane] = __builtin_amdgcn_exp2f((float)G);
+        tab[kTGhi * kGdrC + lane] = hi;
+        tab[kTGlo * kGdrC + lane] = (float)(G - (double)hi);
+        tab[kTStep * kGdrC + lane] = s.step;
+        tab[kTDstep * kGdrC + lane] = s.dstep;
+        tab[kTDbeta * kGdrC + lane] = s.dbeta;
+        sT[lane] = __builtin_amdgcn_exp2f((float)G);
+        sR[lane] = __builtin_amdgcn_exp2f((float)(Gc - G));
+    }
+    __syncthreads();
+    {
+        // row lengths: 4 threads per row
+        const int row = tid >> 2, part = tid & 3;
+        float k2 = 0.0f, q2 = 0.0f;
+        if (p.qk_norm)
+            for (int c = part * (N / 4); c < (part + 1) * (N / 4); ++c) {
+                const float kv = ssd_bf(sK[row * KS + c]), qv = ssd_bf(sQ[row * KS + c]);
+                k2 = fmaf(kv, kv, k2);
+                q2 = fmaf(qv, qv, q2);
+            }
+        k2 += __shfl_xor(k2, 1);
+        q2 += __shfl_xor(q2, 1);
+        k2 += __shfl_xor(k2, 2);
+        q2 += __shfl_xor(q2, 2);
+        if (part == 0) {
+            const float rk = p.qk_norm ? 1.0f / sqrtf(k2 + p.qk_eps) : 1.0f;
+            const float uq = p.qk_norm ? 1.0f / sqrtf(q2 + p.qk_eps) : 1.0f;
+            const float rq = uq * p.scale, head = sT[row], tail = sR[row];
+            sRk[row] = rk;
+            sRq[row] = rq;
+            tab[kTHk * kGdrC + row] = head * rk;
+            tab[kTHq * kGdrC + row] = head * rq;
+            tab[kTTk * kGdrC + row] = tail * rk;
+            tab[kTRk * kGdrC + row] = rk;
+            tab[kTRq * kGdrC + row] = rq;
+            tab[kTUq * kGdrC + row] = uq;
+        }
+    }
+    __syncthreads();
+    float *score = p.score + id * (kGdrTiles * 256);
+    for (int J = 0; J <= w; ++J) {
+        ssd_f32x4 kk = gdr_zero4(), qk = gdr_zero4();
+#pragma unroll
+        for (int s = 0; s < N / 32; ++s) {
+            const ssd_bf16x8 bop = ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]);
+            kk = ssd_mfma(ssd_ld16(&sK[(16 * w + r16) * KS + 32 * s + 8 * g4]), bop, kk);
+            qk = ssd_mfma(ssd_ld16(&sQ[(16 * w + r16) * KS + 32 * s + 8 * g4]), bop, qk);
+        }
+        const int j = 16 * J + r16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * w + 4 * g4 + r;
+            const float gam =
+                i >= j ? __builtin_amdgcn_exp2f((sGh[i] - sGh[j]) + (sGl[i] - sGl[j])) * sRk[j] : 0.0f;
+            sT[i * TS + j] = i > j ? kk[r] * gam * sRk[i] * sB[i] : 0.0f;
+            score[gdr_tile(w, J) * 256 + (4 * g4 + r) * 16 + r16] = qk[r] * gam * sRq[i];
+        }
+    }
+    __syncthreads();
+    {
+        // (I + T)^-1 of diagonal block w, a column per lane, by substitution
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == r16 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int k = 0; k < i; ++k) v = fmaf(-sT[(16 * w + i) * TS + 16 * w + k], x[k], v);
+            x[i] = v;
+        }
+        if (g4 == 0)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sR[(16 * w + i) * TS + 16 * w + r16] = x[i];
+    }
+    __syncthreads();
+    // block column w below the diagonal: R_iw = -R_ii sum_k T_ik R_kw
+    for (int i = w + 1; i < 4; ++i) {
+        ssd_f32x4 acc = gdr_zero4();
+        for (int k = w; k < i; ++k)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(sT[(16 * i + r16) * TS + 16 * k + 4 * s + g4],
+                                                           sR[(16 * k + 4 * s + g4) * TS + 16 * w + r16], acc, 0, 0, 0);
+        ssd_f32x4 out = gdr_zero4();
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            out = __builtin_amdgcn_mfma_f32_16x16x4f32(-sR[(16 * i + r16) * TS + 16 * i + 4 * g4 + s], acc[s], out, 0, 0,
+                                                       0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sR[(16 * i + 4 * g4 + r) * TS + 16 * w + r16] = out[r];
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    float *R = p.R + id * (kGdrTiles * 256);
+    for (int q = tid; q < kGdrTiles * 256; q += 256) {
+        const int t = q >> 8, i = (q >> 4) & 15, j = q & 15;
+        const int T = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - T * (T + 1) / 2;
+        R[q] = sR[(16 * T + i) * TS + 16 * J + j];
+    }
+}
+
+// The 10 lower tiles of a chunk's matrix into PARTS bf16 planes of LDS, row major
+template <int PARTS>
+__device__ __forceinline__ void gdr_stage_tiles(uint16_t *dst, const float *src, int tid, int threads) {
+    for (int q = tid; q < kGdrTiles * 64; q += threads) {
+        const int t = q >> 6, i = (q >> 2) & 15, c = q & 3;
+        const int T = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - T * (T + 1) / 2;
+        gdr_store_parts<PARTS>(dst + (16 * T + i) * kGdrMS + 16 * J + 4 * c, kGdrC * kGdrMS,
+                               *reinterpret_cast<const float4 *>(src + 4 * q));
+    }
+}
+
+// the two tiles above the diagonal that share a 32-token operand with one on it
+template <int PARTS>
+__device__ __forceinline__ void gdr_zero_upper(uint16_t *dst, int tid, int threads) {
+    for (int q = tid; q < PARTS * 2 * 64; q += threads) {
+        const int plane = q >> 7, t = (q >> 6) & 1, i = (q >> 2) & 15, c = q & 3;
+        *reinterpret_cast<uint2 *>(dst + plane * kGdrC * kGdrMS + (32 * t + i) * kGdrMS + 32 * t + 16 + 4 * c) =
+            uint2{0u, 0u};
+    }
+}
+
+__device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    return ssd_f32x4{v.x, v.y, v.z, v.w};
+}
+
+// ---------------------------------------------------------------------------
+// Forward over the chunks. A wave holds columns p0 .. p0 + 15.
+template <int N, bool SAVE>
+__global__ __launch_bounds__(512) void gdr_fwd_kernel(const GdrParams p, int splits) {
+    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrC * kGdrMS;
+    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
+    __shared__ __attribute__((aligned(16))) uint16_t sR[3 * PL], sA[2 * PL];
+    __shared__ __attribute__((aligned(16))) float sTab[4 * kGdrC];
+    __shared__ float sEnd;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int threads = blockDim.x;
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
+    const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
+    const int p0 = 16 * (split * (threads >> 6) + w);
+    const bool live = p0 < p.P;
+    const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
+    ssd_f32x4 S[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        S[nt] = live && p.h0 ? gdr_ld4(p.h0 + sbase + 16 * nt + 4 * g4) : gdr_zero4();
+    gdr_zero_upper<3>(sR, tid, threads);
+    gdr_zero_upper<2>(sA, tid, threads);
+    for (int ci = 0; ci < p.nc; ++ci) {
+        const int nv = gdr_valid(p, ci);
+        const int64_t id = (int64_t)bh * p.nc + ci;
+        const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
+        __syncthreads();
+        gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, threads);
+        gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, threads);
+        gdr_stage_tiles<3>(sR, p.R + id * (kGdrTiles * 256), tid, threads);
+        gdr_stage_tiles<2>(sA, p.score + id * (kGdrTiles * 256), tid, threads);
+        const float *tab = p.tab + id * (kGdrTab * kGdrC);
+        for (int q = tid; q < 4 * kGdrC; q += threads) sTab[q] = tab[q];
+        if (tid == 0) sEnd = tab[kTHead * kGdrC + kGdrC - 1];
+        __syncthreads();
+        if (!live) continue;
+        if constexpr (SAVE) {
+            float *dst = p.S + (id * p.P + p0 + r16) * N + 4 * g4;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = S[nt];
+        }
+        ssd_f32x4 X[4], Y[4];
+#pragma unroll
+        for (int T = 0; T < 4; ++T) X[T] = Y[T] = gdr_zero4();
+#pragma unroll
+        for (int s = 0; s < N / 32; ++s) {
+            const GdrSplit<3> so = gdr_split<3>(S[2 * s], S[2 * s + 1]);
+            GdrSplit<2> so2;
+            so2.part[0] = so.part[0];
+            so2.part[1] = so.part[1];
+#pragma unroll
+            for (int T = 0; T < 4; ++T) {
+                const int o = (16 * T + r16) * KS + 32 * s + 4 * g4;
+                X[T] = gdr_mfma(gdr_whole(gdr_ld_perm(&sK[o])), so, X[T]);
+                Y[T] = gdr_mfma(so2, gdr_whole(gdr_ld_perm(&sQ[o])), Y[T]);
+            }
+        }
+        // beta X, from v
+        const __amdgpu_buffer_rsrc_t rv =
+            ssd_buffer(p.v + row0 * p.vs + (int64_t)h * p.P, 2u * ((uint32_t)(nv - 1) * (uint32_t)p.vs + p.P));
+#pragma unroll
+        for (int T = 0; T < 4; ++T) {
+            const ssd_f32x4 hk = gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
+            const ssd_f32x4 be = gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * T + 4 * g4 + r;
+                const uint16_t vw = __builtin_amdgcn_raw_buffer_load_b16(
+                    rv, (int)(2u * ((uint32_t)i * (uint32_t)p.vs + p0 + r16)), 0, 0);
+                const float v = i < nv ? ssd_bf(vw) : 0.0f;
+                X[T][r] = be[r] * (v - hk[r] * X[T][r]);
+            }
+        }
+        // U = R (beta X)
+        ssd_f32x4 U[4];
+        GdrSplit<3> xo[2] = {gdr_split<3>(X[0], X[1]), gdr_split<3>(X[2], X[3])};
+#pragma unroll
+        for (int T = 0; T < 4; ++T) {
+            U[T] = gdr_zero4();
+#pragma unroll
+            for (int s = 0; s <= T / 2; ++s)
+                U[T] = gdr_mfma(gdr_ld_perm_parts<3>(&sR[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL), xo[s], U[T]);
+        }
+        if constexpr (SAVE) {
+            float *dst = p.U + (id * p.P + p0 + r16) * kGdrC + 4 * g4;
+#pragma unroll
+            for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = U[T];
+        }
+        // Y^T = exp(G) S Q^T + U^T A^T; the backward's recomputation stores none
+        if (p.y != nullptr) {
+            const GdrSplit<2> uo[2] = {gdr_split<2>(U[0], U[1]), gdr_split<2>(U[2], U[3])};
+            const __amdgpu_buffer_rsrc_t ry = ssd_buffer(p.y + (row0 * p.H + h) * p.P,
+                                                         2u * ((uint32_t)(nv - 1) * (uint32_t)(p.H * p.P) + p.P));
+#pragma unroll
+            for (int T = 0; T < 4; ++T) {
+                Y[T] *= sTab[kTHq * kGdrC + 16 * T + r16];
+#pragma unroll
+                for (int s = 0; s <= T / 2; ++s)
+                    Y[T] = gdr_mfma(uo[s], gdr_ld_perm_parts<2>(&sA[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL),
+                                    Y[T]);
+                if (16 * T + r16 < nv)
+                    ssd_bstore8(ry, 2u * ((uint32_t)(16 * T + r16) * (uint32_t)(p.H * p.P) + p0 + 4 * g4),
+                                uint2{ssd_pack(Y[T][0], Y[T][1]), ssd_pack(Y[T][2], Y[T][3])});
+            }
+        }
+        // S' = exp(G_C) S + K^T (exp(G_C - G) U)
+#pragma unroll
+        for (int T = 0; T < 4; ++T) U[T] *= gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
+        const float end = sEnd;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[nt] *= end;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const GdrSplit<3> uo = gdr_split<3>(U[2 * s], U[2 * s + 1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                S[nt] = gdr_mfma(gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, 16 * nt, r16)), uo, S[nt]);
+        }
+    }
+    if (live && p.h_last)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(p.h_last + sbase + 16 * nt + 4 * g4) = S[nt];
+}
+
+// ---------------------------------------------------------------------------
+// Backwards over the chunks: D' of every chunk, W, dv and dh0.
+template <int N>
+__global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrParams p, int splits) {
+    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrC * kGdrMS;
+    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
+    __shared__ __attribute__((aligned(16))) uint16_t sR[3 * PL], sA[3 * PL];
+    __shared__ __attribute__((aligned(16))) float sTab[4 * kGdrC];
+    __shared__ float sEnd;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int threads = blockDim.x;
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
+    const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
+    const int p0 = 16 * (split * (threads >> 6) + w);
+    const bool live = p0 < p.P;
+    const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
+    const uint32_t ys = (uint32_t)(p.H * p.P);
+    ssd_f32x4 D[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        D[nt] = live && p.dh_last ? gdr_ld4(p.dh_last + sbase + 16 * nt + 4 * g4) : gdr_zero4();
+    gdr_zero_upper<3>(sR, tid, threads);
+    gdr_zero_upper<3>(sA, tid, threads);
+    for (int ci = p.nc - 1; ci >= 0; --ci) {
+        const int nv = gdr_valid(p, ci);
+        const int64_t id = (int64_t)bh * p.nc + ci;
+        const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
+        __syncthreads();
+        gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, threads);
+        gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, threads);
+        gdr_stage_tiles<3>(sR, p.R + id * (kGdrTiles * 256), tid, threads);
+        gdr_stage_tiles<3>(sA, p.score + id * (kGdrTiles * 256), tid, threads);
+        const float *tab = p.tab + id * (kGdrTab * kGdrC);
+        for (int q = tid; q < 4 * kGdrC; q += threads) sTab[q] = tab[q];
+        if (tid == 0) sEnd = tab[kTHead * kGdrC + kGdrC - 1];
+        __syncthreads();
+        if (!live) continue;
+        {
+            float *dst = p.D + (id * p.P + p0 + r16) * N + 4 * g4;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = D[nt];
+        }
+        // dY of the wave's columns
+        ssd_f32x4 dY[4];
+        {
+            const __amdgpu_buffer_rsrc_t rd =
+                ssd_buffer(p.dy + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + p.P));
+#pragma unroll
+            for (int T = 0; T < 4; ++T)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * T + 4 * g4 + r;
+                    const uint16_t vw =
+                        __builtin_amdgcn_raw_buffer_load_b16(rd, (int)(2u * ((uint32_t)i * ys + p0 + r16)), 0, 0);
+                    dY[T][r] = i < nv ? ssd_bf(vw) : 0.0f;
+                }
+        }
+        // dU = exp(G_C - G) K D'^T + A^T dY
+        ssd_f32x4 dU[4];
+#pragma unroll
+        for (int T = 0; T < 4; ++T) dU[T] = gdr_zero4();
+#pragma unroll
+        for (int s = 0; s < N / 32; ++s) {
+            const GdrSplit<3> so = gdr_split<3>(D[2 * s], D[2 * s + 1]);
+#pragma unroll
+            for (int T = 0; T < 4; ++T)
+                dU[T] = gdr_mfma(gdr_whole(gdr_ld_perm(&sK[(16 * T + r16) * KS + 32 * s + 4 * g4])), so, dU[T]);
+        }
+        const GdrSplit<1> yo[2] = {gdr_split<1>(dY[0], dY[1]), gdr_split<1>(dY[2], dY[3])};   // exact
+#pragma unroll
+        for (int T = 0; T < 4; ++T) {
+            dU[T] *= gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
+#pragma unroll
+            for (int s = T / 2; s < 2; ++s)
+                dU[T] = gdr_mfma(gdr_ld_col_parts<3>(sA, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), yo[s], dU[T]);
+        }
+        // W = R^T dU
+        ssd_f32x4 W[4];
+        const GdrSplit<3> uo[2] = {gdr_split<3>(dU[0], dU[1]), gdr_split<3>(dU[2], dU[3])};
+#pragma unroll
+        for (int T = 0; T < 4; ++T) {
+            W[T] = gdr_zero4();
+#pragma unroll
+            for (int s = T / 2; s < 2; ++s)
+                W[T] = gdr_mfma(gdr_ld_col_parts<3>(sR, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), uo[s], W[T]);
+        }
+        {
+            float *dst = p.W + (id * p.P + p0 + r16) * kGdrC + 4 * g4;
+#pragma unroll
+            for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = W[T];
+        }
+        // dv = beta W; then the two sources of D
+        const __amdgpu_buffer_rsrc_t rdv =
+            ssd_buffer(p.dv + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + p.P));
+#pragma unroll
+        for (int T = 0; T < 4; ++T) {
+            W[T] *= gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * T + 4 * g4 + r;
+                if (i < nv)
+                    __builtin_amdgcn_raw_buffer_store_b16(ssd_to_bf(W[T][r]), rdv,
+                                                          (int)(2u * ((uint32_t)i * ys + p0 + r16)), 0, 0);
+            }
+            W[T] *= -gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
+            dY[T] *= gdr_ld4(&sTab[kTHq * kGdrC + 16 * T + 4 * g4]);
+        }
+        const float end = sEnd;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) D[nt] *= end;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const GdrSplit<3> wo = gdr_split<3>(W[2 * s], W[2 * s + 1]);
+            const GdrSplit<3> qo = gdr_split<3>(dY[2 * s], dY[2 * s + 1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                D[nt] = gdr_mfma(gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, 16 * nt, r16)), wo, D[nt]);
+                D[nt] = gdr_mfma(gdr_whole(gdr_ld_col(sQ, KS, 32 * s + 4 * g4, 16 * nt, r16)), qo, D[nt]);
+            }
+        }
+    }
+    if (live && p.dh0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(p.dh0 + sbase + 16 * nt + 4 * g4) = D[nt];
+}
+
+// ---------------------------------------------------------------------------
+// dq, dk, dbeta, ddt of one chunk and group. Wave w holds n tile w; the heads
+// of the group follow one another and add into dq and dk in that order.
+template <int N>
+__global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
+    constexpr int KS = N + kGdrPad, NW = N / 16, TH = 64 * NW, PL = kGdrC * kGdrMS;
+    constexpr int PB = 32;                 // columns p per step
+    constexpr int YS = PB + 8;             // LDS row stride of dY, V (token rows)
+    constexpr int UPL = PB * kGdrMS;       // plane of U, W ([p][token])
+    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
+    __shared__ __attribute__((aligned(16))) uint16_t sdY[kGdrC * YS], sV[kGdrC * YS];
+    __shared__ __attribute__((aligned(16))) uint16_t sU[3 * UPL], sW[3 * UPL];
+    __shared__ __attribute__((aligned(16))) uint16_t sPA[3 * PL], sPE[3 * PL];   // scaled dY U^T and W U^T
+    __shared__ __attribute__((aligned(16))) float sTab[kGdrTab * kGdrC];
+    __shared__ float sDot[NW][2][kGdrC];   // per wave: dG and k . (W S) of its columns n
+    __shared__ float sEs[4][kGdrC];        // sum_j E_ij W_i . U_j per column tile
+    __shared__ float sWv[kGdrC];
+    __shared__ double sDs[NW];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g4 = lane >> 4;
+    const int ci = (int)(blockIdx.x % p.nc);
+    const int bg = (int)(blockIdx.x / p.nc);
+    const int b = bg / p.G, g = bg % p.G;
+    const int nv = gdr_valid(p, ci);
+    const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
+    const uint32_t ys = (uint32_t)(p.H * p.P);
+    const int n0 = 16 * w;
+    gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, TH);
+    gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, TH);
+    gdr_zero_upper<3>(sPA, tid, TH);
+    gdr_zero_upper<3>(sPE, tid, TH);
+    ssd_f32x4 dq[4], dk[4];
+#pragma unroll
+    for (int T = 0; T < 4; ++T) dq[T] = dk[T] = gdr_zero4();
+    for (int hh = 0; hh < p.hpg; ++hh) {
+        const int h = g * p.hpg + hh;
+        const int bh = b * p.H + h;
+        const int64_t id = (int64_t)bh * p.nc + ci;
+        __syncthreads();
+        for (int q = tid; q < kGdrTab * kGdrC; q += TH) sTab[q] = p.tab[id * (kGdrTab * kGdrC) + q];
+        // products over p: dY S, W S, U D' (this wave's n), dY U^T and W U^T
+        // (C x C lower tiles dealt over the waves), W V^T (its diagonal)
+        ssd_f32x4 aq[4], ar[4], ac[4], pa[3], pw[3], wv = gdr_zero4();
+#pragma unroll
+        for (int T = 0; T < 4; ++T) aq[T] = ar[T] = ac[T] = gdr_zero4();
+#pragma unroll
+        for (int t = 0; t < 3; ++t) pa[t] = pw[t] = gdr_zero4();
+        double ds = 0.0;                   // <D', S> of this wave's columns n: every token of the chunk gets it
+        for (int c0 = 0; c0 < p.P; c0 += PB) {
+            const int pw_ = min(PB, p.P - c0);
+            __syncthreads();
+            const uint16_t *dyb = p.dy + (row0 * p.H + h) * p.P + c0;
+            const uint16_t *vb = p.v + row0 * p.vs + (int64_t)h * p.P + c0;
+            for (int q = tid; q < kGdrC * (PB / 8); q += TH) {
+                const int row = q / (PB / 8), c = 8 * (q % (PB / 8));
+                uint4 a = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+                if (row < nv && c < pw_) {
+                    a = *reinterpret_cast<const uint4 *>(dyb + (int64_t)row * ys + c);
+                    v = *reinterpret_cast<const uint4 *>(vb + (int64_t)row * p.vs + c);
+                }
+                *reinterpret_cast<uint4 *>(&sdY[row * YS + c]) = a;
+                *reinterpret_cast<uint4 *>(&sV[row * YS + c]) = v;
+            }
+            for (int q = tid; q < PB * (kGdrC / 4); q += TH) {
+                const int row = q / (kGdrC / 4), c = 4 * (q % (kGdrC / 4));
+                float4 u = {0, 0, 0, 0}, ww = {0, 0, 0, 0};
+                if (row < pw_) {
+                    u = *reinterpret_cast<const float4 *>(p.U + (id * p.P + c0 + row) * kGdrC + c);
+                    ww = *reinterpret_cast<const float4 *>(p.W + (id * p.P + c0 + row) * kGdrC + c);
+                }
+                gdr_store_parts<3>(&sU[row * kGdrMS + c], UPL, u);
+                gdr_store_parts<3>(&sW[row * kGdrMS + c], UPL, ww);
+            }
+            __syncthreads();
+            // S and D' columns n0 + r16, rows p = c0 + 16 (e / 4) + 4 g4 + e % 4
+            float sv[8], dv[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int pr = 16 * (e >> 2) + 4 * g4 + (e & 3);
+                const int64_t o = (id * p.P + c0 + pr) * N + n0 + r16;
+                sv[e] = pr < pw_ ? p.S[o] : 0.0f;
+                dv[e] = pr < pw_ ? p.D[o] : 0.0f;
+                ds = fma((double)sv[e], (double)dv[e], ds);
+            }
+            const GdrSplit<3> so = gdr_split<3>(sv), dd = gdr_split<3>(dv);
+#pragma unroll
+            for (int T = 0; T < 4; ++T) {
+                const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&sdY[(16 * T + r16) * YS + 4 * g4]));
+                const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrMS, 4 * g4, 16 * T, r16, UPL);
+                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrMS, 4 * g4, 16 * T, r16, UPL);
+                aq[T] = gdr_mfma(yo, so, aq[T]);
+                ar[T] = gdr_mfma(wo, so, ar[T]);
+                ac[T] = gdr_mfma(uo, dd, ac[T]);
+            }
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                const int q = w + NW * t;
+                if (q < kGdrTiles) {
+                    const int T = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, J = q - T * (T + 1) / 2;
+                    const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrMS, 4 * g4, 16 * J, r16, UPL);
+                    const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&sdY[(16 * T + r16) * YS + 4 * g4]));
+                    const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrMS, 4 * g4, 16 * T, r16, UPL);
+                    pa[t] = gdr_mfma(yo, uo, pa[t]);
+                    pw[t] = gdr_mfma(wo, uo, pw[t]);
+                }
+            }
+            if (w < 4) {
+                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrMS, 4 * g4, 16 * w, r16, UPL);
+                wv = gdr_mfma(wo, gdr_whole(gdr_ld_perm(&sV[(16 * w + r16) * YS + 4 * g4])), wv);
+            }
+        }
+        // row i = 16 w + 4 g4 + r, column 16 w + r16: the diagonal of W V^T
+        if (w < 4 && (r16 >> 2) == g4) sWv[16 * w + r16] = wv[r16 & 3];
+        // C x C: decayed and scaled
+        for (int t = 0; t < 3; ++t) {
+            const int q = w + NW * t;
+            if (q >= kGdrTiles) break;
+            const int T = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, J = q - T * (T + 1) / 2;
+            ssd_f32x4 kk = gdr_zero4();
+#pragma unroll
+            for (int s = 0; s < N / 32; ++s)
+                kk = ssd_mfma(ssd_ld16(&sK[(16 * T + r16) * KS + 32 * s + 8 * g4]),
+                              ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]), kk);
+            const int j = 16 * J + r16;
+            const float ghj = sTab[kTGhi * kGdrC + j], glj = sTab[kTGlo * kGdrC + j], rkj = sTab[kTRk * kGdrC + j];
+            const ssd_f32x4 pat = t == 0 ? pa[0] : t == 1 ? pa[1] : pa[2];
+            const ssd_f32x4 pwt = t == 0 ? pw[0] : t == 1 ? pw[1] : pw[2];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * T + 4 * g4 + r;
+                const float gam = i >= j ? __builtin_amdgcn_exp2f((sTab[kTGhi * kGdrC + i] - ghj) +
+                                                                  (sTab[kTGlo * kGdrC + i] - glj)) * rkj
+                                         : 0.0f;
+                const float rki = sTab[kTRk * kGdrC + i];
+                float a = pat[r] * gam * sTab[kTRq * kGdrC + i];
+                float e = i > j ? pwt[r] * gam * rki : 0.0f;
+                // sum_j E_ij W_i . U_j over the tile's 16 columns
+                float es = e * kk[r];
+                es += __shfl_xor(es, 1);
+                es += __shfl_xor(es, 2);
+                es += __shfl_xor(es, 4);
+                es += __shfl_xor(es, 8);
+                if (r16 == 0) sEs[J][i] = es;
+                e *= -sTab[kTBeta * kGdrC + i];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const uint16_t ah = ssd_to_bf(a), eh = ssd_to_bf(e);
+                    sPA[k * PL + i * kGdrMS + j] = ah;
+                    sPE[k * PL + i * kGdrMS + j] = eh;
+                    a -= ssd_bf(ah);
+                    e -= ssd_bf(eh);
+                }
+            }
+        }
+        __syncthreads();
+        // products over tokens, scaled by the tokens' rows
+        double kd = 0.0;                   // sum_j exp(G_C - G_j) k_j . (U D')_j of this wave's n
+        float dot[4][4], kws[4][4];
+#pragma unroll
+        for (int T = 0; T < 4; ++T) {
+            const ssd_f32x4 hq = gdr_ld4(&sTab[kTHq * kGdrC + 16 * T + 4 * g4]);
+            const ssd_f32x4 hk = gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
+            const ssd_f32x4 tk = gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
+            const ssd_f32x4 be = gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+            aq[T] *= hq;
+            ac[T] *= tk;
+            ar[T] *= hk;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float kv = ssd_bf(sK[(16 * T + 4 * g4 + r) * KS + n0 + r16]);
+                kws[T][r] = kv * ar[T][r];
+                kd = fma((double)kv, (double)ac[T][r], kd);
+            }
+            ar[T] *= -be;
+#pragma unroll
+            for (int s = 0; s <= T / 2; ++s) {
+                const GdrSplit<1> ko = gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16));
+                aq[T] = gdr_mfma(gdr_ld_perm_parts<3>(&sPA[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL), ko, aq[T]);
+                ar[T] = gdr_mfma(gdr_ld_perm_parts<3>(&sPE[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL), ko, ar[T]);
+            }
+#pragma unroll
+            for (int s = T / 2; s < 2; ++s) {
+                const GdrSplit<1> ko = gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16));
+                const GdrSplit<1> qo = gdr_whole(gdr_ld_col(sQ, KS, 32 * s + 4 * g4, n0, r16));
+                ac[T] = gdr_mfma(gdr_ld_col_parts<3>(sPE, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), ko, ac[T]);
+                ac[T] = gdr_mfma(gdr_ld_col_parts<3>(sPA, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), qo, ac[T]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * T + 4 * g4 + r;
+                const float kv = ssd_bf(sK[i * KS + n0 + r16]), qv = ssd_bf(sQ[i * KS + n0 + r16]);
+                dot[T][r] = fmaf(qv, aq[T][r], kv * (ar[T][r] - ac[T][r]));
+            }
+            dq[T] += aq[T];
+            dk[T] += ar[T] + ac[T];
+        }
+#pragma unroll
+        for (int T = 0; T < 4; ++T)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float a = dot[T][r], c = kws[T][r];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    a += __shfl_xor(a, o);
+                    c += __shfl_xor(c, o);
+                }
+                if (r16 == 0) {
+                    sDot[w][0][16 * T + 4 * g4 + r] = a;
+                    sDot[w][1][16 * T + 4 * g4 + r] = c;
+                }
+            }
+        // <D', S'> = exp(G_C) <D', S> + sum_j exp(G_C - G_j) k_j . (U D')_j
+        ds = ds * (double)sTab[kTHead * kGdrC + kGdrC - 1] + kd;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) ds += __shfl_xor(ds, o);
+        if (lane == 0) sDs[w] = ds;
+        __syncthreads();
+        if (w == 0) {
+            double dG = 0.0, whole = 0.0;
+            float kw = 0.0f, es = 0.0f;
+            for (int k = 0; k < NW; ++k) {
+                dG += sDot[k][0][lane];
+                kw += sDot[k][1][lane];
+                whole += sDs[k];
+            }
+            for (int J = 0; J <= lane / 16; ++J) es += sEs[J][lane];
+            for (int o = 1; o < kGdrC; o <<= 1) {
+                const double dn = __shfl_down(dG, o);
+                if (lane + o < kGdrC) dG += dn;
+            }
+            // d(log a_t) = a_t <.., S_{t-1}>, but the sum leaves the rounding of
+            // its terms, which a long step would multiply: a token that forgets
+            // all (a_t below 2^-64) has none
+            const float step = sTab[kTStep * kGdrC + lane];
+            const float dlog = step * p.A[h] * kLog2e < -64.0f ? 0.0f : (float)(dG + whole);
+            const float ddt = dlog * p.A[h] * sTab[kTDstep * kGdrC + lane];
+            double pA = lane < nv ? (double)dlog * step : 0.0;
+            double pb = lane < nv ? (double)ddt : 0.0;
+            if (lane < nv) {
+                const int64_t o = (row0 + lane) * p.H + h;
+                p.ddt[o] = ssd_to_bf(ddt);
+                p.dbeta[o] = ssd_to_bf((sWv[lane] - kw - es) * sTab[kTDbeta * kGdrC + lane]);
+            }
+            for (int o = 1; o < 64; o <<= 1) {
+                pA += __shfl_xor(pA, o);
+                pb += __shfl_xor(pb, o);
+            }
+            if (lane == 0) {
+                p.part[2 * id] = (float)pA;
+                p.part[2 * id + 1] = (float)pb;
+            }
+        }
+    }
+    // the gradients of the rows as given: through the unit lengths
+    if (p.qk_norm) {
+        __syncthreads();
+#pragma unroll
+        for (int T = 0; T < 4; ++T)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * T + 4 * g4 + r;
+                float a = ssd_bf(sQ[i * KS + n0 + r16]) * dq[T][r], c = ssd_bf(sK[i * KS + n0 + r16]) * dk[T][r];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    a += __shfl_xor(a, o);
+                    c += __shfl_xor(c, o);
+                }
+                if (r16 == 0) {
+                    sDot[w][0][i] = a;
+                    sDot[w][1][i] = c;
+                }
+            }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int T = 0; T < 4; ++T)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * T + 4 * g4 + r;
+            if (i >= nv) continue;
+            float a = dq[T][r], c = dk[T][r];
+            if (p.qk_norm) {
+                float qd = 0.0f, kd = 0.0f;
+                for (int k = 0; k < NW; ++k) {
+                    qd += sDot[k][0][i];
+                    kd += sDot[k][1][i];
+                }
+                const float uq = sTab[kTUq * kGdrC + i], rk = sTab[kTRk * kGdrC + i];
+                a -= uq * uq * qd * ssd_bf(sQ[i * KS + n0 + r16]);
+                c -= rk * rk * kd * ssd_bf(sK[i * KS + n0 + r16]);
+            }
+            const int64_t o = ((row0 + i) * p.G + g) * N + n0 + r16;
+            p.dq[o] = ssd_to_bf(a);
+            p.dk[o] = ssd_to_bf(c);
+        }
+}
+
+// dA and ddt_bias of head h: the chunks' parts, batch row by batch row
+static __global__ __launch_bounds__(256) void gdr_reduce_kernel(const GdrParams p) {
+    __shared__ double s[2][256];
+    const int h = blockIdx.x, tid = threadIdx.x;
+    double a = 0.0, c = 0.0;
+    const int64_t n = (int64_t)p.batch * p.nc;
+    for (int64_t q = tid; q < n; q += 256) {
+        const int64_t id = ((q / p.nc) * p.H + h) * p.nc + q % p.nc;
+        a += p.part[2 * id];
+        c += p.part[2 * id + 1];
+    }
+    s[0][tid] = a;
+    s[1][tid] = c;
+    __syncthreads();
+    for (int o = 128; o >= 1; o >>= 1) {
+        if (tid < o) {
+            s[0][tid] += s[0][tid + o];
+            s[1][tid] += s[1][tid + o];
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        p.dA[h] = (float)s[0][0];
+        if (p.ddt_bias) p.ddt_bias[h] = (float)s[1][0];
+    }
+}
+
+#endif  // SSM_GDR_INSTANTIATE
+
+}  // namespace ssm_detail

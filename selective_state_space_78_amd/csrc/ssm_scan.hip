@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "ssm_scan.h"
+#include "abi_util.hpp"
 #include "scan_kernels.hpp"
 #include "bwd_kernels.hpp"
 #include "ssd_kernels.hpp"
@@ -666,30 +667,6 @@ __global__ __launch_bounds__(256) void bwd_reduce_kernel(const BwdReduceParams p
 
 // ---------------------------------------------------------------------------
 // Host side: validation, planning, dispatch
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range range_of(const void *p, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + (uintptr_t)bytes};
-}
-
-bool overlaps(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi || a.lo == 0 || b.lo == 0) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// a * b without overflow, both >= 0
-bool mul_ok(int64_t a, int64_t b, int64_t *out) {
-    if (a == 0 || b == 0) { *out = 0; return true; }
-    if (a > INT64_MAX / b) return false;
-    *out = a * b;
-    return true;
-}
 
 int padded_states(int64_t N) {
     if (N <= 4) return 4;

@@ -1,0 +1,238 @@
+"""GPU: the norms around a block and their gradients against the fp64
+reference.
+
+Tolerances relative to max(|reference|, rms of the row's reference values):
+bf16 outputs one rounding, 2^-8, and 2^-12 for what precedes it; fp32 outputs
+64 half steps of fp32 (a row's sums are pairwise over lanes); sums over rows
+256 half steps of the sum of their terms' magnitudes.
+
+dx is inv (w dy - n mean(n w dy)), a difference: each of its two terms is rounded
+by some half steps of its own size, whatever the difference is. Where they
+cancel (a row of one channel with f^2 >> eps: n = 1 - eps / 2 f^2, so df = inv
+w dy eps / f^2, thousands of times smaller than its terms) the error is still
+that of the terms. So dx, and dz where the gate comes first (df x silu'(z)), are
+held relative to max(|reference|, rms, the terms' size).
+"""
+import numpy as np
+import pytest
+
+from gpu_util import say, torch_cuda
+from oracle import delta
+from test_delta_gpu import TOL_BF, err, np64
+
+pytestmark = pytest.mark.gpu
+
+TOL_32 = 64 * 2.0 ** -24
+TOL_SUM = 256 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = torch_cuda()
+    import selective_state_space_78_amd as ssm
+    ssm.lib()
+    return torch, ssm
+
+
+def terms_err(got, ref, terms):
+    got = np64(got)
+    rms = float(np.sqrt(np.mean(ref * ref)))
+    return float(np.max(np.abs(got - ref) / np.maximum(np.maximum(np.maximum(np.abs(ref), rms), terms), 1e-30)))
+
+
+def tol(t):
+    return TOL_BF if str(t.dtype) == "torch.bfloat16" else TOL_32
+
+
+def sums(g, ref, names):
+    return {n: float(np.max(np.abs(np64(g[n]) - ref[n]) / np.maximum(ref[n + "_abs"], 1e-30))) for n in names}
+
+
+TYPES = [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "float32")]
+# every team of lanes, both sides of its border, odd and long rows
+DIMS = [1, 5, 8, 64, 100, 203, 512, 768, 1000, 2048, 2056, 4096, 8192, 8200, 1025, 20000]
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("dim", DIMS)
+def test_prenorm(env, dim, types):
+    torch, ssm = env
+    t, rt = (getattr(torch, n) for n in types)
+    rows = 300 if dim <= 2048 else 9
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x, res, w, s = rnd(rows, dim).to(t), (2 * rnd(rows, dim)).to(rt), 1 + 0.2 * rnd(dim), rnd(dim)
+    dy, dr = rnd(rows, dim).to(t), rnd(rows, dim).to(rt)
+    y, r = ssm.ssm_prenorm_fwd(x, w, residual=res, scale=s)
+    got = ssm.ssm_prenorm_bwd(dy, r, w, dr=dr, x=x, scale=s)
+    torch.cuda.synchronize()
+    # r itself, then the norm of what was stored
+    assert err(np64(r), np64(res) + np64(s) * np64(x)) <= tol(r)
+    yr, _, ref = delta.prenorm(np64(x), np64(w), np64(res), np64(s), dy=np64(dy), dr=np64(dr), store=lambda _: np64(r))
+    e = dict(y=err(np64(y), yr), dx=err(np64(got["dx"]), ref["dx"]), dresidual=err(np64(got["dresidual"]), ref["dresidual"]))
+    e.update(sums(got, ref, ("dweight", "dscale")))
+    say("prenorm", dim, types, ", ".join("%s %.1e" % p for p in e.items()))
+    assert e["y"] <= tol(y) and e["dx"] <= tol(x) and e["dresidual"] <= tol(r), e
+    assert e["dweight"] <= TOL_SUM and e["dscale"] <= TOL_SUM, e
+
+
+def test_prenorm_forms(env):
+    """Without residual, scale, outgoing residual or its gradient; strided x;
+    the residual updated in place; one row and none."""
+    torch, ssm = env
+    x = torch.randn(7, 3, 200, device="cuda")[..., :128]
+    w = torch.randn(128, device="cuda")
+    y, r = ssm.ssm_prenorm_fwd(x, w, want_r=False)
+    assert r is None and err(np64(y), delta.prenorm(np64(x), np64(w))[0]) <= TOL_32
+    xc = x.contiguous()
+    dy = torch.randn_like(xc)
+    g = ssm.ssm_prenorm_bwd(dy, xc, w, want_dresidual=False)
+    ref = delta.prenorm(np64(x), np64(w), dy=np64(dy))[2]
+    assert g["dresidual"] is None and g["dscale"] is None and err(np64(g["dx"]), ref["dx"]) <= TOL_32
+    for dim in (128, 2 * 8192 + 3):
+        x, res, w = torch.randn(5, dim, device="cuda"), torch.randn(5, dim, device="cuda"), torch.randn(dim, device="cuda")
+        y, r = ssm.ssm_prenorm_fwd(x, w, residual=res)
+        keep = res.clone()
+        y2, r2 = ssm.ssm_prenorm_fwd(x, w, residual=keep, r=keep)
+        assert torch.equal(r, r2) and torch.equal(y, y2) and r2.data_ptr() == keep.data_ptr()
+        dy, dr = torch.randn_like(x), torch.randn_like(x)
+        a = ssm.ssm_prenorm_bwd(dy, r, w, dr=dr)
+        b = ssm.ssm_prenorm_bwd(dy, r, w, dr=dr, out=dict(dresidual=dr))
+        assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dresidual"], b["dresidual"])
+    e = torch.empty(0, 128, device="cuda")
+    y, r = ssm.ssm_prenorm_fwd(e, torch.ones(128, device="cuda"))
+    g = ssm.ssm_prenorm_bwd(e, e, torch.ones(128, device="cuda"), x=e, scale=torch.ones(128, device="cuda"))
+    assert y.shape == (0, 128) and not g["dweight"].any() and not g["dscale"].any()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("rows,groups,dim,shared,strided", [
+    (1, 1, 1, True, False), (50, 4, 64, True, True), (33, 3, 128, False, True), (129, 2, 96, False, False),
+    (5, 7, 203, True, False), (40, 1, 1536, False, True), (6, 2, 4096, False, False), (4, 2, 2050, True, True),
+    (3, 2, 9000, False, False), (700, 5, 16, True, True)])
+def test_gated_norm(env, rows, groups, dim, shared, strided, first, dtype):
+    torch, ssm = env
+    t = getattr(torch, dtype)
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x, z, dy = rnd(rows, groups, dim).to(t), (2 * rnd(rows, groups, dim)).to(t), rnd(rows, groups, dim).to(t)
+    w = 1 + 0.2 * (rnd(dim) if shared else rnd(groups, dim))
+    if strided:
+        both = torch.cat([x.reshape(rows, -1), z.reshape(rows, -1)], -1)
+        x, z = (both[:, k * groups * dim:(k + 1) * groups * dim].unflatten(-1, (groups, dim)) for k in (0, 1))
+    y = ssm.ssm_gated_norm_fwd(x, z, w, gate_first=first)
+    got = ssm.ssm_gated_norm_bwd(dy, x, z, w, gate_first=first)
+    torch.cuda.synchronize()
+    yr, ref = delta.gated_norm(np64(x), np64(z), np64(w), gate_first=first, dy=np64(dy))
+    e = dict(y=err(np64(y), yr), dx=terms_err(got["dx"], ref["dx"], ref["dx_terms"]),
+             dz=terms_err(got["dz"], ref["dz"], ref["dz_terms"]))
+    e.update(sums(got, ref, ("dweight",)))
+    say("gated norm", rows, groups, dim, shared, strided, first, dtype, ", ".join("%s %.1e" % p for p in e.items()))
+    assert max(e["y"], e["dx"], e["dz"]) <= tol(x) and e["dweight"] <= TOL_SUM, e
+
+
+def test_gated_norm_forms(env):
+    """No gate; rows of zeros; no rows; guards around the outputs; replays."""
+    torch, ssm = env
+    x, w = torch.randn(9, 2, 40, device="cuda"), torch.randn(40, device="cuda")
+    x[3] = 0.0
+    dy = torch.randn_like(x)
+    y, g = ssm.ssm_gated_norm_fwd(x, None, w), ssm.ssm_gated_norm_bwd(dy, x, None, w)
+    yr, ref = delta.gated_norm(np64(x), None, np64(w), dy=np64(dy))
+    assert g["dz"] is None and err(np64(y), yr) <= TOL_32 and err(np64(g["dx"]), ref["dx"]) <= TOL_32
+    e = torch.empty(0, 2, 40, device="cuda")
+    assert ssm.ssm_gated_norm_fwd(e, e, w).shape == e.shape
+    assert not ssm.ssm_gated_norm_bwd(e, e, e, w)["dweight"].any()
+    z = torch.randn_like(x)
+    buf = torch.full((x.numel() + 128,), 7.0, device="cuda")
+    ssm.ssm_gated_norm_fwd(x, z, w, y=buf[64:64 + x.numel()].view(x.shape))
+    assert bool((buf[:64] == 7).all()) and bool((buf[-64:] == 7).all())
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ssm.ssm_gated_norm_bwd(dy, x, z, w, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ssm.ssm_gated_norm_bwd(dy, x, z, w, workspace=ws)
+    for k in range(3):
+        x.copy_(torch.randn_like(x))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = {n: t.clone() for n, t in got.items()}
+        want = ssm.ssm_gated_norm_bwd(dy, x, z, w)
+        for n in kept:
+            assert torch.equal(kept[n], want[n]), (k, n)
+
+
+def test_block_run(env):
+    """A block as it is used: prenorm, projections, delta rule, gated norm,
+    projection, the next residual add; its gradients against differences of the
+    whole in the loss direction, and its decode by single tokens against the
+    sequence."""
+    torch, ssm = env
+    B, L, D, G, H, P, N = 2, 90, 256, 2, 4, 64, 64
+    bf, f32 = torch.bfloat16, torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    wide = 2 * G * N + 2 * H * P + 2 * H
+    Wi, Wo = rnd(D, wide) * D ** -0.5, rnd(H * P, D) * (H * P) ** -0.5
+    w1, w2, s = 1 + 0.1 * rnd(D), 1 + 0.1 * rnd(P), 0.5 + 0.1 * rnd(D)
+    A, bias = -1 - rnd(H).abs(), rnd(H) - 3
+    opts = dict(dt_bias=bias, dt_softplus=True, beta_sigmoid=True, qk_norm=True)
+    cuts = np.cumsum([0, G * N, G * N, H * P, H * P, H, H])
+
+    def cut(p):
+        part = [p[..., a:b] for a, b in zip(cuts[:-1], cuts[1:])]
+        return [t.unflatten(-1, sh) if sh else t for t, sh in
+                zip(part, ((G, N), (G, N), (H, P), (H, P), None, None))]
+
+    def forward(x, res):
+        y1, r = ssm.ssm_prenorm_fwd(x, w1, residual=res, scale=s)
+        q, k, v, z, dt, beta = cut((y1.float() @ Wi).to(bf))
+        y2, h, ws = ssm.ssm_gdr_fwd_save(q, k, v, dt, beta, A, **opts)
+        y3 = ssm.ssm_gated_norm_fwd(y2, z, w2)
+        out = (y3.float().flatten(-2) @ Wo).to(bf)
+        return out, r, h, (y1, q, k, v, z, dt, beta, y2, ws)
+    x, res = rnd(B, L, D).to(bf), rnd(B, L, D)
+    out, r, h, kept = forward(x, res)
+    # decode: the same block, a token at a time
+    state = torch.zeros(B, H, P, N, device="cuda")
+    steps = []
+    for t in range(L):
+        y1, _ = ssm.ssm_prenorm_fwd(x[:, t].contiguous(), w1, residual=res[:, t].contiguous(), scale=s)
+        q, k, v, z, dt, beta = cut((y1.float() @ Wi).to(bf))
+        y2 = ssm.ssm_gdr_state_update(q, k, v, dt, beta, A, state, **opts)
+        steps.append((ssm.ssm_gated_norm_fwd(y2, z, w2).float().flatten(-2) @ Wo).to(bf))
+    e = err(np64(torch.stack(steps, 1)), np64(out))
+    say("block decode against sequence: out %.2e, state %.2e" % (e, err(np64(state), np64(h))))
+    # two bf16 roundings of y2 and y3 on each side enter a sum of H * P terms of
+    # random sign, and out is rounded once more
+    assert e <= 8 * TOL_BF
+    # gradients: d loss along a random direction of x and res
+    dout, dr = rnd(B, L, D).to(bf), rnd(B, L, D)
+    y1, q, k, v, z, dt, beta, y2, ws = kept
+    dy3 = (dout.float() @ Wo.t()).unflatten(-1, (H, P)).to(bf).contiguous()
+    gn = ssm.ssm_gated_norm_bwd(dy3, y2, z, w2)
+    gd = ssm.ssm_gdr_bwd_saved(q, k, v, dt, beta, A, gn["dx"], ws, **opts)
+    dp = torch.cat([gd["dq"].flatten(-2), gd["dk"].flatten(-2), gd["dv"].flatten(-2), gn["dz"].flatten(-2), gd["ddt"],
+                    gd["dbeta"]], -1)
+    dy1 = (dp.float() @ Wi.t()).to(bf).contiguous()
+    gp = ssm.ssm_prenorm_bwd(dy1, r, w1, dr=dr, x=x, scale=s)
+    torch.cuda.synchronize()
+    # the reference: the same block in fp64 through the references, differenced
+    n = {k_: np64(t) for k_, t in dict(Wi=Wi, Wo=Wo, w1=w1, w2=w2, s=s, A=A, bias=bias, dout=dout, dr=dr, x=x, res=res).items()}
+    dirx, dirr = np64(rnd(B, L, D)), np64(rnd(B, L, D))
+
+    def loss(eps):
+        y1_, r_ = delta.prenorm(n["x"] + eps * dirx, n["w1"], n["res"] + eps * dirr, n["s"])
+        q_, k_, v_, z_, dt_, b_ = cut(torch.from_numpy(y1_ @ n["Wi"]))
+        y2_, _ = delta.delta_rule(q_.numpy(), k_.numpy(), v_.numpy(), dt_.numpy(), b_.numpy(), n["A"], dt_bias=n["bias"],
+                                  dt_softplus=True, beta_sigmoid=True, qk_norm=True)
+        y3_ = delta.gated_norm(y2_, z_.numpy(), n["w2"])
+        return (y3_.reshape(B, L, -1) @ n["Wo"] * n["dout"]).sum() + (r_ * n["dr"]).sum()
+    want = (loss(1e-4) - loss(-1e-4)) / 2e-4
+    got = float((np64(gp["dx"]) * dirx).sum() + (np64(gp["dresidual"]) * dirr).sum())
+    size = float(np.sqrt((np64(gp["dx"]) ** 2).sum() + (np64(gp["dresidual"]) ** 2).sum()))
+    say("block gradient along a direction: %.5f, differences %.5f, norm %.3f" % (got, want, size))
+    # ten bf16 roundings (2^-8 each, of random sign per element) lie between; a
+    # projection on a random direction of unit variance sees their norm
+    assert abs(got - want) <= 10 * 2.0 ** -8 * size

@@ -1,0 +1,331 @@
+"""GPU: the gated delta rule (sequence, gradients, one token) against the fp64
+reference, token by token, through the public binding.
+
+Tolerances, all relative to max(|reference|, rms of the reference):
+* bf16 outputs: one rounding, 2^-8, and 2^-12 for what precedes it.
+* fp32 states: sums of up to 64 tokens and 128 + 64 products each, every term
+  and partial sum within half a step of fp32: 256 * 2^-24.
+* dA, ddt_bias: the same, relative to the sum of their terms' magnitudes.
+"""
+import numpy as np
+import pytest
+
+from gpu_util import say, torch_cuda
+from oracle import delta
+
+pytestmark = pytest.mark.gpu
+
+TOL_BF = 2.0 ** -8 + 2.0 ** -12
+TOL_32 = 256 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = torch_cuda()
+    import selective_state_space_78_amd as ssm
+    ssm.lib()
+    return torch, ssm
+
+
+def err(got, ref):
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    assert got.shape == ref.shape and np.isfinite(got).all()
+    if got.size == 0:
+        return 0.0
+    rms = float(np.sqrt(np.mean(ref * ref)))
+    return float(np.max(np.abs(got - ref) / np.maximum(np.maximum(np.abs(ref), rms), 1e-30)))
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def inputs(torch, seed, B, L, G, H, P, N, strided=False, h0=True, bias=True, unit=False, grads=False, spread=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")
+    bf = torch.bfloat16
+    q, k, v = rnd(B, L, G, N), rnd(B, L, G, N) + 0.3, rnd(B, L, H, P)
+    if unit:
+        k = k / k.norm(dim=-1, keepdim=True)
+        q = q / q.norm(dim=-1, keepdim=True)
+    q, k, v, dt, beta = q.to(bf), k.to(bf), v.to(bf), (spread * rnd(B, L, H)).to(bf), rnd(B, L, H).to(bf)
+    if strided:
+        row = torch.cat([q.reshape(B, L, G * N), k.reshape(B, L, G * N), v.reshape(B, L, H * P), dt, beta,
+                         rnd(B, L, (-2 * H) % 8 + 8).to(bf)], -1)
+        cut = np.cumsum([0, G * N, G * N, H * P, H, H])
+        q, k = (row[..., a:b].unflatten(-1, (G, N)) for a, b in ((cut[0], cut[1]), (cut[1], cut[2])))
+        v = row[..., cut[2]:cut[3]].unflatten(-1, (H, P))
+        dt, beta = row[..., cut[3]:cut[4]], row[..., cut[4]:cut[5]]
+    x = dict(q=q, k=k, v=v, dt=dt, beta=beta, A=-(0.05 + 2.0 * torch.rand(H, generator=g, device="cuda")))
+    x["h0"] = rnd(B, H, P, N) if h0 else None
+    x["dt_bias"] = rnd(H) - 2.0 if bias else None
+    if grads:
+        x["dy"], x["dh_last"] = rnd(B, L, H, P).to(bf), rnd(B, H, P, N)
+    return x
+
+
+OPTS = dict(dt_softplus=True, beta_sigmoid=True, qk_norm=True)
+
+
+def reference(x, **opts):
+    return delta.delta_rule(**{n: None if t is None else np64(t) for n, t in x.items()}, **opts)
+
+
+def check_fwd(torch, ssm, x, **opts):
+    y, h = ssm.ssm_gdr_fwd(**x, **opts)
+    torch.cuda.synchronize()
+    yr, hr = reference(x, **opts)
+    ey, eh = err(np64(y), yr), err(np64(h), hr)
+    say("  y %.2e, h_last %.2e" % (ey, eh))
+    assert ey <= TOL_BF and eh <= TOL_32, (ey, eh)
+    return y, h
+
+
+def check_grads(torch, ssm, x, saved=True, **opts):
+    ins = {n: t for n, t in x.items() if n not in ("dy", "dh_last")}
+    if saved:
+        _, _, ws = ssm.ssm_gdr_fwd_save(**ins, **opts)
+        g = ssm.ssm_gdr_bwd_saved(**x, saved=ws, **opts)
+    else:
+        g = ssm.ssm_gdr_bwd(**x, **opts)
+    torch.cuda.synchronize()
+    ref = reference(x, **opts)[2]
+    e = {n: err(np64(g[n]), ref[n]) for n in ("dq", "dk", "dv", "ddt", "dbeta", "dh0")}
+    for n in ("dA", "ddt_bias"):
+        if g[n] is not None:
+            e[n] = float(np.max(np.abs(np64(g[n]) - ref[n]) / np.maximum(ref[n + "_abs"], 1e-30)))
+    say("  " + ", ".join("%s %.2e" % p for p in e.items()))
+    for n, v in e.items():
+        assert v <= (TOL_BF if n in ("dq", "dk", "dv", "ddt", "dbeta") else TOL_32), (n, v)
+    return g
+
+
+SHAPES = [   # B, L, G, H, P, N: one token to several chunks, ragged ends, every split of columns
+    (1, 1, 1, 1, 16, 64), (2, 2, 1, 2, 48, 128), (1, 63, 2, 2, 64, 64), (2, 64, 1, 3, 80, 128), (1, 65, 3, 3, 96, 64),
+    (2, 130, 2, 4, 128, 128), (1, 200, 1, 1, 256, 128), (3, 77, 2, 6, 112, 64), (1, 257, 1, 5, 160, 64)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("strided", [False, True])
+def test_forward(env, shape, strided):
+    torch, ssm = env
+    say("gdr forward", shape, "strided" if strided else "dense")
+    check_fwd(torch, ssm, inputs(torch, sum(shape), *shape, strided=strided), **OPTS)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("strided", [False, True])
+def test_gradients(env, shape, strided):
+    torch, ssm = env
+    say("gdr gradients", shape, "strided" if strided else "dense")
+    check_grads(torch, ssm, inputs(torch, sum(shape), *shape, strided=strided, grads=True), **OPTS)
+
+
+@pytest.mark.parametrize("softplus,sigmoid,norm", [(False, False, False), (True, False, False), (False, True, True)])
+def test_options(env, softplus, sigmoid, norm):
+    """Steps and strengths as given, without initial state, bias or a gradient
+    of the last state; another readout scale."""
+    torch, ssm = env
+    x = inputs(torch, 5, 2, 100, 2, 4, 64, 64, h0=False, bias=softplus, unit=not norm, grads=True)
+    x["dh_last"] = None
+    if not softplus:
+        x["dt"] = x["dt"].abs()
+    if not sigmoid:
+        x["beta"] = (x["beta"].abs() * 0.3).clamp(max=1.0)
+    opts = dict(dt_softplus=softplus, beta_sigmoid=sigmoid, qk_norm=norm, scale=0.3)
+    say("gdr options", opts)
+    check_fwd(torch, ssm, {n: t for n, t in x.items() if n not in ("dy", "dh_last")}, **opts)
+    check_grads(torch, ssm, x, saved=False, **opts)
+
+
+def test_repeated_keys(env):
+    """Every key the same and every strength 1: the chunk's triangular system at
+    its least regular (its entries do not decay away from the diagonal)."""
+    torch, ssm = env
+    x = inputs(torch, 6, 1, 150, 1, 2, 32, 64, unit=True, grads=True)
+    x["k"] = x["k"][:, :1].expand_as(x["k"]).contiguous()
+    x["beta"] = torch.ones_like(x["beta"])
+    x["A"] = torch.tensor([-1e-4, 0.0], device="cuda")
+    say("gdr repeated keys")
+    check_fwd(torch, ssm, {n: t for n, t in x.items() if n not in ("dy", "dh_last")}, dt_softplus=True)
+    check_grads(torch, ssm, x, dt_softplus=True)
+
+
+def test_resets_and_idle_tokens(env):
+    """Tokens that forget everything (a decay of exp(-1e4)), tokens that write
+    nothing (strength 0), and zero keys and queries under unit lengths."""
+    torch, ssm = env
+    x = inputs(torch, 7, 2, 140, 1, 2, 48, 128, bias=False, grads=True)
+    x["dt"] = x["dt"].abs() * 0.1
+    x["dt"][:, 30] = 1e4
+    x["dt"][:, 101:104] = 300.0
+    x["beta"] = x["beta"].abs().clamp(max=1.0)
+    x["beta"][:, 40:60] = 0.0
+    x["k"][:, 70] = 0.0
+    x["q"][:, 71] = 0.0
+    x["A"] = torch.tensor([-1.0, -0.5], device="cuda")
+    opts = dict(qk_norm=True, qk_eps=1e-3)
+    say("gdr resets")
+    check_fwd(torch, ssm, {n: t for n, t in x.items() if n not in ("dy", "dh_last")}, **opts)
+    check_grads(torch, ssm, x, **opts)
+
+
+def test_split_and_resume(env):
+    """Two calls, the second continuing the first's state in place, equal one
+    over the whole, also where the cut is inside a chunk."""
+    torch, ssm = env
+    x = inputs(torch, 8, 2, 150, 1, 2, 64, 128)
+    y, h = ssm.ssm_gdr_fwd(**x, **OPTS)
+    for cut in (64, 101):
+        def part(a, b):
+            return {n: (t[:, a:b].contiguous() if n in ("q", "k", "v", "dt", "beta") else t) for n, t in x.items()}
+        y1, state = ssm.ssm_gdr_fwd(**part(0, cut), **OPTS)
+        y2, _ = ssm.ssm_gdr_fwd(**dict(part(cut, 150), h0=state), h_last=state, **OPTS)
+        torch.cuda.synchronize()
+        ey, eh = err(np64(torch.cat([y1, y2], 1)), np64(y)), err(np64(state), np64(h))
+        say("gdr split at %d: y %.2e, h %.2e" % (cut, ey, eh))
+        # each side within its own rounding of the exact value
+        assert ey <= 2 * TOL_BF and eh <= 2 * TOL_32
+
+
+@pytest.mark.parametrize("shape", [(1, 16, 32, 128, 128), (3, 2, 6, 48, 64), (2, 1, 3, 256, 128), (70, 1, 1, 16, 64)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_steps(env, shape, strided):
+    """Three tokens one at a time, the state in place and once to a second
+    buffer, against the reference, and the layer of length one."""
+    torch, ssm = env
+    B, G, H, P, N = shape
+    x = inputs(torch, sum(shape), B, 3, G, H, P, N, strided=strided)
+    yr, hr = reference(x, **OPTS)
+    h = x["h0"].clone()
+    for t in range(3):
+        tok = [x[n][:, t] for n in ("q", "k", "v", "dt", "beta")]
+        if t == 1:
+            out = torch.full_like(h, float("nan"))
+            keep = h.clone()
+            y = ssm.ssm_gdr_state_update(*tok, x["A"], h, h_out=out, dt_bias=x["dt_bias"], **OPTS)
+            torch.cuda.synchronize()
+            assert torch.equal(h, keep)
+            h = out
+        else:
+            y = ssm.ssm_gdr_state_update(*tok, x["A"], h, dt_bias=x["dt_bias"], **OPTS)
+        torch.cuda.synchronize()
+        assert err(np64(y), yr[:, t]) <= TOL_BF, t
+    e = err(np64(h), hr)
+    say("gdr steps", shape, "h %.2e" % e)
+    assert e <= TOL_32
+
+
+def test_empty(env):
+    torch, ssm = env
+    x = inputs(torch, 9, 2, 0, 1, 2, 32, 64, grads=True)
+    ins = {n: t for n, t in x.items() if n not in ("dy", "dh_last")}
+    y, h = ssm.ssm_gdr_fwd(**ins, **OPTS)
+    assert y.shape == (2, 0, 2, 32) and torch.equal(h, x["h0"])
+    g = ssm.ssm_gdr_bwd(**x, **OPTS)
+    assert torch.equal(g["dh0"], x["dh_last"]) and not g["dA"].any() and not g["ddt_bias"].any()
+    _, h = ssm.ssm_gdr_fwd(**dict(ins, h0=None), **OPTS)
+    assert not h.any()
+    z = inputs(torch, 9, 0, 5, 1, 2, 32, 64, grads=True)
+    g = ssm.ssm_gdr_bwd(**z, **OPTS)
+    assert g["dq"].numel() == 0 and not g["dA"].any()
+
+
+def test_neighbours_untouched(env):
+    """What lies around the outputs keeps its values, at a ragged end and a
+    head size that ends inside a workgroup's columns."""
+    torch, ssm = env
+    B, L, G, H, P, N = 1, 70, 1, 2, 48, 64
+    x = inputs(torch, 10, B, L, G, H, P, N, grads=True)
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 512,), 7.0, dtype=dtype, device="cuda")
+        return buf, buf[256:256 + n].view(shape)
+    spec = dict(dq=((B, L, G, N), torch.bfloat16), dk=((B, L, G, N), torch.bfloat16), dv=((B, L, H, P), torch.bfloat16),
+                ddt=((B, L, H), torch.bfloat16), dbeta=((B, L, H), torch.bfloat16), dA=((H,), torch.float32),
+                ddt_bias=((H,), torch.float32), dh0=((B, H, P, N), torch.float32))
+    bufs = {n: guarded(*s) for n, s in spec.items()}
+    by, y = guarded((B, L, H, P), torch.bfloat16)
+    bh, h = guarded((B, H, P, N), torch.float32)
+    ins = {n: t for n, t in x.items() if n not in ("dy", "dh_last")}
+    need = ssm.ssm_gdr_bwd_workspace_size(B, L, H, P, G, N)
+    bw = torch.full((need + 512,), 9, dtype=torch.uint8, device="cuda")
+    ws = bw[256:256 + need]
+    _, _, saved = ssm.ssm_gdr_fwd_save(**ins, y=y, h_last=h, workspace=ws, **OPTS)
+    ssm.ssm_gdr_bwd_saved(**x, saved=saved, out={n: v for n, (_, v) in bufs.items()}, **OPTS)
+    torch.cuda.synchronize()
+    for n, b in list((n, b) for n, (b, _) in bufs.items()) + [("y", by), ("h", bh)]:
+        assert bool((b[:256] == 7).all()) and bool((b[-256:] == 7).all()), n
+    assert bool((bw[:256] == 9).all()) and bool((bw[-256:] == 9).all())
+
+
+def test_same_bits_and_recomputation(env):
+    """Runs repeat bit for bit, the saved and the recomputing backward agree bit
+    for bit, and a saved workspace serves twice."""
+    torch, ssm = env
+    x = inputs(torch, 11, 2, 200, 2, 4, 96, 128, grads=True)
+    ins = {n: t for n, t in x.items() if n not in ("dy", "dh_last")}
+    a = ssm.ssm_gdr_bwd(**x, **OPTS)
+    y, h, ws = ssm.ssm_gdr_fwd_save(**ins, **OPTS)
+    y2, h2 = ssm.ssm_gdr_fwd(**ins, **OPTS)
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    for _ in range(2):
+        b = ssm.ssm_gdr_bwd_saved(**x, saved=ws, **OPTS)
+        for n in a:
+            assert torch.equal(a[n], b[n]), n
+
+
+def test_streams_and_graph(env):
+    """On a stream of its own, and captured: the replays, with new inputs and
+    eager work between them, equal the eager results."""
+    torch, ssm = env
+    x = inputs(torch, 12, 1, 130, 1, 2, 64, 64, grads=True)
+    ins = {n: t for n, t in x.items() if n not in ("dy", "dh_last")}
+    ws = torch.empty(ssm.ssm_gdr_bwd_workspace_size(1, 130, 2, 64, 1, 64), dtype=torch.uint8, device="cuda")
+
+    def step():
+        y, h, _ = ssm.ssm_gdr_fwd_save(**ins, workspace=ws, **OPTS)
+        return (y, h, *[g for g in ssm.ssm_gdr_bwd_saved(**x, saved=ws, **OPTS).values()])
+    want = step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = step()
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for k in range(4):
+        x["v"].copy_(torch.randn_like(x["v"]))
+        x["dy"].copy_(torch.randn_like(x["dy"]))
+        graph.replay()
+        kept = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(want, kept):
+            assert torch.equal(a, b), k
+
+
+def test_refusals(env):
+    torch, ssm = env
+    x = inputs(torch, 13, 2, 10, 1, 2, 32, 64)
+    with pytest.raises(ssm.SsmError) as e:
+        ssm.ssm_gdr_fwd(**{n: (t.float() if n in ("q", "k", "v", "dt", "beta") else t) for n, t in x.items()})
+    assert e.value.status == -4
+    with pytest.raises(TypeError):
+        ssm.ssm_gdr_fwd(**dict(x, k=x["k"].float()))
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_fwd(**dict(x, k=x["k"][:, :9]))
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_fwd(**dict(x, q=x["q"].transpose(0, 1).contiguous().transpose(0, 1)))   # batch rows interleaved
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_fwd(**dict(x, k=x["k"][:, :1].expand_as(x["k"])))                        # rows overlap
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_fwd(**dict(x, A=x["A"].cpu()))
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_fwd(**x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_bwd_saved(**x, dy=x["v"], saved=None)
