@@ -85,7 +85,8 @@ struct GdrParams {
 #ifdef SSM_GDR_INSTANTIATE
 
 constexpr int kGdrPad = 8;                 // LDS row padding of K, Q (elements)
-constexpr int kGdrMS = kGdrC + 8;          // LDS row stride of C x C operands
+constexpr int kGdrRS = kGdrC + 4;          // LDS row stride of C x C operands: 8-byte reads down a column of rows free of conflicts
+constexpr int kGdrPlane = kGdrC * kGdrRS;  // one bf16 part of one
 constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ ssd_f32x4 gdr_zero4() { return ssd_f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
@@ -367,23 +368,12 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
     }
 }
 
-// The 10 lower tiles of a chunk's matrix into PARTS bf16 planes of LDS, row major
-template <int PARTS>
-__device__ __forceinline__ void gdr_stage_tiles(uint16_t *dst, const float *src, int tid, int threads) {
-    for (int q = tid; q < kGdrTiles * 64; q += threads) {
-        const int t = q >> 6, i = (q >> 2) & 15, c = q & 3;
-        const int T = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - T * (T + 1) / 2;
-        gdr_store_parts<PARTS>(dst + (16 * T + i) * kGdrMS + 16 * J + 4 * c, kGdrC * kGdrMS,
-                               *reinterpret_cast<const float4 *>(src + 4 * q));
-    }
-}
-
 // the two tiles above the diagonal that share a 32-token operand with one on it
 template <int PARTS>
 __device__ __forceinline__ void gdr_zero_upper(uint16_t *dst, int tid, int threads) {
     for (int q = tid; q < PARTS * 2 * 64; q += threads) {
         const int plane = q >> 7, t = (q >> 6) & 1, i = (q >> 2) & 15, c = q & 3;
-        *reinterpret_cast<uint2 *>(dst + plane * kGdrC * kGdrMS + (32 * t + i) * kGdrMS + 32 * t + 16 + 4 * c) =
+        *reinterpret_cast<uint2 *>(dst + plane * kGdrPlane + (32 * t + i) * kGdrRS + 32 * t + 16 + 4 * c) =
             uint2{0u, 0u};
     }
 }
@@ -394,255 +384,411 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward over the chunks. A wave holds columns p0 .. p0 + 15.
-template <int N, bool SAVE>
-__global__ __launch_bounds__(512) void gdr_fwd_kernel(const GdrParams p, int splits) {
-    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrC * kGdrMS;
-    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
-    __shared__ __attribute__((aligned(16))) uint16_t sR[3 * PL], sA[2 * PL];
-    __shared__ __attribute__((aligned(16))) float sTab[4 * kGdrC];
-    __shared__ float sEnd;
+// The kernels that walk the chunks.
+//
+// A workgroup of NW waves takes 16 NW columns of one head. The next chunk's
+// rows and matrices are loaded into registers while this one is computed, and
+// written to the other half of double-buffered LDS (the C x C matrices split
+// into bf16 planes on the way) at the start of the next, so a chunk costs one
+// barrier and no wait on memory.
+//
+// The matrix cores round a sum towards minus infinity (measured: states had a
+// mean error of -4e-8 of their mean size, positive and negative ones alike),
+// which over many chunks would add up where the gradient of the decay sums
+// them. So the state's sign alternates: odd chunks hold -S, through the signs
+// of the scales that are applied anyway, and the errors cancel.
+
+// LDS of one chunk: K and Q rows, R in three parts, the first four tables and
+// the decay over the whole chunk. The scores are apart.
+template <int N> struct GdrChunkLds {
+    uint16_t k[kGdrC * (N + kGdrPad)], q[kGdrC * (N + kGdrPad)];
+    uint16_t r[3 * kGdrPlane];
+    float tab[4 * kGdrC];
+    float end[4];
+};
+
+template <int N, int NW> struct GdrChunkRegs {
+    static constexpr int TH = 64 * NW, KS = N + kGdrPad;
+    static constexpr int KI = kGdrC * N / 8 / TH, RI = (kGdrTiles * 64 + TH - 1) / TH, TI = (4 * kGdrC + TH - 1) / TH;
+    uint4 k[KI], q[KI];
+    float4 r[RI], a[RI];
+    float tab[TI], end;
+    __device__ __forceinline__ void load(const GdrParams &p, int b, int g, int64_t id, int ci, int tid) {
+        const uint32_t nv = (uint32_t)gdr_valid(p, ci);
+        const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
+        const uint32_t ks = (uint32_t)p.ks, qs = (uint32_t)p.qs;
+        // rows past the end have offsets past the ranges: they read zero
+        const __amdgpu_buffer_rsrc_t rk = ssd_buffer(p.k + row0 * p.ks + (int64_t)g * N, 2u * ((nv - 1) * ks + N));
+        const __amdgpu_buffer_rsrc_t rq = ssd_buffer(p.q + row0 * p.qs + (int64_t)g * N, 2u * ((nv - 1) * qs + N));
+        const __amdgpu_buffer_rsrc_t rr = ssd_buffer(p.R + id * (kGdrTiles * 256), kGdrTiles * 1024);
+        const __amdgpu_buffer_rsrc_t ra = ssd_buffer(p.score + id * (kGdrTiles * 256), kGdrTiles * 1024);
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const uint32_t x = i * TH + tid, row = x / (N / 8), c = 8 * (x % (N / 8));
+            k[i] = ssd_bload16(rk, 2u * (row * ks + c));
+            q[i] = ssd_bload16(rq, 2u * (row * qs + c));
+        }
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+            r[i] = __builtin_bit_cast(float4, ssd_bload16(rr, 16u * (i * TH + tid)));
+            a[i] = __builtin_bit_cast(float4, ssd_bload16(ra, 16u * (i * TH + tid)));
+        }
+        const float *t = p.tab + id * (kGdrTab * kGdrC);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) tab[i] = t[(i * TH + tid) & (4 * kGdrC - 1)];
+        end = t[kTHead * kGdrC + kGdrC - 1];
+    }
+    // element of a row-major C x C plane that this thread's i-th piece of the tiles starts at
+    static __device__ __forceinline__ int place(int x) {
+        const int t = x >> 6, T = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - T * (T + 1) / 2;
+        return (16 * T + ((x >> 2) & 15)) * kGdrRS + 16 * J + 4 * (x & 3);
+    }
+    template <int AP> __device__ __forceinline__ void store_scores(uint16_t *dst, int tid) const {
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
+            if (i * TH + tid < kGdrTiles * 64) gdr_store_parts<AP>(dst + place(i * TH + tid), kGdrPlane, a[i]);
+    }
+    __device__ __forceinline__ void store(GdrChunkLds<N> &s, int tid) const {
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int x = i * TH + tid, o = (x / (N / 8)) * KS + 8 * (x % (N / 8));
+            *reinterpret_cast<uint4 *>(&s.k[o]) = k[i];
+            *reinterpret_cast<uint4 *>(&s.q[o]) = q[i];
+        }
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
+            if (i * TH + tid < kGdrTiles * 64) gdr_store_parts<3>(&s.r[place(i * TH + tid)], kGdrPlane, r[i]);
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            if (TH * TI == 4 * kGdrC || i * TH + tid < 4 * kGdrC) s.tab[i * TH + tid] = tab[i];
+        if (tid == 0) s.end[0] = end;
+    }
+};
+
+// a 16 x 16 tile's products of parts, small ones first, each over every T in
+// turn so that consecutive instructions do not wait for one another
+template <int N, bool SAVE, int NW>
+__global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int splits) {
+    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrPlane;
+    __shared__ __attribute__((aligned(16))) GdrChunkLds<N> lds[2];
+    __shared__ __attribute__((aligned(16))) uint16_t sA[2][2 * PL];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int threads = blockDim.x;
     const int r16 = lane & 15, g4 = lane >> 4;
     const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
     const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
-    const int p0 = 16 * (split * (threads >> 6) + w);
+    const int p0 = 16 * (split * NW + w);
     const bool live = p0 < p.P;
     const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
+    const uint32_t vs = (uint32_t)p.vs, ysr = (uint32_t)(p.H * p.P);
+    const int64_t id0 = (int64_t)bh * p.nc, rowb = (int64_t)b * p.L;
     ssd_f32x4 S[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         S[nt] = live && p.h0 ? gdr_ld4(p.h0 + sbase + 16 * nt + 4 * g4) : gdr_zero4();
-    gdr_zero_upper<3>(sR, tid, threads);
-    gdr_zero_upper<2>(sA, tid, threads);
+    for (int k = 0; k < 2; ++k) {
+        gdr_zero_upper<3>(lds[k].r, tid, 64 * NW);
+        gdr_zero_upper<2>(sA[k], tid, 64 * NW);
+    }
+    uint16_t vn[16];
+    auto load_v = [&](int ci) {
+        const uint32_t nv = (uint32_t)gdr_valid(p, ci);
+        const __amdgpu_buffer_rsrc_t rv = ssd_buffer(p.v + (rowb + (int64_t)ci * kGdrC) * p.vs + (int64_t)h * p.P,
+                                                     2u * ((nv - 1) * vs + (uint32_t)p.P));
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            vn[e] = __builtin_amdgcn_raw_buffer_load_b16(
+                rv, (int)(2u * ((uint32_t)(16 * (e >> 2) + 4 * g4 + (e & 3)) * vs + p0 + r16)), 0, 0);
+    };
+    GdrChunkRegs<N, NW> regs;
+    regs.load(p, b, g, id0, 0, tid);
+    if (live) load_v(0);
+    regs.store(lds[0], tid);
+    regs.template store_scores<2>(sA[0], tid);
+    if (p.nc > 1) regs.load(p, b, g, id0 + 1, 1, tid);
+    __syncthreads();
+    float sign = 1.0f;
     for (int ci = 0; ci < p.nc; ++ci) {
+        const GdrChunkLds<N> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
-        const int64_t id = (int64_t)bh * p.nc + ci;
-        const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
-        __syncthreads();
-        gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, threads);
-        gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, threads);
-        gdr_stage_tiles<3>(sR, p.R + id * (kGdrTiles * 256), tid, threads);
-        gdr_stage_tiles<2>(sA, p.score + id * (kGdrTiles * 256), tid, threads);
-        const float *tab = p.tab + id * (kGdrTab * kGdrC);
-        for (int q = tid; q < 4 * kGdrC; q += threads) sTab[q] = tab[q];
-        if (tid == 0) sEnd = tab[kTHead * kGdrC + kGdrC - 1];
-        __syncthreads();
-        if (!live) continue;
-        if constexpr (SAVE) {
-            float *dst = p.S + (id * p.P + p0 + r16) * N + 4 * g4;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = S[nt];
+        const int64_t id = id0 + ci;
+        const int64_t row0 = rowb + (int64_t)ci * kGdrC;
+        if (ci + 1 < p.nc) {
+            regs.store(lds[(ci + 1) & 1], tid);
+            regs.template store_scores<2>(sA[(ci + 1) & 1], tid);
         }
-        ssd_f32x4 X[4], Y[4];
+        if (ci + 2 < p.nc) regs.load(p, b, g, id + 2, ci + 2, tid);
+        if (live) {
+            float vc[16];
 #pragma unroll
-        for (int T = 0; T < 4; ++T) X[T] = Y[T] = gdr_zero4();
+            for (int e = 0; e < 16; ++e) vc[e] = ssd_bf(vn[e]) * sign;
+            if (ci + 1 < p.nc) load_v(ci + 1);
+            if constexpr (SAVE) {
+                float *dst = p.S + (id * p.P + p0 + r16) * N + 4 * g4;
 #pragma unroll
-        for (int s = 0; s < N / 32; ++s) {
-            const GdrSplit<3> so = gdr_split<3>(S[2 * s], S[2 * s + 1]);
-            GdrSplit<2> so2;
-            so2.part[0] = so.part[0];
-            so2.part[1] = so.part[1];
+                for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = S[nt] * sign;
+            }
+            ssd_f32x4 X[4], Y[4], U[4];
+#pragma unroll
+            for (int T = 0; T < 4; ++T) X[T] = Y[T] = U[T] = gdr_zero4();
+#pragma unroll
+            for (int s = 0; s < N / 32; ++s) {
+                const GdrSplit<3> so = gdr_split<3>(S[2 * s], S[2 * s + 1]);
+                ssd_bf16x8 ko[4], qo[4];
+#pragma unroll
+                for (int T = 0; T < 4; ++T) {
+                    const int o = (16 * T + r16) * KS + 32 * s + 4 * g4;
+                    ko[T] = gdr_ld_perm(&L.k[o]);
+                    qo[T] = gdr_ld_perm(&L.q[o]);
+                }
+#pragma unroll
+                for (int k = 2; k >= 0; --k)
+#pragma unroll
+                    for (int T = 0; T < 4; ++T) {
+                        X[T] = ssd_mfma(ko[T], so.part[k], X[T]);
+                        if (k < 2) Y[T] = ssd_mfma(so.part[k], qo[T], Y[T]);
+                    }
+            }
+            // beta X
 #pragma unroll
             for (int T = 0; T < 4; ++T) {
-                const int o = (16 * T + r16) * KS + 32 * s + 4 * g4;
-                X[T] = gdr_mfma(gdr_whole(gdr_ld_perm(&sK[o])), so, X[T]);
-                Y[T] = gdr_mfma(so2, gdr_whole(gdr_ld_perm(&sQ[o])), Y[T]);
+                const ssd_f32x4 hk = gdr_ld4(&L.tab[kTHk * kGdrC + 16 * T + 4 * g4]);
+                const ssd_f32x4 be = gdr_ld4(&L.tab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[T][r] = be[r] * (vc[4 * T + r] - hk[r] * X[T][r]);
+            }
+            // U = R (beta X)
+            {
+                const GdrSplit<3> xo[2] = {gdr_split<3>(X[0], X[1]), gdr_split<3>(X[2], X[3])};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    GdrSplit<3> ro[4];
+#pragma unroll
+                    for (int T = 2 * s; T < 4; ++T)
+                        ro[T] = gdr_ld_perm_parts<3>(&L.r[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL);
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)
+#pragma unroll
+                        for (int i = 0; i <= k; ++i)
+#pragma unroll
+                            for (int T = 2 * s; T < 4; ++T) U[T] = ssd_mfma(ro[T].part[i], xo[s].part[k - i], U[T]);
+                }
+            }
+            if constexpr (SAVE) {
+                float *dst = p.U + (id * p.P + p0 + r16) * kGdrC + 4 * g4;
+#pragma unroll
+                for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = U[T] * sign;
+            }
+            // Y^T = exp(G) S Q^T + U^T A^T; the backward's recomputation stores none
+            if (p.y != nullptr) {
+                const __amdgpu_buffer_rsrc_t ry = ssd_buffer(p.y + (row0 * p.H + h) * p.P,
+                                                             2u * ((uint32_t)(nv - 1) * ysr + (uint32_t)p.P));
+                const GdrSplit<2> uo[2] = {gdr_split<2>(U[0], U[1]), gdr_split<2>(U[2], U[3])};
+#pragma unroll
+                for (int T = 0; T < 4; ++T) Y[T] *= L.tab[kTHq * kGdrC + 16 * T + r16];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    GdrSplit<2> ao[4];
+#pragma unroll
+                    for (int T = 2 * s; T < 4; ++T)
+                        ao[T] = gdr_ld_perm_parts<2>(&sA[ci & 1][(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL);
+#pragma unroll
+                    for (int k = 1; k >= 0; --k)
+#pragma unroll
+                        for (int i = 0; i <= k; ++i)
+#pragma unroll
+                            for (int T = 2 * s; T < 4; ++T) Y[T] = ssd_mfma(uo[s].part[k - i], ao[T].part[i], Y[T]);
+                }
+                // rows past the end are dropped by the buffer's range
+#pragma unroll
+                for (int T = 0; T < 4; ++T)
+                    ssd_bstore8(ry, 2u * ((uint32_t)(16 * T + r16) * ysr + p0 + 4 * g4),
+                                uint2{ssd_pack(sign * Y[T][0], sign * Y[T][1]), ssd_pack(sign * Y[T][2], sign * Y[T][3])});
+            }
+            // -S' = -exp(G_C) S - K^T (exp(G_C - G) U)
+#pragma unroll
+            for (int T = 0; T < 4; ++T) U[T] *= -gdr_ld4(&L.tab[kTTk * kGdrC + 16 * T + 4 * g4]);
+            const float end = -L.end[0];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) S[nt] *= end;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const GdrSplit<3> uo = gdr_split<3>(U[2 * s], U[2 * s + 1]);
+                ssd_bf16x8 ko[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) ko[nt] = gdr_ld_col(L.k, KS, 32 * s + 4 * g4, 16 * nt, r16);
+#pragma unroll
+                for (int k = 2; k >= 0; --k)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) S[nt] = ssd_mfma(ko[nt], uo.part[k], S[nt]);
             }
         }
-        // beta X, from v
-        const __amdgpu_buffer_rsrc_t rv =
-            ssd_buffer(p.v + row0 * p.vs + (int64_t)h * p.P, 2u * ((uint32_t)(nv - 1) * (uint32_t)p.vs + p.P));
-#pragma unroll
-        for (int T = 0; T < 4; ++T) {
-            const ssd_f32x4 hk = gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
-            const ssd_f32x4 be = gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * T + 4 * g4 + r;
-                const uint16_t vw = __builtin_amdgcn_raw_buffer_load_b16(
-                    rv, (int)(2u * ((uint32_t)i * (uint32_t)p.vs + p0 + r16)), 0, 0);
-                const float v = i < nv ? ssd_bf(vw) : 0.0f;
-                X[T][r] = be[r] * (v - hk[r] * X[T][r]);
-            }
-        }
-        // U = R (beta X)
-        ssd_f32x4 U[4];
-        GdrSplit<3> xo[2] = {gdr_split<3>(X[0], X[1]), gdr_split<3>(X[2], X[3])};
-#pragma unroll
-        for (int T = 0; T < 4; ++T) {
-            U[T] = gdr_zero4();
-#pragma unroll
-            for (int s = 0; s <= T / 2; ++s)
-                U[T] = gdr_mfma(gdr_ld_perm_parts<3>(&sR[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL), xo[s], U[T]);
-        }
-        if constexpr (SAVE) {
-            float *dst = p.U + (id * p.P + p0 + r16) * kGdrC + 4 * g4;
-#pragma unroll
-            for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = U[T];
-        }
-        // Y^T = exp(G) S Q^T + U^T A^T; the backward's recomputation stores none
-        if (p.y != nullptr) {
-            const GdrSplit<2> uo[2] = {gdr_split<2>(U[0], U[1]), gdr_split<2>(U[2], U[3])};
-            const __amdgpu_buffer_rsrc_t ry = ssd_buffer(p.y + (row0 * p.H + h) * p.P,
-                                                         2u * ((uint32_t)(nv - 1) * (uint32_t)(p.H * p.P) + p.P));
-#pragma unroll
-            for (int T = 0; T < 4; ++T) {
-                Y[T] *= sTab[kTHq * kGdrC + 16 * T + r16];
-#pragma unroll
-                for (int s = 0; s <= T / 2; ++s)
-                    Y[T] = gdr_mfma(uo[s], gdr_ld_perm_parts<2>(&sA[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL),
-                                    Y[T]);
-                if (16 * T + r16 < nv)
-                    ssd_bstore8(ry, 2u * ((uint32_t)(16 * T + r16) * (uint32_t)(p.H * p.P) + p0 + 4 * g4),
-                                uint2{ssd_pack(Y[T][0], Y[T][1]), ssd_pack(Y[T][2], Y[T][3])});
-            }
-        }
-        // S' = exp(G_C) S + K^T (exp(G_C - G) U)
-#pragma unroll
-        for (int T = 0; T < 4; ++T) U[T] *= gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
-        const float end = sEnd;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) S[nt] *= end;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const GdrSplit<3> uo = gdr_split<3>(U[2 * s], U[2 * s + 1]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                S[nt] = gdr_mfma(gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, 16 * nt, r16)), uo, S[nt]);
-        }
+        sign = -sign;
+        __syncthreads();
     }
     if (live && p.h_last)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(p.h_last + sbase + 16 * nt + 4 * g4) = S[nt];
+        for (int nt = 0; nt < NT; ++nt)
+            *reinterpret_cast<ssd_f32x4 *>(p.h_last + sbase + 16 * nt + 4 * g4) = S[nt] * sign;
 }
 
 // ---------------------------------------------------------------------------
 // Backwards over the chunks: D' of every chunk, W, dv and dh0.
-template <int N>
-__global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrParams p, int splits) {
-    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrC * kGdrMS;
-    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
-    __shared__ __attribute__((aligned(16))) uint16_t sR[3 * PL], sA[3 * PL];
-    __shared__ __attribute__((aligned(16))) float sTab[4 * kGdrC];
-    __shared__ float sEnd;
+template <int N, int NW>
+__global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int splits) {
+    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrPlane;
+    __shared__ __attribute__((aligned(16))) GdrChunkLds<N> lds[2];
+    // a third part of the scores in both halves would not fit: one copy, and a
+    // second barrier between its use and the next chunk's
+    __shared__ __attribute__((aligned(16))) uint16_t sA[3 * PL];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int threads = blockDim.x;
     const int r16 = lane & 15, g4 = lane >> 4;
     const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
     const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
-    const int p0 = 16 * (split * (threads >> 6) + w);
+    const int p0 = 16 * (split * NW + w);
     const bool live = p0 < p.P;
     const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
     const uint32_t ys = (uint32_t)(p.H * p.P);
+    const int64_t id0 = (int64_t)bh * p.nc, rowb = (int64_t)b * p.L;
     ssd_f32x4 D[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         D[nt] = live && p.dh_last ? gdr_ld4(p.dh_last + sbase + 16 * nt + 4 * g4) : gdr_zero4();
-    gdr_zero_upper<3>(sR, tid, threads);
-    gdr_zero_upper<3>(sA, tid, threads);
-    for (int ci = p.nc - 1; ci >= 0; --ci) {
+    for (int k = 0; k < 2; ++k) gdr_zero_upper<3>(lds[k].r, tid, 64 * NW);
+    gdr_zero_upper<3>(sA, tid, 64 * NW);
+    uint16_t dn[16];
+    auto load_dy = [&](int ci) {
+        const uint32_t nv = (uint32_t)gdr_valid(p, ci);
+        const __amdgpu_buffer_rsrc_t rd = ssd_buffer(p.dy + ((rowb + (int64_t)ci * kGdrC) * p.H + h) * p.P,
+                                                     2u * ((nv - 1) * ys + (uint32_t)p.P));
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            dn[e] = __builtin_amdgcn_raw_buffer_load_b16(
+                rd, (int)(2u * ((uint32_t)(16 * (e >> 2) + 4 * g4 + (e & 3)) * ys + p0 + r16)), 0, 0);
+    };
+    const int last = p.nc - 1;
+    GdrChunkRegs<N, NW> regs;
+    regs.load(p, b, g, id0 + last, last, tid);
+    if (live) load_dy(last);
+    regs.store(lds[last & 1], tid);
+    regs.template store_scores<3>(sA, tid);
+    if (last > 0) regs.load(p, b, g, id0 + last - 1, last - 1, tid);
+    __syncthreads();
+    float sign = 1.0f;
+    for (int ci = last; ci >= 0; --ci) {
+        const GdrChunkLds<N> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
-        const int64_t id = (int64_t)bh * p.nc + ci;
-        const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
-        __syncthreads();
-        gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, threads);
-        gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, threads);
-        gdr_stage_tiles<3>(sR, p.R + id * (kGdrTiles * 256), tid, threads);
-        gdr_stage_tiles<3>(sA, p.score + id * (kGdrTiles * 256), tid, threads);
-        const float *tab = p.tab + id * (kGdrTab * kGdrC);
-        for (int q = tid; q < 4 * kGdrC; q += threads) sTab[q] = tab[q];
-        if (tid == 0) sEnd = tab[kTHead * kGdrC + kGdrC - 1];
-        __syncthreads();
-        if (!live) continue;
-        {
-            float *dst = p.D + (id * p.P + p0 + r16) * N + 4 * g4;
+        const int64_t id = id0 + ci;
+        const int64_t row0 = rowb + (int64_t)ci * kGdrC;
+        if (ci > 0) regs.store(lds[(ci - 1) & 1], tid);
+        ssd_f32x4 dY[4], dU[4], W[4];
+        if (live) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = D[nt];
+            for (int e = 0; e < 16; ++e) dY[e >> 2][e & 3] = ssd_bf(dn[e]) * sign;
+            if (ci > 0) load_dy(ci - 1);
+            {
+                float *dst = p.D + (id * p.P + p0 + r16) * N + 4 * g4;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = D[nt] * sign;
+            }
+            // dU = exp(G_C - G) K D'^T + A^T dY
+#pragma unroll
+            for (int T = 0; T < 4; ++T) dU[T] = W[T] = gdr_zero4();
+#pragma unroll
+            for (int s = 0; s < N / 32; ++s) {
+                const GdrSplit<3> so = gdr_split<3>(D[2 * s], D[2 * s + 1]);
+                ssd_bf16x8 ko[4];
+#pragma unroll
+                for (int T = 0; T < 4; ++T) ko[T] = gdr_ld_perm(&L.k[(16 * T + r16) * KS + 32 * s + 4 * g4]);
+#pragma unroll
+                for (int k = 2; k >= 0; --k)
+#pragma unroll
+                    for (int T = 0; T < 4; ++T) dU[T] = ssd_mfma(ko[T], so.part[k], dU[T]);
+            }
+#pragma unroll
+            for (int T = 0; T < 4; ++T) dU[T] *= gdr_ld4(&L.tab[kTTk * kGdrC + 16 * T + 4 * g4]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const GdrSplit<1> yo = gdr_split<1>(dY[2 * s], dY[2 * s + 1]);   // exact
+                GdrSplit<3> ao[4];
+#pragma unroll
+                for (int T = 0; T < 2 * s + 2; ++T)
+                    ao[T] = gdr_ld_col_parts<3>(sA, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
+#pragma unroll
+                for (int k = 2; k >= 0; --k)
+#pragma unroll
+                    for (int T = 0; T < 2 * s + 2; ++T) dU[T] = ssd_mfma(ao[T].part[k], yo.part[0], dU[T]);
+            }
         }
-        // dY of the wave's columns
-        ssd_f32x4 dY[4];
-        {
-            const __amdgpu_buffer_rsrc_t rd =
-                ssd_buffer(p.dy + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + p.P));
+        __syncthreads();
+        if (ci > 0) regs.template store_scores<3>(sA, tid);
+        if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, tid);
+        if (live) {
+            // W = R^T dU
 #pragma unroll
-            for (int T = 0; T < 4; ++T)
+            for (int s = 0; s < 2; ++s) {
+                const GdrSplit<3> uo = gdr_split<3>(dU[2 * s], dU[2 * s + 1]);
+                GdrSplit<3> ro[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * T + 4 * g4 + r;
-                    const uint16_t vw =
-                        __builtin_amdgcn_raw_buffer_load_b16(rd, (int)(2u * ((uint32_t)i * ys + p0 + r16)), 0, 0);
-                    dY[T][r] = i < nv ? ssd_bf(vw) : 0.0f;
+                for (int T = 0; T < 2 * s + 2; ++T)
+                    ro[T] = gdr_ld_col_parts<3>(L.r, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
+#pragma unroll
+                for (int k = 2; k >= 0; --k)
+#pragma unroll
+                    for (int i = 0; i <= k; ++i)
+#pragma unroll
+                        for (int T = 0; T < 2 * s + 2; ++T) W[T] = ssd_mfma(ro[T].part[i], uo.part[k - i], W[T]);
+            }
+            {
+                float *dst = p.W + (id * p.P + p0 + r16) * kGdrC + 4 * g4;
+#pragma unroll
+                for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = W[T] * sign;
+            }
+            // dv = beta W (rows past the end dropped by the range); then the two sources of -D
+            const __amdgpu_buffer_rsrc_t rdv =
+                ssd_buffer(p.dv + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + (uint32_t)p.P));
+#pragma unroll
+            for (int T = 0; T < 4; ++T) {
+                W[T] *= gdr_ld4(&L.tab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b16(ssd_to_bf(sign * W[T][r]), rdv,
+                                                          (int)(2u * ((uint32_t)(16 * T + 4 * g4 + r) * ys + p0 + r16)),
+                                                          0, 0);
+                W[T] *= gdr_ld4(&L.tab[kTHk * kGdrC + 16 * T + 4 * g4]);
+                dY[T] *= -gdr_ld4(&L.tab[kTHq * kGdrC + 16 * T + 4 * g4]);
+            }
+            const float end = -L.end[0];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) D[nt] *= end;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const GdrSplit<3> wo = gdr_split<3>(W[2 * s], W[2 * s + 1]);
+                const GdrSplit<3> qo = gdr_split<3>(dY[2 * s], dY[2 * s + 1]);
+#pragma unroll
+                for (int n0 = 0; n0 < NT; n0 += 4) {
+                    ssd_bf16x8 ko[4], qr[4];
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        ko[nt] = gdr_ld_col(L.k, KS, 32 * s + 4 * g4, 16 * (n0 + nt), r16);
+                        qr[nt] = gdr_ld_col(L.q, KS, 32 * s + 4 * g4, 16 * (n0 + nt), r16);
+                    }
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt) {
+                            D[n0 + nt] = ssd_mfma(ko[nt], wo.part[k], D[n0 + nt]);
+                            D[n0 + nt] = ssd_mfma(qr[nt], qo.part[k], D[n0 + nt]);
+                        }
                 }
-        }
-        // dU = exp(G_C - G) K D'^T + A^T dY
-        ssd_f32x4 dU[4];
-#pragma unroll
-        for (int T = 0; T < 4; ++T) dU[T] = gdr_zero4();
-#pragma unroll
-        for (int s = 0; s < N / 32; ++s) {
-            const GdrSplit<3> so = gdr_split<3>(D[2 * s], D[2 * s + 1]);
-#pragma unroll
-            for (int T = 0; T < 4; ++T)
-                dU[T] = gdr_mfma(gdr_whole(gdr_ld_perm(&sK[(16 * T + r16) * KS + 32 * s + 4 * g4])), so, dU[T]);
-        }
-        const GdrSplit<1> yo[2] = {gdr_split<1>(dY[0], dY[1]), gdr_split<1>(dY[2], dY[3])};   // exact
-#pragma unroll
-        for (int T = 0; T < 4; ++T) {
-            dU[T] *= gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
-#pragma unroll
-            for (int s = T / 2; s < 2; ++s)
-                dU[T] = gdr_mfma(gdr_ld_col_parts<3>(sA, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), yo[s], dU[T]);
-        }
-        // W = R^T dU
-        ssd_f32x4 W[4];
-        const GdrSplit<3> uo[2] = {gdr_split<3>(dU[0], dU[1]), gdr_split<3>(dU[2], dU[3])};
-#pragma unroll
-        for (int T = 0; T < 4; ++T) {
-            W[T] = gdr_zero4();
-#pragma unroll
-            for (int s = T / 2; s < 2; ++s)
-                W[T] = gdr_mfma(gdr_ld_col_parts<3>(sR, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), uo[s], W[T]);
-        }
-        {
-            float *dst = p.W + (id * p.P + p0 + r16) * kGdrC + 4 * g4;
-#pragma unroll
-            for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = W[T];
-        }
-        // dv = beta W; then the two sources of D
-        const __amdgpu_buffer_rsrc_t rdv =
-            ssd_buffer(p.dv + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + p.P));
-#pragma unroll
-        for (int T = 0; T < 4; ++T) {
-            W[T] *= gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * T + 4 * g4 + r;
-                if (i < nv)
-                    __builtin_amdgcn_raw_buffer_store_b16(ssd_to_bf(W[T][r]), rdv,
-                                                          (int)(2u * ((uint32_t)i * ys + p0 + r16)), 0, 0);
-            }
-            W[T] *= -gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
-            dY[T] *= gdr_ld4(&sTab[kTHq * kGdrC + 16 * T + 4 * g4]);
-        }
-        const float end = sEnd;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) D[nt] *= end;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const GdrSplit<3> wo = gdr_split<3>(W[2 * s], W[2 * s + 1]);
-            const GdrSplit<3> qo = gdr_split<3>(dY[2 * s], dY[2 * s + 1]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                D[nt] = gdr_mfma(gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, 16 * nt, r16)), wo, D[nt]);
-                D[nt] = gdr_mfma(gdr_whole(gdr_ld_col(sQ, KS, 32 * s + 4 * g4, 16 * nt, r16)), qo, D[nt]);
             }
         }
+        sign = -sign;
+        __syncthreads();
     }
     if (live && p.dh0)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(p.dh0 + sbase + 16 * nt + 4 * g4) = D[nt];
+        for (int nt = 0; nt < NT; ++nt)
+            *reinterpret_cast<ssd_f32x4 *>(p.dh0 + sbase + 16 * nt + 4 * g4) = D[nt] * sign;
 }
 
 // ---------------------------------------------------------------------------
@@ -650,10 +796,10 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrParams p, int spl
 // of the group follow one another and add into dq and dk in that order.
 template <int N>
 __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
-    constexpr int KS = N + kGdrPad, NW = N / 16, TH = 64 * NW, PL = kGdrC * kGdrMS;
+    constexpr int KS = N + kGdrPad, NW = N / 16, TH = 64 * NW, PL = kGdrPlane;
     constexpr int PB = 32;                 // columns p per step
     constexpr int YS = PB + 8;             // LDS row stride of dY, V (token rows)
-    constexpr int UPL = PB * kGdrMS;       // plane of U, W ([p][token])
+    constexpr int UPL = PB * kGdrRS;       // plane of U, W ([p][token])
     __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
     __shared__ __attribute__((aligned(16))) uint16_t sdY[kGdrC * YS], sV[kGdrC * YS];
     __shared__ __attribute__((aligned(16))) uint16_t sU[3 * UPL], sW[3 * UPL];
@@ -695,6 +841,10 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
         double ds = 0.0;                   // <D', S> of this wave's columns n: every token of the chunk gets it
         for (int c0 = 0; c0 < p.P; c0 += PB) {
             const int pw_ = min(PB, p.P - c0);
+            // every second step's products are taken negative, each step's in a
+            // sum of its own: the matrix cores round towards minus infinity, and
+            // so their errors cancel instead of adding up in dG
+            const float flip = (c0 / PB) & 1 ? -1.0f : 1.0f;
             __syncthreads();
             const uint16_t *dyb = p.dy + (row0 * p.H + h) * p.P + c0;
             const uint16_t *vb = p.v + row0 * p.vs + (int64_t)h * p.P + c0;
@@ -715,8 +865,9 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                     u = *reinterpret_cast<const float4 *>(p.U + (id * p.P + c0 + row) * kGdrC + c);
                     ww = *reinterpret_cast<const float4 *>(p.W + (id * p.P + c0 + row) * kGdrC + c);
                 }
-                gdr_store_parts<3>(&sU[row * kGdrMS + c], UPL, u);
-                gdr_store_parts<3>(&sW[row * kGdrMS + c], UPL, ww);
+                u.x *= flip; u.y *= flip; u.z *= flip; u.w *= flip;
+                gdr_store_parts<3>(&sU[row * kGdrRS + c], UPL, u);
+                gdr_store_parts<3>(&sW[row * kGdrRS + c], UPL, ww);
             }
             __syncthreads();
             // S and D' columns n0 + r16, rows p = c0 + 16 (e / 4) + 4 g4 + e % 4
@@ -728,31 +879,32 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                 sv[e] = pr < pw_ ? p.S[o] : 0.0f;
                 dv[e] = pr < pw_ ? p.D[o] : 0.0f;
                 ds = fma((double)sv[e], (double)dv[e], ds);
+                sv[e] *= flip;
             }
             const GdrSplit<3> so = gdr_split<3>(sv), dd = gdr_split<3>(dv);
 #pragma unroll
             for (int T = 0; T < 4; ++T) {
                 const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&sdY[(16 * T + r16) * YS + 4 * g4]));
-                const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrMS, 4 * g4, 16 * T, r16, UPL);
-                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrMS, 4 * g4, 16 * T, r16, UPL);
-                aq[T] = gdr_mfma(yo, so, aq[T]);
-                ar[T] = gdr_mfma(wo, so, ar[T]);
-                ac[T] = gdr_mfma(uo, dd, ac[T]);
+                const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                aq[T] += gdr_mfma(yo, so, gdr_zero4()) * flip;
+                ar[T] += gdr_mfma(wo, so, gdr_zero4()) * flip;
+                ac[T] += gdr_mfma(uo, dd, gdr_zero4()) * flip;
             }
 #pragma unroll
             for (int t = 0; t < 3; ++t) {
                 const int q = w + NW * t;
                 if (q < kGdrTiles) {
                     const int T = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, J = q - T * (T + 1) / 2;
-                    const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrMS, 4 * g4, 16 * J, r16, UPL);
+                    const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrRS, 4 * g4, 16 * J, r16, UPL);
                     const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&sdY[(16 * T + r16) * YS + 4 * g4]));
-                    const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrMS, 4 * g4, 16 * T, r16, UPL);
-                    pa[t] = gdr_mfma(yo, uo, pa[t]);
-                    pw[t] = gdr_mfma(wo, uo, pw[t]);
+                    const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                    pa[t] += gdr_mfma(yo, uo, gdr_zero4()) * flip;
+                    pw[t] += gdr_mfma(wo, uo, gdr_zero4()) * flip;
                 }
             }
             if (w < 4) {
-                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrMS, 4 * g4, 16 * w, r16, UPL);
+                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrRS, 4 * g4, 16 * w, r16, UPL);
                 wv = gdr_mfma(wo, gdr_whole(gdr_ld_perm(&sV[(16 * w + r16) * YS + 4 * g4])), wv);
             }
         }
@@ -788,12 +940,12 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                 es += __shfl_xor(es, 4);
                 es += __shfl_xor(es, 8);
                 if (r16 == 0) sEs[J][i] = es;
-                e *= -sTab[kTBeta * kGdrC + i];
+                e *= sTab[kTBeta * kGdrC + i];   // subtracted below
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                     const uint16_t ah = ssd_to_bf(a), eh = ssd_to_bf(e);
-                    sPA[k * PL + i * kGdrMS + j] = ah;
-                    sPE[k * PL + i * kGdrMS + j] = eh;
+                    sPA[k * PL + i * kGdrRS + j] = ah;
+                    sPE[k * PL + i * kGdrRS + j] = eh;
                     a -= ssd_bf(ah);
                     e -= ssd_bf(eh);
                 }
@@ -819,19 +971,23 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                 kd = fma((double)kv, (double)ac[T][r], kd);
             }
             ar[T] *= -be;
+            ssd_f32x4 tq = gdr_zero4(), tr = gdr_zero4(), te = gdr_zero4(), ta = gdr_zero4();
 #pragma unroll
             for (int s = 0; s <= T / 2; ++s) {
                 const GdrSplit<1> ko = gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16));
-                aq[T] = gdr_mfma(gdr_ld_perm_parts<3>(&sPA[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL), ko, aq[T]);
-                ar[T] = gdr_mfma(gdr_ld_perm_parts<3>(&sPE[(16 * T + r16) * kGdrMS + 32 * s + 4 * g4], PL), ko, ar[T]);
+                tq = gdr_mfma(gdr_ld_perm_parts<3>(&sPA[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL), ko, tq);
+                tr = gdr_mfma(gdr_ld_perm_parts<3>(&sPE[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL), ko, tr);
             }
 #pragma unroll
             for (int s = T / 2; s < 2; ++s) {
                 const GdrSplit<1> ko = gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16));
                 const GdrSplit<1> qo = gdr_whole(gdr_ld_col(sQ, KS, 32 * s + 4 * g4, n0, r16));
-                ac[T] = gdr_mfma(gdr_ld_col_parts<3>(sPE, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), ko, ac[T]);
-                ac[T] = gdr_mfma(gdr_ld_col_parts<3>(sPA, kGdrMS, 32 * s + 4 * g4, 16 * T, r16, PL), qo, ac[T]);
+                te = gdr_mfma(gdr_ld_col_parts<3>(sPE, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL), ko, te);
+                ta = gdr_mfma(gdr_ld_col_parts<3>(sPA, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL), qo, ta);
             }
+            aq[T] += tq;
+            ar[T] -= tr;
+            ac[T] += ta - te;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 16 * T + 4 * g4 + r;
