@@ -188,6 +188,45 @@ __device__ __forceinline__ void gdr_store_parts(uint16_t *dst, int plane, float4
     }
 }
 
+// Sum over a row of 16 lanes, in every lane of it (DPP rotations by 8, 4, 2, 1)
+template <int CTRL> __device__ __forceinline__ float gdr_add_rot(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float gdr_sum16(float v) {
+    v = gdr_add_rot<0x128>(v);
+    v = gdr_add_rot<0x124>(v);
+    v = gdr_add_rot<0x122>(v);
+    return gdr_add_rot<0x121>(v);
+}
+
+// Inclusive prefix sum over the 64 lanes in 64 bits (DPP shifts within rows of
+// 16, then the row totals carried across)
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double gdr_dpp_add(double v, bool take) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROW_MASK, 0xF, false);
+    const double u = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    return take ? v + u : v;
+}
+__device__ __forceinline__ double gdr_prefix64(double v, int lane) {
+    const int r = lane & 15;
+    v = gdr_dpp_add<0x111, 0xF>(v, r >= 1);
+    v = gdr_dpp_add<0x112, 0xF>(v, r >= 2);
+    v = gdr_dpp_add<0x114, 0xF>(v, r >= 4);
+    v = gdr_dpp_add<0x118, 0xF>(v, r >= 8);
+    v = gdr_dpp_add<0x142, 0xA>(v, (lane & 16) != 0);
+    v = gdr_dpp_add<0x143, 0xC>(v, (lane & 32) != 0);
+    return v;
+}
+// lane 63's value, in every lane
+__device__ __forceinline__ double gdr_last64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // tile (T, J), J <= T, of a C x C lower triangular matrix
 __device__ __forceinline__ constexpr int gdr_tile(int T, int J) { return T * (T + 1) / 2 + J; }
 
@@ -798,17 +837,23 @@ template <int N>
 __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
     constexpr int KS = N + kGdrPad, NW = N / 16, TH = 64 * NW, PL = kGdrPlane;
     constexpr int PB = 32;                 // columns p per step
+    constexpr int TW = (kGdrTiles + NW - 1) / NW;   // C x C tiles per wave, at most
     constexpr int YS = PB + 8;             // LDS row stride of dY, V (token rows)
     constexpr int UPL = PB * kGdrRS;       // plane of U, W ([p][token])
+    constexpr int UI = PB * kGdrC / 4 / TH, YI = (kGdrC * PB / 8 + TH - 1) / TH;
+    // a step's columns: U, W in three parts, dY, V
+    struct Step { uint16_t u[3 * UPL], w[3 * UPL], dy[kGdrC * YS], v[kGdrC * YS]; };
+    // dY U^T and W U^T, decayed and scaled, once the steps are done
+    struct Pairs { uint16_t a[3 * PL], e[3 * PL]; };
+    union StepsOrPairs { Step step[2]; Pairs pairs; };
     __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
-    __shared__ __attribute__((aligned(16))) uint16_t sdY[kGdrC * YS], sV[kGdrC * YS];
-    __shared__ __attribute__((aligned(16))) uint16_t sU[3 * UPL], sW[3 * UPL];
-    __shared__ __attribute__((aligned(16))) uint16_t sPA[3 * PL], sPE[3 * PL];   // scaled dY U^T and W U^T
+    __shared__ __attribute__((aligned(16))) StepsOrPairs sX;
     __shared__ __attribute__((aligned(16))) float sTab[kGdrTab * kGdrC];
-    __shared__ float sDot[NW][2][kGdrC];   // per wave: dG and k . (W S) of its columns n
+    __shared__ __attribute__((aligned(16))) float sDot[NW][2][kGdrC];   // per wave: dG and k . (W S) of its columns n
     __shared__ float sEs[4][kGdrC];        // sum_j E_ij W_i . U_j per column tile
     __shared__ float sWv[kGdrC];
     __shared__ double sDs[NW];
+    uint16_t *const sPA = sX.pairs.a, *const sPE = sX.pairs.e;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int ci = (int)(blockIdx.x % p.nc);
@@ -816,12 +861,66 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
     const int b = bg / p.G, g = bg % p.G;
     const int nv = gdr_valid(p, ci);
     const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
-    const uint32_t ys = (uint32_t)(p.H * p.P);
+    const uint32_t ys = (uint32_t)(p.H * p.P), vs = (uint32_t)p.vs;
     const int n0 = 16 * w;
+
+    // what a step reads, one step ahead in registers; reads past the columns or
+    // tokens that exist give zero
+    float4 ur[UI], wr[UI];
+    uint4 yr[YI], vr[YI];
+    float sn[8], dn[8];
+    auto load = [&](int h, int c0) {
+        const int64_t id = (int64_t)(b * p.H + h) * p.nc + ci;
+        const uint32_t pw = (uint32_t)min(PB, p.P - c0);
+        const __amdgpu_buffer_rsrc_t ru = ssd_buffer(p.U + (id * p.P + c0) * kGdrC, pw * kGdrC * 4);
+        const __amdgpu_buffer_rsrc_t rw = ssd_buffer(p.W + (id * p.P + c0) * kGdrC, pw * kGdrC * 4);
+        const __amdgpu_buffer_rsrc_t rs = ssd_buffer(p.S + (id * p.P + c0) * N, pw * N * 4);
+        const __amdgpu_buffer_rsrc_t rd = ssd_buffer(p.D + (id * p.P + c0) * N, pw * N * 4);
+        const __amdgpu_buffer_rsrc_t ry =
+            ssd_buffer(p.dy + (row0 * p.H + h) * p.P + c0, 2u * ((uint32_t)(nv - 1) * ys + pw));
+        const __amdgpu_buffer_rsrc_t rv =
+            ssd_buffer(p.v + row0 * p.vs + (int64_t)h * p.P + c0, 2u * ((uint32_t)(nv - 1) * vs + pw));
+#pragma unroll
+        for (int i = 0; i < UI; ++i) {
+            ur[i] = __builtin_bit_cast(float4, ssd_bload16(ru, 16u * (i * TH + tid)));
+            wr[i] = __builtin_bit_cast(float4, ssd_bload16(rw, 16u * (i * TH + tid)));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t o = 4u * ((uint32_t)(16 * (e >> 2) + 4 * g4 + (e & 3)) * N + n0 + r16);
+            sn[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)o, 0, 0));
+            dn[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rd, (int)o, 0, 0));
+        }
+#pragma unroll
+        for (int i = 0; i < YI; ++i) {
+            const uint32_t x = i * TH + tid, row = x / (PB / 8), c = 8 * (x % (PB / 8));
+            const bool in = row < kGdrC && c < pw;
+            yr[i] = ssd_bload16(ry, in ? 2u * (row * ys + c) : 0x7fffffffu);
+            vr[i] = ssd_bload16(rv, in ? 2u * (row * vs + c) : 0x7fffffffu);
+        }
+    };
+    // Every second step's products are taken negative (U and S carry the sign),
+    // each step's in a sum of its own: the matrix cores round towards minus
+    // infinity, and so their errors cancel instead of adding up in dG.
+    auto store = [&](Step &s, float flip) {
+#pragma unroll
+        for (int i = 0; i < UI; ++i) {
+            const int x = i * TH + tid, o = (x / (kGdrC / 4)) * kGdrRS + 4 * (x % (kGdrC / 4));
+            gdr_store_parts<3>(&s.u[o], UPL, make_float4(flip * ur[i].x, flip * ur[i].y, flip * ur[i].z, flip * ur[i].w));
+            gdr_store_parts<3>(&s.w[o], UPL, wr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < YI; ++i) {
+            const int x = i * TH + tid, o = (x / (PB / 8)) * YS + 8 * (x % (PB / 8));
+            if (x < kGdrC * PB / 8) {
+                *reinterpret_cast<uint4 *>(&s.dy[o]) = yr[i];
+                *reinterpret_cast<uint4 *>(&s.v[o]) = vr[i];
+            }
+        }
+    };
+    load(g * p.hpg, 0);
     gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, TH);
     gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, TH);
-    gdr_zero_upper<3>(sPA, tid, TH);
-    gdr_zero_upper<3>(sPE, tid, TH);
     ssd_f32x4 dq[4], dk[4];
 #pragma unroll
     for (int T = 0; T < 4; ++T) dq[T] = dk[T] = gdr_zero4();
@@ -829,208 +928,197 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
         const int h = g * p.hpg + hh;
         const int bh = b * p.H + h;
         const int64_t id = (int64_t)bh * p.nc + ci;
-        __syncthreads();
-        for (int q = tid; q < kGdrTab * kGdrC; q += TH) sTab[q] = p.tab[id * (kGdrTab * kGdrC) + q];
         // products over p: dY S, W S, U D' (this wave's n), dY U^T and W U^T
         // (C x C lower tiles dealt over the waves), W V^T (its diagonal)
-        ssd_f32x4 aq[4], ar[4], ac[4], pa[3], pw[3], wv = gdr_zero4();
+        ssd_f32x4 aq[4], ar[4], ac[4], pa[TW], pw[TW], wv = gdr_zero4();
 #pragma unroll
         for (int T = 0; T < 4; ++T) aq[T] = ar[T] = ac[T] = gdr_zero4();
 #pragma unroll
-        for (int t = 0; t < 3; ++t) pa[t] = pw[t] = gdr_zero4();
+        for (int t = 0; t < TW; ++t) pa[t] = pw[t] = gdr_zero4();
         double ds = 0.0;                   // <D', S> of this wave's columns n: every token of the chunk gets it
-        for (int c0 = 0; c0 < p.P; c0 += PB) {
-            const int pw_ = min(PB, p.P - c0);
-            // every second step's products are taken negative, each step's in a
-            // sum of its own: the matrix cores round towards minus infinity, and
-            // so their errors cancel instead of adding up in dG
-            const float flip = (c0 / PB) & 1 ? -1.0f : 1.0f;
-            __syncthreads();
-            const uint16_t *dyb = p.dy + (row0 * p.H + h) * p.P + c0;
-            const uint16_t *vb = p.v + row0 * p.vs + (int64_t)h * p.P + c0;
-            for (int q = tid; q < kGdrC * (PB / 8); q += TH) {
-                const int row = q / (PB / 8), c = 8 * (q % (PB / 8));
-                uint4 a = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-                if (row < nv && c < pw_) {
-                    a = *reinterpret_cast<const uint4 *>(dyb + (int64_t)row * ys + c);
-                    v = *reinterpret_cast<const uint4 *>(vb + (int64_t)row * p.vs + c);
-                }
-                *reinterpret_cast<uint4 *>(&sdY[row * YS + c]) = a;
-                *reinterpret_cast<uint4 *>(&sV[row * YS + c]) = v;
-            }
-            for (int q = tid; q < PB * (kGdrC / 4); q += TH) {
-                const int row = q / (kGdrC / 4), c = 4 * (q % (kGdrC / 4));
-                float4 u = {0, 0, 0, 0}, ww = {0, 0, 0, 0};
-                if (row < pw_) {
-                    u = *reinterpret_cast<const float4 *>(p.U + (id * p.P + c0 + row) * kGdrC + c);
-                    ww = *reinterpret_cast<const float4 *>(p.W + (id * p.P + c0 + row) * kGdrC + c);
-                }
-                u.x *= flip; u.y *= flip; u.z *= flip; u.w *= flip;
-                gdr_store_parts<3>(&sU[row * kGdrRS + c], UPL, u);
-                gdr_store_parts<3>(&sW[row * kGdrRS + c], UPL, ww);
-            }
-            __syncthreads();
+        __syncthreads();                   // the head before is done with sTab and sX
+        for (int q = tid; q < kGdrTab * kGdrC; q += TH) sTab[q] = p.tab[id * (kGdrTab * kGdrC) + q];
+        store(sX.step[0], 1.0f);
+        for (int c0 = 0, buf = 0; c0 < p.P; c0 += PB, buf ^= 1) {
+            const float flip = buf ? -1.0f : 1.0f;
             // S and D' columns n0 + r16, rows p = c0 + 16 (e / 4) + 4 g4 + e % 4
-            float sv[8], dv[8];
+            GdrSplit<3> so, dd;
+            {
+                float sv[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int pr = 16 * (e >> 2) + 4 * g4 + (e & 3);
-                const int64_t o = (id * p.P + c0 + pr) * N + n0 + r16;
-                sv[e] = pr < pw_ ? p.S[o] : 0.0f;
-                dv[e] = pr < pw_ ? p.D[o] : 0.0f;
-                ds = fma((double)sv[e], (double)dv[e], ds);
-                sv[e] *= flip;
+                for (int e = 0; e < 8; ++e) {
+                    ds = fma((double)sn[e], (double)dn[e], ds);
+                    sv[e] = sn[e] * flip;
+                }
+                so = gdr_split<3>(sv);
+                dd = gdr_split<3>(dn);
             }
-            const GdrSplit<3> so = gdr_split<3>(sv), dd = gdr_split<3>(dv);
+            // the next step's reads: the next head's first behind the last
+            if (c0 + PB < p.P) load(h, c0 + PB);
+            else if (hh + 1 < p.hpg) load(h + 1, 0);
+            __syncthreads();
+            const Step &X = sX.step[buf];
 #pragma unroll
             for (int T = 0; T < 4; ++T) {
-                const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&sdY[(16 * T + r16) * YS + 4 * g4]));
-                const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrRS, 4 * g4, 16 * T, r16, UPL);
-                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrRS, 4 * g4, 16 * T, r16, UPL);
-                aq[T] += gdr_mfma(yo, so, gdr_zero4()) * flip;
-                ar[T] += gdr_mfma(wo, so, gdr_zero4()) * flip;
-                ac[T] += gdr_mfma(uo, dd, gdr_zero4()) * flip;
+                const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&X.dy[(16 * T + r16) * YS + 4 * g4]));
+                const GdrSplit<3> uo = gdr_ld_col_parts<3>(X.u, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                const GdrSplit<3> wo = gdr_ld_col_parts<3>(X.w, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                ssd_f32x4 tq = gdr_zero4(), tr = gdr_zero4(), tc = gdr_zero4();
+#pragma unroll
+                for (int k = 2; k >= 0; --k) {
+#pragma unroll
+                    for (int i = 0; i <= k; ++i) {
+                        tr = ssd_mfma(wo.part[i], so.part[k - i], tr);
+                        tc = ssd_mfma(uo.part[i], dd.part[k - i], tc);
+                    }
+                    tq = ssd_mfma(yo.part[0], so.part[k], tq);
+                }
+                aq[T] += tq * flip;
+                ar[T] += tr * flip;
+                ac[T] += tc * flip;
+                __builtin_amdgcn_sched_barrier(0);   // one tile's operands in registers at a time
             }
 #pragma unroll
-            for (int t = 0; t < 3; ++t) {
+            for (int t = 0; t < TW; ++t) {
                 const int q = w + NW * t;
                 if (q < kGdrTiles) {
                     const int T = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, J = q - T * (T + 1) / 2;
-                    const GdrSplit<3> uo = gdr_ld_col_parts<3>(sU, kGdrRS, 4 * g4, 16 * J, r16, UPL);
-                    const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&sdY[(16 * T + r16) * YS + 4 * g4]));
-                    const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrRS, 4 * g4, 16 * T, r16, UPL);
-                    pa[t] += gdr_mfma(yo, uo, gdr_zero4()) * flip;
-                    pw[t] += gdr_mfma(wo, uo, gdr_zero4()) * flip;
+                    const GdrSplit<3> uo = gdr_ld_col_parts<3>(X.u, kGdrRS, 4 * g4, 16 * J, r16, UPL);
+                    const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&X.dy[(16 * T + r16) * YS + 4 * g4]));
+                    const GdrSplit<3> wo = gdr_ld_col_parts<3>(X.w, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                    pa[t] += gdr_mfma(uo, yo, gdr_zero4()) * flip;
+                    pw[t] += gdr_mfma(uo, wo, gdr_zero4()) * flip;
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (w < 4) {
-                const GdrSplit<3> wo = gdr_ld_col_parts<3>(sW, kGdrRS, 4 * g4, 16 * w, r16, UPL);
-                wv = gdr_mfma(wo, gdr_whole(gdr_ld_perm(&sV[(16 * w + r16) * YS + 4 * g4])), wv);
+            // (waves 0 and 1 hold two tiles: the diagonal goes to the others)
+            if (w >= NW - 4) {
+                const int T = w - (NW - 4);
+                const GdrSplit<3> wo = gdr_ld_col_parts<3>(X.w, kGdrRS, 4 * g4, 16 * T, r16, UPL);
+                wv = gdr_mfma(wo, gdr_whole(gdr_ld_perm(&X.v[(16 * T + r16) * YS + 4 * g4])), wv);
             }
+            if (c0 + PB < p.P) store(sX.step[buf ^ 1], -flip);
         }
+        __syncthreads();                   // every wave is done with the steps: their place holds the pairs
+        gdr_zero_upper<3>(sPA, tid, TH);
+        gdr_zero_upper<3>(sPE, tid, TH);
         // row i = 16 w + 4 g4 + r, column 16 w + r16: the diagonal of W V^T
-        if (w < 4 && (r16 >> 2) == g4) sWv[16 * w + r16] = wv[r16 & 3];
-        // C x C: decayed and scaled
-        for (int t = 0; t < 3; ++t) {
+        if (w >= NW - 4 && (r16 >> 2) == g4) {
+            const int r = r16 & 3;
+            sWv[16 * (w - (NW - 4)) + r16] = r == 0 ? wv[0] : r == 1 ? wv[1] : r == 2 ? wv[2] : wv[3];
+        }
+        // C x C: decayed and scaled. A tile is held transposed: row i = 16 T + r16
+        // is the lane's, columns j = 16 J + 4 g4 .. + 3
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
             const int q = w + NW * t;
             if (q >= kGdrTiles) break;
             const int T = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, J = q - T * (T + 1) / 2;
             ssd_f32x4 kk = gdr_zero4();
 #pragma unroll
             for (int s = 0; s < N / 32; ++s)
-                kk = ssd_mfma(ssd_ld16(&sK[(16 * T + r16) * KS + 32 * s + 8 * g4]),
-                              ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]), kk);
-            const int j = 16 * J + r16;
-            const float ghj = sTab[kTGhi * kGdrC + j], glj = sTab[kTGlo * kGdrC + j], rkj = sTab[kTRk * kGdrC + j];
-            const ssd_f32x4 pat = t == 0 ? pa[0] : t == 1 ? pa[1] : pa[2];
-            const ssd_f32x4 pwt = t == 0 ? pw[0] : t == 1 ? pw[1] : pw[2];
+                kk = ssd_mfma(ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]),
+                              ssd_ld16(&sK[(16 * T + r16) * KS + 32 * s + 8 * g4]), kk);
+            const int i = 16 * T + r16, j0 = 16 * J + 4 * g4;
+            const float ghi = sTab[kTGhi * kGdrC + i], gli = sTab[kTGlo * kGdrC + i], rki = sTab[kTRk * kGdrC + i];
+            const float rqi = sTab[kTRq * kGdrC + i], bei = sTab[kTBeta * kGdrC + i];
+            const ssd_f32x4 ghj = gdr_ld4(&sTab[kTGhi * kGdrC + j0]), glj = gdr_ld4(&sTab[kTGlo * kGdrC + j0]);
+            const ssd_f32x4 rkj = gdr_ld4(&sTab[kTRk * kGdrC + j0]);
+            float a[4], e[4], es = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * T + 4 * g4 + r;
-                const float gam = i >= j ? __builtin_amdgcn_exp2f((sTab[kTGhi * kGdrC + i] - ghj) +
-                                                                  (sTab[kTGlo * kGdrC + i] - glj)) * rkj
-                                         : 0.0f;
-                const float rki = sTab[kTRk * kGdrC + i];
-                float a = pat[r] * gam * sTab[kTRq * kGdrC + i];
-                float e = i > j ? pwt[r] * gam * rki : 0.0f;
-                // sum_j E_ij W_i . U_j over the tile's 16 columns
-                float es = e * kk[r];
-                es += __shfl_xor(es, 1);
-                es += __shfl_xor(es, 2);
-                es += __shfl_xor(es, 4);
-                es += __shfl_xor(es, 8);
-                if (r16 == 0) sEs[J][i] = es;
-                e *= sTab[kTBeta * kGdrC + i];   // subtracted below
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const uint16_t ah = ssd_to_bf(a), eh = ssd_to_bf(e);
-                    sPA[k * PL + i * kGdrRS + j] = ah;
-                    sPE[k * PL + i * kGdrRS + j] = eh;
-                    a -= ssd_bf(ah);
-                    e -= ssd_bf(eh);
-                }
+                // above the diagonal exp2(-inf): no branch
+                const float x = i >= j0 + r ? (ghi - ghj[r]) + (gli - glj[r]) : -__builtin_inff();
+                const float gam = __builtin_amdgcn_exp2f(x) * rkj[r];
+                a[r] = pa[t][r] * gam * rqi;
+                const float ev = i > j0 + r ? pw[t][r] * gam * rki : 0.0f;
+                es = fmaf(ev, kk[r], es);          // sum_j E_ij W_i . U_j
+                e[r] = ev * bei;                   // subtracted below
             }
+            es += __shfl_xor(es, 16);
+            es += __shfl_xor(es, 32);
+            if (g4 == 0) sEs[J][i] = es;
+            gdr_store_parts<3>(&sPA[i * kGdrRS + j0], PL, make_float4(a[0], a[1], a[2], a[3]));
+            gdr_store_parts<3>(&sPE[i * kGdrRS + j0], PL, make_float4(e[0], e[1], e[2], e[3]));
         }
         __syncthreads();
-        // products over tokens, scaled by the tokens' rows
+        // products over tokens, scaled by the tokens' rows. The K and Q operands
+        // are the wave's columns n of rows 16 T + 4 g4 + r as well: element
+        // 4 (T % 2) + r of operand T / 2
+        ssd_bf16x8 ko[2], qo[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            ko[s] = gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16);
+            qo[s] = gdr_ld_col(sQ, KS, 32 * s + 4 * g4, n0, r16);
+        }
         double kd = 0.0;                   // sum_j exp(G_C - G_j) k_j . (U D')_j of this wave's n
-        float dot[4][4], kws[4][4];
 #pragma unroll
         for (int T = 0; T < 4; ++T) {
             const ssd_f32x4 hq = gdr_ld4(&sTab[kTHq * kGdrC + 16 * T + 4 * g4]);
             const ssd_f32x4 hk = gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
             const ssd_f32x4 tk = gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
             const ssd_f32x4 be = gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
-            aq[T] *= hq;
-            ac[T] *= tk;
-            ar[T] *= hk;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float kv = ssd_bf(sK[(16 * T + 4 * g4 + r) * KS + n0 + r16]);
-                kws[T][r] = kv * ar[T][r];
-                kd = fma((double)kv, (double)ac[T][r], kd);
-            }
-            ar[T] *= -be;
             ssd_f32x4 tq = gdr_zero4(), tr = gdr_zero4(), te = gdr_zero4(), ta = gdr_zero4();
 #pragma unroll
-            for (int s = 0; s <= T / 2; ++s) {
-                const GdrSplit<1> ko = gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16));
-                tq = gdr_mfma(gdr_ld_perm_parts<3>(&sPA[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL), ko, tq);
-                tr = gdr_mfma(gdr_ld_perm_parts<3>(&sPE[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL), ko, tr);
-            }
+            for (int s = 0; s < 2; ++s) {
+                if (s <= T / 2) {
+                    const GdrSplit<3> ao = gdr_ld_perm_parts<3>(&sPA[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL);
+                    const GdrSplit<3> eo = gdr_ld_perm_parts<3>(&sPE[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL);
 #pragma unroll
-            for (int s = T / 2; s < 2; ++s) {
-                const GdrSplit<1> ko = gdr_whole(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16));
-                const GdrSplit<1> qo = gdr_whole(gdr_ld_col(sQ, KS, 32 * s + 4 * g4, n0, r16));
-                te = gdr_mfma(gdr_ld_col_parts<3>(sPE, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL), ko, te);
-                ta = gdr_mfma(gdr_ld_col_parts<3>(sPA, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL), qo, ta);
+                    for (int k = 2; k >= 0; --k) {
+                        tq = ssd_mfma(ao.part[k], ko[s], tq);
+                        tr = ssd_mfma(eo.part[k], ko[s], tr);
+                    }
+                }
+                if (s >= T / 2) {
+                    const GdrSplit<3> eo = gdr_ld_col_parts<3>(sPE, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
+                    const GdrSplit<3> ao = gdr_ld_col_parts<3>(sPA, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
+#pragma unroll
+                    for (int k = 2; k >= 0; --k) {
+                        te = ssd_mfma(eo.part[k], ko[s], te);
+                        ta = ssd_mfma(ao.part[k], qo[s], ta);
+                    }
+                }
             }
-            aq[T] += tq;
-            ar[T] -= tr;
-            ac[T] += ta - te;
+            aq[T] = aq[T] * hq + tq;
+            ac[T] *= tk;
+            ar[T] *= hk;
+            ssd_f32x4 dot, kw;
+            const ssd_f32x4 row = ar[T] * -be - tr, col = ac[T] + (ta - te);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * T + 4 * g4 + r;
-                const float kv = ssd_bf(sK[i * KS + n0 + r16]), qv = ssd_bf(sQ[i * KS + n0 + r16]);
-                dot[T][r] = fmaf(qv, aq[T][r], kv * (ar[T][r] - ac[T][r]));
+                const float kv = (float)ko[T / 2][4 * (T % 2) + r], qv = (float)qo[T / 2][4 * (T % 2) + r];
+                kw[r] = gdr_sum16(kv * ar[T][r]);
+                kd = fma((double)kv, (double)ac[T][r], kd);
+                dot[r] = gdr_sum16(fmaf(qv, aq[T][r], kv * (row[r] - col[r])));
+            }
+            if (r16 == 0) {
+                *reinterpret_cast<ssd_f32x4 *>(&sDot[w][0][16 * T + 4 * g4]) = dot;
+                *reinterpret_cast<ssd_f32x4 *>(&sDot[w][1][16 * T + 4 * g4]) = kw;
             }
             dq[T] += aq[T];
-            dk[T] += ar[T] + ac[T];
+            dk[T] += row + col;
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int T = 0; T < 4; ++T)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float a = dot[T][r], c = kws[T][r];
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-                    a += __shfl_xor(a, o);
-                    c += __shfl_xor(c, o);
-                }
-                if (r16 == 0) {
-                    sDot[w][0][16 * T + 4 * g4 + r] = a;
-                    sDot[w][1][16 * T + 4 * g4 + r] = c;
-                }
-            }
         // <D', S'> = exp(G_C) <D', S> + sum_j exp(G_C - G_j) k_j . (U D')_j
         ds = ds * (double)sTab[kTHead * kGdrC + kGdrC - 1] + kd;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) ds += __shfl_xor(ds, o);
+        ds = gdr_last64(gdr_prefix64(ds, lane));
         if (lane == 0) sDs[w] = ds;
         __syncthreads();
         if (w == 0) {
             double dG = 0.0, whole = 0.0;
             float kw = 0.0f, es = 0.0f;
+#pragma unroll
             for (int k = 0; k < NW; ++k) {
                 dG += sDot[k][0][lane];
                 kw += sDot[k][1][lane];
                 whole += sDs[k];
             }
-            for (int J = 0; J <= lane / 16; ++J) es += sEs[J][lane];
-            for (int o = 1; o < kGdrC; o <<= 1) {
-                const double dn = __shfl_down(dG, o);
-                if (lane + o < kGdrC) dG += dn;
-            }
+#pragma unroll
+            for (int J = 0; J < 4; ++J) es += J <= lane / 16 ? sEs[J][lane] : 0.0f;
+            // sum over tokens from this one on
+            const double upto = gdr_prefix64(dG, lane);
+            dG += gdr_last64(upto) - upto;
             // d(log a_t) = a_t <.., S_{t-1}>, but the sum leaves the rounding of
             // its terms, which a long step would multiply: a token that forgets
             // all (a_t below 2^-64) has none
@@ -1044,58 +1132,64 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                 p.ddt[o] = ssd_to_bf(ddt);
                 p.dbeta[o] = ssd_to_bf((sWv[lane] - kw - es) * sTab[kTDbeta * kGdrC + lane]);
             }
-            for (int o = 1; o < 64; o <<= 1) {
-                pA += __shfl_xor(pA, o);
-                pb += __shfl_xor(pb, o);
-            }
+            pA = gdr_last64(gdr_prefix64(pA, lane));
+            pb = gdr_last64(gdr_prefix64(pb, lane));
             if (lane == 0) {
                 p.part[2 * id] = (float)pA;
                 p.part[2 * id + 1] = (float)pb;
             }
         }
     }
-    // the gradients of the rows as given: through the unit lengths
+    // the gradients of the rows as given: through the unit lengths, whose rows'
+    // products with their gradients all waves need
     if (p.qk_norm) {
         __syncthreads();
 #pragma unroll
-        for (int T = 0; T < 4; ++T)
+        for (int T = 0; T < 4; ++T) {
+            ssd_f32x4 qd, kd;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * T + 4 * g4 + r;
-                float a = ssd_bf(sQ[i * KS + n0 + r16]) * dq[T][r], c = ssd_bf(sK[i * KS + n0 + r16]) * dk[T][r];
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-                    a += __shfl_xor(a, o);
-                    c += __shfl_xor(c, o);
-                }
-                if (r16 == 0) {
-                    sDot[w][0][i] = a;
-                    sDot[w][1][i] = c;
-                }
+                qd[r] = gdr_sum16(ssd_bf(sQ[(16 * T + 4 * g4 + r) * KS + n0 + r16]) * dq[T][r]);
+                kd[r] = gdr_sum16(ssd_bf(sK[(16 * T + 4 * g4 + r) * KS + n0 + r16]) * dk[T][r]);
             }
+            if (r16 == 0) {
+                *reinterpret_cast<ssd_f32x4 *>(&sDot[w][0][16 * T + 4 * g4]) = qd;
+                *reinterpret_cast<ssd_f32x4 *>(&sDot[w][1][16 * T + 4 * g4]) = kd;
+            }
+        }
+        __syncthreads();
+        if (tid < 2 * kGdrC) {
+            // rq^2 q . dq and rk^2 k . dk of row tid % 64, into the table's place
+            const int of = tid >> 6;
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) sum += sDot[k][of][lane];
+            const float u = sTab[(of ? kTRk : kTUq) * kGdrC + lane];
+            sTab[(of ? kTRk : kTUq) * kGdrC + lane] = u * u * sum;
+        }
         __syncthreads();
     }
+    const uint32_t gs = (uint32_t)(p.G * N);
+    const __amdgpu_buffer_rsrc_t rdq = ssd_buffer(p.dq + (row0 * p.G + g) * N, 2u * ((uint32_t)(nv - 1) * gs + N));
+    const __amdgpu_buffer_rsrc_t rdk = ssd_buffer(p.dk + (row0 * p.G + g) * N, 2u * ((uint32_t)(nv - 1) * gs + N));
 #pragma unroll
-    for (int T = 0; T < 4; ++T)
+    for (int T = 0; T < 4; ++T) {
+        ssd_f32x4 fq = gdr_zero4(), fk = gdr_zero4();
+        if (p.qk_norm) {
+            fq = gdr_ld4(&sTab[kTUq * kGdrC + 16 * T + 4 * g4]);
+            fk = gdr_ld4(&sTab[kTRk * kGdrC + 16 * T + 4 * g4]);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 16 * T + 4 * g4 + r;
-            if (i >= nv) continue;
-            float a = dq[T][r], c = dk[T][r];
-            if (p.qk_norm) {
-                float qd = 0.0f, kd = 0.0f;
-                for (int k = 0; k < NW; ++k) {
-                    qd += sDot[k][0][i];
-                    kd += sDot[k][1][i];
-                }
-                const float uq = sTab[kTUq * kGdrC + i], rk = sTab[kTRk * kGdrC + i];
-                a -= uq * uq * qd * ssd_bf(sQ[i * KS + n0 + r16]);
-                c -= rk * rk * kd * ssd_bf(sK[i * KS + n0 + r16]);
-            }
-            const int64_t o = ((row0 + i) * p.G + g) * N + n0 + r16;
-            p.dq[o] = ssd_to_bf(a);
-            p.dk[o] = ssd_to_bf(c);
+            const float a = dq[T][r] - fq[r] * ssd_bf(sQ[i * KS + n0 + r16]);
+            const float c = dk[T][r] - fk[r] * ssd_bf(sK[i * KS + n0 + r16]);
+            // rows past the end are dropped by the buffers' ranges
+            const int o = (int)(2u * ((uint32_t)i * gs + n0 + r16));
+            __builtin_amdgcn_raw_buffer_store_b16(ssd_to_bf(a), rdq, o, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16(ssd_to_bf(c), rdk, o, 0, 0);
         }
+    }
 }
 
 // dA and ddt_bias of head h: the chunks' parts, batch row by batch row
