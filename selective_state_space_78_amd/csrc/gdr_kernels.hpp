@@ -91,6 +91,20 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ ssd_f32x4 gdr_zero4() { return ssd_f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 
+// What bf16 rounding left of a and b, given their rounded pair: one dot product
+// of the pair with (-1, 0) or (0, -1) each, exact (a shift or mask and a
+// subtraction otherwise: 5.5 instead of 3.5 instructions per split value). The
+// first constant goes through a register: as an inline constant it would be
+// read as (0, -1).
+__device__ __forceinline__ void gdr_rest(uint32_t pair, float &a, float &b) {
+    uint32_t first = 0x0000bf80u;
+    asm("" : "+s"(first));
+    const ssd_bf16x2 v = __builtin_bit_cast(ssd_bf16x2, pair);
+    const ssd_bf16x2 second = {(__bf16)0.0f, (__bf16)-1.0f};
+    a = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(ssd_bf16x2, first), a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(v, second, b, false);
+}
+
 // v as PARTS bf16 operands whose sum carries 8 PARTS significant bits
 template <int PARTS> struct GdrSplit { ssd_bf16x8 part[PARTS]; };
 
@@ -106,10 +120,7 @@ __device__ __forceinline__ GdrSplit<PARTS> gdr_split(const float (&v)[8]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w[e] = ssd_pack(r[2 * e], r[2 * e + 1]);
-            if (k + 1 < PARTS) {
-                r[2 * e] -= __uint_as_float(w[e] << 16);
-                r[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
-            }
+            if (k + 1 < PARTS) gdr_rest(w[e], r[2 * e], r[2 * e + 1]);
         }
         out.part[k] = __builtin_bit_cast(ssd_bf16x8, uint4{w[0], w[1], w[2], w[3]});
     }
@@ -181,10 +192,10 @@ __device__ __forceinline__ void gdr_store_parts(uint16_t *dst, int plane, float4
     for (int k = 0; k < PARTS; ++k) {
         const uint2 w = {ssd_pack(r[0], r[1]), ssd_pack(r[2], r[3])};
         *reinterpret_cast<uint2 *>(dst + k * plane) = w;
-        r[0] -= __uint_as_float(w.x << 16);
-        r[1] -= __uint_as_float(w.x & 0xffff0000u);
-        r[2] -= __uint_as_float(w.y << 16);
-        r[3] -= __uint_as_float(w.y & 0xffff0000u);
+        if (k + 1 < PARTS) {
+            gdr_rest(w.x, r[0], r[1]);
+            gdr_rest(w.y, r[2], r[3]);
+        }
     }
 }
 
@@ -437,16 +448,71 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 // them. So the state's sign alternates: odd chunks hold -S, through the signs
 // of the scales that are applied anyway, and the errors cancel.
 
-// LDS of one chunk: K and Q rows, R in three parts, the first four tables and
-// the decay over the whole chunk. The scores are apart.
-template <int N> struct GdrChunkLds {
+// LDS of one chunk: K and Q rows; the lower tiles of R in three parts and of the
+// scores in AP; the first four tables and the decay over the whole chunk. Tiles
+// have no padding: a wave's 8-byte reads of a 16-bit tile 16 columns wide, along
+// rows or transposed, cover it in order.
+constexpr int kGdrPart = kGdrTiles * 256;   // elements of one part of a C x C matrix
+template <int N, int AP> struct GdrChunkLds {
     uint16_t k[kGdrC * (N + kGdrPad)], q[kGdrC * (N + kGdrPad)];
-    uint16_t r[3 * kGdrPlane];
+    uint16_t r[3 * kGdrPart], a[AP * kGdrPart];
     float tab[4 * kGdrC];
     float end[4];
 };
 
-template <int N, int NW> struct GdrChunkRegs {
+// rows of row tile T, columns of tiles 2 s and 2 s + 1, of a lower triangular matrix
+template <int PARTS>
+__device__ __forceinline__ GdrSplit<PARTS> gdr_ld_tile_rows(const uint16_t *m, int T, int s, int r16, int g4) {
+    GdrSplit<PARTS> o;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        const uint16_t *p = m + k * kGdrPart + 16 * r16 + 4 * g4;
+        const uint2 a = *reinterpret_cast<const uint2 *>(p + 256 * gdr_tile(T, 2 * s));
+        uint2 b = {0u, 0u};
+        if (2 * s + 1 <= T) b = *reinterpret_cast<const uint2 *>(p + 256 * gdr_tile(T, 2 * s + 1));
+        o.part[k] = __builtin_bit_cast(ssd_bf16x8, uint4{a.x, a.y, b.x, b.y});
+    }
+    return o;
+}
+
+// columns of column tile T, rows of tiles 2 s and 2 s + 1
+template <int PARTS>
+__device__ __forceinline__ GdrSplit<PARTS> gdr_ld_tile_cols(const uint16_t *m, int T, int s, int r16, int g4) {
+    GdrSplit<PARTS> o;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        const uint16_t *p = m + k * kGdrPart + 16 * (4 * g4 + (r16 >> 2)) + 4 * (r16 & 3);
+        uint2 a = {0u, 0u};
+        if (2 * s >= T) a = ssd_ld_tr(p + 256 * gdr_tile(2 * s, T));
+        const uint2 b = ssd_ld_tr(p + 256 * gdr_tile(2 * s + 1, T));
+        o.part[k] = __builtin_bit_cast(ssd_bf16x8, uint4{a.x, a.y, b.x, b.y});
+    }
+    return o;
+}
+
+// A wave's own 16 columns of V (or dY), a chunk ahead in registers (a row per
+// lane), turned through a 64 x 16 tile of LDS that no other wave touches
+struct GdrColumns {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const GdrParams &p, const uint16_t *col, int64_t stride, int64_t rowb, int ci,
+                                         int lane) {
+        const uint32_t nv = (uint32_t)gdr_valid(p, ci), st = (uint32_t)stride;
+        const __amdgpu_buffer_rsrc_t r = ssd_buffer(col + (rowb + (int64_t)ci * kGdrC) * stride, 2u * ((nv - 1) * st + 16));
+        v[0] = ssd_bload16(r, 2u * ((uint32_t)lane * st));
+        v[1] = ssd_bload16(r, 2u * ((uint32_t)lane * st + 8));
+    }
+    // the lane's column of rows 16 T + 4 g4 .. + 3, for every T
+    __device__ __forceinline__ void turn(uint16_t *tile, int lane, uint2 (&out)[4]) const {
+        const int r16 = lane & 15, g4 = lane >> 4;
+        *reinterpret_cast<uint4 *>(tile + 16 * lane) = v[0];
+        *reinterpret_cast<uint4 *>(tile + 16 * lane + 8) = v[1];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int T = 0; T < 4; ++T) out[T] = ssd_ld_tr(tile + 16 * (16 * T + 4 * g4 + (r16 >> 2)) + 4 * (r16 & 3));
+    }
+};
+
+template <int N, int AP, int NW> struct GdrChunkRegs {
     static constexpr int TH = 64 * NW, KS = N + kGdrPad;
     static constexpr int KI = kGdrC * N / 8 / TH, RI = (kGdrTiles * 64 + TH - 1) / TH, TI = (4 * kGdrC + TH - 1) / TH;
     uint4 k[KI], q[KI];
@@ -459,8 +525,8 @@ template <int N, int NW> struct GdrChunkRegs {
         // rows past the end have offsets past the ranges: they read zero
         const __amdgpu_buffer_rsrc_t rk = ssd_buffer(p.k + row0 * p.ks + (int64_t)g * N, 2u * ((nv - 1) * ks + N));
         const __amdgpu_buffer_rsrc_t rq = ssd_buffer(p.q + row0 * p.qs + (int64_t)g * N, 2u * ((nv - 1) * qs + N));
-        const __amdgpu_buffer_rsrc_t rr = ssd_buffer(p.R + id * (kGdrTiles * 256), kGdrTiles * 1024);
-        const __amdgpu_buffer_rsrc_t ra = ssd_buffer(p.score + id * (kGdrTiles * 256), kGdrTiles * 1024);
+        const __amdgpu_buffer_rsrc_t rr = ssd_buffer(p.R + id * kGdrPart, kGdrPart * 4);
+        const __amdgpu_buffer_rsrc_t ra = ssd_buffer(p.score + id * kGdrPart, kGdrPart * 4);
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
             const uint32_t x = i * TH + tid, row = x / (N / 8), c = 8 * (x % (N / 8));
@@ -477,17 +543,7 @@ template <int N, int NW> struct GdrChunkRegs {
         for (int i = 0; i < TI; ++i) tab[i] = t[(i * TH + tid) & (4 * kGdrC - 1)];
         end = t[kTHead * kGdrC + kGdrC - 1];
     }
-    // element of a row-major C x C plane that this thread's i-th piece of the tiles starts at
-    static __device__ __forceinline__ int place(int x) {
-        const int t = x >> 6, T = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - T * (T + 1) / 2;
-        return (16 * T + ((x >> 2) & 15)) * kGdrRS + 16 * J + 4 * (x & 3);
-    }
-    template <int AP> __device__ __forceinline__ void store_scores(uint16_t *dst, int tid) const {
-#pragma unroll
-        for (int i = 0; i < RI; ++i)
-            if (i * TH + tid < kGdrTiles * 64) gdr_store_parts<AP>(dst + place(i * TH + tid), kGdrPlane, a[i]);
-    }
-    __device__ __forceinline__ void store(GdrChunkLds<N> &s, int tid) const {
+    __device__ __forceinline__ void store(GdrChunkLds<N, AP> &s, int tid) const {
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
             const int x = i * TH + tid, o = (x / (N / 8)) * KS + 8 * (x % (N / 8));
@@ -495,8 +551,13 @@ template <int N, int NW> struct GdrChunkRegs {
             *reinterpret_cast<uint4 *>(&s.q[o]) = q[i];
         }
 #pragma unroll
-        for (int i = 0; i < RI; ++i)
-            if (i * TH + tid < kGdrTiles * 64) gdr_store_parts<3>(&s.r[place(i * TH + tid)], kGdrPlane, r[i]);
+        for (int i = 0; i < RI; ++i) {
+            const int x = i * TH + tid;
+            if (x < kGdrTiles * 64) {
+                gdr_store_parts<3>(&s.r[4 * x], kGdrPart, r[i]);
+                gdr_store_parts<AP>(&s.a[4 * x], kGdrPart, a[i]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < TI; ++i)
             if (TH * TI == 4 * kGdrC || i * TH + tid < 4 * kGdrC) s.tab[i * TH + tid] = tab[i];
@@ -508,9 +569,9 @@ template <int N, int NW> struct GdrChunkRegs {
 // turn so that consecutive instructions do not wait for one another
 template <int N, bool SAVE, int NW>
 __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int splits) {
-    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrPlane;
-    __shared__ __attribute__((aligned(16))) GdrChunkLds<N> lds[2];
-    __shared__ __attribute__((aligned(16))) uint16_t sA[2][2 * PL];
+    constexpr int KS = N + kGdrPad, NT = N / 16;
+    __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 2> lds[2];
+    __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
@@ -518,49 +579,32 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
     const int p0 = 16 * (split * NW + w);
     const bool live = p0 < p.P;
     const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
-    const uint32_t vs = (uint32_t)p.vs, ysr = (uint32_t)(p.H * p.P);
+    const uint32_t ysr = (uint32_t)(p.H * p.P);
     const int64_t id0 = (int64_t)bh * p.nc, rowb = (int64_t)b * p.L;
     ssd_f32x4 S[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         S[nt] = live && p.h0 ? gdr_ld4(p.h0 + sbase + 16 * nt + 4 * g4) : gdr_zero4();
-    for (int k = 0; k < 2; ++k) {
-        gdr_zero_upper<3>(lds[k].r, tid, 64 * NW);
-        gdr_zero_upper<2>(sA[k], tid, 64 * NW);
-    }
-    uint16_t vn[16];
-    auto load_v = [&](int ci) {
-        const uint32_t nv = (uint32_t)gdr_valid(p, ci);
-        const __amdgpu_buffer_rsrc_t rv = ssd_buffer(p.v + (rowb + (int64_t)ci * kGdrC) * p.vs + (int64_t)h * p.P,
-                                                     2u * ((nv - 1) * vs + (uint32_t)p.P));
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            vn[e] = __builtin_amdgcn_raw_buffer_load_b16(
-                rv, (int)(2u * ((uint32_t)(16 * (e >> 2) + 4 * g4 + (e & 3)) * vs + p0 + r16)), 0, 0);
-    };
-    GdrChunkRegs<N, NW> regs;
+    const uint16_t *vcol = p.v + (int64_t)h * p.P + p0;
+    GdrChunkRegs<N, 2, NW> regs;
+    GdrColumns vr;
     regs.load(p, b, g, id0, 0, tid);
-    if (live) load_v(0);
+    if (live) vr.load(p, vcol, p.vs, rowb, 0, lane);
     regs.store(lds[0], tid);
-    regs.template store_scores<2>(sA[0], tid);
     if (p.nc > 1) regs.load(p, b, g, id0 + 1, 1, tid);
     __syncthreads();
     float sign = 1.0f;
     for (int ci = 0; ci < p.nc; ++ci) {
-        const GdrChunkLds<N> &L = lds[ci & 1];
+        const GdrChunkLds<N, 2> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
-        if (ci + 1 < p.nc) {
-            regs.store(lds[(ci + 1) & 1], tid);
-            regs.template store_scores<2>(sA[(ci + 1) & 1], tid);
-        }
+        if (ci + 1 < p.nc) regs.store(lds[(ci + 1) & 1], tid);
         if (ci + 2 < p.nc) regs.load(p, b, g, id + 2, ci + 2, tid);
         if (live) {
-            float vc[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) vc[e] = ssd_bf(vn[e]) * sign;
-            if (ci + 1 < p.nc) load_v(ci + 1);
+            uint2 vw[4];
+            vr.turn(sV[w], lane, vw);
+            if (ci + 1 < p.nc) vr.load(p, vcol, p.vs, rowb, ci + 1, lane);
             if constexpr (SAVE) {
                 float *dst = p.S + (id * p.P + p0 + r16) * N + 4 * g4;
 #pragma unroll
@@ -592,8 +636,10 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
             for (int T = 0; T < 4; ++T) {
                 const ssd_f32x4 hk = gdr_ld4(&L.tab[kTHk * kGdrC + 16 * T + 4 * g4]);
                 const ssd_f32x4 be = gdr_ld4(&L.tab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+                const float vc[4] = {ssd_bf(vw[T].x), __uint_as_float(vw[T].x & 0xffff0000u), ssd_bf(vw[T].y),
+                                     __uint_as_float(vw[T].y & 0xffff0000u)};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) X[T][r] = be[r] * (vc[4 * T + r] - hk[r] * X[T][r]);
+                for (int r = 0; r < 4; ++r) X[T][r] = be[r] * (sign * vc[r] - hk[r] * X[T][r]);
             }
             // U = R (beta X)
             {
@@ -603,7 +649,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
                     GdrSplit<3> ro[4];
 #pragma unroll
                     for (int T = 2 * s; T < 4; ++T)
-                        ro[T] = gdr_ld_perm_parts<3>(&L.r[(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL);
+                        ro[T] = gdr_ld_tile_rows<3>(L.r, T, s, r16, g4);
 #pragma unroll
                     for (int k = 2; k >= 0; --k)
 #pragma unroll
@@ -629,7 +675,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
                     GdrSplit<2> ao[4];
 #pragma unroll
                     for (int T = 2 * s; T < 4; ++T)
-                        ao[T] = gdr_ld_perm_parts<2>(&sA[ci & 1][(16 * T + r16) * kGdrRS + 32 * s + 4 * g4], PL);
+                        ao[T] = gdr_ld_tile_rows<2>(L.a, T, s, r16, g4);
 #pragma unroll
                     for (int k = 1; k >= 0; --k)
 #pragma unroll
@@ -674,11 +720,9 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
 // Backwards over the chunks: D' of every chunk, W, dv and dh0.
 template <int N, int NW>
 __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int splits) {
-    constexpr int KS = N + kGdrPad, NT = N / 16, PL = kGdrPlane;
-    __shared__ __attribute__((aligned(16))) GdrChunkLds<N> lds[2];
-    // a third part of the scores in both halves would not fit: one copy, and a
-    // second barrier between its use and the next chunk's
-    __shared__ __attribute__((aligned(16))) uint16_t sA[3 * PL];
+    constexpr int KS = N + kGdrPad, NT = N / 16;
+    __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 3> lds[2];
+    __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
@@ -692,44 +736,51 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         D[nt] = live && p.dh_last ? gdr_ld4(p.dh_last + sbase + 16 * nt + 4 * g4) : gdr_zero4();
-    for (int k = 0; k < 2; ++k) gdr_zero_upper<3>(lds[k].r, tid, 64 * NW);
-    gdr_zero_upper<3>(sA, tid, 64 * NW);
-    uint16_t dn[16];
-    auto load_dy = [&](int ci) {
-        const uint32_t nv = (uint32_t)gdr_valid(p, ci);
-        const __amdgpu_buffer_rsrc_t rd = ssd_buffer(p.dy + ((rowb + (int64_t)ci * kGdrC) * p.H + h) * p.P,
-                                                     2u * ((nv - 1) * ys + (uint32_t)p.P));
+    // operands that pick tile 0 or 1 of a pair: W^T in bf16 from an operand
+    GdrSplit<1> pick[2];
+    {
+        float one[2][8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            dn[e] = __builtin_amdgcn_raw_buffer_load_b16(
-                rd, (int)(2u * ((uint32_t)(16 * (e >> 2) + 4 * g4 + (e & 3)) * ys + p0 + r16)), 0, 0);
-    };
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) one[t][e] = (e >> 2) == t && 4 * g4 + (e & 3) == r16 ? 1.0f : 0.0f;
+        pick[0] = gdr_split<1>(one[0]);
+        pick[1] = gdr_split<1>(one[1]);
+    }
+    const uint16_t *ycol = p.dy + (int64_t)h * p.P + p0;
     const int last = p.nc - 1;
-    GdrChunkRegs<N, NW> regs;
+    GdrChunkRegs<N, 3, NW> regs;
+    GdrColumns yr;
     regs.load(p, b, g, id0 + last, last, tid);
-    if (live) load_dy(last);
+    if (live) yr.load(p, ycol, ys, rowb, last, lane);
     regs.store(lds[last & 1], tid);
-    regs.template store_scores<3>(sA, tid);
     if (last > 0) regs.load(p, b, g, id0 + last - 1, last - 1, tid);
     __syncthreads();
     float sign = 1.0f;
     for (int ci = last; ci >= 0; --ci) {
-        const GdrChunkLds<N> &L = lds[ci & 1];
+        const GdrChunkLds<N, 3> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
         if (ci > 0) regs.store(lds[(ci - 1) & 1], tid);
-        ssd_f32x4 dY[4], dU[4], W[4];
+        if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, tid);
         if (live) {
+            // dY with the chunk's sign, as operands
+            const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
+            uint2 yt[4];
+            yr.turn(sV[w], lane, yt);
+            if (ci > 0) yr.load(p, ycol, ys, rowb, ci - 1, lane);
+            uint4 yw[2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) dY[e >> 2][e & 3] = ssd_bf(dn[e]) * sign;
-            if (ci > 0) load_dy(ci - 1);
+            for (int s = 0; s < 2; ++s)
+                yw[s] = uint4{yt[2 * s].x ^ flip, yt[2 * s].y ^ flip, yt[2 * s + 1].x ^ flip, yt[2 * s + 1].y ^ flip};
             {
                 float *dst = p.D + (id * p.P + p0 + r16) * N + 4 * g4;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = D[nt] * sign;
             }
             // dU = exp(G_C - G) K D'^T + A^T dY
+            ssd_f32x4 dU[4], W[4];
 #pragma unroll
             for (int T = 0; T < 4; ++T) dU[T] = W[T] = gdr_zero4();
 #pragma unroll
@@ -747,21 +798,16 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
             for (int T = 0; T < 4; ++T) dU[T] *= gdr_ld4(&L.tab[kTTk * kGdrC + 16 * T + 4 * g4]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const GdrSplit<1> yo = gdr_split<1>(dY[2 * s], dY[2 * s + 1]);   // exact
+                const ssd_bf16x8 yo = __builtin_bit_cast(ssd_bf16x8, yw[s]);
                 GdrSplit<3> ao[4];
 #pragma unroll
                 for (int T = 0; T < 2 * s + 2; ++T)
-                    ao[T] = gdr_ld_col_parts<3>(sA, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
+                    ao[T] = gdr_ld_tile_cols<3>(L.a, T, s, r16, g4);
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
 #pragma unroll
-                    for (int T = 0; T < 2 * s + 2; ++T) dU[T] = ssd_mfma(ao[T].part[k], yo.part[0], dU[T]);
+                    for (int T = 0; T < 2 * s + 2; ++T) dU[T] = ssd_mfma(ao[T].part[k], yo, dU[T]);
             }
-        }
-        __syncthreads();
-        if (ci > 0) regs.template store_scores<3>(sA, tid);
-        if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, tid);
-        if (live) {
             // W = R^T dU
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -769,7 +815,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
                 GdrSplit<3> ro[4];
 #pragma unroll
                 for (int T = 0; T < 2 * s + 2; ++T)
-                    ro[T] = gdr_ld_col_parts<3>(L.r, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
+                    ro[T] = gdr_ld_tile_cols<3>(L.r, T, s, r16, g4);
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
 #pragma unroll
@@ -782,19 +828,34 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
 #pragma unroll
                 for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = W[T] * sign;
             }
-            // dv = beta W (rows past the end dropped by the range); then the two sources of -D
-            const __amdgpu_buffer_rsrc_t rdv =
-                ssd_buffer(p.dv + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + (uint32_t)p.P));
+            // dv = beta W, rounded, turned so that a lane holds 4 columns of a row
+            // (rows past the end dropped by the range)
+#pragma unroll
+            for (int T = 0; T < 4; ++T) W[T] *= gdr_ld4(&L.tab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+            {
+                const __amdgpu_buffer_rsrc_t rdv =
+                    ssd_buffer(p.dv + (row0 * p.H + h) * p.P, 2u * ((uint32_t)(nv - 1) * ys + (uint32_t)p.P));
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const GdrSplit<1> wo = gdr_split<1>(W[2 * s], W[2 * s + 1]);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const ssd_f32x4 o = ssd_mfma(wo.part[0], pick[t].part[0], gdr_zero4());
+                        const int i = 16 * (2 * s + t) + r16;
+                        ssd_bstore8(rdv, 2u * ((uint32_t)i * ys + p0 + 4 * g4),
+                                    uint2{ssd_pack(o[0], o[1]) ^ flip, ssd_pack(o[2], o[3]) ^ flip});
+                    }
+                }
+            }
+            // the two sources of -D
+            ssd_f32x4 dY[4];
 #pragma unroll
             for (int T = 0; T < 4; ++T) {
-                W[T] *= gdr_ld4(&L.tab[kTBeta * kGdrC + 16 * T + 4 * g4]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b16(ssd_to_bf(sign * W[T][r]), rdv,
-                                                          (int)(2u * ((uint32_t)(16 * T + 4 * g4 + r) * ys + p0 + r16)),
-                                                          0, 0);
+                const uint32_t y0 = T & 1 ? yw[T / 2].z : yw[T / 2].x, y1 = T & 1 ? yw[T / 2].w : yw[T / 2].y;
+                const ssd_f32x4 y = {ssd_bf(y0), __uint_as_float(y0 & 0xffff0000u), ssd_bf(y1),
+                                     __uint_as_float(y1 & 0xffff0000u)};
                 W[T] *= gdr_ld4(&L.tab[kTHk * kGdrC + 16 * T + 4 * g4]);
-                dY[T] *= -gdr_ld4(&L.tab[kTHq * kGdrC + 16 * T + 4 * g4]);
+                dY[T] = y * -gdr_ld4(&L.tab[kTHq * kGdrC + 16 * T + 4 * g4]);
             }
             const float end = -L.end[0];
 #pragma unroll
