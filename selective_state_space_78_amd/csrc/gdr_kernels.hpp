@@ -91,18 +91,17 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ ssd_f32x4 gdr_zero4() { return ssd_f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
 
-// What bf16 rounding left of a and b, given their rounded pair: one dot product
-// of the pair with (-1, 0) or (0, -1) each, exact (a shift or mask and a
-// subtraction otherwise: 5.5 instead of 3.5 instructions per split value). The
-// first constant goes through a register: as an inline constant it would be
-// read as (0, -1).
-__device__ __forceinline__ void gdr_rest(uint32_t pair, float &a, float &b) {
-    uint32_t first = 0x0000bf80u;
-    asm("" : "+s"(first));
-    const ssd_bf16x2 v = __builtin_bit_cast(ssd_bf16x2, pair);
-    const ssd_bf16x2 second = {(__bf16)0.0f, (__bf16)-1.0f};
-    a = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(ssd_bf16x2, first), a, false);
-    b = __builtin_amdgcn_fdot2_f32_bf16(v, second, b, false);
+// a and b rounded to a bf16 pair, and what the rounding left of them (exact). The
+// pair is opaque to the compiler, which would otherwise round a once more, alone,
+// to take it apart (a tenth of the walks' vector instructions). Remainders by
+// dot products of the pair with (-1, 0) and (0, -1) would be 2 instructions less
+// per pair, and measured the same.
+__device__ __forceinline__ uint32_t gdr_take(float &a, float &b) {
+    uint32_t pair = ssd_pack(a, b);
+    asm("" : "+v"(pair));
+    a -= __uint_as_float(pair << 16);
+    b -= __uint_as_float(pair & 0xffff0000u);
+    return pair;
 }
 
 // v as PARTS bf16 operands whose sum carries 8 PARTS significant bits
@@ -119,8 +118,7 @@ __device__ __forceinline__ GdrSplit<PARTS> gdr_split(const float (&v)[8]) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            w[e] = ssd_pack(r[2 * e], r[2 * e + 1]);
-            if (k + 1 < PARTS) gdr_rest(w[e], r[2 * e], r[2 * e + 1]);
+            w[e] = k + 1 < PARTS ? gdr_take(r[2 * e], r[2 * e + 1]) : ssd_pack(r[2 * e], r[2 * e + 1]);
         }
         out.part[k] = __builtin_bit_cast(ssd_bf16x8, uint4{w[0], w[1], w[2], w[3]});
     }
@@ -190,12 +188,9 @@ __device__ __forceinline__ void gdr_store_parts(uint16_t *dst, int plane, float4
     float r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
-        const uint2 w = {ssd_pack(r[0], r[1]), ssd_pack(r[2], r[3])};
+        const uint2 w = k + 1 < PARTS ? uint2{gdr_take(r[0], r[1]), gdr_take(r[2], r[3])}
+                                      : uint2{ssd_pack(r[0], r[1]), ssd_pack(r[2], r[3])};
         *reinterpret_cast<uint2 *>(dst + k * plane) = w;
-        if (k + 1 < PARTS) {
-            gdr_rest(w.x, r[0], r[1]);
-            gdr_rest(w.y, r[2], r[3]);
-        }
     }
 }
 
