@@ -485,22 +485,23 @@ __device__ __forceinline__ GdrSplit<PARTS> gdr_ld_tile_cols(const uint16_t *m, i
     return o;
 }
 
-// A wave's own 16 columns of V (or dY), a chunk ahead in registers (a row per
-// lane), turned through a 64 x 16 tile of LDS that no other wave touches
+// A wave's own 16 columns of V (or dY), a chunk ahead in registers (half a row
+// per lane), turned through a 64 x 16 tile of LDS that no other wave touches
 struct GdrColumns {
     uint4 v[2];
     __device__ __forceinline__ void load(const GdrParams &p, const uint16_t *col, int64_t stride, int64_t rowb, int ci,
                                          int lane) {
         const uint32_t nv = (uint32_t)gdr_valid(p, ci), st = (uint32_t)stride;
         const __amdgpu_buffer_rsrc_t r = ssd_buffer(col + (rowb + (int64_t)ci * kGdrC) * stride, 2u * ((nv - 1) * st + 16));
-        v[0] = ssd_bload16(r, 2u * ((uint32_t)lane * st));
-        v[1] = ssd_bload16(r, 2u * ((uint32_t)lane * st + 8));
+        const uint32_t o = 2u * ((uint32_t)(lane >> 1) * st + 8u * (lane & 1));
+        v[0] = ssd_bload16(r, o);
+        v[1] = ssd_bload16(r, o + 64u * st);
     }
     // the lane's column of rows 16 T + 4 g4 .. + 3, for every T
     __device__ __forceinline__ void turn(uint16_t *tile, int lane, uint2 (&out)[4]) const {
         const int r16 = lane & 15, g4 = lane >> 4;
-        *reinterpret_cast<uint4 *>(tile + 16 * lane) = v[0];
-        *reinterpret_cast<uint4 *>(tile + 16 * lane + 8) = v[1];
+        *reinterpret_cast<uint4 *>(tile + 8 * lane) = v[0];
+        *reinterpret_cast<uint4 *>(tile + 512 + 8 * lane) = v[1];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
         for (int T = 0; T < 4; ++T) out[T] = ssd_ld_tr(tile + 16 * (16 * T + 4 * g4 + (r16 >> 2)) + 4 * (r16 & 3));
@@ -589,13 +590,19 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
     if (p.nc > 1) regs.load(p, b, g, id0 + 1, 1, tid);
     __syncthreads();
     float sign = 1.0f;
+    // two waves share a SIMD: one stages while the other computes
+    const bool early = w < 4;
     for (int ci = 0; ci < p.nc; ++ci) {
         const GdrChunkLds<N, 2> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
-        if (ci + 1 < p.nc) regs.store(lds[(ci + 1) & 1], tid);
-        if (ci + 2 < p.nc) regs.load(p, b, g, id + 2, ci + 2, tid);
+        auto stage = [&]() {
+            if (ci + 1 < p.nc) regs.store(lds[(ci + 1) & 1], tid);
+            if (ci + 2 < p.nc) regs.load(p, b, g, id + 2, ci + 2, tid);
+        };
+        if (early) stage();
+        ssd_f32x4 X[4], Y[4], U[4];
         if (live) {
             uint2 vw[4];
             vr.turn(sV[w], lane, vw);
@@ -605,7 +612,6 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = S[nt] * sign;
             }
-            ssd_f32x4 X[4], Y[4], U[4];
 #pragma unroll
             for (int T = 0; T < 4; ++T) X[T] = Y[T] = U[T] = gdr_zero4();
 #pragma unroll
@@ -658,6 +664,9 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
 #pragma unroll
                 for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = U[T] * sign;
             }
+        }
+        if (!early) stage();
+        if (live) {
             // Y^T = exp(G) S Q^T + U^T A^T; the backward's recomputation stores none
             if (p.y != nullptr) {
                 const __amdgpu_buffer_rsrc_t ry = ssd_buffer(p.y + (row0 * p.H + h) * p.P,
@@ -752,20 +761,25 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
     if (last > 0) regs.load(p, b, g, id0 + last - 1, last - 1, tid);
     __syncthreads();
     float sign = 1.0f;
+    const bool early = w < 4;   // as in the forward
     for (int ci = last; ci >= 0; --ci) {
         const GdrChunkLds<N, 3> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
-        if (ci > 0) regs.store(lds[(ci - 1) & 1], tid);
-        if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, tid);
+        auto stage = [&]() {
+            if (ci > 0) regs.store(lds[(ci - 1) & 1], tid);
+            if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, tid);
+        };
+        if (early) stage();
+        const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
+        uint4 yw[2];
+        ssd_f32x4 W[4];
         if (live) {
             // dY with the chunk's sign, as operands
-            const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
             uint2 yt[4];
             yr.turn(sV[w], lane, yt);
             if (ci > 0) yr.load(p, ycol, ys, rowb, ci - 1, lane);
-            uint4 yw[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 yw[s] = uint4{yt[2 * s].x ^ flip, yt[2 * s].y ^ flip, yt[2 * s + 1].x ^ flip, yt[2 * s + 1].y ^ flip};
@@ -775,7 +789,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
                 for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * nt) = D[nt] * sign;
             }
             // dU = exp(G_C - G) K D'^T + A^T dY
-            ssd_f32x4 dU[4], W[4];
+            ssd_f32x4 dU[4];
 #pragma unroll
             for (int T = 0; T < 4; ++T) dU[T] = W[T] = gdr_zero4();
 #pragma unroll
@@ -823,6 +837,9 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
 #pragma unroll
                 for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = W[T] * sign;
             }
+        }
+        if (!early) stage();
+        if (live) {
             // dv = beta W, rounded, turned so that a lane holds 4 columns of a row
             // (rows past the end dropped by the range)
 #pragma unroll
