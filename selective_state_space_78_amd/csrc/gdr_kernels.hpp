@@ -276,14 +276,22 @@ __device__ __forceinline__ GdrStep gdr_step_of(float dt, float beta, float bias,
 }
 
 // ---------------------------------------------------------------------------
-// Tables, R and scores of one chunk and head
+// Tables, R and scores of one chunk and head. Everything before the first
+// barrier is independent: K and Q go to LDS, row lengths are summed from the
+// pieces on their way, and wave 0 forms the step's tables while they arrive. T
+// and R take the place of K and Q, so that four workgroups fit a CU (they hide
+// each other's latencies, which bound this kernel).
 template <int N>
 __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
-    constexpr int KS = N + kGdrPad;
+    constexpr int KS = N + kGdrPad, KI = kGdrC * N / 8 / 256, LPR = N / 8;   // lanes per row
     constexpr int TS = kGdrC + 4;          // fp32 row stride of T and R
-    __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
-    __shared__ __attribute__((aligned(16))) float sT[kGdrC * TS], sR[kGdrC * TS];
-    __shared__ float sGh[kGdrC], sGl[kGdrC], sB[kGdrC], sRk[kGdrC], sRq[kGdrC];
+    union Lds {
+        struct { uint16_t k[kGdrC * KS], q[kGdrC * KS]; } in;
+        struct { float t[kGdrC * TS], r[kGdrC * TS]; } sys;
+    };
+    __shared__ __attribute__((aligned(16))) Lds u;
+    __shared__ __attribute__((aligned(16))) float sGh[kGdrC], sGl[kGdrC], sB[kGdrC], sRk[kGdrC], sUq[kGdrC];
+    __shared__ float sHead[kGdrC], sTail[kGdrC];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
     const int64_t id = blockIdx.x;                // (b, h) major, chunk minor
@@ -292,84 +300,130 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
     const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
     const int nv = gdr_valid(p, ci);
     const int64_t row0 = (int64_t)b * p.L + (int64_t)ci * kGdrC;
-    gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, 256);
-    gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, 256);
     float *tab = p.tab + id * (kGdrTab * kGdrC);
-    if (w == 0) {
-        GdrStep s = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (lane < nv)
-            s = gdr_step_of(ssd_bf(p.dt[(row0 + lane) * p.dts + h]), ssd_bf(p.beta[(row0 + lane) * p.bs + h]),
-                            p.dt_bias ? p.dt_bias[h] : 0.0f, p.dt_softplus, p.beta_sigmoid);
-        // the running sum in 64 bits: differences of it are exponents, and a
-        // rounding of the sum would be an error relative to the product
-        double G = (double)s.step * (double)p.A[h] * 1.4426950408889634074;
-        for (int o = 1; o < kGdrC; o <<= 1) {
-            const double up = __shfl_up(G, o);
-            if (lane >= o) G += up;
-        }
-        const double Gc = __shfl(G, kGdrC - 1);
-        const float hi = (float)G;
-        sGh[lane] = hi;
-        sGl[lane] = (float)(G - (double)hi);
-        sB[lane] = s.beta;
-        tab[kTBeta * kGdrC + lane] = s.beta;
-        tab[kTHead * kGdrC + lane] = __builtin_amdgcn_exp2f((float)G);
-        tab[kTGhi * kGdrC + lane] = hi;
-        tab[kTGlo * kGdrC + lane] = (float)(G - (double)hi);
-        tab[kTStep * kGdrC + lane] = s.step;
-        tab[kTDstep * kGdrC + lane] = s.dstep;
-        tab[kTDbeta * kGdrC + lane] = s.dbeta;
-        sT[lane] = __builtin_amdgcn_exp2f((float)G);
-        sR[lane] = __builtin_amdgcn_exp2f((float)(Gc - G));
-    }
-    __syncthreads();
     {
-        // row lengths: 4 threads per row
-        const int row = tid >> 2, part = tid & 3;
-        float k2 = 0.0f, q2 = 0.0f;
-        if (p.qk_norm)
-            for (int c = part * (N / 4); c < (part + 1) * (N / 4); ++c) {
-                const float kv = ssd_bf(sK[row * KS + c]), qv = ssd_bf(sQ[row * KS + c]);
-                k2 = fmaf(kv, kv, k2);
-                q2 = fmaf(qv, qv, q2);
+        const uint32_t ks = (uint32_t)p.ks, qs = (uint32_t)p.qs;
+        const __amdgpu_buffer_rsrc_t rk =
+            ssd_buffer(p.k + row0 * p.ks + (int64_t)g * N, 2u * ((uint32_t)(nv - 1) * ks + N));
+        const __amdgpu_buffer_rsrc_t rq =
+            ssd_buffer(p.q + row0 * p.qs + (int64_t)g * N, 2u * ((uint32_t)(nv - 1) * qs + N));
+        uint4 kr[KI], qr[KI];
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const uint32_t x = i * 256 + tid, row = x / LPR, c = 8 * (x % LPR);
+            kr[i] = ssd_bload16(rk, 2u * (row * ks + c));
+            qr[i] = ssd_bload16(rq, 2u * (row * qs + c));
+        }
+        if (w == 0) {
+            GdrStep s = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (lane < nv)
+                s = gdr_step_of(ssd_bf(p.dt[(row0 + lane) * p.dts + h]), ssd_bf(p.beta[(row0 + lane) * p.bs + h]),
+                                p.dt_bias ? p.dt_bias[h] : 0.0f, p.dt_softplus, p.beta_sigmoid);
+            // the running sum in 64 bits: differences of it are exponents, and a
+            // rounding of the sum would be an error relative to the product
+            const double G = gdr_prefix64((double)s.step * (double)p.A[h] * 1.4426950408889634074, lane);
+            const double Gc = gdr_last64(G);
+            const float hi = (float)G, lo = (float)(G - (double)hi);
+            sGh[lane] = hi;
+            sGl[lane] = lo;
+            sB[lane] = s.beta;
+            const float head = __builtin_amdgcn_exp2f(hi);
+            sHead[lane] = head;
+            sTail[lane] = __builtin_amdgcn_exp2f((float)(Gc - G));
+            tab[kTBeta * kGdrC + lane] = s.beta;
+            tab[kTHead * kGdrC + lane] = head;
+            tab[kTGhi * kGdrC + lane] = hi;
+            tab[kTGlo * kGdrC + lane] = lo;
+            tab[kTStep * kGdrC + lane] = s.step;
+            tab[kTDstep * kGdrC + lane] = s.dstep;
+            tab[kTDbeta * kGdrC + lane] = s.dbeta;
+        }
+        auto square = [](const uint4 &v) {
+            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float a = ssd_bf(e[k]), c = __uint_as_float(e[k] & 0xffff0000u);
+                s = fmaf(a, a, fmaf(c, c, s));
             }
-        k2 += __shfl_xor(k2, 1);
-        q2 += __shfl_xor(q2, 1);
-        k2 += __shfl_xor(k2, 2);
-        q2 += __shfl_xor(q2, 2);
-        if (part == 0) {
-            const float rk = p.qk_norm ? 1.0f / sqrtf(k2 + p.qk_eps) : 1.0f;
-            const float uq = p.qk_norm ? 1.0f / sqrtf(q2 + p.qk_eps) : 1.0f;
-            const float rq = uq * p.scale, head = sT[row], tail = sR[row];
-            sRk[row] = rk;
-            sRq[row] = rq;
-            tab[kTHk * kGdrC + row] = head * rk;
-            tab[kTHq * kGdrC + row] = head * rq;
-            tab[kTTk * kGdrC + row] = tail * rk;
-            tab[kTRk * kGdrC + row] = rk;
-            tab[kTRq * kGdrC + row] = rq;
-            tab[kTUq * kGdrC + row] = uq;
+            return s;
+        };
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int x = i * 256 + tid, row = x / LPR, o = row * KS + 8 * (x % LPR);
+            *reinterpret_cast<uint4 *>(&u.in.k[o]) = kr[i];
+            *reinterpret_cast<uint4 *>(&u.in.q[o]) = qr[i];
+            if (p.qk_norm) {
+                float k2 = square(kr[i]), q2 = square(qr[i]);
+                if (LPR == 16) {
+                    k2 = gdr_sum16(k2);
+                    q2 = gdr_sum16(q2);
+                } else {
+#pragma unroll
+                    for (int o2 = 1; o2 < 8; o2 <<= 1) {
+                        k2 += __shfl_xor(k2, o2);
+                        q2 += __shfl_xor(q2, o2);
+                    }
+                }
+                if (x % LPR == 0) {
+                    sRk[row] = 1.0f / sqrtf(k2 + p.qk_eps);
+                    sUq[row] = 1.0f / sqrtf(q2 + p.qk_eps);
+                }
+            } else if (x % LPR == 0) {
+                sRk[row] = sUq[row] = 1.0f;
+            }
         }
     }
     __syncthreads();
-    float *score = p.score + id * (kGdrTiles * 256);
-    for (int J = 0; J <= w; ++J) {
-        ssd_f32x4 kk = gdr_zero4(), qk = gdr_zero4();
+    if (w == 3) {
+        const float rk = sRk[lane], uq = sUq[lane], rq = uq * p.scale;
+        tab[kTHk * kGdrC + lane] = sHead[lane] * rk;
+        tab[kTHq * kGdrC + lane] = sHead[lane] * rq;
+        tab[kTTk * kGdrC + lane] = sTail[lane] * rk;
+        tab[kTRk * kGdrC + lane] = rk;
+        tab[kTRq * kGdrC + lane] = rq;
+        tab[kTUq * kGdrC + lane] = uq;
+    }
+    // tiles w, w + 4, w + 8, held transposed: row i = 16 T + r16 is the lane's,
+    // columns j = 16 J + 4 g4 .. + 3
+    ssd_f32x4 kk[3], qk[3];
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        const int x = w + 4 * t;
+        kk[t] = qk[t] = gdr_zero4();
+        if (x >= kGdrTiles) continue;
+        const int T = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, J = x - T * (T + 1) / 2;
 #pragma unroll
         for (int s = 0; s < N / 32; ++s) {
-            const ssd_bf16x8 bop = ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]);
-            kk = ssd_mfma(ssd_ld16(&sK[(16 * w + r16) * KS + 32 * s + 8 * g4]), bop, kk);
-            qk = ssd_mfma(ssd_ld16(&sQ[(16 * w + r16) * KS + 32 * s + 8 * g4]), bop, qk);
+            const ssd_bf16x8 kj = ssd_ld16(&u.in.k[(16 * J + r16) * KS + 32 * s + 8 * g4]);
+            kk[t] = ssd_mfma(kj, ssd_ld16(&u.in.k[(16 * T + r16) * KS + 32 * s + 8 * g4]), kk[t]);
+            qk[t] = ssd_mfma(kj, ssd_ld16(&u.in.q[(16 * T + r16) * KS + 32 * s + 8 * g4]), qk[t]);
         }
-        const int j = 16 * J + r16;
+    }
+    __syncthreads();
+    float *sT = u.sys.t, *sR = u.sys.r;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        const int x = w + 4 * t;
+        if (x >= kGdrTiles) continue;
+        const int T = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, J = x - T * (T + 1) / 2;
+        const int i = 16 * T + r16, j0 = 16 * J + 4 * g4;
+        const float gh = sGh[i], gl = sGl[i], ki = sRk[i] * sB[i], qi = sUq[i] * p.scale;
+        const float4 ghj = *reinterpret_cast<const float4 *>(&sGh[j0]), glj = *reinterpret_cast<const float4 *>(&sGl[j0]);
+        const float4 rkj = *reinterpret_cast<const float4 *>(&sRk[j0]);
+        const float gj[4] = {ghj.x, ghj.y, ghj.z, ghj.w}, lj[4] = {glj.x, glj.y, glj.z, glj.w};
+        const float rj[4] = {rkj.x, rkj.y, rkj.z, rkj.w};
+        ssd_f32x4 tt, sc;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = 16 * w + 4 * g4 + r;
-            const float gam =
-                i >= j ? __builtin_amdgcn_exp2f((sGh[i] - sGh[j]) + (sGl[i] - sGl[j])) * sRk[j] : 0.0f;
-            sT[i * TS + j] = i > j ? kk[r] * gam * sRk[i] * sB[i] : 0.0f;
-            score[gdr_tile(w, J) * 256 + (4 * g4 + r) * 16 + r16] = qk[r] * gam * sRq[i];
+            // above the diagonal exp2(-inf): no branch
+            const float e = i >= j0 + r ? (gh - gj[r]) + (gl - lj[r]) : -__builtin_inff();
+            const float gam = __builtin_amdgcn_exp2f(e) * rj[r];
+            tt[r] = i > j0 + r ? kk[t][r] * gam * ki : 0.0f;
+            sc[r] = qk[t][r] * gam * qi;
         }
+        *reinterpret_cast<ssd_f32x4 *>(&sT[i * TS + j0]) = tt;
+        *reinterpret_cast<ssd_f32x4 *>(p.score + id * (kGdrTiles * 256) + 256 * x + 16 * r16 + 4 * g4) = sc;
     }
     __syncthreads();
     {
@@ -378,8 +432,14 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float v = i == r16 ? 1.0f : 0.0f;
+            float row[16];
 #pragma unroll
-            for (int k = 0; k < i; ++k) v = fmaf(-sT[(16 * w + i) * TS + 16 * w + k], x[k], v);
+            for (int k = 0; k < i; k += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(&sT[(16 * w + i) * TS + 16 * w + k]);
+                row[k] = f.x; row[k + 1] = f.y; row[k + 2] = f.z; row[k + 3] = f.w;
+            }
+#pragma unroll
+            for (int k = 0; k < i; ++k) v = fmaf(-row[k], x[k], v);
             x[i] = v;
         }
         if (g4 == 0)
@@ -402,14 +462,15 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
                                                        0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) sR[(16 * i + 4 * g4 + r) * TS + 16 * w + r16] = out[r];
-        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     __syncthreads();
     float *R = p.R + id * (kGdrTiles * 256);
-    for (int q = tid; q < kGdrTiles * 256; q += 256) {
-        const int t = q >> 8, i = (q >> 4) & 15, j = q & 15;
+    for (int x = tid; x < kGdrTiles * 64; x += 256) {
+        const int t = x >> 6, i = (x >> 2) & 15, c = x & 3;
         const int T = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, J = t - T * (T + 1) / 2;
-        R[q] = sR[(16 * T + i) * TS + 16 * J + j];
+        *reinterpret_cast<float4 *>(R + 4 * x) =
+            *reinterpret_cast<const float4 *>(&sR[(16 * T + i) * TS + 16 * J + 4 * c]);
     }
 }
 
