@@ -239,22 +239,32 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward of VEC channels, given 1/rms and m = mean(n w dy): the outputs, and
-// what the channels add to dweight and dscale.
-template <typename P, int VEC>
-struct BwdIn { float f[VEC], up[VEC], dy[VEC]; };   // normed, incoming (before weight), dy
+// Backward of VEC channels: what is read (kept until the row's sums are known),
+// then, given 1/rms and m = mean(n w dy), the outputs and what the channels add
+// to dweight and dscale.
+template <typename P, int VEC> struct BwdIn {
+    float f[VEC], up[VEC];             // normed, incoming (before weight)
+    float x[VEC], z[VEC], dy[VEC];     // gated: as read; prenorm: x with a scale, dr in z
+};
 
 template <typename P, int VEC>
 __device__ __forceinline__ void bwd_load(const NormParams &p, int64_t row, int64_t g, int64_t c, BwdIn<P, VEC> &o) {
+    typedef typename P::T T;
     const int64_t yo = row * p.groups * p.dim + g * p.dim + c;
-    ld<typename P::T, VEC>(p.dy, yo, o.dy);
+    ld<T, VEC>(p.dy, yo, o.dy);
     if constexpr (P::kGated) {
-        float gate[VEC];
-        P::template normed<VEC>(p, row, g, c, o.f, gate);
+        ld<T, VEC>(p.x, row * p.xs + g * p.dim + c, o.x);
+        if (p.z) ld<T, VEC>(p.z, row * p.zs + g * p.dim + c, o.z);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) o.up[e] = p.gate_first ? o.dy[e] : o.dy[e] * gate[e];
+        for (int e = 0; e < VEC; ++e) {
+            const float gate = p.z ? o.z[e] * sigm(o.z[e]) : 1.0f;
+            o.f[e] = p.gate_first ? o.x[e] * gate : o.x[e];
+            o.up[e] = p.gate_first ? o.dy[e] : o.dy[e] * gate;
+        }
     } else {
         ld<typename P::R, VEC>(p.res, row * p.dim + c, o.f);
+        if (p.dr) ld<typename P::R, VEC>(p.dr, yo, o.z);
+        if (p.scale) ld<T, VEC>(p.x, row * p.xs + c, o.x);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o.up[e] = o.dy[e];
     }
@@ -263,6 +273,7 @@ __device__ __forceinline__ void bwd_load(const NormParams &p, int64_t row, int64
 template <typename P, int VEC>
 __device__ __forceinline__ void bwd_finish(const NormParams &p, int64_t row, int64_t g, int64_t c, const BwdIn<P, VEC> &in,
                                            const float (&wt)[VEC], float inv, float m, float (&dw)[VEC], float (&dsc)[VEC]) {
+    typedef typename P::T T;
     const int64_t yo = row * p.groups * p.dim + g * p.dim + c;
     float df[VEC];
 #pragma unroll
@@ -272,43 +283,36 @@ __device__ __forceinline__ void bwd_finish(const NormParams &p, int64_t row, int
         dw[e] = fmaf(in.up[e], n, dw[e]);
     }
     if constexpr (P::kGated) {
-        float dx[VEC];
         if (p.z) {
-            float x[VEC], z[VEC], dz[VEC];
-            ld<typename P::T, VEC>(p.x, row * p.xs + g * p.dim + c, x);
-            ld<typename P::T, VEC>(p.z, row * p.zs + g * p.dim + c, z);
+            float dx[VEC], dz[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float s = sigm(z[e]);
-                const float dgate = s * (1.0f + z[e] * (1.0f - s));
-                dx[e] = p.gate_first ? df[e] * z[e] * s : df[e];
-                dz[e] = (p.gate_first ? df[e] * x[e] : in.dy[e] * in.f[e] * inv * wt[e]) * dgate;
+                const float z = in.z[e], s = sigm(z);
+                const float dgate = s * (1.0f + z * (1.0f - s));
+                dx[e] = p.gate_first ? df[e] * z * s : df[e];
+                dz[e] = (p.gate_first ? df[e] * in.x[e] : in.dy[e] * in.f[e] * inv * wt[e]) * dgate;
             }
-            st<typename P::T, VEC>(p.dz, yo, dz);
+            st<T, VEC>(p.dz, yo, dz);
+            st<T, VEC>(p.dx, yo, dx);
         } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) dx[e] = df[e];
+            st<T, VEC>(p.dx, yo, df);
         }
-        st<typename P::T, VEC>(p.dx, yo, dx);
     } else {
         if (p.dr) {
-            float dr[VEC];
-            ld<typename P::R, VEC>(p.dr, yo, dr);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) df[e] += dr[e];
+            for (int e = 0; e < VEC; ++e) df[e] += in.z[e];
         }
         if (p.dres) st<typename P::R, VEC>(p.dres, yo, df);
         if (p.scale) {
-            float x[VEC], s[VEC];
-            ld<typename P::T, VEC>(p.x, row * p.xs + c, x);
+            float s[VEC];
             ld<float, VEC>(p.scale, c, s);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                dsc[e] = fmaf(df[e], x[e], dsc[e]);
+                dsc[e] = fmaf(df[e], in.x[e], dsc[e]);
                 df[e] *= s[e];
             }
         }
-        st<typename P::T, VEC>(p.dx, yo, df);
+        st<T, VEC>(p.dx, yo, df);
     }
 }
 
@@ -448,23 +452,25 @@ __global__ __launch_bounds__(256) void norm_bwd_cols_kernel(const NormParams p) 
     }
 }
 
-// Column sums of the partial rows (slabs of `cols` floats): 64 columns and 4
-// runs of slabs per workgroup
-__global__ __launch_bounds__(256) void norm_reduce_kernel(const float *part, int slabs, int64_t cols, int64_t first,
-                                                          float *o0, float *o1) {
-    __shared__ float s[4][64];
-    const int l = threadIdx.x & 63, run = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + l;
-    const int per = (slabs + 3) / 4;
+// Column sums of the partial rows (slabs of `cols` floats): 16 columns and 64 runs
+// of slabs per workgroup, each run in order, then the runs pairwise
+constexpr int kRunCols = 16, kRuns = 64;
+__global__ __launch_bounds__(kRunCols * kRuns) void norm_reduce_kernel(const float *part, int slabs, int64_t cols,
+                                                                       int64_t first, float *o0, float *o1) {
+    __shared__ float s[kRuns][kRunCols];
+    const int l = threadIdx.x % kRunCols, run = threadIdx.x / kRunCols;
+    const int64_t c = (int64_t)blockIdx.x * kRunCols + l;
     float a = 0.0f;
     if (c < cols)
-        for (int k = run * per; k < min(slabs, (run + 1) * per); ++k) a += part[(int64_t)k * cols + c];
+        for (int k = run; k < slabs; k += kRuns) a += part[(int64_t)k * cols + c];
     s[run][l] = a;
-    __syncthreads();
+    for (int o = kRuns / 2; o >= 1; o >>= 1) {
+        __syncthreads();
+        if (run < o) s[run][l] += s[run + o][l];
+    }
     if (run == 0 && c < cols) {
-        const float v = (s[0][l] + s[1][l]) + (s[2][l] + s[3][l]);
-        if (c < first) o0[c] = v;
-        else if (o1) o1[c - first] = v;
+        if (c < first) o0[c] = s[0][l];
+        else if (o1) o1[c - first] = s[0][l];
     }
 }
 
@@ -543,7 +549,8 @@ hipError_t launch_bwd(NormParams &p, hipStream_t st) {
     if (e != hipSuccess) return e;
     // without a scale the second half of a partial row is not written, and not read
     const int64_t read = P::kGated || p.scale ? cols : p.dim;
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((read + 63) / 64)), dim3(256), 0, st, p.part, p.slabs, cols,
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((read + kRunCols - 1) / kRunCols)),
+                       dim3(kRunCols * kRuns), 0, st, p.part, p.slabs, cols,
                        P::kGated ? cols : p.dim, p.dweight, p.dscale);
     return hipGetLastError();
 }
