@@ -89,6 +89,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIBRARY):
@@ -161,7 +163,7 @@ def _dtype_code(t) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check(t, name, shape=None, dtype=None, device=None):
@@ -169,7 +171,7 @@ def _check(t, name, shape=None, dtype=None, device=None):
         return
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
@@ -178,10 +180,12 @@ def _check(t, name, shape=None, dtype=None, device=None):
 
 
 def _stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    # the handle alone: a Stream object costs more than a launch of a small kernel
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _tuning(tuning):
@@ -531,13 +535,14 @@ def _row_stride(t, name, lead, tail, dtype, device):
     """Elements from one row of `t` (the `tail` dimensions, dense) to the next,
     where the rows of the `lead` dimensions follow one another evenly; raises
     for any other layout."""
-    shape = tuple(lead) + tuple(tail)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if t.shape != lead + tail:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), lead + tail))
     if t.dtype != dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.is_contiguous():
+        return 0
     width = 1
     for n, st in zip(reversed(tail), reversed(t.stride()[len(lead):])):
         if n != 1 and st != width and t.numel() > 0:
@@ -565,6 +570,8 @@ def _row_stride(t, name, lead, tail, dtype, device):
 def _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, qk_norm, qk_eps):
     import torch
     code = _dtype_code(v)
+    if q.dim() < 2:
+        raise ValueError("q must be (..., G, N)")
     lead, (H, P), (G, N) = tuple(v.shape[:-2]), v.shape[-2:], q.shape[-2:]
     dev, t = v.device, v.dtype
     strides = [_row_stride(x, n, lead, tail, t, dev)
