@@ -504,6 +504,12 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 // them. So the state's sign alternates: odd chunks hold -S, through the signs
 // of the scales that are applied anyway, and the errors cancel.
 
+// With fewer than 8 computing waves a workgroup has as many helpers, which do
+// the staging: a computing wave's time per chunk is then its own arithmetic. With
+// 8 (two to a SIMD) there are no registers for helpers, and the two waves of a
+// SIMD stage at different times instead.
+constexpr int gdr_helpers(int nw) { return nw < 8 ? nw : 0; }
+
 // LDS of one chunk: K and Q rows; the lower tiles of R in three parts and of the
 // scores in AP; the first four tables and the decay over the whole chunk. Tiles
 // have no padding: a wave's 8-byte reads of a 16-bit tile 16 columns wide, along
@@ -625,7 +631,7 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
 // a 16 x 16 tile's products of parts, small ones first, each over every T in
 // turn so that consecutive instructions do not wait for one another
 template <int N, bool SAVE, int NW>
-__global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int splits) {
+__global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(const GdrParams p, int splits) {
     constexpr int KS = N + kGdrPad, NT = N / 16;
     __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 2> lds[2];
     __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
@@ -634,7 +640,9 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
     const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
     const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
     const int p0 = 16 * (split * NW + w);
-    const bool live = p0 < p.P;
+    constexpr bool HELP = gdr_helpers(NW) > 0;
+    const int sid = HELP ? tid - 64 * NW : tid;   // place among the staging threads
+    const bool live = w < NW && p0 < p.P;
     const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
     const uint32_t ysr = (uint32_t)(p.H * p.P);
     const int64_t id0 = (int64_t)bh * p.nc, rowb = (int64_t)b * p.L;
@@ -645,22 +653,23 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
     const uint16_t *vcol = p.v + (int64_t)h * p.P + p0;
     GdrChunkRegs<N, 2, NW> regs;
     GdrColumns vr;
-    regs.load(p, b, g, id0, 0, tid);
     if (live) vr.load(p, vcol, p.vs, rowb, 0, lane);
-    regs.store(lds[0], tid);
-    if (p.nc > 1) regs.load(p, b, g, id0 + 1, 1, tid);
+    if (!HELP || w >= NW) {
+        regs.load(p, b, g, id0, 0, sid);
+        regs.store(lds[0], sid);
+        if (p.nc > 1) regs.load(p, b, g, id0 + 1, 1, sid);
+    }
     __syncthreads();
     float sign = 1.0f;
-    // two waves share a SIMD: one stages while the other computes
-    const bool early = w < 4;
+    const bool early = HELP ? w >= NW : w < 4, late = !HELP && !early;
     for (int ci = 0; ci < p.nc; ++ci) {
         const GdrChunkLds<N, 2> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
         auto stage = [&]() {
-            if (ci + 1 < p.nc) regs.store(lds[(ci + 1) & 1], tid);
-            if (ci + 2 < p.nc) regs.load(p, b, g, id + 2, ci + 2, tid);
+            if (ci + 1 < p.nc) regs.store(lds[(ci + 1) & 1], sid);
+            if (ci + 2 < p.nc) regs.load(p, b, g, id + 2, ci + 2, sid);
         };
         if (early) stage();
         ssd_f32x4 X[4], Y[4], U[4];
@@ -726,7 +735,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
                 for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = U[T] * sign;
             }
         }
-        if (!early) stage();
+        if (late) stage();
         if (live) {
             // Y^T = exp(G) S Q^T + U^T A^T; the backward's recomputation stores none
             if (p.y != nullptr) {
@@ -784,7 +793,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_fwd_kernel(const GdrParams p, int
 // ---------------------------------------------------------------------------
 // Backwards over the chunks: D' of every chunk, W, dv and dh0.
 template <int N, int NW>
-__global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int splits) {
+__global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(const GdrParams p, int splits) {
     constexpr int KS = N + kGdrPad, NT = N / 16;
     __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 3> lds[2];
     __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
@@ -793,7 +802,9 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
     const int bh = blockIdx.x / splits, split = blockIdx.x % splits;
     const int b = bh / p.H, h = bh % p.H, g = h / p.hpg;
     const int p0 = 16 * (split * NW + w);
-    const bool live = p0 < p.P;
+    constexpr bool HELP = gdr_helpers(NW) > 0;
+    const int sid = HELP ? tid - 64 * NW : tid;   // place among the staging threads
+    const bool live = w < NW && p0 < p.P;
     const int64_t sbase = ((int64_t)bh * p.P + p0 + r16) * N;
     const uint32_t ys = (uint32_t)(p.H * p.P);
     const int64_t id0 = (int64_t)bh * p.nc, rowb = (int64_t)b * p.L;
@@ -816,21 +827,23 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
     const int last = p.nc - 1;
     GdrChunkRegs<N, 3, NW> regs;
     GdrColumns yr;
-    regs.load(p, b, g, id0 + last, last, tid);
     if (live) yr.load(p, ycol, ys, rowb, last, lane);
-    regs.store(lds[last & 1], tid);
-    if (last > 0) regs.load(p, b, g, id0 + last - 1, last - 1, tid);
+    if (!HELP || w >= NW) {
+        regs.load(p, b, g, id0 + last, last, sid);
+        regs.store(lds[last & 1], sid);
+        if (last > 0) regs.load(p, b, g, id0 + last - 1, last - 1, sid);
+    }
     __syncthreads();
     float sign = 1.0f;
-    const bool early = w < 4;   // as in the forward
+    const bool early = HELP ? w >= NW : w < 4, late = !HELP && !early;   // as in the forward
     for (int ci = last; ci >= 0; --ci) {
         const GdrChunkLds<N, 3> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
         auto stage = [&]() {
-            if (ci > 0) regs.store(lds[(ci - 1) & 1], tid);
-            if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, tid);
+            if (ci > 0) regs.store(lds[(ci - 1) & 1], sid);
+            if (ci > 1) regs.load(p, b, g, id - 2, ci - 2, sid);
         };
         if (early) stage();
         const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;
@@ -899,7 +912,7 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
                 for (int T = 0; T < 4; ++T) *reinterpret_cast<ssd_f32x4 *>(dst + 16 * T) = W[T] * sign;
             }
         }
-        if (!early) stage();
+        if (late) stage();
         if (live) {
             // dv = beta W, rounded, turned so that a lane holds 4 columns of a row
             // (rows past the end dropped by the range)
@@ -967,7 +980,8 @@ __global__ __launch_bounds__(64 * NW) void gdr_rev_kernel(const GdrParams p, int
 // ---------------------------------------------------------------------------
 // dq, dk, dbeta, ddt of one chunk and group. Wave w holds n tile w; the heads
 // of the group follow one another and add into dq and dk in that order.
-template <int N>
+// ONE: a head per group, whose dq and dk need no second accumulators.
+template <int N, bool ONE>
 __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
     constexpr int KS = N + kGdrPad, NW = N / 16, TH = 64 * NW, PL = kGdrPlane;
     constexpr int PB = 32;                 // columns p per step
@@ -988,8 +1002,9 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
     __shared__ float sWv[kGdrC];
     __shared__ double sDs[NW];
     uint16_t *const sPA = sX.pairs.a, *const sPE = sX.pairs.e;
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r16 = lane & 15, g4 = lane >> 4;
+    int tid = threadIdx.x;
+    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int r16 = lane & 15, g4 = lane >> 4;
     const int ci = (int)(blockIdx.x % p.nc);
     const int bg = (int)(blockIdx.x / p.nc);
     const int b = bg / p.G, g = bg % p.G;
@@ -1052,6 +1067,9 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
             }
         }
     };
+    // Addresses from the lane's place are formed where they are used: hoisted out of
+    // the loops they would fill the registers.
+    auto fresh = [&]() { asm volatile("" : "+v"(r16), "+v"(g4), "+v"(tid)); };
     load(g * p.hpg, 0);
     gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, TH);
     gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, TH);
@@ -1075,6 +1093,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
         store(sX.step[0], 1.0f);
         for (int c0 = 0, buf = 0; c0 < p.P; c0 += PB, buf ^= 1) {
             const float flip = buf ? -1.0f : 1.0f;
+            fresh();
             // S and D' columns n0 + r16, rows p = c0 + 16 (e / 4) + 4 g4 + e % 4
             GdrSplit<3> so, dd;
             {
@@ -1092,6 +1111,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
             else if (hh + 1 < p.hpg) load(h + 1, 0);
             __syncthreads();
             const Step &X = sX.step[buf];
+            fresh();
 #pragma unroll
             for (int T = 0; T < 4; ++T) {
                 const GdrSplit<1> yo = gdr_whole(gdr_ld_perm(&X.dy[(16 * T + r16) * YS + 4 * g4]));
@@ -1133,6 +1153,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
             }
             if (c0 + PB < p.P) store(sX.step[buf ^ 1], -flip);
         }
+        fresh();
         __syncthreads();                   // every wave is done with the steps: their place holds the pairs
         gdr_zero_upper<3>(sPA, tid, TH);
         gdr_zero_upper<3>(sPE, tid, TH);
@@ -1204,6 +1225,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                         tr = ssd_mfma(eo.part[k], ko[s], tr);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 if (s >= T / 2) {
                     const GdrSplit<3> eo = gdr_ld_col_parts<3>(sPE, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
                     const GdrSplit<3> ao = gdr_ld_col_parts<3>(sPA, kGdrRS, 32 * s + 4 * g4, 16 * T, r16, PL);
@@ -1230,8 +1252,8 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                 *reinterpret_cast<ssd_f32x4 *>(&sDot[w][0][16 * T + 4 * g4]) = dot;
                 *reinterpret_cast<ssd_f32x4 *>(&sDot[w][1][16 * T + 4 * g4]) = kw;
             }
-            dq[T] += aq[T];
-            dk[T] += row + col;
+            dq[T] = ONE ? aq[T] : dq[T] + aq[T];
+            dk[T] = ONE ? row + col : dk[T] + (row + col);
             __builtin_amdgcn_sched_barrier(0);
         }
         // <D', S'> = exp(G_C) <D', S> + sum_j exp(G_C - G_j) k_j . (U D')_j

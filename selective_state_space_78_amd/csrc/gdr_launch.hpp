@@ -7,12 +7,17 @@ namespace ssm_detail {
 
 #ifdef SSM_GDR_INSTANTIATE
 
-// Waves (of 16 columns) per workgroup of the kernels that walk the chunks: 8
-// when that leaves a workgroup for most CUs, else 4, so that a head's columns
-// spread over two
+constexpr int kGdrCus = 256;
+
+// Computing waves (of 16 columns) per workgroup of the kernels that walk the
+// chunks. LDS allows one workgroup per CU, so the rounds over the CUs count, times
+// what a chunk takes: about 1.1 times as long with 4 waves as with 2, and 1.7
+// times with 8 (measured on 48 and 256 heads of 128 x 128)
 inline int gdr_waves(const GdrParams &p) {
-    const int64_t heads = (int64_t)p.batch * p.H;
-    return p.P > 64 && heads * ((p.P / 16 + 7) / 8) >= 192 ? 8 : 4;
+    const int64_t heads = (int64_t)p.batch * p.H, tiles = p.P / 16;
+    auto time = [&](int nw, double chunk) { return (double)((heads * ((tiles + nw - 1) / nw) + kGdrCus - 1) / kGdrCus) * chunk; };
+    const double t2 = time(2, 1.0), t4 = time(4, 1.1), t8 = time(8, 1.7);
+    return t2 <= t4 && t2 <= t8 ? 2 : t4 <= t8 ? 4 : 8;
 }
 
 template <int N>
@@ -27,32 +32,40 @@ void gdr_fwd_nw(const GdrParams &p, bool save, hipStream_t st) {
     const int splits = (p.P / 16 + NW - 1) / NW;
     const dim3 grid((unsigned)((int64_t)p.batch * p.H * splits));
     if (save)
-        hipLaunchKernelGGL((gdr_fwd_kernel<N, true, NW>), grid, dim3(64 * NW), 0, st, p, splits);
+        hipLaunchKernelGGL((gdr_fwd_kernel<N, true, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
     else
-        hipLaunchKernelGGL((gdr_fwd_kernel<N, false, NW>), grid, dim3(64 * NW), 0, st, p, splits);
+        hipLaunchKernelGGL((gdr_fwd_kernel<N, false, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
 }
 
 template <int N>
 hipError_t gdr_fwd_launch(const GdrParams &p, bool save, hipStream_t st) {
-    if (gdr_waves(p) == 8) gdr_fwd_nw<N, 8>(p, save, st);
-    else gdr_fwd_nw<N, 4>(p, save, st);
+    const int nw = gdr_waves(p);
+    if (nw == 8) gdr_fwd_nw<N, 8>(p, save, st);
+    else if (nw == 4) gdr_fwd_nw<N, 4>(p, save, st);
+    else gdr_fwd_nw<N, 2>(p, save, st);
     return hipGetLastError();
 }
 
 template <int N, int NW>
 void gdr_rev_nw(const GdrParams &p, hipStream_t st) {
     const int splits = (p.P / 16 + NW - 1) / NW;
-    hipLaunchKernelGGL((gdr_rev_kernel<N, NW>), dim3((unsigned)((int64_t)p.batch * p.H * splits)), dim3(64 * NW), 0, st,
-                       p, splits);
+    hipLaunchKernelGGL((gdr_rev_kernel<N, NW>), dim3((unsigned)((int64_t)p.batch * p.H * splits)),
+                       dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
 }
 
 template <int N>
 hipError_t gdr_bwd_launch(const GdrParams &p, hipStream_t st) {
-    if (gdr_waves(p) == 8) gdr_rev_nw<N, 8>(p, st);
-    else gdr_rev_nw<N, 4>(p, st);
+    const int nw = gdr_waves(p);
+    if (nw == 8) gdr_rev_nw<N, 8>(p, st);
+    else if (nw == 4) gdr_rev_nw<N, 4>(p, st);
+    else gdr_rev_nw<N, 2>(p, st);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdr_grad_kernel<N>), dim3((unsigned)((int64_t)p.batch * p.G * p.nc)), dim3(4 * N), 0, st, p);
+    const dim3 grid((unsigned)((int64_t)p.batch * p.G * p.nc));
+    if (p.hpg == 1)
+        hipLaunchKernelGGL((gdr_grad_kernel<N, true>), grid, dim3(4 * N), 0, st, p);
+    else
+        hipLaunchKernelGGL((gdr_grad_kernel<N, false>), grid, dim3(4 * N), 0, st, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(gdr_reduce_kernel, dim3((unsigned)p.H), dim3(256), 0, st, p);
