@@ -630,7 +630,8 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
 
 // a 16 x 16 tile's products of parts, small ones first, each over every T in
 // turn so that consecutive instructions do not wait for one another
-template <int N, bool SAVE, int NW>
+// SAVE: keep S and U for the gradients; WANT_Y: write y (the backward's recomputation does not)
+template <int N, bool SAVE, bool WANT_Y, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(const GdrParams p, int splits) {
     constexpr int KS = N + kGdrPad, NT = N / 16;
     __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 2> lds[2];
@@ -692,14 +693,15 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
                 for (int T = 0; T < 4; ++T) {
                     const int o = (16 * T + r16) * KS + 32 * s + 4 * g4;
                     ko[T] = gdr_ld_perm(&L.k[o]);
-                    qo[T] = gdr_ld_perm(&L.q[o]);
+                    if constexpr (WANT_Y) qo[T] = gdr_ld_perm(&L.q[o]);
                 }
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
 #pragma unroll
                     for (int T = 0; T < 4; ++T) {
                         X[T] = ssd_mfma(ko[T], so.part[k], X[T]);
-                        if (k < 2) Y[T] = ssd_mfma(so.part[k], qo[T], Y[T]);
+                        if constexpr (WANT_Y)
+                            if (k < 2) Y[T] = ssd_mfma(so.part[k], qo[T], Y[T]);
                     }
             }
             // beta X
@@ -737,8 +739,8 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
         }
         if (late) stage();
         if (live) {
-            // Y^T = exp(G) S Q^T + U^T A^T; the backward's recomputation stores none
-            if (p.y != nullptr) {
+            // Y^T = exp(G) S Q^T + U^T A^T
+            if constexpr (WANT_Y) {
                 const __amdgpu_buffer_rsrc_t ry = ssd_buffer(p.y + (row0 * p.H + h) * p.P,
                                                              2u * ((uint32_t)(nv - 1) * ysr + (uint32_t)p.P));
                 const GdrSplit<2> uo[2] = {gdr_split<2>(U[0], U[1]), gdr_split<2>(U[2], U[3])};

@@ -31,10 +31,12 @@ template <int N, int NW>
 void gdr_fwd_nw(const GdrParams &p, bool save, hipStream_t st) {
     const int splits = (p.P / 16 + NW - 1) / NW;
     const dim3 grid((unsigned)((int64_t)p.batch * p.H * splits));
-    if (save)
-        hipLaunchKernelGGL((gdr_fwd_kernel<N, true, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
+    if (save && p.y == nullptr)
+        hipLaunchKernelGGL((gdr_fwd_kernel<N, true, false, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
+    else if (save)
+        hipLaunchKernelGGL((gdr_fwd_kernel<N, true, true, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
     else
-        hipLaunchKernelGGL((gdr_fwd_kernel<N, false, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
+        hipLaunchKernelGGL((gdr_fwd_kernel<N, false, true, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
 }
 
 template <int N>
