@@ -511,16 +511,45 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 constexpr int gdr_helpers(int nw) { return nw < 8 ? nw : 0; }
 
 // LDS of one chunk: K and Q rows; the lower tiles of R in three parts and of the
-// scores in AP; the first four tables and the decay over the whole chunk. Tiles
-// have no padding: a wave's 8-byte reads of a 16-bit tile 16 columns wide, along
-// rows or transposed, cover it in order.
+// scores in AP; the first four tables and the decay over the whole chunk.
+//
+// Layouts are chosen for the banks (64 of 4 bytes): with padded rows the walk
+// spent more LDS cycles on conflicts than on data (7.4 of 12 thousand per chunk).
+//  * A 16 x 16 tile is kept as units of 4 columns, unit column by unit column, rows
+//    8 apart swapped in the last two unit columns: 16 lanes that read a unit column
+//    (an operand's rows) or a 4 x 4 square of units (a transposing read) touch
+//    every bank once.
+//  * A row of K or Q is kept in 16-byte pieces, each the columns 4 g .. + 3 and 16 +
+//    4 g .. + 3 of a block of 32 (an operand's lane reads just that), at a place
+//    exchanged by the row's low bits, so that the pieces of 16 rows, and the squares
+//    of a transposing read, lie in different banks.
 constexpr int kGdrPart = kGdrTiles * 256;   // elements of one part of a C x C matrix
 template <int N, int AP> struct GdrChunkLds {
-    uint16_t k[kGdrC * (N + kGdrPad)], q[kGdrC * (N + kGdrPad)];
+    uint16_t k[kGdrC * N], q[kGdrC * N];
     uint16_t r[3 * kGdrPart], a[AP * kGdrPart];
     float tab[4 * kGdrC];
     float end[4];
 };
+
+// element offset of row `row`, unit column c of a tile
+__device__ __forceinline__ constexpr int gdr_unit(int row, int c) { return 4 * (16 * c + (row ^ ((c & 2) << 2))); }
+
+// element offset of piece `piece` (4 block + g) of a row of K or Q
+template <int N> __device__ __forceinline__ constexpr int gdr_piece(int row, int piece) {
+    const int x = N == 128 ? (row & 3) << 2 | ((row >> 2) & 3) : (row & 2) << 1 | ((row >> 2) & 3);
+    return row * N + 8 * (piece ^ x);
+}
+
+// the operand of rows 16 T + r16, columns 32 s + 16 (e / 4) + 4 g4 + e % 4
+template <int N> __device__ __forceinline__ ssd_bf16x8 gdr_ld_row(const uint16_t *m, int T, int s, int r16, int g4) {
+    return ssd_ld16(m + 16 * T * N + gdr_piece<N>(r16, 4 * s + g4));
+}
+
+// the operand of column 16 nt + r16, rows 32 s + 16 (e / 4) + 4 g4 + e % 4
+template <int N> __device__ __forceinline__ ssd_bf16x8 gdr_ld_column(const uint16_t *m, int nt, int s, int r16, int g4) {
+    const uint16_t *p = m + 32 * s * N + gdr_piece<N>(4 * g4 + (r16 >> 2), 4 * (nt >> 1) + (r16 & 3)) + 4 * (nt & 1);
+    return ssd_ld_tr2(p, p + 16 * N);
+}
 
 // rows of row tile T, columns of tiles 2 s and 2 s + 1, of a lower triangular matrix
 template <int PARTS>
@@ -528,7 +557,7 @@ __device__ __forceinline__ GdrSplit<PARTS> gdr_ld_tile_rows(const uint16_t *m, i
     GdrSplit<PARTS> o;
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
-        const uint16_t *p = m + k * kGdrPart + 16 * r16 + 4 * g4;
+        const uint16_t *p = m + k * kGdrPart + gdr_unit(r16, g4);
         const uint2 a = *reinterpret_cast<const uint2 *>(p + 256 * gdr_tile(T, 2 * s));
         uint2 b = {0u, 0u};
         if (2 * s + 1 <= T) b = *reinterpret_cast<const uint2 *>(p + 256 * gdr_tile(T, 2 * s + 1));
@@ -543,7 +572,7 @@ __device__ __forceinline__ GdrSplit<PARTS> gdr_ld_tile_cols(const uint16_t *m, i
     GdrSplit<PARTS> o;
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
-        const uint16_t *p = m + k * kGdrPart + 16 * (4 * g4 + (r16 >> 2)) + 4 * (r16 & 3);
+        const uint16_t *p = m + k * kGdrPart + gdr_unit(4 * g4 + (r16 >> 2), r16 & 3);
         uint2 a = {0u, 0u};
         if (2 * s >= T) a = ssd_ld_tr(p + 256 * gdr_tile(2 * s, T));
         const uint2 b = ssd_ld_tr(p + 256 * gdr_tile(2 * s + 1, T));
@@ -567,16 +596,22 @@ struct GdrColumns {
     // the lane's column of rows 16 T + 4 g4 .. + 3, for every T
     __device__ __forceinline__ void turn(uint16_t *tile, int lane, uint2 (&out)[4]) const {
         const int r16 = lane & 15, g4 = lane >> 4;
-        *reinterpret_cast<uint4 *>(tile + 8 * lane) = v[0];
-        *reinterpret_cast<uint4 *>(tile + 512 + 8 * lane) = v[1];
+        // half h of row i: unit columns 2 h and 2 h + 1 of tile i / 16
+        uint16_t *at = tile + 256 * (lane >> 5);
+        const int row = (lane >> 1) & 15, c = 2 * (lane & 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<uint2 *>(at + 512 * i + gdr_unit(row, c)) = uint2{v[i].x, v[i].y};
+            *reinterpret_cast<uint2 *>(at + 512 * i + gdr_unit(row, c + 1)) = uint2{v[i].z, v[i].w};
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int T = 0; T < 4; ++T) out[T] = ssd_ld_tr(tile + 16 * (16 * T + 4 * g4 + (r16 >> 2)) + 4 * (r16 & 3));
+        for (int T = 0; T < 4; ++T) out[T] = ssd_ld_tr(tile + 256 * T + gdr_unit(4 * g4 + (r16 >> 2), r16 & 3));
     }
 };
 
 template <int N, int AP, int NW> struct GdrChunkRegs {
-    static constexpr int TH = 64 * NW, KS = N + kGdrPad;
+    static constexpr int TH = 64 * NW;
     static constexpr int KI = kGdrC * N / 8 / TH, RI = (kGdrTiles * 64 + TH - 1) / TH, TI = (4 * kGdrC + TH - 1) / TH;
     uint4 k[KI], q[KI];
     float4 r[RI], a[RI];
@@ -609,16 +644,22 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
     __device__ __forceinline__ void store(GdrChunkLds<N, AP> &s, int tid) const {
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
-            const int x = i * TH + tid, o = (x / (N / 8)) * KS + 8 * (x % (N / 8));
-            *reinterpret_cast<uint4 *>(&s.k[o]) = k[i];
-            *reinterpret_cast<uint4 *>(&s.q[o]) = q[i];
+            // columns 8 j .. + 7 of a row: halves of two pieces
+            const int x = i * TH + tid, row = x / (N / 8), j = x % (N / 8);
+            const int o0 = gdr_piece<N>(row & 15, 4 * (j >> 2) + 2 * (j & 1)) + (row & ~15) * N + 4 * ((j >> 1) & 1);
+            const int o1 = gdr_piece<N>(row & 15, 4 * (j >> 2) + 2 * (j & 1) + 1) + (row & ~15) * N + 4 * ((j >> 1) & 1);
+            *reinterpret_cast<uint2 *>(&s.k[o0]) = uint2{k[i].x, k[i].y};
+            *reinterpret_cast<uint2 *>(&s.k[o1]) = uint2{k[i].z, k[i].w};
+            *reinterpret_cast<uint2 *>(&s.q[o0]) = uint2{q[i].x, q[i].y};
+            *reinterpret_cast<uint2 *>(&s.q[o1]) = uint2{q[i].z, q[i].w};
         }
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
             const int x = i * TH + tid;
             if (x < kGdrTiles * 64) {
-                gdr_store_parts<3>(&s.r[4 * x], kGdrPart, r[i]);
-                gdr_store_parts<AP>(&s.a[4 * x], kGdrPart, a[i]);
+                const int o = 256 * (x >> 6) + gdr_unit((x >> 2) & 15, x & 3);
+                gdr_store_parts<3>(&s.r[o], kGdrPart, r[i]);
+                gdr_store_parts<AP>(&s.a[o], kGdrPart, a[i]);
             }
         }
 #pragma unroll
@@ -633,7 +674,7 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
 // SAVE: keep S and U for the gradients; WANT_Y: write y (the backward's recomputation does not)
 template <int N, bool SAVE, bool WANT_Y, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(const GdrParams p, int splits) {
-    constexpr int KS = N + kGdrPad, NT = N / 16;
+    constexpr int NT = N / 16;
     __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 2> lds[2];
     __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -691,9 +732,8 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
                 ssd_bf16x8 ko[4], qo[4];
 #pragma unroll
                 for (int T = 0; T < 4; ++T) {
-                    const int o = (16 * T + r16) * KS + 32 * s + 4 * g4;
-                    ko[T] = gdr_ld_perm(&L.k[o]);
-                    if constexpr (WANT_Y) qo[T] = gdr_ld_perm(&L.q[o]);
+                    ko[T] = gdr_ld_row<N>(L.k, T, s, r16, g4);
+                    if constexpr (WANT_Y) qo[T] = gdr_ld_row<N>(L.q, T, s, r16, g4);
                 }
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
@@ -776,7 +816,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
                 const GdrSplit<3> uo = gdr_split<3>(U[2 * s], U[2 * s + 1]);
                 ssd_bf16x8 ko[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) ko[nt] = gdr_ld_col(L.k, KS, 32 * s + 4 * g4, 16 * nt, r16);
+                for (int nt = 0; nt < NT; ++nt) ko[nt] = gdr_ld_column<N>(L.k, nt, s, r16, g4);
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
 #pragma unroll
@@ -796,7 +836,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
 // Backwards over the chunks: D' of every chunk, W, dv and dh0.
 template <int N, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(const GdrParams p, int splits) {
-    constexpr int KS = N + kGdrPad, NT = N / 16;
+    constexpr int NT = N / 16;
     __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 3> lds[2];
     __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -873,7 +913,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(co
                 const GdrSplit<3> so = gdr_split<3>(D[2 * s], D[2 * s + 1]);
                 ssd_bf16x8 ko[4];
 #pragma unroll
-                for (int T = 0; T < 4; ++T) ko[T] = gdr_ld_perm(&L.k[(16 * T + r16) * KS + 32 * s + 4 * g4]);
+                for (int T = 0; T < 4; ++T) ko[T] = gdr_ld_row<N>(L.k, T, s, r16, g4);
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
 #pragma unroll
@@ -957,8 +997,8 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(co
                     ssd_bf16x8 ko[4], qr[4];
 #pragma unroll
                     for (int nt = 0; nt < 4; ++nt) {
-                        ko[nt] = gdr_ld_col(L.k, KS, 32 * s + 4 * g4, 16 * (n0 + nt), r16);
-                        qr[nt] = gdr_ld_col(L.q, KS, 32 * s + 4 * g4, 16 * (n0 + nt), r16);
+                        ko[nt] = gdr_ld_column<N>(L.k, n0 + nt, s, r16, g4);
+                        qr[nt] = gdr_ld_column<N>(L.q, n0 + nt, s, r16, g4);
                     }
 #pragma unroll
                     for (int k = 2; k >= 0; --k)
