@@ -382,7 +382,10 @@ int ssm_ssd_state_update(const ssm_ssd_desc *desc, const void *x, const void *dt
  * are as exact as fp32 arithmetic makes them; y is formed from two parts and
  * rounded once to bf16. The matrix inverse of a chunk is that of a unit lower
  * triangular matrix, by substitution, and needs no bound on the keys; but the
- * recurrence itself grows without bound unless w_t |k_t|^2 <= 2.
+ * recurrence itself grows without bound unless w_t |k_t|^2 <= 2. A step that
+ * decays the state to nothing (also an infinite one with A < 0) is a reset. Any
+ * other NaN or infinity, in a token's row or a state, makes its whole chunk of 64
+ * tokens and what follows NaN, earlier tokens of the chunk among them.
  */
 typedef struct {
     int64_t batch;     /* >= 0 */

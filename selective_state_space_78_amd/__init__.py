@@ -180,12 +180,23 @@ def _check(t, name, shape=None, dtype=None, device=None):
 
 
 def _stream(stream, device):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % device)
     if stream is not None:
         return stream.cuda_stream
     import torch
     # the handle alone: a Stream object costs more than a launch of a small kernel
     index = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+
+
+def _on(device, fn, *args):
+    """fn(*args) with the tensors' GPU as the current one."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def _tuning(tuning):
@@ -585,10 +596,16 @@ def _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, q
                    None if dt_bias is None else dt_bias.data_ptr())
 
 
-def _workspace(workspace, need, device, name):
+def _workspace(workspace, need, device, name, stream):
     import torch
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None, need
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            # the allocator may hand it to the current stream as soon as it is dropped here
+            workspace.record_stream(stream)
+        return workspace, need
     _check(workspace, "workspace", device=device)
     have = workspace.numel() * workspace.element_size()
     if have < need:
@@ -639,8 +656,8 @@ def ssm_gdr_fwd(q, k, v, dt, beta, A, h0=None, y=None, h_last=None, scale=None, 
     L_ = lib()
     name = "ssm_gdr_fwd_save" if _save else "ssm_gdr_fwd"
     size = L_.ssm_gdr_bwd_workspace_size if _save else L_.ssm_gdr_workspace_size
-    workspace, ws_bytes = _workspace(workspace, size(ctypes.byref(desc)), dev, name)
-    rc = getattr(L_, name)(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
+    workspace, ws_bytes = _workspace(workspace, size(ctypes.byref(desc)), dev, name, stream)
+    rc = _on(dev, getattr(L_, name), ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
                            _ptr(y), _ptr(h_last), _ptr(workspace), ws_bytes, _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, name)
@@ -694,8 +711,8 @@ def ssm_gdr_bwd(q, k, v, dt, beta, A, dy, h0=None, dh_last=None, scale=None, dt_
              dh0=get("dh0", (batch, H, P, N), f32, want_dh0))
     L_ = lib()
     name = "ssm_gdr_bwd_saved" if _saved else "ssm_gdr_bwd"
-    workspace, ws_bytes = _workspace(workspace, L_.ssm_gdr_bwd_workspace_size(ctypes.byref(desc)), dev, name)
-    rc = getattr(L_, name)(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_gdr_bwd_workspace_size(ctypes.byref(desc)), dev, name, stream)
+    rc = _on(dev, getattr(L_, name), ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
                            _ptr(dy), _ptr(dh_last), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["ddt"]),
                            _ptr(g["dbeta"]), _ptr(g["dA"]), _ptr(g["ddt_bias"]), _ptr(g["dh0"]), _ptr(workspace),
                            ws_bytes, _stream(stream, dev))
@@ -736,7 +753,7 @@ def ssm_gdr_state_update(q, k, v, dt, beta, A, h, y=None, h_out=None, scale=None
     if y is None:
         y = torch.empty((batch, H, P), dtype=v.dtype, device=dev)
     _check(y, "y", (batch, H, P), v.dtype, dev)
-    rc = lib().ssm_gdr_state_update(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A),
+    rc = _on(dev, lib().ssm_gdr_state_update, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A),
                                     _ptr(h), _ptr(h_out), _ptr(y), _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gdr_state_update")
@@ -771,7 +788,7 @@ def ssm_prenorm_fwd(x, weight, residual=None, scale=None, eps=1e-5, y=None, r=No
     _check(r, "r", x.shape, rt, dev)
     desc = PrenormDesc(x.numel() // dim if dim else 0, dim, code, SSM_F32 if rt == torch.float32 else SSM_BF16,
                        float(eps), 0, xs)
-    rc = lib().ssm_prenorm_fwd(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), _ptr(r),
+    rc = _on(dev, lib().ssm_prenorm_fwd, ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), _ptr(r),
                                _ptr(y), _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_prenorm_fwd")
@@ -814,8 +831,8 @@ def ssm_prenorm_bwd(dy, r, weight, dr=None, x=None, scale=None, eps=1e-5, want_d
                        float(eps), 0, xs)
     L_ = lib()
     workspace, ws_bytes = _workspace(workspace, L_.ssm_prenorm_bwd_workspace_size(ctypes.byref(desc)), dev,
-                                     "ssm_prenorm_bwd")
-    rc = L_.ssm_prenorm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(r), _ptr(dr), _ptr(x if scale is not None else None),
+                                     "ssm_prenorm_bwd", stream)
+    rc = _on(dev, L_.ssm_prenorm_bwd, ctypes.byref(desc), _ptr(dy), _ptr(r), _ptr(dr), _ptr(x if scale is not None else None),
                             _ptr(scale), _ptr(weight), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
                             _ptr(g["dscale"]), _ptr(workspace), ws_bytes, _stream(stream, dev))
     if rc != 0:
@@ -853,7 +870,7 @@ def ssm_gated_norm_fwd(x, z, weight, eps=1e-5, gate_first=False, y=None, stream=
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _check(y, "y", x.shape, x.dtype, x.device)
-    rc = lib().ssm_gated_norm_fwd(ctypes.byref(desc), _ptr(x), _ptr(z), _ptr(weight), _ptr(y),
+    rc = _on(x.device, lib().ssm_gated_norm_fwd, ctypes.byref(desc), _ptr(x), _ptr(z), _ptr(weight), _ptr(y),
                                   _stream(stream, x.device))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_norm_fwd")
@@ -881,8 +898,8 @@ def ssm_gated_norm_bwd(dy, x, z, weight, eps=1e-5, gate_first=False, out=None, w
              dweight=get("dweight", tuple(weight.shape), torch.float32))
     L_ = lib()
     workspace, ws_bytes = _workspace(workspace, L_.ssm_gated_norm_bwd_workspace_size(ctypes.byref(desc)), dev,
-                                     "ssm_gated_norm_bwd")
-    rc = L_.ssm_gated_norm_bwd(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(z), _ptr(weight), _ptr(g["dx"]),
+                                     "ssm_gated_norm_bwd", stream)
+    rc = _on(dev, L_.ssm_gated_norm_bwd, ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(z), _ptr(weight), _ptr(g["dx"]),
                                _ptr(g["dz"]), _ptr(g["dweight"]), _ptr(workspace), ws_bytes, _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_norm_bwd")

@@ -321,7 +321,9 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
                                 p.dt_bias ? p.dt_bias[h] : 0.0f, p.dt_softplus, p.beta_sigmoid);
             // the running sum in 64 bits: differences of it are exponents, and a
             // rounding of the sum would be an error relative to the product
-            const double G = gdr_prefix64((double)s.step * (double)p.A[h] * 1.4426950408889634074, lane);
+            // (a decay below 2^-1024 is 0 with any state: held there, a reset of any
+            // size leaves the later differences their digits)
+            const double G = gdr_prefix64(fmax((double)s.step * (double)p.A[h] * 1.4426950408889634074, -1024.0), lane);
             const double Gc = gdr_last64(G);
             const float hi = (float)G, lo = (float)(G - (double)hi);
             sGh[lane] = hi;
@@ -1323,7 +1325,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
             const float step = sTab[kTStep * kGdrC + lane];
             const float dlog = step * p.A[h] * kLog2e < -64.0f ? 0.0f : (float)(dG + whole);
             const float ddt = dlog * p.A[h] * sTab[kTDstep * kGdrC + lane];
-            double pA = lane < nv ? (double)dlog * step : 0.0;
+            double pA = lane < nv && dlog != 0.0f ? (double)dlog * step : 0.0;   // (step may be infinite)
             double pb = lane < nv ? (double)ddt : 0.0;
             if (lane < nv) {
                 const int64_t o = (row0 + lane) * p.H + h;

@@ -170,6 +170,54 @@ def test_resets_and_idle_tokens(env):
     check_grads(torch, ssm, x, **opts)
 
 
+@pytest.mark.parametrize("shape", [(1, 66, 200, 200, 80, 64), (2, 70, 9, 45, 112, 128), (1, 65, 64, 128, 144, 128)])
+def test_many_heads(env, shape):
+    """Heads enough for every launch shape of the kernels that walk the chunks:
+    8 columns' waves per workgroup with a ragged end, 4, and 8 in two parts."""
+    torch, ssm = env
+    say("gdr many heads", shape)
+    x = inputs(torch, sum(shape), *shape, grads=True)
+    check_fwd(torch, ssm, {n: t for n, t in x.items() if n not in ("dy", "dh_last")}, **OPTS)
+    check_grads(torch, ssm, x, saved=False, **OPTS)
+
+
+def test_resets_of_any_size(env):
+    """Steps from 100 to the largest bf16 and an infinite one: the state is
+    forgotten, and the tokens behind keep their own decays."""
+    torch, ssm = env
+    x = inputs(torch, 17, 1, 100, 1, 2, 32, 64, bias=False, grads=True)
+    x["dt"] = x["dt"].abs() * 0.1
+    big = torch.tensor([100.0, 1e8, 1e20, 3e38, float("inf")], device="cuda").to(torch.bfloat16)
+    x["dt"][0, [5, 20, 40, 41, 80]] = big[:, None]
+    x["beta"] = x["beta"].abs().clamp(max=1.0)
+    x["A"] = torch.tensor([-1.0, -16.0], device="cuda")
+    opts = dict(qk_norm=True)
+    y, h = ssm.ssm_gdr_fwd(**{n: t for n, t in x.items() if n not in ("dy", "dh_last")}, **opts)
+    g = ssm.ssm_gdr_bwd(**x, **opts)
+    torch.cuda.synchronize()
+    # the reference with steps long enough to forget all, short enough to square
+    ref = dict(x, dt=torch.where(x["dt"] > 50, torch.full_like(x["dt"], 1e5), x["dt"]))
+    yr, hr, gr = reference(ref, **opts)
+    assert err(np64(y), yr) <= TOL_BF and err(np64(h), hr) <= TOL_32
+    for n in ("dq", "dk", "dv", "ddt", "dbeta"):
+        assert err(np64(g[n]), gr[n]) <= TOL_BF, n
+    # no term of dA comes from a reset
+    assert float(np.max(np.abs(np64(g["dA"]) - gr["dA"]) / gr["dA_abs"])) <= TOL_32
+
+
+def test_non_finite_tokens(env):
+    """A NaN or an infinity stays out of the chunks before its own."""
+    torch, ssm = env
+    x = inputs(torch, 18, 1, 200, 1, 2, 32, 64)
+    y, _ = ssm.ssm_gdr_fwd(**x, **OPTS)
+    for name, value in (("v", float("nan")), ("k", float("inf")), ("beta", float("nan"))):
+        bad = dict(x, **{name: x[name].clone()})
+        bad[name][0, 150] = value
+        z, h = ssm.ssm_gdr_fwd(**bad, **OPTS)
+        torch.cuda.synchronize()
+        assert torch.equal(z[:, :128], y[:, :128]) and bool(z[:, 150:].isnan().any()), name
+
+
 def test_split_and_resume(env):
     """Two calls, the second continuing the first's state in place, equal one
     over the whole, also where the cut is inside a chunk."""
@@ -295,6 +343,12 @@ def test_streams_and_graph(env):
     torch.cuda.current_stream().wait_stream(s)
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+    # a stream handed over, on which the call allocates its workspace itself
+    y, h, ws2 = ssm.ssm_gdr_fwd_save(**ins, stream=s, **OPTS)
+    other = ssm.ssm_gdr_bwd_saved(**x, saved=ws2, stream=s, **OPTS)
+    s.synchronize()
+    for a, b in zip(want, (y, h, *other.values())):
+        assert torch.equal(a, b)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = step()
@@ -325,6 +379,11 @@ def test_refusals(env):
         ssm.ssm_gdr_fwd(**dict(x, k=x["k"][:, :1].expand_as(x["k"])))                        # rows overlap
     with pytest.raises(ValueError):
         ssm.ssm_gdr_fwd(**dict(x, A=x["A"].cpu()))
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_fwd(**{n: t.cpu() for n, t in x.items()})
+    with pytest.raises(ValueError):
+        ssm.ssm_gdr_state_update(**{n: t.cpu()[:, 0] for n, t in x.items() if n in ("q", "k", "v", "dt", "beta")},
+                                 A=x["A"].cpu(), h=x["h0"].cpu())
     with pytest.raises(ValueError):
         ssm.ssm_gdr_fwd(**x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
