@@ -94,6 +94,14 @@ __device__ __forceinline__ void st(void *base, int64_t off, const float (&v)[VEC
     }
 }
 
+// row and group of a segment; segments fit 32 bits (64-bit division costs more than
+// a short row's arithmetic)
+__device__ __forceinline__ void place(int64_t seg, int64_t groups, int64_t &row, int64_t &g) {
+    const uint32_t q = (uint32_t)seg / (uint32_t)groups;
+    row = q;
+    g = (uint32_t)seg - q * (uint32_t)groups;
+}
+
 template <typename T> __device__ __forceinline__ float rounded(float v) {
     if constexpr (sizeof(T) == 2) return ssd_bf(ssd_to_bf(v));
     else return v;
@@ -187,7 +195,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormParams p) {
     const int l = threadIdx.x % LPS;
     const int64_t seg = (int64_t)blockIdx.x * RPW + threadIdx.x / LPS;
     const bool live = seg < p.rows * p.groups;
-    const int64_t row = live ? seg / p.groups : 0, g = live ? seg % p.groups : 0;
+    int64_t row, g;
+    place(live ? seg : 0, p.groups, row, g);
     const float *wt = p.weight + (P::kGated && !p.shared ? g * p.dim : 0);
     const int64_t yo = row * p.groups * p.dim + g * p.dim;
     float ss = 0.0f, unused = 0.0f;
@@ -339,8 +348,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const NormParams p) {
     for (int64_t s0 = slab * RPW; s0 < total; s0 += (int64_t)p.slabs * RPW) {
         const int64_t seg = s0 + slot;
         const bool live = seg < total;
-        const int64_t row = fixed ? (live ? seg : 0) : live ? seg / p.groups : 0;
-        const int64_t g = fixed ? gfix : live ? seg % p.groups : 0;
+        int64_t row = live ? seg : 0, g = gfix;
+        if (!fixed) place(live ? seg : 0, p.groups, row, g);
         BwdIn<P, VEC> in[NV];
         float ss = 0.0f, sw = 0.0f;
 #pragma unroll
@@ -401,7 +410,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const NormParams p) {
 template <typename P, int VEC>
 __global__ __launch_bounds__(256) void norm_bwd_stat_kernel(const NormParams p) {
     __shared__ float buf[4][2];
-    const int64_t seg = blockIdx.x, row = seg / p.groups, g = seg % p.groups;
+    const int64_t seg = blockIdx.x;
+    int64_t row, g;
+    place(seg, p.groups, row, g);
     const float *weight = p.weight + (P::kGated && !p.shared ? g * p.dim : 0);
     float ss = 0.0f, sw = 0.0f;
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < p.dim; c += 256 * VEC) {
@@ -437,7 +448,8 @@ __global__ __launch_bounds__(256) void norm_bwd_cols_kernel(const NormParams p) 
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[e] = dsc[e] = 0.0f;
     for (int64_t s = slab; s < total; s += p.slabs) {
-        const int64_t row = fixed ? s : s / p.groups, g = fixed ? gfix : s % p.groups;
+        int64_t row = s, g = gfix;
+        if (!fixed) place(s, p.groups, row, g);
         const int64_t seg = fixed ? row * p.groups + g : s;
         BwdIn<P, VEC> in;
         bwd_load<P, VEC>(p, row, g, c, in);
