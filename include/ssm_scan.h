@@ -402,7 +402,8 @@ typedef struct {
     float qk_eps;           /* > 0 with qk_norm, else unused */
     /* elements from one token's row to the next of q, k, v, dt, beta (of one
      * batch row to the next: seqlen times that); 0 for densely packed rows. A
-     * row itself is dense. Strides of q, k, v are multiples of 8. */
+     * row itself is dense. Strides of q, k, v are multiples of 8; over a
+     * sequence (not for the one-token step) none is over 2^24 - 1. */
     int64_t q_stride, k_stride, v_stride, dt_stride, beta_stride;
     const float *dt_bias;   /* (nheads) fp32 device pointer, or NULL */
 } ssm_gdr_desc;

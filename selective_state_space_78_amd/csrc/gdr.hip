@@ -123,7 +123,8 @@ struct Sizes {
     int64_t qs, ks, vs, dts, bs;           // resolved strides
 };
 
-int check(const ssm_gdr_desc *desc, Sizes *s) {
+// one: a single token, whose kernel addresses rows in 64 bits
+int check(const ssm_gdr_desc *desc, Sizes *s, bool one = false) {
     if (desc == nullptr) return SSM_ERR_NULL;
     const ssm_gdr_desc &d = *desc;
     if (d.batch < 0 || d.seqlen < 0 || d.nheads < 1 || d.ngroups < 1 || d.nheads % d.ngroups != 0) return SSM_ERR_SHAPE;
@@ -146,7 +147,7 @@ int check(const ssm_gdr_desc *desc, Sizes *s) {
         // a chunk's rows are addressed by 32-bit byte offsets
         if (given[k] < 0 || (given[k] != 0 && given[k] < width[k])) return SSM_ERR_SHAPE;
         *out[k] = given[k] ? given[k] : width[k];
-        if (*out[k] > (INT32_MAX / 2) / kGdrC || !mul_ok(s->tokens, *out[k], &n) || n > INT64_MAX / 4)
+        if ((!one && *out[k] > (INT32_MAX / 2) / kGdrC) || !mul_ok(s->tokens, *out[k], &n) || n > INT64_MAX / 4)
             return SSM_ERR_SHAPE;
     }
     if (!mul_ok(s->tokens, H * P, &n) || H * P > (INT32_MAX / 2) / kGdrC) return SSM_ERR_SHAPE;
@@ -408,7 +409,7 @@ extern "C" int ssm_gdr_state_update(const ssm_gdr_desc *desc, const void *q, con
                                     const void *dt, const void *beta, const float *A, const float *h, float *h_out,
                                     void *y, hipStream_t stream) {
     Sizes s;
-    if (const int rc = check(desc, &s)) return rc;
+    if (const int rc = check(desc, &s, true)) return rc;
     const ssm_gdr_desc &d = *desc;
     if (d.seqlen != 1) return SSM_ERR_SHAPE;
     if (s.heads == 0) return SSM_OK;

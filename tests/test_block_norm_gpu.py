@@ -163,6 +163,32 @@ def test_gated_norm_forms(env):
             assert torch.equal(kept[n], want[n]), (k, n)
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_unaligned_views(env, dtype):
+    """Tensors that start between 16-byte boundaries give what aligned copies give,
+    to the order of a row's sums (64 half steps) and one rounding."""
+    torch, ssm = env
+    t = getattr(torch, dtype)
+
+    def odd(v):
+        return torch.cat([v.new_zeros(1), v.flatten()])[1:].view(v.shape)
+    x, z, dy = (torch.randn(40, 3, 64, device="cuda").to(t) for _ in range(3))
+    w, s = torch.randn(64, device="cuda"), torch.randn(192, device="cuda")
+    a = ssm.ssm_gated_norm_bwd(dy, x, z, w)
+    b = ssm.ssm_gated_norm_bwd(odd(dy), odd(x), odd(z), odd(w))
+    fa, fb = ssm.ssm_gated_norm_fwd(x, z, w), ssm.ssm_gated_norm_fwd(odd(x), odd(z), w)
+    xf, rf, df = (v.flatten(-2) for v in (x, z, dy))
+    wf = torch.randn(192, device="cuda")
+    ya, ra = ssm.ssm_prenorm_fwd(xf, wf, residual=rf, scale=s)
+    yb, rb = ssm.ssm_prenorm_fwd(odd(xf), odd(wf), residual=odd(rf), scale=odd(s))
+    ga = ssm.ssm_prenorm_bwd(df, ra, wf, dr=rf, x=xf, scale=s)
+    gb = ssm.ssm_prenorm_bwd(odd(df), odd(ra), wf, dr=odd(rf), x=odd(xf), scale=s)
+    torch.cuda.synchronize()
+    assert torch.equal(ra, rb)
+    for p, q in [(fa, fb), (ya, yb)] + [(a[n], b[n]) for n in a] + [(ga[n], gb[n]) for n in ga]:
+        assert err(np64(p), np64(q)) <= (2 * TOL_BF if p.dtype == torch.bfloat16 else 2 * TOL_SUM)
+
+
 def test_block_run(env):
     """A block as it is used: prenorm, projections, delta rule, gated norm,
     projection, the next residual add; its gradients against differences of the

@@ -115,6 +115,10 @@ def test_gdr_step(L):
     assert call(fn, gdr(L=1), STEP, **one, h_out=7 * GB + 256) == EALIAS
     assert call(fn, gdr(L=1), STEP, **one, y=7 * GB) == EALIAS
     assert call(fn, gdr(L=1), STEP, **one, y=3 * GB) == EALIAS
+    # one token's rows may lie as far apart as a long sequence's: the refusal is the null pointer's
+    far = gdr(L=1, strides=(1 << 26, 0, 1 << 26, 0, 0))
+    assert call(fn, far, STEP, **one, y=0) == ENULL
+    assert call(L.ssm_gdr_fwd, far, FWD, y=0) == ESHAPE
 
 
 def pre(rows=4, dim=64, dt=ssm.SSM_BF16, rt=ssm.SSM_BF16, eps=1e-5, reserved=0, xs=0):

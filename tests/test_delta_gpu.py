@@ -138,6 +138,42 @@ def test_options(env, softplus, sigmoid, norm):
     check_grads(torch, ssm, x, saved=False, **opts)
 
 
+def test_bias_without_softplus(env):
+    """A step that is dt + bias as given (here also negative: a growing state),
+    and dh0 written over dh_last."""
+    torch, ssm = env
+    x = inputs(torch, 15, 1, 80, 1, 2, 32, 128, unit=True, grads=True)
+    x["dt"] = (0.02 * x["dt"]).to(torch.bfloat16)
+    x["dt_bias"] = torch.tensor([0.05, -0.01], device="cuda")
+    opts = dict(beta_sigmoid=True)
+    g = check_grads(torch, ssm, x, **opts)
+    dh = x["dh_last"].clone()
+    h = ssm.ssm_gdr_bwd(**dict(x, dh_last=dh), out=dict(dh0=dh), **opts)
+    torch.cuda.synchronize()
+    assert h["dh0"].data_ptr() == dh.data_ptr()
+    for n in g:
+        assert torch.equal(g[n], h[n]), n
+
+
+def test_step_of_a_long_sequence(env):
+    """Tokens taken out of a (batch, L, ...) tensor: batch rows L rows apart, here
+    further than 2^24 elements."""
+    torch, ssm = env
+    L, G, H, P, N = 9000, 16, 16, 128, 128
+    far = torch.empty((2, L, G * N), dtype=torch.bfloat16, device="cuda")
+    x = inputs(torch, 16, 2, 1, G, H, P, N)
+    cut = []
+    for n, w in (("q", (G, N)), ("k", (G, N)), ("v", (H, P))):
+        far[:, 7] = x[n].flatten(-2)[:, 0]
+        cut.append(far.clone()[:, 7].unflatten(-1, w))
+    assert cut[0].stride(0) > 1 << 24
+    h = x["h0"].clone()
+    y = ssm.ssm_gdr_state_update(*cut, x["dt"][:, 0], x["beta"][:, 0], x["A"], h, dt_bias=x["dt_bias"], **OPTS)
+    torch.cuda.synchronize()
+    yr, hr = reference(x, **OPTS)
+    assert err(np64(y), yr[:, 0]) <= TOL_BF and err(np64(h), hr) <= TOL_32
+
+
 def test_repeated_keys(env):
     """Every key the same and every strength 1: the chunk's triangular system at
     its least regular (its entries do not decay away from the diagonal)."""
@@ -369,6 +405,10 @@ def test_refusals(env):
     with pytest.raises(ssm.SsmError) as e:
         ssm.ssm_gdr_fwd(**{n: (t.float() if n in ("q", "k", "v", "dt", "beta") else t) for n, t in x.items()})
     assert e.value.status == -4
+    off = torch.empty(x["q"].numel() + 4, dtype=x["q"].dtype, device="cuda")[4:].view(x["q"].shape)
+    with pytest.raises(ssm.SsmError) as e:
+        ssm.ssm_gdr_fwd(**dict(x, q=off))                                                     # 8-byte aligned
+    assert e.value.status == -8
     with pytest.raises(TypeError):
         ssm.ssm_gdr_fwd(**dict(x, k=x["k"].float()))
     with pytest.raises(ValueError):
