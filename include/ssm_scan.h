@@ -475,7 +475,8 @@ int ssm_gdr_bwd_saved(const ssm_gdr_desc *desc, const void *q, const void *k, co
  *   h_out     the same shape, written; h itself for an update in place
  *   y         (batch, nheads, headdim)  bf16, written
  * Computed in fp32 without matrix cores. y must not overlap anything else,
- * h_out nothing but h, and that exactly.
+ * h_out nothing but h, and that exactly. A workgroup takes a head's 64 rows of 64
+ * or 32 of 128; 2^24 workgroups are refused (SSM_ERR_SHAPE).
  */
 int ssm_gdr_state_update(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
                          const void *beta, const float *A, const float *h, float *h_out, void *y,
@@ -490,6 +491,11 @@ int ssm_gdr_state_update(const ssm_gdr_desc *desc, const void *q, const void *k,
  *
  * r is first rounded to residual_dtype, and y is that of the rounded r: what
  * the next layer adds to is what was normed.
+ *
+ * A row takes a part of a workgroup up to 2048 channels of 16 bits (1024 of 32;
+ * 256 when rows or pointers are not 16-byte aligned) and a workgroup of 256 work
+ * items beyond. Sizes that need 2^32 work items are refused (SSM_ERR_SHAPE): from
+ * 2^24 such long rows.
  */
 typedef struct {
     int64_t rows;            /* >= 0 */
@@ -540,7 +546,9 @@ int ssm_prenorm_bwd(const ssm_prenorm_desc *desc, const void *dy, const void *r,
  *   gate_first 1:  f = x * silu(z),  y = f / sqrt(mean(f^2) + eps) * weight
  *
  * z NULL: no gate. weight is (groups, dim), or (dim) for every group with
- * weight_shared (a norm per head with one weight for all heads).
+ * weight_shared (a norm per head with one weight for all heads). Sizes that need
+ * 2^32 work items are refused as above, a group counting as a row; so is the
+ * backward of 2^26 weights.
  */
 typedef struct {
     int64_t rows;            /* >= 0 */

@@ -30,4 +30,7 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t *out) {
     return true;
 }
 
+// Whether a launch's work items stay below 2^32, the most that one may have
+inline bool grid_ok(int64_t blocks, int threads) { return blocks <= (int64_t)(UINT32_MAX / (unsigned)threads); }
+
 }  // namespace ssm_detail

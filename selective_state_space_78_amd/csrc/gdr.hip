@@ -106,14 +106,18 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(const GdrStepParams p, in
     }
 }
 
-// seqlen 0: the state passes through, sums over no tokens are 0
+// No tokens: the state passes through, sums over them are 0
 __global__ __launch_bounds__(256) void gdr_empty_kernel(const float *from, float *to, int64_t n, float *dA, float *db,
                                                         int H) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (to != nullptr && i < n) to[i] = from != nullptr ? from[i] : 0.0f;
-    if (dA != nullptr && i < H) dA[i] = 0.0f;
-    if (db != nullptr && i < H) db[i] = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * 256, end = n > H ? n : H;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < end; i += step) {
+        if (to != nullptr && i < n) to[i] = from != nullptr ? from[i] : 0.0f;
+        if (dA != nullptr && i < H) dA[i] = 0.0f;
+        if (db != nullptr && i < H) db[i] = 0.0f;
+    }
 }
+
+unsigned empty_blocks(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 8192); }
 
 // ---------------------------------------------------------------------------
 // Descriptors, layouts
@@ -273,10 +277,8 @@ int run_fwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *
     if (overlaps(ry, rh) || overlaps(ws, ry) || overlaps(ws, rh)) return SSM_ERR_ALIAS;
     if (s.tokens == 0) {
         if (h_last == nullptr || h_last == h0) return SSM_OK;
-        const int64_t blocks = (s.state + 255) / 256;
-        if (blocks > INT32_MAX) return SSM_ERR_SHAPE;
-        hipLaunchKernelGGL(gdr_empty_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, h0, h_last, s.state, nullptr,
-                           nullptr, 0);
+        hipLaunchKernelGGL(gdr_empty_kernel, dim3(empty_blocks(s.state)), dim3(256), 0, stream, h0, h_last, s.state,
+                           nullptr, nullptr, 0);
         return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
     }
     GdrParams p = params_of(d, s, l, workspace);
@@ -330,10 +332,8 @@ int run_bwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *
     for (int i = 0; i < 11; ++i)
         if (i != 9 && overlaps(in[9], in[i])) return SSM_ERR_ALIAS;
     if (s.tokens == 0) {
-        const int64_t blocks = (std::max<int64_t>(s.state, H) + 255) / 256;
-        if (blocks > INT32_MAX) return SSM_ERR_SHAPE;
-        hipLaunchKernelGGL(gdr_empty_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, dh_last,
-                           dh0 == dh_last ? nullptr : dh0, s.state, dA, ddt_bias, (int)H);
+        hipLaunchKernelGGL(gdr_empty_kernel, dim3(empty_blocks(std::max<int64_t>(s.state, H))), dim3(256), 0, stream,
+                           dh_last, dh0 == dh_last ? nullptr : dh0, s.state, dA, ddt_bias, (int)H);
         return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
     }
     GdrParams p = params_of(d, s, l, workspace);
@@ -457,7 +457,7 @@ extern "C" int ssm_gdr_state_update(const ssm_gdr_desc *desc, const void *q, con
     p.qk_eps = d.qk_eps;
     const int rows = (d.dstate == 64 ? 16 : 8) * kStepRows, bph = (d.headdim + rows - 1) / rows;
     const int64_t blocks = s.heads * bph;
-    if (blocks > INT32_MAX) return SSM_ERR_SHAPE;
+    if (!grid_ok(blocks, 256)) return SSM_ERR_SHAPE;
     if (d.dstate == 64)
         hipLaunchKernelGGL((gdr_step_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, p, bph);
     else

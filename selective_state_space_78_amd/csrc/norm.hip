@@ -520,7 +520,7 @@ template <typename P, int VEC>
 hipError_t launch_fwd(const NormParams &p, hipStream_t st) {
     const Shape s = shape_for(p.dim, VEC);
     const int64_t blocks = (p.rows * p.groups + 256 / s.lps - 1) / (256 / s.lps);
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (!grid_ok(blocks, 256)) return hipErrorInvalidConfiguration;
 #define NORM_CASE(LPS, NV)                                                                                              \
     if (s.lps == LPS && s.nv == NV)                                                                                    \
         hipLaunchKernelGGL((norm_fwd_kernel<P, VEC, LPS, NV>), dim3((unsigned)blocks), dim3(256), 0, st, p);
@@ -547,17 +547,20 @@ hipError_t launch_bwd(NormParams &p, hipStream_t st) {
     p.slabs = slabs_for(p.rows, p.groups, p.dim, fixed, VEC);
     const int64_t walks = fixed ? p.groups : 1;
     const int64_t cols = (P::kGated ? 1 : 2) * walks * p.dim;
+    // without a scale the second half of a partial row is not written, and not read
+    const int64_t sums = ((P::kGated || p.scale ? cols : p.dim) + kRunCols - 1) / kRunCols;
+    if (!grid_ok(sums, kRunCols * kRuns)) return hipErrorInvalidConfiguration;
     if (s.nv == 0) {
         const int64_t cb = (p.dim + 256 * VEC - 1) / (256 * VEC);
         const int64_t b1 = p.rows * p.groups, b2 = cb * walks * p.slabs;
-        if (b1 > INT32_MAX || b2 > INT32_MAX) return hipErrorInvalidValue;
+        if (!grid_ok(b1, 256) || !grid_ok(b2, 256)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((norm_bwd_stat_kernel<P, VEC>), dim3((unsigned)b1), dim3(256), 0, st, p);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((norm_bwd_cols_kernel<P, VEC>), dim3((unsigned)b2), dim3(256), 0, st, p);
     } else {
         const int64_t blocks = walks * p.slabs;
-        if (blocks > INT32_MAX) return hipErrorInvalidValue;
+        if (!grid_ok(blocks, 256)) return hipErrorInvalidConfiguration;
 #define NORM_CASE(LPS, NV)                                                                                              \
     if (s.lps == LPS && s.nv == NV)                                                                                    \
         hipLaunchKernelGGL((norm_bwd_kernel<P, VEC, LPS, NV>), dim3((unsigned)blocks), dim3(256), 0, st, p);
@@ -566,10 +569,7 @@ hipError_t launch_bwd(NormParams &p, hipStream_t st) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // without a scale the second half of a partial row is not written, and not read
-    const int64_t read = P::kGated || p.scale ? cols : p.dim;
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((read + kRunCols - 1) / kRunCols)),
-                       dim3(kRunCols * kRuns), 0, st, p.part, p.slabs, cols,
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)sums), dim3(kRunCols * kRuns), 0, st, p.part, p.slabs, cols,
                        P::kGated ? cols : p.dim, p.dweight, p.dscale);
     return hipGetLastError();
 }
@@ -657,6 +657,11 @@ hipError_t go_gated(const ssm_gated_norm_desc &d, NormParams &p, bool w, hipStre
     return w ? go<BWD, Gated<uint16_t>, 8>(p, st) : go<BWD, Gated<uint16_t>, 1>(p, st);
 }
 
+// What a launch came to; sizes that need too many work items are refused before the first
+int status(hipError_t e) {
+    return e == hipSuccess ? SSM_OK : e == hipErrorInvalidConfiguration ? SSM_ERR_SHAPE : SSM_ERR_HIP;
+}
+
 NormParams params_of(const ssm_prenorm_desc &d) {
     NormParams p{};
     p.rows = d.rows;
@@ -682,7 +687,7 @@ NormParams params_of(const ssm_gated_norm_desc &d) {
     return p;
 }
 
-// seqlen 0: sums over no rows
+// No rows: sums over them are 0
 __global__ __launch_bounds__(256) void norm_zero_kernel(float *a, int64_t n, float *b, int64_t m) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n) a[i] = 0.0f;
@@ -690,6 +695,7 @@ __global__ __launch_bounds__(256) void norm_zero_kernel(float *a, int64_t n, flo
 }
 
 int zero_sums(float *a, int64_t n, float *b, int64_t m, hipStream_t st) {
+    if (!grid_ok((std::max(n, m) + 255) / 256, 256)) return SSM_ERR_SHAPE;
     hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)((std::max(n, m) + 255) / 256)), dim3(256), 0, st, a, n, b, m);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
@@ -720,7 +726,7 @@ extern "C" int ssm_prenorm_fwd(const ssm_prenorm_desc *desc, const void *x, cons
     p.y = y;
     const void *ptr[] = {x, residual, scale, weight, r, y};
     const bool w = wide(d.dim, d.dtype == SSM_F32 ? 4 : 8, &p.xs, 1, ptr, 6);
-    return go_pre<false>(d, p, w, stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    return status(go_pre<false>(d, p, w, stream));
 }
 
 extern "C" size_t ssm_prenorm_bwd_workspace_size(const ssm_prenorm_desc *desc) {
@@ -773,7 +779,7 @@ extern "C" int ssm_prenorm_bwd(const ssm_prenorm_desc *desc, const void *dy, con
     p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + align256((size_t)d.rows * 8));
     const void *ptr[] = {dy, r, dr, scale ? x : nullptr, scale, weight, dx, dresidual};
     const bool w = wide(d.dim, d.dtype == SSM_F32 ? 4 : 8, &p.xs, scale ? 1 : 0, ptr, 8);
-    return go_pre<true>(d, p, w, stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    return status(go_pre<true>(d, p, w, stream));
 }
 
 extern "C" int ssm_gated_norm_fwd(const ssm_gated_norm_desc *desc, const void *x, const void *z, const float *weight,
@@ -796,7 +802,7 @@ extern "C" int ssm_gated_norm_fwd(const ssm_gated_norm_desc *desc, const void *x
     const int64_t strides[] = {p.xs, z ? p.zs : 0};
     const void *ptr[] = {x, z, weight, y};
     const bool w = wide(d.dim, d.dtype == SSM_F32 ? 4 : 8, strides, 2, ptr, 4);
-    return go_gated<false>(d, p, w, stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    return status(go_gated<false>(d, p, w, stream));
 }
 
 extern "C" size_t ssm_gated_norm_bwd_workspace_size(const ssm_gated_norm_desc *desc) {
@@ -846,5 +852,5 @@ extern "C" int ssm_gated_norm_bwd(const ssm_gated_norm_desc *desc, const void *d
     const int64_t strides[] = {p.xs, z ? p.zs : 0};
     const void *ptr[] = {dy, x, z, weight, dx, z ? dz : nullptr};
     const bool w = wide(d.dim, d.dtype == SSM_F32 ? 4 : 8, strides, 2, ptr, 6);
-    return go_gated<true>(d, p, w, stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    return status(go_gated<true>(d, p, w, stream));
 }

@@ -121,6 +121,23 @@ def test_gdr_step(L):
     assert call(L.ssm_gdr_fwd, far, FWD, y=0) == ESHAPE
 
 
+def test_launch_limits(L):
+    """Sizes whose launch would have 2^32 work items are refused by their shape;
+    operands here lie 4 TiB apart."""
+    T = 4096
+    far = lambda names: {n: (k + 1) * T * GB for k, n in enumerate(names)}
+    ws = dict(ws=64 * T * GB, ws_bytes=1 << 42)
+    step = lambda **kw: call(L.ssm_gdr_state_update, gdr(L=1, **kw), STEP, ws=None, **far(STEP))
+    assert step(b=1 << 22, H=4, P=16) == ESHAPE
+    assert step(b=1 << 21, H=4, P=256, N=128, G=4) == ESHAPE
+    for d in (pre(rows=1 << 24, dim=4096), pre(rows=1 << 26, dim=1024), pre(rows=1 << 29, dim=64)):
+        assert call(L.ssm_prenorm_fwd, d, PRE, ws=None, **far(PRE)) == ESHAPE
+    assert call(L.ssm_gated_norm_fwd, gated(rows=1 << 25, groups=16), GAT, ws=None, **far(GAT)) == ESHAPE
+    for d in (gated(rows=1, groups=1 << 20, dim=64), gated(rows=1 << 24, groups=1, dim=16384)):
+        assert call(L.ssm_gated_norm_bwd, d, GATB, **ws, **far(GATB)) == ESHAPE
+    assert call(L.ssm_prenorm_bwd, pre(rows=1 << 24, dim=16384), PREB, **ws, **far(PREB)) == ESHAPE
+
+
 def pre(rows=4, dim=64, dt=ssm.SSM_BF16, rt=ssm.SSM_BF16, eps=1e-5, reserved=0, xs=0):
     return ssm.PrenormDesc(rows, dim, dt, rt, eps, reserved, xs)
 
