@@ -155,6 +155,27 @@ def test_bias_without_softplus(env):
         assert torch.equal(g[n], h[n]), n
 
 
+def test_no_lean_with_rows_of_one_sign(env):
+    """The gradients are linear in dy and dh_last: those of the negative are the
+    negative, but for the matrix cores' rounding downwards. With keys and queries
+    behind a SiLU that must not gather in the decay's gradients: what a pair of
+    gradients adds up to is as often above zero as below it, so over 64 heads its mean
+    is within 4 standard errors of zero (all but one draw in 16000), and the
+    sums are within twice this file's tolerance of sums."""
+    torch, ssm = env
+    x = inputs(torch, 17, 8, 2048, 64, 64, 64, 128, h0=False, grads=True)
+    for n in "qk":
+        x[n] = torch.nn.functional.silu(1.5 * x[n].float()).to(torch.bfloat16)
+    g = ssm.ssm_gdr_bwd(**x, **OPTS)
+    m = ssm.ssm_gdr_bwd(**dict(x, dy=-x["dy"], dh_last=-x["dh_last"]), **OPTS)
+    torch.cuda.synchronize()
+    for n in ("dA", "ddt_bias"):
+        a, d = np64(g[n]), np64(g[n]) + np64(m[n])
+        z = d.mean() / (d.std() / 8)
+        say("  %s: sums %.2e of the gradients, mean %.2f standard errors" % (n, np.linalg.norm(d) / np.linalg.norm(a), z))
+        assert abs(z) <= 4 and np.linalg.norm(d) <= 2 * TOL_32 * np.linalg.norm(a), n
+
+
 def test_step_of_a_long_sequence(env):
     """Tokens taken out of a (batch, L, ...) tensor: batch rows L rows apart, here
     further than 2^24 elements."""
