@@ -379,8 +379,8 @@ int ssm_ssd_state_update(const ssm_ssd_desc *desc, const void *x, const void *dt
  *
  * The sequence is evaluated in chunks of 64 tokens on bf16 matrix cores. Every
  * fp32 operand is split into three bf16 parts, so states and fp32 gradients
- * are as exact as fp32 arithmetic makes them; y is formed from two parts and
- * rounded once to bf16. The matrix inverse of a chunk is that of a unit lower
+ * are as exact as fp32 arithmetic makes them, and y is such a value rounded once
+ * to bf16. The matrix inverse of a chunk is that of a unit lower
  * triangular matrix, by substitution, and needs no bound on the keys; but the
  * recurrence itself grows without bound unless w_t |k_t|^2 <= 2. A step that
  * decays the state to nothing (also an infinite one with A < 0) is a reset. Any

@@ -32,7 +32,7 @@
 // What is fp32 stays fp32 through the matrix cores: a computed operand is
 // split into three bf16 parts (24 significant bits) and products of parts
 // below 2^-24 are left out, so a state or a parameter's gradient is as exact
-// as fp32 arithmetic gives it. Only y, a bf16 output, takes two parts.
+// as fp32 arithmetic gives it, and a bf16 output is rounded once, from that.
 //
 // Kernels:
 //  * gdr_prep_kernel, one workgroup per chunk and head, every chunk at once:
@@ -520,8 +520,8 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 // SIMD stage at different times instead.
 constexpr int gdr_helpers(int nw) { return nw < 8 ? nw : 0; }
 
-// LDS of one chunk: K and Q rows; the lower tiles of R in three parts and of the
-// scores in AP; the first four tables and the decay over the whole chunk.
+// LDS of one chunk: K and Q rows; the lower tiles of R and of the scores in three
+// parts; the first four tables and the decay over the whole chunk.
 //
 // Layouts are chosen for the banks (64 of 4 bytes): with padded rows the walk
 // spent more LDS cycles on conflicts than on data (7.4 of 12 thousand per chunk).
@@ -534,9 +534,9 @@ constexpr int gdr_helpers(int nw) { return nw < 8 ? nw : 0; }
 //    exchanged by the row's low bits, so that the pieces of 16 rows, and the squares
 //    of a transposing read, lie in different banks.
 constexpr int kGdrPart = kGdrTiles * 256;   // elements of one part of a C x C matrix
-template <int N, int AP> struct GdrChunkLds {
+template <int N> struct GdrChunkLds {
     uint16_t k[kGdrC * N], q[kGdrC * N];
-    uint16_t r[3 * kGdrPart], a[AP * kGdrPart];
+    uint16_t r[3 * kGdrPart], a[3 * kGdrPart];
     float tab[4 * kGdrC];
     float end[4];
 };
@@ -620,7 +620,7 @@ struct GdrColumns {
     }
 };
 
-template <int N, int AP, int NW> struct GdrChunkRegs {
+template <int N, int NW> struct GdrChunkRegs {
     static constexpr int TH = 64 * NW;
     static constexpr int KI = kGdrC * N / 8 / TH, RI = (kGdrTiles * 64 + TH - 1) / TH, TI = (4 * kGdrC + TH - 1) / TH;
     uint4 k[KI], q[KI];
@@ -651,7 +651,7 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
         for (int i = 0; i < TI; ++i) tab[i] = t[(i * TH + tid) & (4 * kGdrC - 1)];
         end = t[kTHead * kGdrC + kGdrC - 1];
     }
-    __device__ __forceinline__ void store(GdrChunkLds<N, AP> &s, int tid) const {
+    __device__ __forceinline__ void store(GdrChunkLds<N> &s, int tid) const {
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
             // columns 8 j .. + 7 of a row: halves of two pieces
@@ -669,7 +669,7 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
             if (x < kGdrTiles * 64) {
                 const int o = 256 * (x >> 6) + gdr_unit((x >> 2) & 15, x & 3);
                 gdr_store_parts<3>(&s.r[o], kGdrPart, r[i]);
-                gdr_store_parts<AP>(&s.a[o], kGdrPart, a[i]);
+                gdr_store_parts<3>(&s.a[o], kGdrPart, a[i]);
             }
         }
 #pragma unroll
@@ -693,7 +693,7 @@ template <int N, int AP, int NW> struct GdrChunkRegs {
 template <int N, bool SAVE, bool WANT_Y, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(const GdrParams p, int splits) {
     constexpr int NT = N / 16;
-    __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 2> lds[2];
+    __shared__ __attribute__((aligned(16))) GdrChunkLds<N> lds[2];
     __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
@@ -711,7 +711,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
     for (int nt = 0; nt < NT; ++nt)
         S[nt] = live && p.h0 ? gdr_ld4(p.h0 + sbase + 16 * nt + 4 * g4) : gdr_zero4();
     const uint16_t *vcol = p.v + (int64_t)h * p.P + p0;
-    GdrChunkRegs<N, 2, NW> regs;
+    GdrChunkRegs<N, NW> regs;
     GdrColumns vr;
     if (live) vr.load(p, vcol, p.vs, rowb, 0, lane);
     if (!HELP || w >= NW) {
@@ -723,7 +723,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
     float sign = 1.0f;
     const bool early = HELP ? w >= NW : w < 4, late = !HELP && !early;
     for (int ci = 0; ci < p.nc; ++ci) {
-        const GdrChunkLds<N, 2> &L = lds[ci & 1];
+        const GdrChunkLds<N> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;
@@ -758,8 +758,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
 #pragma unroll
                     for (int T = 0; T < 4; ++T) {
                         X[T] = ssd_mfma(ko[T], so.part[k], X[T]);
-                        if constexpr (WANT_Y)
-                            if (k < 2) Y[T] = ssd_mfma(so.part[k], qo[T], Y[T]);
+                        if constexpr (WANT_Y) Y[T] = ssd_mfma(so.part[k], qo[T], Y[T]);
                     }
             }
             // beta X
@@ -801,17 +800,17 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
             if constexpr (WANT_Y) {
                 const __amdgpu_buffer_rsrc_t ry = ssd_buffer(p.y + (row0 * p.H + h) * p.P,
                                                              2u * ((uint32_t)(nv - 1) * ysr + (uint32_t)p.P));
-                const GdrSplit<2> uo[2] = {gdr_split<2>(U[0], U[1]), gdr_split<2>(U[2], U[3])};
+                const GdrSplit<3> uo[2] = {gdr_split<3>(U[0], U[1]), gdr_split<3>(U[2], U[3])};
 #pragma unroll
                 for (int T = 0; T < 4; ++T) Y[T] *= L.tab[kTHq * kGdrC + 16 * T + r16];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    GdrSplit<2> ao[4];
+                    GdrSplit<3> ao[4];
 #pragma unroll
                     for (int T = 2 * s; T < 4; ++T)
-                        ao[T] = gdr_ld_tile_rows<2>(L.a, T, s, r16, g4);
+                        ao[T] = gdr_ld_tile_rows<3>(L.a, T, s, r16, g4);
 #pragma unroll
-                    for (int k = 1; k >= 0; --k)
+                    for (int k = 2; k >= 0; --k)
 #pragma unroll
                         for (int i = 0; i <= k; ++i)
 #pragma unroll
@@ -857,7 +856,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
 template <int N, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(const GdrParams p, int splits) {
     constexpr int NT = N / 16;
-    __shared__ __attribute__((aligned(16))) GdrChunkLds<N, 3> lds[2];
+    __shared__ __attribute__((aligned(16))) GdrChunkLds<N> lds[2];
     __shared__ __attribute__((aligned(16))) uint16_t sV[NW][kGdrC * 16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g4 = lane >> 4;
@@ -887,7 +886,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(co
     }
     const uint16_t *ycol = p.dy + (int64_t)h * p.P + p0;
     const int last = p.nc - 1;
-    GdrChunkRegs<N, 3, NW> regs;
+    GdrChunkRegs<N, NW> regs;
     GdrColumns yr;
     if (live) yr.load(p, ycol, ys, rowb, last, lane);
     if (!HELP || w >= NW) {
@@ -899,7 +898,7 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(co
     float sign = 1.0f;
     const bool early = HELP ? w >= NW : w < 4, late = !HELP && !early;   // as in the forward
     for (int ci = last; ci >= 0; --ci) {
-        const GdrChunkLds<N, 3> &L = lds[ci & 1];
+        const GdrChunkLds<N> &L = lds[ci & 1];
         const int nv = gdr_valid(p, ci);
         const int64_t id = id0 + ci;
         const int64_t row0 = rowb + (int64_t)ci * kGdrC;

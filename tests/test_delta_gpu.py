@@ -138,6 +138,27 @@ def test_options(env, softplus, sigmoid, norm):
     check_grads(torch, ssm, x, saved=False, **opts)
 
 
+@pytest.mark.parametrize("shape", [(2, 300, 2, 4, 128, 128), (2, 300, 2, 4, 128, 64), (1, 200, 160, 160, 128, 128)])
+def test_y_rounded_once(env, shape):
+    """y is the exact value rounded to bf16, but where what fp32 arithmetic leaves
+    carries it over a border between two roundings: an error e before the rounding
+    does so for a share |e| / step of the elements, and moves each by a step. Sums of
+    up to 256 products, each rounded by half a step of fp32 in a direction of its own,
+    leave sqrt(256) half steps of the rms."""
+    torch, ssm = env
+    x = inputs(torch, sum(shape), *shape, h0=False)
+    y, _ = ssm.ssm_gdr_fwd(**x, **OPTS)
+    torch.cuda.synchronize()
+    ref = reference(x, **OPTS)[0]
+    want = torch.from_numpy(ref).to(torch.bfloat16).double().numpy()
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(ref), 1e-30))) - 7)
+    size = 16 * 2.0 ** -24 * np.sqrt(np.mean(ref * ref))
+    moved = np64(y) - want
+    share = float((moved * moved).sum() / (size * step).sum())
+    say("gdr rounding of y", shape, "%d of %d elements, %.3f of the bound" % ((moved != 0).sum(), moved.size, share))
+    assert share <= 1
+
+
 def test_bias_without_softplus(env):
     """A step that is dt + bias as given (here also negative: a growing state),
     and dh0 written over dh_last."""
