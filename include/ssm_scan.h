@@ -384,8 +384,12 @@ int ssm_ssd_state_update(const ssm_ssd_desc *desc, const void *x, const void *dt
  * triangular matrix, by substitution, and needs no bound on the keys; but the
  * recurrence itself grows without bound unless w_t |k_t|^2 <= 2. A step that
  * decays the state to nothing (also an infinite one with A < 0) is a reset. Any
- * other NaN or infinity, in a token's row or a state, makes its whole chunk of 64
- * tokens and what follows NaN, earlier tokens of the chunk among them.
+ * other NaN or infinity among step_t, A, w_t, k_t, q_t, v, the states and the
+ * incoming gradients makes whatever depends on it by the formulas NaN or infinite:
+ * step, A, w and k of a head its y and state from that token on, a value of v or
+ * h0 those of its row p, q_t its own y. Tokens of the same chunk of 64 that do not
+ * depend on it (the earlier ones, in a backward the later ones) may become NaN
+ * too; chunks that do not, other heads and other batch rows keep their values.
  */
 typedef struct {
     int64_t batch;     /* >= 0 */

@@ -330,8 +330,11 @@ __global__ __launch_bounds__(256) void gdr_prep_kernel(const GdrParams p) {
             // the running sum in 64 bits: differences of it are exponents, and a
             // rounding of the sum would be an error relative to the product
             // (a decay below 2^-1024 is 0 with any state: held there, a reset of any
-            // size leaves the later differences their digits)
-            const double G = gdr_prefix64(fmax((double)s.step * (double)p.A[h] * 1.4426950408889634074, -1024.0), lane);
+            // size leaves the later differences their digits. The comparison lets a
+            // NaN through, as a maximum would not. Rows past the end decay nothing.)
+            double log_a = (double)s.step * (double)p.A[h] * 1.4426950408889634074;
+            log_a = log_a < -1024.0 ? -1024.0 : log_a;
+            const double G = gdr_prefix64(lane < nv ? log_a : 0.0, lane);
             const double Gc = gdr_last64(G);
             const float hi = (float)G, lo = (float)(G - (double)hi);
             sGh[lane] = hi;

@@ -296,6 +296,70 @@ def test_non_finite_tokens(env):
         assert torch.equal(z[:, :128], y[:, :128]) and bool(z[:, 150:].isnan().any()), name
 
 
+NOT_FINITE = [("dt", float("nan")), ("beta", float("nan")), ("k", float("nan")), ("q", float("nan")), ("v", float("nan")),
+              ("A", float("nan")), ("dt_bias", float("nan")), ("dt of A = 0", float("inf")), ("k", float("inf")),
+              ("v", float("-inf")), ("h0", float("nan")), ("dy", float("nan")), ("dh_last", float("inf"))]
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("name,value", NOT_FINITE)
+def test_what_a_non_finite_value_reaches(env, name, value, norm):
+    """One value of head 1 (of token 150, in the third of five chunks): whatever is
+    not finite by the formulas is not finite here, in both directions and in the
+    one-token step; chunks before it, other heads and batch rows keep every bit."""
+    torch, ssm = env
+    x = inputs(torch, 19, 2, 300, 3, 3, 32, 64, unit=not norm, grads=True)
+    if name == "dt of A = 0":
+        x["A"][1] = 0.0
+    bad = {n: t.clone() for n, t in x.items()}
+    if name in ("A", "dt_bias"):
+        bad[name][1] = value
+    elif name in ("h0", "dh_last"):
+        bad[name][0, 1, 3, 7] = value
+    elif name in ("dt of A = 0", "beta", "dt"):
+        bad[name.split()[0]][0, 150, 1] = value
+    else:
+        bad[name][0, 150, 1, 5] = value
+    opts = dict(OPTS, qk_norm=norm)
+    ins = lambda d: {n: t for n, t in d.items() if n not in ("dy", "dh_last")}
+    y0, h0, _ = ssm.ssm_gdr_fwd_save(**ins(x), **opts)
+    y, h, ws = ssm.ssm_gdr_fwd_save(**ins(bad), **opts)
+    g0, g = ssm.ssm_gdr_bwd(**x, **opts), ssm.ssm_gdr_bwd_saved(**bad, saved=ws, **opts)
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        yr, hr, gr = reference(bad, **opts)
+    every = [("y", y, y0, yr, 2), ("h_last", h, h0, hr, 1)]
+    every += [(n, g[n], g0[n], gr[n], {"dA": 0, "ddt_bias": 0, "dh0": 1}.get(n, 2)) for n in g]
+    for n, got, clean, ref, dim in every:
+        assert not (np.isfinite(np64(got)) & ~np.isfinite(ref)).any(), n
+        for head in (0, 2):
+            assert torch.equal(got.select(dim, head), clean.select(dim, head)), (n, head)
+    if name not in ("A", "dt_bias", "h0"):
+        assert torch.equal(y[:, :128], y0[:, :128])
+    if name not in ("A", "dt_bias"):
+        for n, got, clean, _, dim in every:
+            assert dim == 0 or torch.equal(got[1], clean[1]), n
+    if name in ("dy", "dh_last"):
+        assert torch.equal(y, y0) and torch.equal(h, h0)
+        return
+    tok = {n: (t[:, 150:151] if n in ("q", "k", "v", "dt", "beta") else t) for n, t in ins(bad).items()}
+    state = bad["h0"].clone()
+    yt = ssm.ssm_gdr_state_update(*(tok[n][:, 0] for n in ("q", "k", "v", "dt", "beta")), bad["A"], state,
+                                  dt_bias=bad["dt_bias"], **opts)
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        yr, hr = reference(tok, **opts)
+    assert not (np.isfinite(np64(yt)) & ~np.isfinite(yr[:, 0])).any() and not (np.isfinite(np64(state)) & ~np.isfinite(hr)).any()
+
+
+def test_infinite_rate(env):
+    """A = -inf makes every token a reset, also where the last chunk is ragged."""
+    torch, ssm = env
+    x = inputs(torch, 20, 1, 70, 1, 2, 32, 64)
+    x["A"][1] = float("-inf")
+    check_fwd(torch, ssm, x, **OPTS)
+
+
 def test_split_and_resume(env):
     """Two calls, the second continuing the first's state in place, equal one
     over the whole, also where the cut is inside a chunk."""
