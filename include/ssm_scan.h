@@ -455,7 +455,9 @@ int ssm_gdr_fwd(const ssm_gdr_desc *desc, const void *q, const void *k, const vo
  * workspace of an ssm_gdr_fwd_save call with the same descriptor and inputs,
  * unmodified; nothing checks this. It clobbers the workspace's other parts
  * only, so it may run again on the same saved contents.
- * Every sum is taken in a fixed order: results do not depend on timing.
+ * Every sum is taken in a fixed order: results do not depend on timing. Each term
+ * of ddt, dA and ddt_bias has the token's own decay as a factor, so that strong
+ * decays keep their digits.
  * seqlen == 0 writes dA = 0, ddt_bias = 0, dh0 = dh_last (or zeros).
  */
 int ssm_gdr_bwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,

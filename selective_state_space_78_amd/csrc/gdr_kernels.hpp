@@ -22,8 +22,15 @@
 //   dk = [row] -exp(G) beta W S - (beta W U^T * Gam) K
 //      + [col] exp(G_C - G) U D' + (dY U^T * Gam)^T Q - (beta W U^T * Gam)^T K
 //   dbeta_i = W_i . V_i - exp(G_i) k_i . (W S)_i - sum_{j<i} E_ij W_i . U_j
-//   dG_i = q_i . dq_i + k_i . row_i - k_i . col_i
-//   d(log a_t) = <D', S'> + sum_{i >= t} dG_i
+//   d(log a_t) = exp(G_C) <D', S>
+//      + sum_{j<t} exp(G_C - G_j) k_j . (U D')_j
+//      + sum_{i>=t} exp(G_i) (q_i . (dY S)_i - beta_i k_i . (W S)_i)
+//      + sum_{i>=t>j} ((dY U^T)_ij (Q K^T * Gam)_ij - (beta W U^T)_ij E_ij)
+//
+// Every term of the last sum has exp(log a_t) as a factor, and so has what its
+// rounding leaves. (Shorter is <D', S'> + sum_{i>=t} (q_i . dq_i + k_i . row_i -
+// k_i . col_i), but its terms do not have that factor and cancel: a decay of
+// exp(-16) would keep no digit.)
 //
 // Keys and queries of unit length are rows scaled by rk, rq: the scales (and
 // the query scale) ride on the fp32 tables, so that K and Q stay exact bf16
@@ -171,14 +178,6 @@ __device__ __forceinline__ GdrSplit<PARTS> gdr_ld_perm_parts(const uint16_t *p, 
 __device__ __forceinline__ ssd_bf16x8 gdr_ld_col(const uint16_t *tile, int stride, int row0, int col0, int r16) {
     const uint16_t *p = tile + (row0 + (r16 >> 2)) * stride + col0 + 4 * (r16 & 3);
     return ssd_ld_tr2(p, p + 16 * stride);
-}
-
-// v, or -v
-__device__ __forceinline__ ssd_bf16x8 gdr_flip(ssd_bf16x8 v, int negative) {
-    const uint32_t m = negative ? 0x80008000u : 0u;
-    uint4 u = __builtin_bit_cast(uint4, v);
-    u.x ^= m; u.y ^= m; u.z ^= m; u.w ^= m;
-    return __builtin_bit_cast(ssd_bf16x8, u);
 }
 
 template <int PARTS>
@@ -1062,19 +1061,23 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
     constexpr int UI = PB * kGdrC / 4 / TH, YI = (kGdrC * PB / 8 + TH - 1) / TH;
     // a step's columns: U, W in three parts, dY, V
     struct Step { uint16_t u[3 * UPL], w[3 * UPL], dy[kGdrC * YS], v[kGdrC * YS]; };
-    // dY U^T and W U^T, decayed and scaled, once the steps are done
-    struct Pairs { uint16_t a[3 * PL], e[3 * PL]; };
+    // dY U^T and W U^T, decayed and scaled, once the steps are done, and what each
+    // pair of tokens adds to the gradient of the decays between them
+    constexpr int DS = kGdrC + 4;
+    struct Pairs { uint16_t a[3 * PL], e[3 * PL]; float d[kGdrC * DS]; };
     union StepsOrPairs { Step step[2]; Pairs pairs; };
     __shared__ __attribute__((aligned(16))) uint16_t sK[kGdrC * KS], sQ[kGdrC * KS];
     __shared__ __attribute__((aligned(16))) StepsOrPairs sX;
     __shared__ __attribute__((aligned(16))) float sTab[kGdrTab * kGdrC];
-    __shared__ __attribute__((aligned(16))) float sDot[NW][2][kGdrC];   // per wave: dG and k . (W S) of its columns n
+    // per wave: q . (dY S), k . (W S), k . (U D') of its columns n; the pairs' sums of its rows
+    __shared__ __attribute__((aligned(16))) float sDot[NW][4][kGdrC];
     __shared__ float sEs[4][kGdrC];        // sum_j E_ij W_i . U_j per column tile
     __shared__ float sWv[kGdrC];
     __shared__ double sDs[NW];
     uint16_t *const sPA = sX.pairs.a, *const sPE = sX.pairs.e;
+    float *const sPD = sX.pairs.d;
     int tid = threadIdx.x;
-    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     int r16 = lane & 15, g4 = lane >> 4;
     const int ci = (int)(blockIdx.x % p.nc);
     const int bg = (int)(blockIdx.x / p.nc);
@@ -1122,7 +1125,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
     // Every second step's products are taken negative (U and S carry the sign),
     // each step's in a sum of its own, and in every second chunk the others: the
     // matrix cores round towards minus infinity, and so their errors cancel
-    // instead of adding up in dG.
+    // instead of adding up in the decays' gradient.
     auto store = [&](Step &s, float flip) {
 #pragma unroll
         for (int i = 0; i < UI; ++i) {
@@ -1139,9 +1142,9 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
             }
         }
     };
-    // Addresses from the lane's place are formed where they are used: hoisted out of
-    // the loops they would fill the registers.
-    auto fresh = [&]() { asm volatile("" : "+v"(r16), "+v"(g4), "+v"(tid)); };
+    // Addresses and conditions from the wave's and lane's place are formed where they
+    // are used: hoisted out of the loops they would fill the registers.
+    auto fresh = [&]() { asm volatile("" : "+v"(r16), "+v"(g4), "+v"(tid), "+v"(lane), "+s"(w)); };
     load(g * p.hpg, 0);
     gdr_stage_rows<N>(sK, KS, p.k + row0 * p.ks + (int64_t)g * N, p.ks, nv, tid, TH);
     gdr_stage_rows<N>(sQ, KS, p.q + row0 * p.qs + (int64_t)g * N, p.qs, nv, tid, TH);
@@ -1159,7 +1162,7 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
         for (int T = 0; T < 4; ++T) aq[T] = ar[T] = ac[T] = gdr_zero4();
 #pragma unroll
         for (int t = 0; t < TW; ++t) pa[t] = pw[t] = gdr_zero4();
-        double ds = 0.0;                   // <D', S> of this wave's columns n: every token of the chunk gets it
+        double ds = 0.0;                   // <D', S> of this wave's columns n
         __syncthreads();                   // the head before is done with sTab and sX
         for (int q = tid; q < kGdrTab * kGdrC; q += TH) sTab[q] = p.tab[id * (kGdrTab * kGdrC) + q];
         const float first = ci & 1 ? -1.0f : 1.0f;
@@ -1242,17 +1245,19 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
             const int q = w + NW * t;
             if (q >= kGdrTiles) break;
             const int T = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, J = q - T * (T + 1) / 2;
-            ssd_f32x4 kk = gdr_zero4();
+            ssd_f32x4 kk = gdr_zero4(), qk = gdr_zero4();
 #pragma unroll
-            for (int s = 0; s < N / 32; ++s)
-                kk = ssd_mfma(ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]),
-                              ssd_ld16(&sK[(16 * T + r16) * KS + 32 * s + 8 * g4]), kk);
+            for (int s = 0; s < N / 32; ++s) {
+                const ssd_bf16x8 kj = ssd_ld16(&sK[(16 * J + r16) * KS + 32 * s + 8 * g4]);
+                kk = ssd_mfma(kj, ssd_ld16(&sK[(16 * T + r16) * KS + 32 * s + 8 * g4]), kk);
+                qk = ssd_mfma(kj, ssd_ld16(&sQ[(16 * T + r16) * KS + 32 * s + 8 * g4]), qk);
+            }
             const int i = 16 * T + r16, j0 = 16 * J + 4 * g4;
             const float ghi = sTab[kTGhi * kGdrC + i], gli = sTab[kTGlo * kGdrC + i], rki = sTab[kTRk * kGdrC + i];
             const float rqi = sTab[kTRq * kGdrC + i], bei = sTab[kTBeta * kGdrC + i];
             const ssd_f32x4 ghj = gdr_ld4(&sTab[kTGhi * kGdrC + j0]), glj = gdr_ld4(&sTab[kTGlo * kGdrC + j0]);
             const ssd_f32x4 rkj = gdr_ld4(&sTab[kTRk * kGdrC + j0]);
-            float a[4], e[4], es = 0.0f;
+            float a[4], e[4], d[4], es = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 // above the diagonal exp2(-inf): no branch
@@ -1262,34 +1267,62 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                 const float ev = i > j0 + r ? pw[t][r] * gam * rki : 0.0f;
                 es = fmaf(ev, kk[r], es);          // sum_j E_ij W_i . U_j
                 e[r] = ev * bei;                   // subtracted below
+                d[r] = i > j0 + r ? fmaf(a[r], qk[r], -e[r] * kk[r]) : 0.0f;
             }
             es += __shfl_xor(es, 16);
             es += __shfl_xor(es, 32);
             if (g4 == 0) sEs[J][i] = es;
             gdr_store_parts<3>(&sPA[i * kGdrRS + j0], PL, make_float4(a[0], a[1], a[2], a[3]));
             gdr_store_parts<3>(&sPE[i * kGdrRS + j0], PL, make_float4(e[0], e[1], e[2], e[3]));
+            *reinterpret_cast<float4 *>(&sPD[i * DS + j0]) = make_float4(d[0], d[1], d[2], d[3]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        fresh();
         __syncthreads();
+        // what the pairs i >= t > j add for token t (the lane): a row's sum up to t,
+        // rows from t on
+        {
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int i = w; i < kGdrC; i += NW) {
+                const float d = lane > 0 && lane <= i ? sPD[i * DS + lane - 1] : 0.0f;
+                const float upto = ssd_prefix_sum(d, lane);
+                sum += lane <= i ? upto : 0.0f;
+            }
+            sDot[w][3][lane] = sum;
+        }
         // products over tokens, scaled by the tokens' rows. The K and Q operands
         // are the wave's columns n of rows 16 T + 4 g4 + r as well: element
-        // 4 (T % 2) + r of operand T / 2. Every second wave takes both negative, as
-        // the steps above do: rows of one sign (behind an activation) would gather
-        // the products' downward rounding in dG. (With SiLU keys and queries, 8 x 2048
-        // tokens, 32 heads: dA 2-11e-7 off, without it 7-39e-7; the time is the same.)
-        const float sign = w & 1 ? -1.0f : 1.0f;
+        // 4 (T % 2) + r of operand T / 2.
         ssd_bf16x8 ko[2], qo[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            ko[s] = gdr_flip(gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16), w & 1);
-            qo[s] = gdr_flip(gdr_ld_col(sQ, KS, 32 * s + 4 * g4, n0, r16), w & 1);
+            ko[s] = gdr_ld_col(sK, KS, 32 * s + 4 * g4, n0, r16);
+            qo[s] = gdr_ld_col(sQ, KS, 32 * s + 4 * g4, n0, r16);
         }
-        double kd = 0.0;                   // sum_j exp(G_C - G_j) k_j . (U D')_j of this wave's n
 #pragma unroll
         for (int T = 0; T < 4; ++T) {
-            const ssd_f32x4 hq = gdr_ld4(&sTab[kTHq * kGdrC + 16 * T + 4 * g4]);
-            const ssd_f32x4 hk = gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
-            const ssd_f32x4 tk = gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
-            const ssd_f32x4 be = gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+            // the products with S and D', and what they add to the decays' gradient
+            aq[T] *= gdr_ld4(&sTab[kTHq * kGdrC + 16 * T + 4 * g4]);
+            ar[T] *= gdr_ld4(&sTab[kTHk * kGdrC + 16 * T + 4 * g4]);
+            ac[T] *= gdr_ld4(&sTab[kTTk * kGdrC + 16 * T + 4 * g4]);
+            {
+                ssd_f32x4 qs, kw, ku;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float kv = (float)ko[T / 2][4 * (T % 2) + r], qv = (float)qo[T / 2][4 * (T % 2) + r];
+                    qs[r] = gdr_sum16(qv * aq[T][r]);
+                    kw[r] = gdr_sum16(kv * ar[T][r]);
+                    ku[r] = gdr_sum16(kv * ac[T][r]);
+                }
+                if (r16 == 0) {
+                    *reinterpret_cast<ssd_f32x4 *>(&sDot[w][0][16 * T + 4 * g4]) = qs;
+                    *reinterpret_cast<ssd_f32x4 *>(&sDot[w][1][16 * T + 4 * g4]) = kw;
+                    *reinterpret_cast<ssd_f32x4 *>(&sDot[w][2][16 * T + 4 * g4]) = ku;
+                }
+            }
+            ac[T] -= ar[T] * gdr_ld4(&sTab[kTBeta * kGdrC + 16 * T + 4 * g4]);
+            __builtin_amdgcn_sched_barrier(0);
             ssd_f32x4 tq = gdr_zero4(), tr = gdr_zero4(), te = gdr_zero4(), ta = gdr_zero4();
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -1313,50 +1346,36 @@ __global__ __launch_bounds__(4 * N) void gdr_grad_kernel(const GdrParams p) {
                     }
                 }
             }
-            aq[T] = aq[T] * hq + tq * sign;
-            ac[T] *= tk;
-            ar[T] *= hk;
-            ssd_f32x4 dot, kw;
-            const ssd_f32x4 row = ar[T] * -be - tr * sign, col = ac[T] + (ta - te) * sign;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float kv = (float)ko[T / 2][4 * (T % 2) + r], qv = (float)qo[T / 2][4 * (T % 2) + r];
-                kw[r] = gdr_sum16(kv * ar[T][r]);
-                kd = fma((double)kv, (double)ac[T][r], kd);
-                dot[r] = gdr_sum16(fmaf(qv, aq[T][r], kv * (row[r] - col[r])));
-            }
-            if (r16 == 0) {
-                *reinterpret_cast<ssd_f32x4 *>(&sDot[w][0][16 * T + 4 * g4]) = dot * sign;
-                *reinterpret_cast<ssd_f32x4 *>(&sDot[w][1][16 * T + 4 * g4]) = kw * sign;
-            }
+            aq[T] += tq;
+            ac[T] += ta - te - tr;
             dq[T] = ONE ? aq[T] : dq[T] + aq[T];
-            dk[T] = ONE ? row + col : dk[T] + (row + col);
+            dk[T] = ONE ? ac[T] : dk[T] + ac[T];
             __builtin_amdgcn_sched_barrier(0);
         }
-        // <D', S'> = exp(G_C) <D', S> + sum_j exp(G_C - G_j) k_j . (U D')_j
-        ds = ds * (double)sTab[kTHead * kGdrC + kGdrC - 1] + kd * (double)sign;
         ds = gdr_last64(gdr_prefix64(ds, lane));
         if (lane == 0) sDs[w] = ds;
         __syncthreads();
         if (w == 0) {
-            double dG = 0.0, whole = 0.0;
+            // sums that run on from the tokens before (of U D') and back from those
+            // behind (of S, whose lanes count from the last token)
+            const int back = kGdrC - 1 - lane;
+            double whole = 0.0, before = 0.0, behind = 0.0, pairs = 0.0, kwb = 0.0;
             float kw = 0.0f, es = 0.0f;
 #pragma unroll
             for (int k = 0; k < NW; ++k) {
-                dG += sDot[k][0][lane];
-                kw += sDot[k][1][lane];
                 whole += sDs[k];
+                before += lane > 0 ? sDot[k][2][lane - 1] : 0.0f;
+                behind += sDot[k][0][back];
+                kwb += sDot[k][1][back];
+                kw += sDot[k][1][lane];
+                pairs += sDot[k][3][lane];
             }
 #pragma unroll
             for (int J = 0; J < 4; ++J) es += J <= lane / 16 ? sEs[J][lane] : 0.0f;
-            // sum over tokens from this one on
-            const double upto = gdr_prefix64(dG, lane);
-            dG += gdr_last64(upto) - upto;
-            // d(log a_t) = a_t <.., S_{t-1}>, but the sum leaves the rounding of
-            // its terms, which a long step would multiply: a token that forgets
-            // all (a_t below 2^-64) has none
+            behind = gdr_prefix64(behind - (double)sTab[kTBeta * kGdrC + back] * kwb, lane);
+            before = gdr_prefix64(before, lane);
+            const float dlog = (float)(whole * (double)sTab[kTHead * kGdrC + kGdrC - 1] + before + __shfl(behind, back) + pairs);
             const float step = sTab[kTStep * kGdrC + lane];
-            const float dlog = step * p.A[h] * kLog2e < -64.0f ? 0.0f : (float)(dG + whole);
             const float ddt = dlog * p.A[h] * sTab[kTDstep * kGdrC + lane];
             double pA = lane < nv && dlog != 0.0f ? (double)dlog * step : 0.0;   // (step may be infinite)
             double pb = lane < nv ? (double)ddt : 0.0;

@@ -176,6 +176,42 @@ def test_bias_without_softplus(env):
         assert torch.equal(g[n], h[n]), n
 
 
+@pytest.mark.parametrize("softplus", [False, True])
+@pytest.mark.parametrize("shape", [(2, 150, 3, 6, 64, 64), (1, 200, 6, 6, 96, 128)])
+def test_gradients_of_strong_decays(env, shape, softplus):
+    """Decays per token from exp(-0.5) to exp(-44), a head each: the gradients of the
+    step, its bias and the rate keep their digits relative to that head's own terms,
+    each of which has the token's decay as a factor. Then the same with
+    mild tokens between strong ones."""
+    torch, ssm = env
+    B, L, G, H, P, N = shape
+    x = inputs(torch, sum(shape), *shape, bias=softplus, grads=True)
+    x["dt"] = 1.0 + 0.1 * x["dt"].float()
+    if softplus:
+        x["dt"], x["dt_bias"] = x["dt"] - 0.5, torch.full((H,), 0.5, device="cuda")
+    x["dt"] = x["dt"].to(torch.bfloat16)
+    x["A"] = -torch.tensor([0.5, 4.0, 8.0, 16.0, 28.0, 44.0], device="cuda")
+    opts = dict(OPTS, dt_softplus=softplus)
+
+    def check(what):
+        g = ssm.ssm_gdr_bwd(**x, **opts)
+        torch.cuda.synchronize()
+        ref = reference(x, **opts)[2]
+        bad = []
+        for h in range(H):
+            e = dict(ddt=err(np64(g["ddt"])[..., h], ref["ddt"][..., h]))
+            for n in ("dA", "ddt_bias")[:1 + softplus]:
+                e[n] = float(abs(np64(g[n])[h] - ref[n][h]) / ref[n + "_abs"][h])
+            say("  %s, rate %.1f: " % (what, float(x["A"][h])), ", ".join("%s %.2e" % p for p in e.items()))
+            bad += [(h, n, v) for n, v in e.items() if not v <= (TOL_BF if n == "ddt" else TOL_32)]
+        assert not bad, bad
+    check("every token")
+    # one token in nine decays strongly
+    mild = torch.arange(L, device="cuda") % 9 != 4
+    x["dt"][:, mild] = -6.0 if softplus else 1.0 / 512
+    check("one in nine")
+
+
 def test_no_lean_with_rows_of_one_sign(env):
     """The gradients are linear in dy and dh_last: those of the negative are the
     negative, but for the matrix cores' rounding downwards. With keys and queries
