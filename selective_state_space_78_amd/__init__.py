@@ -10,6 +10,10 @@ Names follow the C ABI: ``ssm_scan_fwd``, ``ssm_scan_fwd_noalloc``, ``ssm_scan_w
 ``ssm_scan_plan``, ``ssm_scan_bwd``, ``ssm_state_update``, ``ssm_ssd_fwd``,
 ``ssm_gdr_fwd``, ``ssm_gdr_bwd``, ``ssm_gdr_state_update``, ``ssm_prenorm_fwd``,
 ``ssm_gated_norm_fwd``, ``ssm_status_string``.
+
+``stream`` runs a call on a stream other than the current one. The caller orders the
+two where inputs or results cross; what the delta rule's and the norms' calls
+allocate comes out of that stream's memory.
 """
 from __future__ import annotations
 
@@ -188,6 +192,27 @@ def _stream(stream, device):
     # the handle alone: a Stream object costs more than a launch of a small kernel
     index = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """A tensor that work on ``stream`` (None: the current one) is to write. Under a
+    stream handed over it comes out of that stream's memory: a block of the current
+    stream's may still be in use by work queued there, and would go back to it as
+    soon as the tensor is dropped, written or not. What the caller gets is held for
+    the work that they queue on the current stream as well."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
 
 
 def _on(device, fn, *args):
@@ -596,16 +621,12 @@ def _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, q
                    None if dt_bias is None else dt_bias.data_ptr())
 
 
-def _workspace(workspace, need, device, name, stream):
+def _workspace(workspace, need, device, name, stream, returned=False):
     import torch
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            # the allocator may hand it to the current stream as soon as it is dropped here
-            workspace.record_stream(stream)
-        return workspace, need
+        return _empty(need, torch.uint8, device, stream, returned), need
     _check(workspace, "workspace", device=device)
     have = workspace.numel() * workspace.element_size()
     if have < need:
@@ -648,15 +669,15 @@ def ssm_gdr_fwd(q, k, v, dt, beta, A, h0=None, y=None, h_last=None, scale=None, 
     N, dev = q.shape[-1], v.device
     _check(h0, "h0", (batch, H, P, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, L, H, P), dtype=v.dtype, device=dev)
+        y = _empty((batch, L, H, P), v.dtype, dev, stream)
     if h_last is None and want_h_last:
-        h_last = torch.empty((batch, H, P, N), dtype=torch.float32, device=dev)
+        h_last = _empty((batch, H, P, N), torch.float32, dev, stream)
     _check(y, "y", (batch, L, H, P), v.dtype, dev)
     _check(h_last, "h_last", (batch, H, P, N), torch.float32, dev)
     L_ = lib()
     name = "ssm_gdr_fwd_save" if _save else "ssm_gdr_fwd"
     size = L_.ssm_gdr_bwd_workspace_size if _save else L_.ssm_gdr_workspace_size
-    workspace, ws_bytes = _workspace(workspace, size(ctypes.byref(desc)), dev, name, stream)
+    workspace, ws_bytes = _workspace(workspace, size(ctypes.byref(desc)), dev, name, stream, _save)
     rc = _on(dev, getattr(L_, name), ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A), _ptr(h0),
                            _ptr(y), _ptr(h_last), _ptr(workspace), ws_bytes, _stream(stream, dev))
     if rc != 0:
@@ -702,7 +723,7 @@ def ssm_gdr_bwd(q, k, v, dt, beta, A, dy, h0=None, dh_last=None, scale=None, dt_
         if not wanted:
             return None
         if o.get(name) is None:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+            o[name] = _empty(shape, dtype, dev, stream)
         _check(o[name], name, shape, dtype, dev)
         return o[name]
     g = dict(dq=get("dq", (batch, L, G, N), t), dk=get("dk", (batch, L, G, N), t), dv=get("dv", (batch, L, H, P), t),
@@ -751,7 +772,7 @@ def ssm_gdr_state_update(q, k, v, dt, beta, A, h, y=None, h_out=None, scale=None
         h_out = h
     _check(h_out, "h_out", (batch, H, P, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, H, P), dtype=v.dtype, device=dev)
+        y = _empty((batch, H, P), v.dtype, dev, stream)
     _check(y, "y", (batch, H, P), v.dtype, dev)
     rc = _on(dev, lib().ssm_gdr_state_update, ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(A),
                                     _ptr(h), _ptr(h_out), _ptr(y), _stream(stream, dev))
@@ -781,9 +802,9 @@ def ssm_prenorm_fwd(x, weight, residual=None, scale=None, eps=1e-5, y=None, r=No
     _check(weight, "weight", (dim,), torch.float32, dev)
     _check(scale, "scale", (dim,), torch.float32, dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _empty(x.shape, x.dtype, dev, stream)
     if r is None and want_r:
-        r = torch.empty(x.shape, dtype=rt, device=dev)
+        r = _empty(x.shape, rt, dev, stream)
     _check(y, "y", x.shape, x.dtype, dev)
     _check(r, "r", x.shape, rt, dev)
     desc = PrenormDesc(x.numel() // dim if dim else 0, dim, code, SSM_F32 if rt == torch.float32 else SSM_BF16,
@@ -822,7 +843,7 @@ def ssm_prenorm_bwd(dy, r, weight, dr=None, x=None, scale=None, eps=1e-5, want_d
         if not wanted:
             return None
         if o.get(name) is None:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+            o[name] = _empty(shape, dtype, dev, stream)
         _check(o[name], name, shape, dtype, dev)
         return o[name]
     g = dict(dx=get("dx", dy.shape, dy.dtype), dresidual=get("dresidual", dy.shape, rt, want_dresidual),
@@ -866,9 +887,8 @@ def ssm_gated_norm_fwd(x, z, weight, eps=1e-5, gate_first=False, y=None, stream=
     or (dim,) for every group, float32. Returns y, allocated when not given.
     """
     desc = _gated_desc(x, z, weight, eps, gate_first)
-    import torch
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _check(y, "y", x.shape, x.dtype, x.device)
     rc = _on(x.device, lib().ssm_gated_norm_fwd, ctypes.byref(desc), _ptr(x), _ptr(z), _ptr(weight), _ptr(y),
                                   _stream(stream, x.device))
@@ -891,7 +911,7 @@ def ssm_gated_norm_bwd(dy, x, z, weight, eps=1e-5, gate_first=False, out=None, w
         if not wanted:
             return None
         if o.get(name) is None:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+            o[name] = _empty(shape, dtype, dev, stream)
         _check(o[name], name, shape, dtype, dev)
         return o[name]
     g = dict(dx=get("dx", x.shape, x.dtype), dz=get("dz", x.shape, x.dtype, z is not None),
