@@ -12,8 +12,8 @@ Names follow the C ABI: ``ssm_scan_fwd``, ``ssm_scan_fwd_noalloc``, ``ssm_scan_w
 ``ssm_gated_norm_fwd``, ``ssm_status_string``.
 
 ``stream`` runs a call on a stream other than the current one. The caller orders the
-two where inputs or results cross; what the delta rule's and the norms' calls
-allocate comes out of that stream's memory.
+two where inputs or results cross; what the call allocates comes out of that stream's
+memory.
 """
 from __future__ import annotations
 
@@ -322,9 +322,9 @@ def _fwd(u, delta, A, B, C, D, z, h0, y, h_last, disc, workspace, tuning, stream
     _check(D, "D", (dim,), torch.float32, dev)
     _check(h0, "h0", (batch, dim, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, L, dim), dtype=dt, device=dev)
+        y = _empty((batch, L, dim), dt, dev, stream)
     if h_last is None and want_h_last:
-        h_last = torch.empty((batch, dim, N), dtype=torch.float32, device=dev)
+        h_last = _empty((batch, dim, N), torch.float32, dev, stream)
     _check(y, "y", (batch, L, dim), dt, dev)
     _check(h_last, "h_last", (batch, dim, N), torch.float32, dev)
     _check(delta_bias, "delta_bias", (dim,), torch.float32, dev)
@@ -346,7 +346,7 @@ def _fwd(u, delta, A, B, C, D, z, h0, y, h_last, disc, workspace, tuning, stream
     else:
         need = L_.ssm_scan_workspace_size_tuned(ctypes.byref(desc), _tuning(tuning))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream, save)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = [ctypes.byref(desc), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
             _ptr(h0), _ptr(y), _ptr(h_last), _ptr(workspace), ws_bytes]
@@ -422,7 +422,7 @@ def ssm_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, h0=None, dh_last=None, d
         if not wanted:
             return None
         if name not in o or o[name] is None:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+            o[name] = _empty(shape, dtype, dev, stream)
         _check(o[name], name, shape, dtype, dev)
         return o[name]
     du = get("du", (batch, L, dim), dt)
@@ -448,7 +448,7 @@ def ssm_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, h0=None, dh_last=None, d
         raise ValueError("workspace has %d bytes, ssm_scan_bwd needs %d" % (
             workspace.numel() * workspace.element_size(), need))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream, False)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     name = "ssm_scan_bwd_saved" if _saved else "ssm_scan_bwd"
     rc = getattr(L_, name)(ctypes.byref(desc), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
@@ -482,7 +482,7 @@ def ssm_state_update(x, delta, A, B, C, h, D=None, z=None, y=None, disc="euler",
     _check(D, "D", (dim,), torch.float32, dev)
     _check(h, "h", (batch, dim, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, dim), dtype=dt, device=dev)
+        y = _empty((batch, dim), dt, dev, stream)
     _check(y, "y", (batch, dim), dt, dev)
     _check(delta_bias, "delta_bias", (dim,), torch.float32, dev)
     rc = lib().ssm_state_update(batch, dim, N, code, _DISC[disc], _ptr(x), _ptr(delta), _ptr(delta_bias),
@@ -523,9 +523,9 @@ def ssm_ssd_fwd(x, dt, A, B, C, D=None, z=None, h0=None, y=None, h_last=None, di
     _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
     _check(h0, "h0", (batch, H, P, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, L, H, P), dtype=x.dtype, device=dev)
+        y = _empty((batch, L, H, P), x.dtype, dev, stream)
     if h_last is None and want_h_last:
-        h_last = torch.empty((batch, H, P, N), dtype=torch.float32, device=dev)
+        h_last = _empty((batch, H, P, N), torch.float32, dev, stream)
     _check(y, "y", (batch, L, H, P), x.dtype, dev)
     _check(h_last, "h_last", (batch, H, P, N), torch.float32, dev)
     desc = make_ssd_desc(batch, L, H, P, G, N, code, disc, dt_bias, dt_softplus)
@@ -557,7 +557,7 @@ def ssm_ssd_state_update(x, dt, A, B, C, h, D=None, z=None, y=None, disc="euler"
     _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
     _check(h, "h", (batch, H, P, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((batch, H, P), dtype=x.dtype, device=dev)
+        y = _empty((batch, H, P), x.dtype, dev, stream)
     _check(y, "y", (batch, H, P), x.dtype, dev)
     desc = make_ssd_desc(batch, 1, H, P, G, N, code, disc, dt_bias, dt_softplus)
     rc = lib().ssm_ssd_state_update(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),

@@ -67,7 +67,27 @@ def rule(L=3):
     return t(1, 64), t(1, 64), t(2, 16), t(2), t(2), torch.zeros(2)
 
 
+def scan():
+    t = torch.zeros(2, 40, 16, dtype=BF)
+    return t, t, torch.zeros(16, 4), torch.zeros(2, 40, 4, dtype=BF), torch.zeros(2, 40, 4, dtype=BF)
+
+
+def ssd(L=40):
+    lead = (2,) if L is None else (2, L)
+    t = lambda *s: torch.zeros(*lead, *s, dtype=BF)
+    return t(2, 16), t(2), torch.zeros(2), t(1, 64), t(1, 64)
+
+
 CALLS = {
+    "scan_fwd": lambda **k: ssm.ssm_scan_fwd(*scan(), **k),
+    "scan_fwd_tuned": lambda **k: ssm.ssm_scan_fwd(*scan(), tuning=(1, 2), **k),
+    "scan_fwd_noalloc": lambda **k: ssm.ssm_scan_fwd_noalloc(*scan(), **k),
+    "scan_fwd_save": lambda **k: ssm.ssm_scan_fwd_save(*scan(), **k),
+    "scan_bwd": lambda **k: ssm.ssm_scan_bwd(*scan(), scan()[0], D=torch.zeros(16), z=scan()[0], **k),
+    "state_update": lambda **k: ssm.ssm_state_update(*(t[:, 0].contiguous() if t.dim() == 3 else t for t in scan()),
+                                                     torch.zeros(2, 16, 4), **k),
+    "ssd_fwd": lambda **k: ssm.ssm_ssd_fwd(*ssd(), **k),
+    "ssd_state_update": lambda **k: ssm.ssm_ssd_state_update(*ssd(None), torch.zeros(2, 2, 16, 64), **k),
     "gdr_fwd": lambda **k: ssm.ssm_gdr_fwd(*rule(), **k),
     "gdr_fwd_save": lambda **k: ssm.ssm_gdr_fwd_save(*rule(), **k),
     "gdr_bwd": lambda **k: ssm.ssm_gdr_bwd(*rule(), rule()[2], dt_bias=torch.zeros(2), **k),

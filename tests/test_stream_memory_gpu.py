@@ -36,7 +36,16 @@ def calls(torch, ssm):
     x, z, w, s = rnd(500, 4, 64), rnd(500, 4, 64), rnd(64), rnd(64)
     flat_x, flat_z = x.flatten(0, 1), z.flatten(0, 1)
     out = torch.empty_like(h)
+    u, de, zz, dyu = (rnd(B, L, 128) for _ in range(4))
+    Bs, Cs, As, D = rnd(B, L, 16), rnd(B, L, 16), -rnd(128, 16).abs(), rnd(128)
+    de = 0.1 * de.abs()
+    sx, sd, sB, sC = rnd(B, L, H, P).to(bf), rnd(B, L, H).abs().to(bf), rnd(B, L, 1, N).to(bf), rnd(B, L, 1, N).to(bf)
+    # (a scan's workspace holds bytes that nothing writes)
     return {
+        "scan_fwd": lambda **kw: ssm.ssm_scan_fwd(u, de, As, Bs, Cs, D, zz, **kw),
+        "scan_fwd_save": lambda **kw: ssm.ssm_scan_fwd_save(u, de, As, Bs, Cs, D, zz, **kw)[:2],
+        "scan_bwd": lambda **kw: ssm.ssm_scan_bwd(u, de, As, Bs, Cs, dyu, D, zz, **kw),
+        "ssd_fwd": lambda **kw: ssm.ssm_ssd_fwd(sx, sd, A, sB, sC, **kw),
         "gdr_fwd": lambda **kw: ssm.ssm_gdr_fwd(q, k, v, dt, beta, A, **o, **kw),
         # (the workspace holds bytes that nothing writes)
         "gdr_fwd_save": lambda **kw: ssm.ssm_gdr_fwd_save(q, k, v, dt, beta, A, **o, **kw)[:2],
@@ -50,8 +59,8 @@ def calls(torch, ssm):
     }
 
 
-NAMES = ["gdr_fwd", "gdr_fwd_save", "gdr_bwd", "gdr_state_update", "prenorm_fwd", "prenorm_bwd", "gated_norm_fwd",
-         "gated_norm_bwd"]
+NAMES = ["scan_fwd", "scan_fwd_save", "scan_bwd", "ssd_fwd", "gdr_fwd", "gdr_fwd_save", "gdr_bwd", "gdr_state_update",
+         "prenorm_fwd", "prenorm_bwd", "gated_norm_fwd", "gated_norm_bwd"]
 WAIT = 10_000_000      # clock cycles: some milliseconds
 
 
