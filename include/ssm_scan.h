@@ -430,7 +430,10 @@ size_t ssm_gdr_bwd_workspace_size(const ssm_gdr_desc *desc);
  *             contents on entry do not matter and are clobbered
  * q, k, v, y, h0 and h_last must be 16-byte aligned (dt, beta 2-byte, A,
  * dt_bias 4-byte). Outputs must not overlap inputs, each other or the
- * workspace. seqlen == 0 writes h_last = h0 (or zeros) and no y.
+ * workspace. seqlen == 0 writes h_last = h0 (or zeros) and no y. Sizes that need
+ * 2^32 work items in a launch are refused (SSM_ERR_SHAPE) before the first: from 2^24
+ * chunks of 64 tokens, counted over batch rows and heads, from 2^22 heads of 256
+ * columns, and in a backward from 2^32 / (4 dstate) chunks counted over groups.
  */
 int ssm_gdr_fwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *v, const void *dt,
                 const void *beta, const float *A, const float *h0, void *y, float *h_last,

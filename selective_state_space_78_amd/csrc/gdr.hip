@@ -158,6 +158,7 @@ int check(const ssm_gdr_desc *desc, Sizes *s, bool one = false) {
     s->nc = (d.seqlen + kGdrC - 1) / kGdrC;
     // one workgroup per chunk and head; the workspace's bytes fit
     if (!mul_ok(s->heads, std::max<int64_t>(s->nc, 16), &n) || n > INT32_MAX) return SSM_ERR_SHAPE;
+    if (!one && s->tokens > 0 && !gdr_fwd_grids_ok(s->heads, s->nc, d.headdim)) return SSM_ERR_SHAPE;
     return SSM_OK;
 }
 
@@ -302,6 +303,7 @@ int run_bwd(const ssm_gdr_desc *desc, const void *q, const void *k, const void *
     Sizes s;
     if (const int rc = check(desc, &s)) return rc;
     const ssm_gdr_desc &d = *desc;
+    if (s.tokens > 0 && !gdr_bwd_grids_ok(d.batch * d.ngroups, s.nc, d.nheads, d.dstate)) return SSM_ERR_SHAPE;
     const int64_t H = d.nheads, gn = (int64_t)d.ngroups * d.dstate, hp = H * d.headdim;
     Range in[11];
     if (const int rc = check_inputs(d, s, q, k, v, dt, beta, A, h0, in)) return rc;

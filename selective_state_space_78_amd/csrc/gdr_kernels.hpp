@@ -89,6 +89,12 @@ struct GdrParams {
     float scale, qk_eps;
 };
 
+// With fewer than 8 computing waves a workgroup of the kernels that walk the chunks
+// has as many helpers, which do the staging: a computing wave's time per chunk is
+// then its own arithmetic. With 8 (two to a SIMD) there are no registers for
+// helpers, and the two waves of a SIMD stage at different times instead.
+constexpr int gdr_helpers(int nw) { return nw < 8 ? nw : 0; }
+
 #ifdef SSM_GDR_INSTANTIATE
 
 constexpr int kGdrPad = 8;                 // LDS row padding of K, Q (elements)
@@ -515,12 +521,6 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 // which over many chunks would add up where the gradient of the decay sums
 // them. So the state's sign alternates: odd chunks hold -S, through the signs
 // of the scales that are applied anyway, and the errors cancel.
-
-// With fewer than 8 computing waves a workgroup has as many helpers, which do
-// the staging: a computing wave's time per chunk is then its own arithmetic. With
-// 8 (two to a SIMD) there are no registers for helpers, and the two waves of a
-// SIMD stage at different times instead.
-constexpr int gdr_helpers(int nw) { return nw < 8 ? nw : 0; }
 
 // LDS of one chunk: K and Q rows; the lower tiles of R and of the scores in three
 // parts; the first four tables and the decay over the whole chunk.

@@ -1,24 +1,37 @@
 // Launches of the gated delta rule's kernels.
 #pragma once
 
+#include "abi_util.hpp"
 #include "gdr_kernels.hpp"
 
 namespace ssm_detail {
 
-#ifdef SSM_GDR_INSTANTIATE
-
 constexpr int kGdrCus = 256;
 
-// Computing waves (of 16 columns) per workgroup of the kernels that walk the
-// chunks. LDS allows one workgroup per CU, so the rounds over the CUs count, times
+// workgroups per head of a walk with nw computing waves (of 16 columns) each
+inline int gdr_splits(int P, int nw) { return (P / 16 + nw - 1) / nw; }
+
+// Computing waves per workgroup of the kernels that walk the chunks of `heads` heads.
+// LDS allows one workgroup per CU, so the rounds over the CUs count, times
 // what a chunk takes: about 1.1 times as long with 4 waves as with 2, and 1.7
 // times with 8 (measured on 48 and 256 heads of 128 x 128)
-inline int gdr_waves(const GdrParams &p) {
-    const int64_t heads = (int64_t)p.batch * p.H, tiles = p.P / 16;
-    auto time = [&](int nw, double chunk) { return (double)((heads * ((tiles + nw - 1) / nw) + kGdrCus - 1) / kGdrCus) * chunk; };
+inline int gdr_waves(int64_t heads, int P) {
+    auto time = [&](int nw, double chunk) { return (double)((heads * gdr_splits(P, nw) + kGdrCus - 1) / kGdrCus) * chunk; };
     const double t2 = time(2, 1.0), t4 = time(4, 1.1), t8 = time(8, 1.7);
     return t2 <= t4 && t2 <= t8 ? 2 : t4 <= t8 ? 4 : 8;
 }
+
+// Whether the launches over `chunks` chunks in each of `heads` heads stay below 2^32
+// work items
+inline bool gdr_fwd_grids_ok(int64_t heads, int64_t chunks, int P) {
+    const int nw = gdr_waves(heads, P);
+    return grid_ok(heads * chunks, 256) && grid_ok(heads * gdr_splits(P, nw), 64 * (nw + gdr_helpers(nw)));
+}
+inline bool gdr_bwd_grids_ok(int64_t groups, int64_t chunks, int H, int N) {
+    return grid_ok(groups * chunks, 4 * N) && grid_ok(H, 256);
+}
+
+#ifdef SSM_GDR_INSTANTIATE
 
 template <int N>
 hipError_t gdr_prep_launch(const GdrParams &p, hipStream_t st) {
@@ -29,7 +42,7 @@ hipError_t gdr_prep_launch(const GdrParams &p, hipStream_t st) {
 
 template <int N, int NW>
 void gdr_fwd_nw(const GdrParams &p, bool save, hipStream_t st) {
-    const int splits = (p.P / 16 + NW - 1) / NW;
+    const int splits = gdr_splits(p.P, NW);
     const dim3 grid((unsigned)((int64_t)p.batch * p.H * splits));
     if (save && p.y == nullptr)
         hipLaunchKernelGGL((gdr_fwd_kernel<N, true, false, NW>), grid, dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
@@ -41,7 +54,7 @@ void gdr_fwd_nw(const GdrParams &p, bool save, hipStream_t st) {
 
 template <int N>
 hipError_t gdr_fwd_launch(const GdrParams &p, bool save, hipStream_t st) {
-    const int nw = gdr_waves(p);
+    const int nw = gdr_waves((int64_t)p.batch * p.H, p.P);
     if (nw == 8) gdr_fwd_nw<N, 8>(p, save, st);
     else if (nw == 4) gdr_fwd_nw<N, 4>(p, save, st);
     else gdr_fwd_nw<N, 2>(p, save, st);
@@ -50,14 +63,14 @@ hipError_t gdr_fwd_launch(const GdrParams &p, bool save, hipStream_t st) {
 
 template <int N, int NW>
 void gdr_rev_nw(const GdrParams &p, hipStream_t st) {
-    const int splits = (p.P / 16 + NW - 1) / NW;
+    const int splits = gdr_splits(p.P, NW);
     hipLaunchKernelGGL((gdr_rev_kernel<N, NW>), dim3((unsigned)((int64_t)p.batch * p.H * splits)),
                        dim3(64 * (NW + gdr_helpers(NW))), 0, st, p, splits);
 }
 
 template <int N>
 hipError_t gdr_bwd_launch(const GdrParams &p, hipStream_t st) {
-    const int nw = gdr_waves(p);
+    const int nw = gdr_waves((int64_t)p.batch * p.H, p.P);
     if (nw == 8) gdr_rev_nw<N, 8>(p, st);
     else if (nw == 4) gdr_rev_nw<N, 4>(p, st);
     else gdr_rev_nw<N, 2>(p, st);

@@ -138,6 +138,29 @@ def test_launch_limits(L):
     assert call(L.ssm_prenorm_bwd, pre(rows=1 << 24, dim=16384), PREB, **ws, **far(PREB)) == ESHAPE
 
 
+def test_sequence_launch_limits(L):
+    """Sequences whose launches would have 2^32 work items, in the preparation, a walk
+    or the gradients: refused by their shape before the first; sizes just below go on
+    to the next check (a null pointer's)."""
+    T = 4096
+    far = lambda names: {n: (k + 1) * T * GB for k, n in enumerate(names)}
+    ws = dict(ws=64 * T * GB, ws_bytes=1 << 42)
+    fwd = lambda d, **o: call(L.ssm_gdr_fwd, d, FWD, **ws, **dict(far(FWD), **o))
+    bwd = lambda fn, d, **o: call(fn, d, BWD, **ws, **dict(far(BWD), **o))
+    walk = dict(H=4, G=4, P=256, L=1)
+    assert fwd(gdr(b=1 << 20, **walk)) == ESHAPE
+    assert fwd(gdr(b=(1 << 20) - 1, **walk), y=0) == ENULL
+    prep = dict(b=1, H=1, G=1, P=16)
+    assert fwd(gdr(L=(1 << 30) - 63, **prep)) == ESHAPE
+    assert fwd(gdr(L=(1 << 30) - 128, **prep), y=0) == ENULL
+    assert fwd(gdr(L=1 << 29, N=128, **prep), y=0) == ENULL
+    for fn in (L.ssm_gdr_bwd, L.ssm_gdr_bwd_saved):
+        assert bwd(fn, gdr(b=1 << 20, **walk)) == ESHAPE
+        assert bwd(fn, gdr(L=1 << 29, N=128, **prep)) == ESHAPE
+        assert bwd(fn, gdr(L=(1 << 29) - 64, N=128, **prep), dq=0) == ENULL
+    assert call(L.ssm_gdr_fwd, gdr(b=1 << 20, **dict(walk, L=0)), FWD, **dict(far(FWD), h_last=0)) == OK
+
+
 def pre(rows=4, dim=64, dt=ssm.SSM_BF16, rt=ssm.SSM_BF16, eps=1e-5, reserved=0, xs=0):
     return ssm.PrenormDesc(rows, dim, dt, rt, eps, reserved, xs)
 
