@@ -132,6 +132,38 @@ def test_gated_norm(env, rows, groups, dim, shared, strided, first, dtype):
     assert max(e["y"], e["dx"], e["dz"]) <= tol(x) and e["dweight"] <= TOL_SUM, e
 
 
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("dim", [128, 101])
+def test_gate_of_any_size(env, dim, first):
+    """Gates from silu(-87) to silu(87), fp32, element by element: y is within 24 half
+    steps of its own size, however small the gate makes it (the row's sum of squares 8,
+    its root and inverse 4, the sigmoid 6, products and the rounding of y 6), and the
+    gradients within 64 of their terms' (the sums of n w dy as the file's tolerance has
+    it; silu' = s (1 + z (1 - s)), where 1 - s of a positive z adds z half steps up to
+    z = 17, where it is 0). Values below 2^-126 are multiples of 2^-149: a rounding
+    there adds up to 2^-150 whatever the value is, f / rms times weight (below 2) two
+    of them, together less than 2^-148."""
+    torch, ssm = env
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    z = torch.linspace(-87.0, 87.0, 40 * dim, device="cuda")[torch.randperm(40 * dim, generator=gen, device="cuda")]
+    z = z.view(40, 1, dim)
+    x, dy, w = rnd(40, 1, dim), rnd(40, 1, dim), 1 + 0.2 * rnd(dim)
+    y = ssm.ssm_gated_norm_fwd(x, z, w, gate_first=first)
+    g = ssm.ssm_gated_norm_bwd(dy, x, z, w, gate_first=first)
+    torch.cuda.synchronize()
+    yr, ref = delta.gated_norm(np64(x), np64(z), np64(w), gate_first=first, dy=np64(dy))
+    half = 2.0 ** -24
+    s = 1.0 / (1.0 + np.exp(-np64(z)))
+    turn = s * (1.0 + np.abs(np64(z)) * (1.0 - s))                   # the size of silu's terms
+    slope = np.maximum(np.abs(s * (1.0 + np64(z) * (1.0 - s))), 1e-300)
+    off = lambda got, want: np.maximum(np.abs(np64(got) - want) - 2.0 ** -148, 0.0)
+    e = dict(y=np.max(off(y, yr) / np.abs(yr)) / half, dx=np.max(off(g["dx"], ref["dx"]) / ref["dx_terms"]) / half,
+             dz=np.max(off(g["dz"], ref["dz"]) / (ref["dz_terms"] * turn / slope)) / half)
+    say("gate of any size", dim, first, ", ".join("%s %.1f half steps" % p for p in e.items()))
+    assert e["y"] <= 24 and e["dx"] <= 64 and e["dz"] <= 64, e
+
+
 def test_gated_norm_forms(env):
     """No gate; rows of zeros; no rows; guards around the outputs; replays."""
     torch, ssm = env
