@@ -60,17 +60,11 @@ __device__ __forceinline__ void ld(const void *base, int64_t off, float (&v)[VEC
         if constexpr (sizeof(T) == 2) v[0] = ssd_bf(*p);
         else v[0] = *p;
     } else if constexpr (sizeof(T) == 2) {
-        static_assert(VEC == 8 || VEC == 4);
-        uint32_t w[VEC / 2];
-        if constexpr (VEC == 8) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p);
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        } else {
-            const uint2 a = *reinterpret_cast<const uint2 *>(p);
-            w[0] = a.x; w[1] = a.y;
-        }
+        static_assert(VEC == 8);
+        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
+        for (int e = 0; e < 4; ++e) {
             v[2 * e] = __uint_as_float(w[e] << 16);
             v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
         }
@@ -90,11 +84,9 @@ __device__ __forceinline__ void st(void *base, int64_t off, const float (&v)[VEC
         if constexpr (sizeof(T) == 2) *p = ssd_to_bf(v[0]);
         else *p = v[0];
     } else if constexpr (sizeof(T) == 2) {
-        uint32_t w[VEC / 2];
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) w[e] = ssd_pack(v[2 * e], v[2 * e + 1]);
-        if constexpr (VEC == 8) *reinterpret_cast<uint4 *>(p) = uint4{w[0], w[1], w[2], w[3]};
-        else *reinterpret_cast<uint2 *>(p) = uint2{w[0], w[1]};
+        static_assert(VEC == 8);
+        *reinterpret_cast<uint4 *>(p) =
+            uint4{ssd_pack(v[0], v[1]), ssd_pack(v[2], v[3]), ssd_pack(v[4], v[5]), ssd_pack(v[6], v[7])};
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; e += 4) *reinterpret_cast<float4 *>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
