@@ -617,7 +617,7 @@ def _gdr_desc(q, k, v, dt, beta, A, scale, dt_bias, dt_softplus, beta_sigmoid, q
     _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
     batch, L = lead if len(lead) == 2 else (lead[0], 1)
     return GdrDesc(batch, L, H, P, G, N, code, int(bool(dt_softplus)), int(bool(beta_sigmoid)), int(bool(qk_norm)),
-                   float(N ** -0.5 if scale is None else scale), float(qk_eps), *strides,
+                   float(max(N, 1) ** -0.5 if scale is None else scale), float(qk_eps), *strides,
                    None if dt_bias is None else dt_bias.data_ptr())
 
 

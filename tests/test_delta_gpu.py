@@ -541,6 +541,16 @@ def test_streams_and_graph(env):
             assert torch.equal(a, b), k
 
 
+def test_keys_without_values_are_refused(env):
+    """dstate 0 is refused as any other unsupported dstate (not by a division)."""
+    torch, ssm = env
+    x = inputs(torch, 21, 2, 10, 1, 2, 32, 64)
+    x["q"], x["k"], x["h0"] = x["q"][..., :0].contiguous(), x["k"][..., :0].contiguous(), x["h0"][..., :0].contiguous()
+    with pytest.raises(ssm.SsmError) as e:
+        ssm.ssm_gdr_fwd(**x)
+    assert e.value.status == -4
+
+
 def test_refusals(env):
     torch, ssm = env
     x = inputs(torch, 13, 2, 10, 1, 2, 32, 64)
