@@ -22,7 +22,7 @@ using namespace ssm_detail;
 // lanes hold a row as 16-byte pieces; a workgroup takes 32 (N 128) or 64 (N
 // 64) rows of a head, so the loads of a thread's 4 rows are in flight together
 // and q and k are read once for them. Bound by memory: 256 users x 40 heads of
-// 128 x 128 (1.35 GB) 0.24 ms, 5.6 TB/s; one user x 32 heads 5 us.
+// 128 x 128 (1.35 GB) 0.233-0.240 ms, 5.6-5.8 TB/s; one user x 32 heads 5 us.
 struct GdrStepParams {
     const uint16_t *q, *k, *v, *dt, *beta;
     const float *A, *dt_bias, *h;

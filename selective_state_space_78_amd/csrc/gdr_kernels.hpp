@@ -526,7 +526,8 @@ __device__ __forceinline__ ssd_f32x4 gdr_ld4(const float *p) {
 // parts; the first four tables and the decay over the whole chunk.
 //
 // Layouts are chosen for the banks (64 of 4 bytes): with padded rows the walk
-// spent more LDS cycles on conflicts than on data (7.4 of 12 thousand per chunk).
+// spent more LDS cycles on conflicts than on data (7.4 of 12 thousand per chunk; so
+// laid out, 2.0 thousand are left, 254 per wave with its 127 LDS instructions).
 //  * A 16 x 16 tile is kept as units of 4 columns, unit column by unit column, rows
 //    8 apart swapped in the last two unit columns: 16 lanes that read a unit column
 //    (an operand's rows) or a 4 x 4 square of units (a transposing read) touch
@@ -684,13 +685,15 @@ template <int N, int NW> struct GdrChunkRegs {
 // Products of parts are issued small ones first, each over every T in turn, so that
 // consecutive instructions do not wait for one another.
 //
-// Measured: 256 heads of 128 x 128 on 8192 tokens 0.78 ms, 6.1 us a chunk, for which
-// a wave issues 900 vector instructions and 182 MFMAs (2900 cycles), two waves to a
-// SIMD: bound by issue and the matrix cores together. With the kept states, 256
+// Measured: 256 heads of 128 x 128 on 8192 tokens 0.85-0.90 ms, 7 us a chunk, for
+// which a wave issues 1000 vector instructions and 216 MFMAs (3500 cycles), two waves
+// to a SIMD: bound by issue and the matrix cores together. With the kept states, 256
 // heads on 2048 tokens 0.31 ms for 1.4 GB, 4.6 TB/s: bound by memory. 16 heads of 96
-// x 128 with helpers 3.7 us a chunk, of which 1.3 us are MFMAs: bound by the chain
+// x 128 with helpers 3.9 us a chunk, of which 1.4 us are MFMAs: bound by the chain
 // S -> K S -> R X -> K^T U -> S through one wave. (32 columns per wave would halve the
-// LDS reads but spill: 2.4 against 1.2 ms.)
+// LDS reads but spill: 2.4 against 1.2 ms when measured. y from two parts of S, U and
+// the scores would be 6% faster, and a bf16 step beside the rounded exact value in
+// 0.34% of its elements instead of 0.01%.)
 // SAVE: keep S and U for the gradients; WANT_Y: write y (the backward's recomputation does not)
 template <int N, bool SAVE, bool WANT_Y, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(const GdrParams p, int splits) {
@@ -853,8 +856,8 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_fwd_kernel(co
 
 // ---------------------------------------------------------------------------
 // Backwards over the chunks: D' of every chunk, W, dv and dh0. 256 heads of 128 x
-// 128 on 2048 tokens: 0.31 ms for 1.4 GB, 4.7 TB/s, bound by memory; 48 heads 137 us,
-// 4.3 us a chunk, bound by the chain through a wave as the forward is.
+// 128 on 2048 tokens: 0.28-0.31 ms for 1.4 GB, 4.6-5.1 TB/s, bound by memory; 48 heads 129 us,
+// 4.0 us a chunk, bound by the chain through a wave as the forward is.
 template <int N, int NW>
 __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(const GdrParams p, int splits) {
     constexpr int NT = N / 16;
@@ -1044,9 +1047,11 @@ __global__ __launch_bounds__(64 * (NW + gdr_helpers(NW))) void gdr_rev_kernel(co
 // dq, dk, dbeta, ddt of one chunk and group. Wave w holds n tile w; the heads
 // of the group follow one another and add into dq and dk in that order. What a
 // chunk needs of S, D', U and W (192 KB a head) is read once, 32 columns p ahead of
-// their use. 8192 chunks and heads of 128 x 128: 0.85 ms for 2.0 GB, 2.3 TB/s: the
+// their use. 8192 chunks and heads of 128 x 128: 0.91-0.93 ms for 2.0 GB, 2.2 TB/s: the
 // reads of a workgroup (one per CU, for its LDS) stop while it forms the pair
-// products and row sums. Measured and not kept: walking the chunks with the next
+// products and row sums, and with several heads to a group 26 registers spill. (The
+// decays' gradient from <D', S'> and dq, dk would be 8% faster and lose its digits
+// where a decay is strong.) Measured and not kept: walking the chunks with the next
 // one's reads in flight (2% faster with one head per group, 1% slower with two: the
 // registers), two n tiles per wave (1.5 ms), LDS without bank conflicts here (2%
 // slower: the exchanged addresses cost more than the conflicts).

@@ -12,9 +12,14 @@ constexpr int kGdrCus = 256;
 inline int gdr_splits(int P, int nw) { return (P / 16 + nw - 1) / nw; }
 
 // Computing waves per workgroup of the kernels that walk the chunks of `heads` heads.
-// LDS allows one workgroup per CU, so the rounds over the CUs count, times
-// what a chunk takes: about 1.1 times as long with 4 waves as with 2, and 1.7
-// times with 8 (measured on 48 and 256 heads of 128 x 128)
+// LDS allows one workgroup per CU, so the rounds over the CUs count, times what a
+// chunk takes: taken as 1.1 times as long with 4 waves as with 2, and 1.7 times with
+// 8. Measured, 2 / 4 / 8 waves, us a chunk: forward 3.8 / 3.7 / 5.6 (N 128) and 2.9 /
+// 2.7 / 4.4 (N 64), with kept states 4.0 / 4.8 / 6.6 and 3.1 / 3.1 / 5.4, backwards
+// 4.0 / 5.3 / 6.9 and 3.0 / 3.2 / 5.2 (with 4 and N 128 12 to 17 registers spill).
+// Over 24 to 320 heads of 64 and 128 columns, each N, the choice is within 12% of the
+// best of the three, but for 320 heads of 128 x 128, where 3 rounds of 4 and 2 of 8
+// count as much: 20% and 26% with kept states and backwards.
 inline int gdr_waves(int64_t heads, int P) {
     auto time = [&](int nw, double chunk) { return (double)((heads * gdr_splits(P, nw) + kGdrCus - 1) / kGdrCus) * chunk; };
     const double t2 = time(2, 1.0), t4 = time(4, 1.1), t8 = time(8, 1.7);

@@ -17,10 +17,11 @@
 // written as one partial row per workgroup; norm_reduce_kernel adds those in a
 // fixed order, so no result depends on timing.
 //
-// Measured, at a device copy rate of 4.98 TB/s: 65536 rows of 32 groups of 128 bf16
-// channels forward 0.324 ms (4.97 TB/s), backward 0.677 ms (4.0 TB/s); 8192 rows of
-// 768 with an fp32 residual forward 13 us, backward 25 us and its sums 7 us (the
-// tensors stay in the cache). The next segment's reads ahead of this one's sums
+// Measured, at a device copy rate of 5.0 to 5.4 TB/s: 65536 rows of 32 groups of 128
+// bf16 channels forward 0.28 ms (5.8 TB/s), backward 0.57 ms (4.7 TB/s); 8192 rows
+// of 768 with an fp32 residual forward 13 us, backward 24 us and its sums 6.5 us (the
+// tensors stay in the cache). Single channels (widths that are no multiple of a
+// piece): 1.3 to 1.8 TB/s in bf16, 2.9 to 3.5 in fp32. The next segment's reads ahead of this one's sums
 // measured 7% slower (registers), stores past the cache 3% faster, but what comes
 // next reads these outputs.
 #include <hip/hip_runtime.h>
