@@ -585,6 +585,100 @@ int ssm_gated_norm_bwd(const ssm_gated_norm_desc *desc, const void *dy, const vo
                        const float *weight, void *dx, void *dz, float *dweight,
                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * The gated linear recurrence. Per batch row and channel, in fp32, with
+ * r = sigmoid(rgate), i = sigmoid(igate):
+ *
+ *   a_t = exp(-rate * softplus(lam) * r_t)          0 where reset_t is set
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t     h_{-1} = h0 (or 0)
+ *   y_t = h_t * gate_t                              gate NULL: h_t
+ *
+ * A reset starts a sequence inside a row: nothing before it reaches what follows,
+ * were it NaN or infinite. rgate of minus infinity (a = 1) leaves the state as it
+ * is, for tokens that pad a row (x, igate finite); a gate of 0 in its place zeroes
+ * y. Any other NaN or infinity makes NaN or infinite what depends on it by the
+ * formulas; tokens of the same run of 8 or 16 behind which it stands, other channels
+ * and other batch rows keep their values.
+ * A row takes one workgroup of 512 work items per 64 channels (32 where channels or
+ * addresses do not allow two at a time) and chunk of 128 or 256 tokens; sizes that
+ * need 2^32 work items in a launch, counted for the smaller pieces, are refused
+ * (SSM_ERR_SHAPE) before the first.
+ */
+typedef struct {
+    int64_t batch;     /* >= 0 */
+    int64_t seqlen;    /* >= 0 */
+    int64_t dim;       /* 1..2^24 - 1 */
+    int32_t dtype;     /* of x, rgate, igate, gate, y and their gradients */
+    float rate;        /* >= 0, finite */
+    /* elements from one token's row to the next (of one batch row to the next:
+     * seqlen times that), up to 2^24 - 1; 0: dim. A row itself is dense. */
+    int64_t x_stride, rgate_stride, igate_stride, gate_stride;
+} ssm_glr_desc;
+
+/* Bytes of device workspace of the forward (0 for one chunk), and of the backward
+ * and the training pair; 0 for an invalid descriptor. */
+size_t ssm_glr_workspace_size(const ssm_glr_desc *desc);
+size_t ssm_glr_bwd_workspace_size(const ssm_glr_desc *desc);
+
+/*
+ *   x, rgate, igate, gate  (batch, seqlen, dim)  dtype; gate may be NULL
+ *   lam       (dim) fp32
+ *   h0        (batch, dim) fp32, or NULL for zeros
+ *   reset     (batch, seqlen) bytes, not 0 at a sequence's first token; or NULL
+ *   y         (batch, seqlen, dim)  dtype, dense, written
+ *   h_last    (batch, dim) fp32, written, or NULL; may equal h0 exactly
+ *   workspace ssm_glr_workspace_size(desc) bytes, 256-byte aligned; its contents on
+ *             entry do not matter and are clobbered
+ * Pointers need their element's alignment only (pairs of channels move faster).
+ * Outputs must not overlap inputs, each other or the workspace. seqlen == 0 writes
+ * h_last = h0 (or zeros). Results do not depend on timing.
+ */
+int ssm_glr_fwd(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                const float *h0, const void *gate, const uint8_t *reset, void *y, float *h_last,
+                void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of  sum dy . y + sum dh_last . h_last.
+ *   dy        (batch, seqlen, dim)  dtype, dense
+ *   dh_last   (batch, dim) fp32, or NULL (0)
+ *   dx, drgate, digate  (batch, seqlen, dim)  dtype, dense, written
+ *   dgate     the same; required with a gate, unused otherwise
+ *   dlam      (dim) fp32, written (summed over batch and time in a fixed order)
+ *   dh0       (batch, dim) fp32, written, or NULL (not wanted); may equal dh_last exactly
+ *   workspace ssm_glr_bwd_workspace_size(desc) bytes, 256-byte aligned
+ * ssm_glr_fwd_save is ssm_glr_fwd (same results) that leaves in `workspace`
+ * (ssm_glr_bwd_workspace_size bytes) the state before every 128 tokens, which
+ * ssm_glr_bwd would first recompute; ssm_glr_bwd_saved is ssm_glr_bwd reading them
+ * there. It must receive the workspace of an ssm_glr_fwd_save call with the same
+ * descriptor and inputs; nothing checks this. It clobbers the workspace's other
+ * parts only, so it may run again on the same saved contents.
+ * seqlen == 0 writes dlam = 0, dh0 = dh_last (or zeros).
+ */
+int ssm_glr_bwd(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                const float *h0, const void *gate, const uint8_t *reset, const void *dy, const float *dh_last,
+                void *dx, void *drgate, void *digate, void *dgate, float *dlam, float *dh0,
+                void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ssm_glr_fwd_save(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                     const float *h0, const void *gate, const uint8_t *reset, void *y, float *h_last,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ssm_glr_bwd_saved(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                      const float *h0, const void *gate, const uint8_t *reset, const void *dy, const float *dh_last,
+                      void *dx, void *drgate, void *digate, void *dgate, float *dlam, float *dh0,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token: desc->seqlen must be 1 (the strides are then those from one batch row
+ * to the next).
+ *   x, rgate, igate, gate  (batch, dim)  dtype; gate may be NULL
+ *   reset     (batch) bytes, or NULL
+ *   h         (batch, dim) fp32, read;  h_out the same shape, written: h itself for
+ *             an update in place, or apart from everything else
+ *   y         (batch, dim)  dtype, dense, written
+ */
+int ssm_glr_state_update(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate,
+                         const float *lam, const void *gate, const uint8_t *reset, const float *h, float *h_out,
+                         void *y, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *ssm_status_string(int status);
 

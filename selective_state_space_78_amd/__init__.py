@@ -9,7 +9,8 @@ raises.
 Names follow the C ABI: ``ssm_scan_fwd``, ``ssm_scan_fwd_noalloc``, ``ssm_scan_workspace_size``,
 ``ssm_scan_plan``, ``ssm_scan_bwd``, ``ssm_state_update``, ``ssm_ssd_fwd``,
 ``ssm_gdr_fwd``, ``ssm_gdr_bwd``, ``ssm_gdr_state_update``, ``ssm_prenorm_fwd``,
-``ssm_gated_norm_fwd``, ``ssm_status_string``.
+``ssm_gated_norm_fwd``, ``ssm_glr_fwd``, ``ssm_glr_bwd``, ``ssm_glr_state_update``,
+``ssm_status_string``.
 
 ``stream`` runs a call on a stream other than the current one. The caller orders the
 two where inputs or results cross; what the call allocates comes out of that stream's
@@ -35,7 +36,8 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_workspace_size_t
            "ssm_scan_fwd_noalloc", "ssm_gdr_workspace_size", "ssm_gdr_bwd_workspace_size", "ssm_gdr_fwd",
            "ssm_gdr_fwd_save", "ssm_gdr_bwd", "ssm_gdr_bwd_saved", "ssm_gdr_state_update", "ssm_prenorm_fwd",
            "ssm_prenorm_bwd", "ssm_prenorm_bwd_workspace_size", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
-           "ssm_gated_norm_bwd_workspace_size", "ssm_status_string")
+           "ssm_gated_norm_bwd_workspace_size", "ssm_glr_workspace_size", "ssm_glr_bwd_workspace_size", "ssm_glr_fwd",
+           "ssm_glr_fwd_save", "ssm_glr_bwd", "ssm_glr_bwd_saved", "ssm_glr_state_update", "ssm_status_string")
 
 # Fixed scratch of ssm_scan_fwd_noalloc per GPU (SSM_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -74,6 +76,12 @@ class GatedNormDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("gate_first", ctypes.c_int32), ("weight_shared", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64)]
+
+
+class GlrDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("rate", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("rgate_stride", ctypes.c_int64), ("igate_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64)]
 
 
 class ScanTuning(ctypes.Structure):
@@ -132,8 +140,10 @@ def lib() -> ctypes.CDLL:
             L.ssm_ssd_state_update.argtypes = [ctypes.POINTER(SsdDesc)] + [vp] * 10
             L.ssm_ssd_state_update.restype = ctypes.c_int
             pg, pp, pn = ctypes.POINTER(GdrDesc), ctypes.POINTER(PrenormDesc), ctypes.POINTER(GatedNormDesc)
+            pl = ctypes.POINTER(GlrDesc)
             for name, d in (("ssm_gdr_workspace_size", pg), ("ssm_gdr_bwd_workspace_size", pg),
-                            ("ssm_prenorm_bwd_workspace_size", pp), ("ssm_gated_norm_bwd_workspace_size", pn)):
+                            ("ssm_prenorm_bwd_workspace_size", pp), ("ssm_gated_norm_bwd_workspace_size", pn),
+                            ("ssm_glr_workspace_size", pl), ("ssm_glr_bwd_workspace_size", pl)):
                 getattr(L, name).argtypes = [d]
                 getattr(L, name).restype = sz
             for name, args in (("ssm_gdr_fwd", [pg] + [vp] * 10 + [sz, vp]),
@@ -144,7 +154,12 @@ def lib() -> ctypes.CDLL:
                                ("ssm_prenorm_fwd", [pp] + [vp] * 7),
                                ("ssm_prenorm_bwd", [pp] + [vp] * 11 + [sz, vp]),
                                ("ssm_gated_norm_fwd", [pn] + [vp] * 5),
-                               ("ssm_gated_norm_bwd", [pn] + [vp] * 8 + [sz, vp])):
+                               ("ssm_gated_norm_bwd", [pn] + [vp] * 8 + [sz, vp]),
+                               ("ssm_glr_fwd", [pl] + [vp] * 10 + [sz, vp]),
+                               ("ssm_glr_fwd_save", [pl] + [vp] * 10 + [sz, vp]),
+                               ("ssm_glr_bwd", [pl] + [vp] * 16 + [sz, vp]),
+                               ("ssm_glr_bwd_saved", [pl] + [vp] * 16 + [sz, vp]),
+                               ("ssm_glr_state_update", [pl] + [vp] * 10)):
                 getattr(L, name).argtypes = args
                 getattr(L, name).restype = ctypes.c_int
             L.ssm_status_string.argtypes = [ctypes.c_int]
@@ -924,3 +939,155 @@ def ssm_gated_norm_bwd(dy, x, z, weight, eps=1e-5, gate_first=False, out=None, w
     if rc != 0:
         raise SsmError(rc, "ssm_gated_norm_bwd")
     return g
+
+
+def _outputs(out, device, stream):
+    """get(name, shape, dtype, wanted): the preallocated output of that name, or a new one."""
+    o = dict(out or {})
+
+    def get(name, shape, dtype, wanted=True):
+        if not wanted:
+            return None
+        if o.get(name) is None:
+            o[name] = _empty(shape, dtype, device, stream)
+        _check(o[name], name, shape, dtype, device)
+        return o[name]
+    return get
+
+
+def _glr_desc(x, rgate, igate, lam, gate, reset, rate):
+    import torch
+    code, dev, dim = _dtype_code(x), x.device, x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    strides = [0 if t is None else _row_stride(t, n, lead, (dim,), x.dtype, dev)
+               for t, n in ((x, "x"), (rgate, "rgate"), (igate, "igate"), (gate, "gate"))]
+    _check(lam, "lam", (dim,), torch.float32, dev)
+    if reset is not None and reset.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("reset must be bool or uint8, got %s" % reset.dtype)
+    _check(reset, "reset", lead, device=dev)
+    batch, L = lead if len(lead) == 2 else (lead[0], 1)
+    return GlrDesc(batch, L, dim, code, float(rate), *strides)
+
+
+def ssm_glr_workspace_size(batch, seqlen, dim, dtype=SSM_BF16) -> int:
+    """Workspace bytes of ssm_glr_fwd."""
+    return int(lib().ssm_glr_workspace_size(ctypes.byref(GlrDesc(batch, seqlen, dim, dtype, 1.0))))
+
+
+def ssm_glr_bwd_workspace_size(batch, seqlen, dim, dtype=SSM_BF16) -> int:
+    """Workspace bytes of ssm_glr_bwd, ssm_glr_fwd_save and ssm_glr_bwd_saved."""
+    return int(lib().ssm_glr_bwd_workspace_size(ctypes.byref(GlrDesc(batch, seqlen, dim, dtype, 1.0))))
+
+
+def ssm_glr_fwd(x, rgate, igate, lam, h0=None, gate=None, reset=None, rate=8.0, y=None, h_last=None, workspace=None,
+                want_h_last=True, stream=None, _save=False):
+    """The gated linear recurrence over a sequence, on device tensors:
+    a = exp(-rate softplus(lam) sigmoid(rgate)),
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(igate_t) x_t, y_t = h_t gate_t.
+
+    x, rgate, igate, gate: (batch, L, dim) bfloat16 or float32, each of which may
+    be cut out of wider rows (one projection's output); gate None: y = h. lam:
+    (dim,) float32; h0: (batch, dim) float32; reset: (batch, L) bool, true at the
+    first token of a sequence inside a row: a_t = 0 there. An rgate of minus
+    infinity leaves the state as it is (tokens that pad a row). Outputs y
+    (batch, L, dim) and h_last (batch, dim) are allocated when not given. Returns
+    (y, h_last).
+    """
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, L, dim)")
+    desc = _glr_desc(x, rgate, igate, lam, gate, reset, rate)
+    batch, L, dim = x.shape
+    dev, f32 = x.device, torch.float32
+    _check(h0, "h0", (batch, dim), f32, dev)
+    if y is None:
+        y = _empty((batch, L, dim), x.dtype, dev, stream)
+    if h_last is None and want_h_last:
+        h_last = _empty((batch, dim), f32, dev, stream)
+    _check(y, "y", (batch, L, dim), x.dtype, dev)
+    _check(h_last, "h_last", (batch, dim), f32, dev)
+    L_ = lib()
+    name = "ssm_glr_fwd_save" if _save else "ssm_glr_fwd"
+    size = L_.ssm_glr_bwd_workspace_size if _save else L_.ssm_glr_workspace_size
+    workspace, ws_bytes = _workspace(workspace, size(ctypes.byref(desc)), dev, name, stream, _save)
+    rc = _on(dev, getattr(L_, name), ctypes.byref(desc), _ptr(x), _ptr(rgate), _ptr(igate), _ptr(lam), _ptr(h0), _ptr(gate),
+             _ptr(reset), _ptr(y), _ptr(h_last), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, name)
+    return (y, h_last, workspace) if _save else (y, h_last)
+
+
+def ssm_glr_fwd_save(x, rgate, igate, lam, h0=None, gate=None, reset=None, rate=8.0, y=None, h_last=None, workspace=None,
+                     want_h_last=True, stream=None):
+    """ssm_glr_fwd that also keeps the states that the backward starts from.
+    Returns (y, h_last, saved): ``saved`` is the workspace (uint8,
+    ssm_glr_bwd_workspace_size bytes; ``workspace`` if given) to pass unchanged to
+    ssm_glr_bwd_saved with the same inputs."""
+    return ssm_glr_fwd(x, rgate, igate, lam, h0, gate, reset, rate, y, h_last, workspace, want_h_last, stream, _save=True)
+
+
+def ssm_glr_bwd(x, rgate, igate, lam, dy, h0=None, dh_last=None, gate=None, reset=None, rate=8.0, workspace=None,
+                want_dh0=True, out=None, stream=None, _saved=False):
+    """Backward of ssm_glr_fwd on device tensors.
+
+    Inputs as ssm_glr_fwd, plus dy (batch, L, dim) of x's dtype and an optional
+    dh_last (batch, dim) float32. Returns a dict with dx, drgate, digate, dgate
+    (with a gate; x's dtype), dlam (dim,) and dh0 (batch, dim) (when ``want_dh0``),
+    float32. ``out`` may hold preallocated outputs (dh0 may be dh_last itself).
+    """
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, L, dim)")
+    desc = _glr_desc(x, rgate, igate, lam, gate, reset, rate)
+    batch, L, dim = x.shape
+    dev, t, f32 = x.device, x.dtype, torch.float32
+    _check(h0, "h0", (batch, dim), f32, dev)
+    _check(dy, "dy", (batch, L, dim), t, dev)
+    _check(dh_last, "dh_last", (batch, dim), f32, dev)
+    get = _outputs(out, dev, stream)
+    g = dict(dx=get("dx", (batch, L, dim), t), drgate=get("drgate", (batch, L, dim), t),
+             digate=get("digate", (batch, L, dim), t), dgate=get("dgate", (batch, L, dim), t, gate is not None),
+             dlam=get("dlam", (dim,), f32), dh0=get("dh0", (batch, dim), f32, want_dh0))
+    L_ = lib()
+    name = "ssm_glr_bwd_saved" if _saved else "ssm_glr_bwd"
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_glr_bwd_workspace_size(ctypes.byref(desc)), dev, name, stream)
+    rc = _on(dev, getattr(L_, name), ctypes.byref(desc), _ptr(x), _ptr(rgate), _ptr(igate), _ptr(lam), _ptr(h0), _ptr(gate),
+             _ptr(reset), _ptr(dy), _ptr(dh_last), _ptr(g["dx"]), _ptr(g["drgate"]), _ptr(g["digate"]), _ptr(g["dgate"]),
+             _ptr(g["dlam"]), _ptr(g["dh0"]), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, name)
+    return g
+
+
+def ssm_glr_bwd_saved(x, rgate, igate, lam, dy, saved, h0=None, dh_last=None, gate=None, reset=None, rate=8.0,
+                      want_dh0=True, out=None, stream=None):
+    """ssm_glr_bwd that reads the states that an ssm_glr_fwd_save call with the same
+    inputs left in ``saved`` (its returned workspace). Arguments and results as
+    ssm_glr_bwd."""
+    if saved is None and x.numel() > 0:
+        raise ValueError("ssm_glr_bwd_saved needs the workspace of an ssm_glr_fwd_save call")
+    return ssm_glr_bwd(x, rgate, igate, lam, dy, h0, dh_last, gate, reset, rate, saved, want_dh0, out, stream, _saved=True)
+
+
+def ssm_glr_state_update(x, rgate, igate, lam, h, y=None, h_out=None, gate=None, reset=None, rate=8.0, stream=None):
+    """One token of the gated linear recurrence: x, rgate, igate, gate (batch, dim),
+    lam (dim,) float32, reset (batch,) bool. h (batch, dim) float32 is updated in
+    place, or left and the new state written to ``h_out``. Returns y (batch, dim),
+    allocated when not given."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be (batch, dim)")
+    desc = _glr_desc(x, rgate, igate, lam, gate, reset, rate)
+    dev = x.device
+    _check(h, "h", x.shape, torch.float32, dev)
+    if h_out is None:
+        h_out = h
+    _check(h_out, "h_out", x.shape, torch.float32, dev)
+    if y is None:
+        y = _empty(x.shape, x.dtype, dev, stream)
+    _check(y, "y", x.shape, x.dtype, dev)
+    rc = _on(dev, lib().ssm_glr_state_update, ctypes.byref(desc), _ptr(x), _ptr(rgate), _ptr(igate), _ptr(lam), _ptr(gate),
+             _ptr(reset), _ptr(h), _ptr(h_out), _ptr(y), _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_glr_state_update")
+    return y

@@ -1,0 +1,994 @@
+// The gated linear recurrence (include/ssm_scan.h states it): per channel,
+//
+//   s = rate softplus(lam) sigmoid(rgate),  a = exp(-s),  m = sqrt(1 - a^2)
+//   h_t = a_t h_{t-1} + m_t sigmoid(igate_t) x_t,   y_t = h_t gate_t
+//
+// A run of tokens maps the state before it to the state behind it by h -> P h + H
+// with P the product of its decays, and maps compose. A workgroup takes one chunk of
+// tokens of a tile of channels: 16 streams of TT tokens, two to a wave, each lane
+// VEC channels. Every lane forms its tokens' a and b = m i x once, into registers,
+// and its stream's map; the streams' maps meet in LDS, the chunk's in device memory,
+// and with the state before its stream a lane runs h = a h + b over its registers.
+// Inputs are read once and outputs written once, however few the channels.
+//
+// Chunks of one sequence are joined by looking back: a workgroup publishes its
+// chunk's map, then takes the state behind the nearest chunk whose state is known and
+// applies the maps of the chunks between in their order of time, the same operations
+// on the same values as the one-by-one chain; results do not depend on timing.
+// Workgroups take their chunk from a counter, in order of time, so that a workgroup
+// waits only for ones that have started, and every wait ends. What is published is
+// one word that is valid by itself (all bits set: not there yet), stored and read by
+// relaxed device-scope atomics: no fence, no cache write-back.
+//
+// Backward: g_t = dy_t gate_t + a_{t+1} g_{t+1}, by the same maps from the end, with
+// the states recomputed from the ones that the forward kept every 128 tokens. With
+// w = a (a i x s / m - s h_{t-1}):  dx = g m i, digate = g m i x (1 - i), drgate =
+// g w (1 - r), dlam = sigmoid(lam) / softplus(lam) sum g w. s / m goes to 0 with s,
+// so an open recurrence gate (a = 1) has gradients.
+//
+// 1 - a is a polynomial in s up to 1/2 and a its difference from 1: decays near 1 are
+// then rounded once, without the exponential's own error, which would add up over
+// 1 / (1 - a) tokens, and m keeps its digits.
+//
+// A reset (a = 0 whatever the gate, m = 1) is carried as a decay of -0: it takes
+// nothing of the state before it, were that infinite.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssm_scan.h"
+#include "abi_util.hpp"
+#include "matrix_ops.hpp"
+#include "scan_kernels.hpp"
+
+namespace {
+
+using namespace ssm_detail;
+
+constexpr int kThreads = 512, kStreams = 16, kRow = 32;   // lanes to a token's row of a tile
+constexpr int kKeep = 128;                                // tokens from one kept state to the next
+constexpr int kBack = 8;                                  // chunks that are looked back over
+constexpr int64_t kMaxStride = (1 << 24) - 1;             // lane offsets stay in 32 bits
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct GlrParams {
+    const void *x, *rg, *ig, *gate, *dy;
+    const float *lam, *h0, *dh_last;
+    const uint8_t *reset;
+    void *y, *dx, *drg, *dig, *dgate;
+    float *h_last, *dh0, *dlam;
+    float *keep, *part;          // (batch, kept, dim) states; (batch, chunks, dim) sums for dlam
+    unsigned long long *map;     // (chunk, batch, dim) P and H of a chunk
+    uint32_t *state;             // (chunk, batch, dim) the state behind a chunk
+    uint32_t *ticket;            // NULL with one chunk
+    int64_t L, dim, xs, rs, is, gs;
+    int batch, chunks, tiles, kept;
+    float rate;
+};
+
+template <typename T, int VEC> struct Raw;
+template <> struct Raw<uint16_t, 1> { typedef uint16_t type; };
+template <> struct Raw<uint16_t, 2> { typedef uint32_t type; };
+template <> struct Raw<float, 1> { typedef float type; };
+template <> struct Raw<float, 2> { typedef float2 type; };
+
+template <int VEC> __device__ __forceinline__ void widen(uint16_t r, float (&v)[VEC]) { v[0] = ssd_bf(r); }
+__device__ __forceinline__ void widen(uint32_t r, float (&v)[2]) {
+    v[0] = __uint_as_float(r << 16);
+    v[1] = __uint_as_float(r & 0xffff0000u);
+}
+template <int VEC> __device__ __forceinline__ void widen(float r, float (&v)[VEC]) { v[0] = r; }
+__device__ __forceinline__ void widen(float2 r, float (&v)[2]) { v[0] = r.x; v[1] = r.y; }
+
+__device__ __forceinline__ void narrow(const float (&v)[1], uint16_t &r) { r = ssd_to_bf(v[0]); }
+__device__ __forceinline__ void narrow(const float (&v)[2], uint32_t &r) { r = ssd_pack(v[0], v[1]); }
+__device__ __forceinline__ void narrow(const float (&v)[1], float &r) { r = v[0]; }
+__device__ __forceinline__ void narrow(const float (&v)[2], float2 &r) { r = make_float2(v[0], v[1]); }
+
+template <int VEC> __device__ __forceinline__ void ldf(const float *p, float (&v)[VEC]) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) v[c] = p[c];
+}
+template <int VEC> __device__ __forceinline__ void stf(float *p, const float (&v)[VEC]) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) p[c] = v[c];
+}
+
+__device__ __forceinline__ float soft_plus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))) + (v != v ? v : 0.0f); }
+
+// sigmoid; e = exp(-v) (infinite where the sigmoid is 0)
+__device__ __forceinline__ float sigm(float v, float &e) {
+    e = __builtin_amdgcn_exp2f(v * -kLog2e);
+    return __builtin_amdgcn_rcpf(1.0f + e);
+}
+// 1 - sigmoid to its own digits
+__device__ __forceinline__ float one_minus(float sig, float e) { return e > 1.0f ? 1.0f - sig : e * sig; }
+
+// a = exp(-s) and 1 - a^2, s >= 0. 1 - a = s - s^2 / 2 + ..., fitted up to s = 1/2 to 1.5e-9 of itself.
+__device__ __forceinline__ float decay(float s, float &w) {
+    float q = fmaf(s, -0.0011259224265813828f, 0.008193295449018478f);
+    q = fmaf(s, q, -0.04163204878568649f);
+    q = fmaf(s, q, 0.16666288673877716f);
+    q = fmaf(s, q, -0.49999985098838806f);
+    const float near = fmaf(s, s * q, s), ex = __builtin_amdgcn_exp2f(s * -kLog2e);
+    const bool small = s < 0.5f;
+    const float em = small ? near : 1.0f - ex, a = small ? 1.0f - near : ex;
+    w = fmaf(em, a, em);
+    return a;
+}
+
+__device__ __forceinline__ bool is_reset(float P) { return __float_as_uint(P) == 0x80000000u; }
+
+// The state behind a run from the one before it
+template <bool RESET> __device__ __forceinline__ float behind(float P, float H, float h) {
+    const float v = fmaf(P, h, H);
+    if constexpr (RESET) return is_reset(P) ? H : v;
+    else return v;
+}
+// The decay of two runs
+template <bool RESET> __device__ __forceinline__ float both(float P, float Q) {
+    if constexpr (RESET) return is_reset(P) || is_reset(Q) ? -0.0f : P * Q;
+    else return P * Q;
+}
+
+constexpr uint32_t kNone = 0xffffffffu;
+__device__ __forceinline__ uint32_t word_of(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u == kNone ? 0x7fc00000u : u;
+}
+
+template <typename W> __device__ __forceinline__ W peek(const W *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W> __device__ __forceinline__ void post(W *p, W v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Streams' maps of a chunk, and the state before it
+template <int VEC> struct Shared {
+    float2 map[kStreams][kRow * VEC];
+    float start[kRow * VEC];
+    float rate[kRow * VEC];
+    uint32_t tile;
+};
+
+// The chunk's place: tiles in order of time (of the direction), batch rows and channels within
+struct Place {
+    int k, b;         // chunk in order of the direction, batch row
+    int64_t c0;       // first channel
+};
+
+template <int VEC> __device__ __forceinline__ Place place(const GlrParams &p, Shared<VEC> &sh) {
+    uint32_t t = blockIdx.x;
+    if (p.ticket) {
+        if (threadIdx.x == 0) sh.tile = atomicAdd(p.ticket, 1u);
+        __syncthreads();
+        t = __builtin_amdgcn_readfirstlane(sh.tile);
+    }
+    const uint32_t per = (uint32_t)p.batch * (uint32_t)p.tiles;
+    Place q;
+    q.k = (int)(t / per);
+    t -= (uint32_t)q.k * per;
+    q.b = (int)(t / (uint32_t)p.tiles);
+    q.c0 = (int64_t)(t - (uint32_t)q.b * (uint32_t)p.tiles) * (kRow * VEC);
+    return q;
+}
+
+// Wave 0: the chunk's map from its streams', in order of the direction; the state
+// before the chunk by looking back; the state behind it published. `first` is the
+// state before the sequence. All 64 lanes take part, the upper half as copies.
+template <int VEC, bool RESET, bool REV>
+__device__ __forceinline__ void join_chunks(const GlrParams &p, Shared<VEC> &sh, const Place &at, const float (&first)[VEC],
+                                            int lane, int64_t ch, bool ok) {
+    const int l = (lane & (kRow - 1)) * VEC;
+    const bool write = ok && lane < kRow;
+    float P[VEC], H[VEC], h[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) { P[c] = 1.0f; H[c] = 0.0f; }
+    const bool last = at.k == p.chunks - 1;
+    if (!last) {
+#pragma unroll 4
+        for (int s = 0; s < kStreams; ++s)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                const float2 m = sh.map[REV ? kStreams - 1 - s : s][l + c];
+                H[c] = behind<RESET>(m.x, m.y, H[c]);
+                P[c] = both<RESET>(P[c], m.x);
+            }
+    }
+    const int64_t row = (int64_t)p.batch * p.dim;
+    const int64_t mine = ((int64_t)at.k * p.batch + at.b) * p.dim + ch;
+    if (at.k == 0) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) h[c] = first[c];
+    } else {
+        float bp[kBack][VEC], bh[kBack][VEC];
+        int found = -1;
+        bool published = last;
+#pragma unroll
+        for (int w = 0; w < kBack; ++w) {
+            if (found >= 0) continue;
+            const int64_t there = mine - (w + 1) * row;      // not reached before chunk 0, whose state comes first
+            for (;;) {
+                uint32_t s[VEC];
+                bool has = true;
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    s[c] = peek(p.state + there + c);
+                    has = has && s[c] != kNone;
+                }
+                if (__all(has)) {
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) h[c] = __uint_as_float(s[c]);
+                    found = w;
+                    break;
+                }
+                if (!published) {
+                    if (write)
+#pragma unroll
+                        for (int c = 0; c < VEC; ++c)
+                            post(p.map + mine + c, (unsigned long long)word_of(P[c]) | ((unsigned long long)word_of(H[c]) << 32));
+                    published = true;
+                }
+                // chunk 0 publishes no map: its state is all that there is to wait for
+                if (w < kBack - 1 && at.k - 1 - w > 0) {
+                    unsigned long long m[VEC];
+                    has = true;
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) {
+                        m[c] = peek(p.map + there + c);
+                        has = has && m[c] != ~0ull;
+                    }
+                    if (__all(has)) {
+#pragma unroll
+                        for (int c = 0; c < VEC; ++c) {
+                            bp[w][c] = __uint_as_float((uint32_t)m[c]);
+                            bh[w][c] = __uint_as_float((uint32_t)(m[c] >> 32));
+                        }
+                        break;
+                    }
+                }
+                __builtin_amdgcn_s_sleep(1);
+            }
+        }
+#pragma unroll
+        for (int w = kBack - 1; w >= 0; --w)
+            if (w < found)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(bp[w][c], bh[w][c], h[c]);
+    }
+    if (!last && write)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) post(p.state + mine + c, word_of(behind<RESET>(P[c], H[c], h[c])));
+    if (lane < kRow)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) sh.start[l + c] = h[c];
+}
+
+// The state before a stream, in order of the direction
+template <int VEC, bool RESET, bool REV>
+__device__ __forceinline__ void stream_start(const Shared<VEC> &sh, int wave, int half, int l, float (&h)[VEC]) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) h[c] = sh.start[l + c];
+    if constexpr (!REV) {
+        for (int s = 0; s < 2 * wave; ++s)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(sh.map[s][l + c].x, sh.map[s][l + c].y, h[c]);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float v = behind<RESET>(sh.map[2 * wave][l + c].x, sh.map[2 * wave][l + c].y, h[c]);
+            h[c] = half ? v : h[c];
+        }
+    } else {
+        for (int s = kStreams - 1; s > 2 * wave + 1; --s)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(sh.map[s][l + c].x, sh.map[s][l + c].y, h[c]);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float v = behind<RESET>(sh.map[2 * wave + 1][l + c].x, sh.map[2 * wave + 1][l + c].y, h[c]);
+            h[c] = half ? h[c] : v;
+        }
+    }
+}
+
+// One token's piece of a lane. Whole chunks: a base that is the same for the wave and
+// a lane offset of 32 bits; in the last, ragged one rows past the end read the last row.
+template <typename R, int TT>
+__device__ __forceinline__ void rows(const void *base, int64_t row0, int64_t stride, uint32_t half_rows, int64_t ch, int esz,
+                                     bool whole, int64_t left, R (&out)[TT]) {
+    const char *b = static_cast<const char *>(base) + row0 * stride * esz;
+    if (whole) {
+        const uint32_t off = (half_rows * (uint32_t)stride + (uint32_t)ch) * (uint32_t)esz;
+        const int64_t step = stride * esz;
+#pragma unroll
+        for (int j = 0; j < TT; ++j) out[j] = *reinterpret_cast<const R *>(b + j * step + off);
+    } else {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int64_t r = min((int64_t)half_rows + j, left - 1);
+            out[j] = *reinterpret_cast<const R *>(b + (r * stride + ch) * esz);
+        }
+    }
+}
+
+// Forward: TT tokens to a stream. y NULL: the kept states and h_last alone.
+template <typename T, int VEC, int TT, bool RESET>
+__global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
+    typedef typename Raw<T, VEC>::type R;
+    constexpr int CT = kStreams * TT;
+    __shared__ Shared<VEC> sh;
+    const Place at = place<VEC>(p, sh);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+    const int l = (lane & (kRow - 1)) * VEC;
+    const bool ok = at.c0 + l < p.dim;
+    const int64_t ch = ok ? at.c0 + l : p.dim - VEC;
+    const int64_t t0 = (int64_t)at.k * CT + wave * 2 * TT;            // the wave's first token
+    const bool whole = (int64_t)at.k * CT + CT <= p.L;
+    const int64_t left = p.L - t0;                                    // tokens from there to the end
+    const int64_t row0 = (int64_t)at.b * p.L + (left > 0 ? t0 : p.L - 1);
+    const int64_t lf = left > 0 ? left : 1;
+    const uint32_t hr = half * TT;
+
+    R rx[TT], rr[TT], ri[TT];
+    rows<R, TT>(p.rg, row0, p.rs, hr, ch, sizeof(T), whole, lf, rr);
+    rows<R, TT>(p.ig, row0, p.is, hr, ch, sizeof(T), whole, lf, ri);
+    rows<R, TT>(p.x, row0, p.xs, hr, ch, sizeof(T), whole, lf, rx);
+    if (threadIdx.x < kRow * VEC) sh.rate[threadIdx.x] = p.rate * soft_plus(p.lam[min(at.c0 + (int64_t)threadIdx.x, p.dim - 1)]);
+    __syncthreads();
+    float k[VEC];
+    ldf<VEC>(sh.rate + l, k);
+    uint32_t first = 0;      // bit j: token j starts a sequence
+    if constexpr (RESET) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int64_t r = min((int64_t)hr + j, lf - 1);
+            first |= (p.reset[row0 + r] ? 1u : 0u) << j;
+        }
+    }
+    float a[TT][VEC], b[TT][VEC], P[VEC], H[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) { P[c] = 1.0f; H[c] = 0.0f; }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        float x[VEC], r[VEC], i[VEC];
+        widen(rx[j], x);
+        widen(rr[j], r);
+        widen(ri[j], i);
+        const bool in = whole || (int64_t)hr + j < left;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            float e, w;
+            const float s = k[c] * sigm(r[c], e);
+            a[j][c] = decay(s, w);
+            float m = __builtin_amdgcn_sqrtf(w);
+            if constexpr (RESET) {
+                if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; }
+            }
+            b[j][c] = m * sigm(i[c], e) * x[c];
+            if (!in) { a[j][c] = 1.0f; b[j][c] = 0.0f; }
+            H[c] = behind<RESET>(a[j][c], b[j][c], H[c]);
+            P[c] = both<RESET>(P[c], a[j][c]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) sh.map[2 * wave + half][l + c] = make_float2(P[c], H[c]);
+    __syncthreads();
+    const int64_t bd = (int64_t)at.b * p.dim + ch;
+    if (wave == 0) {
+        float h0[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) h0[c] = p.h0 ? p.h0[bd + c] : 0.0f;
+        join_chunks<VEC, RESET, false>(p, sh, at, h0, lane, ch, ok);
+    }
+    __syncthreads();
+    float h[VEC];
+    stream_start<VEC, RESET, false>(sh, wave, half, l, h);
+    if (!ok) return;
+    if (p.keep) {
+        const int64_t t = t0 + hr;
+        if (t % kKeep == 0 && t < p.L) stf<VEC>(p.keep + ((int64_t)at.b * p.kept + t / kKeep) * p.dim + ch, h);
+    }
+    if (p.y) {
+        R rg[TT];
+        if (p.gate) rows<R, TT>(p.gate, row0, p.gs, hr, ch, sizeof(T), whole, lf, rg);
+        char *out = static_cast<char *>(p.y) + row0 * p.dim * (int64_t)sizeof(T);
+        const uint32_t off = (hr * (uint32_t)p.dim + (uint32_t)ch) * (uint32_t)sizeof(T);
+        const int64_t step = p.dim * (int64_t)sizeof(T);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            float v[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[c] = h[c] = behind<RESET>(a[j][c], b[j][c], h[c]);
+            if (p.gate) {
+                float g[VEC];
+                widen(rg[j], g);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) v[c] *= g[c];
+            }
+            R o;
+            narrow(v, o);
+            if (whole || (int64_t)hr + j < left) *reinterpret_cast<R *>(out + j * step + off) = o;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(a[j][c], b[j][c], h[c]);
+    }
+    // tokens past the end leave the state as it is
+    if (p.h_last && at.k == p.chunks - 1 && 2 * wave + half == kStreams - 1) stf<VEC>(p.h_last + bd, h);
+}
+
+// Backward: chunks of kKeep tokens from the end.
+constexpr int kBT = kKeep / kStreams;
+
+template <typename T, int VEC, bool RESET, bool GATE>
+__global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
+    typedef typename Raw<T, VEC>::type R;
+    constexpr int TT = kBT, CT = kStreams * TT;
+    __shared__ Shared<VEC> sh;
+    __shared__ float sum[kStreams][kRow * VEC];
+    const Place at = place<VEC>(p, sh);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
+    const int l = (lane & (kRow - 1)) * VEC;
+    const int chunk = p.chunks - 1 - at.k;
+    const bool ok = at.c0 + l < p.dim;
+    const int64_t ch = ok ? at.c0 + l : p.dim - VEC;
+    const int64_t t0 = (int64_t)chunk * CT + wave * 2 * TT;
+    const bool whole = (int64_t)chunk * CT + CT <= p.L;
+    const int64_t left = p.L - t0;
+    const int64_t row0 = (int64_t)at.b * p.L + (left > 0 ? t0 : p.L - 1);
+    const int64_t lf = left > 0 ? left : 1;
+    const uint32_t hr = half * TT;
+
+    R rx[TT], rr[TT], ri[TT], rdy[TT], rga[TT];
+    rows<R, TT>(p.rg, row0, p.rs, hr, ch, sizeof(T), whole, lf, rr);
+    rows<R, TT>(p.ig, row0, p.is, hr, ch, sizeof(T), whole, lf, ri);
+    rows<R, TT>(p.x, row0, p.xs, hr, ch, sizeof(T), whole, lf, rx);
+    rows<R, TT>(p.dy, row0, p.dim, hr, ch, sizeof(T), whole, lf, rdy);
+    if constexpr (GATE) rows<R, TT>(p.gate, row0, p.gs, hr, ch, sizeof(T), whole, lf, rga);
+    if (threadIdx.x < kRow * VEC) sh.rate[threadIdx.x] = p.rate * soft_plus(p.lam[min(at.c0 + (int64_t)threadIdx.x, p.dim - 1)]);
+    __syncthreads();
+    float k[VEC];
+    ldf<VEC>(sh.rate + l, k);
+    uint32_t first = 0;
+    if constexpr (RESET) {
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int64_t r = min((int64_t)hr + j, lf - 1);
+            first |= (p.reset[row0 + r] ? 1u : 0u) << j;
+        }
+    }
+    // per token: a; b, then g's factor of digate; m i; 1 - i; 1 - r; s, then w; a i x s / m; dy gate
+    float a[TT][VEC], b[TT][VEC], mi[TT][VEC], oi[TT][VEC], orr[TT][VEC], sw[TT][VEC], u[TT][VEC], up[TT][VEC];
+    float P[VEC], H[VEC], G[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) { P[c] = 1.0f; H[c] = 0.0f; }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        float x[VEC], r[VEC], i[VEC], dy[VEC];
+        widen(rx[j], x);
+        widen(rr[j], r);
+        widen(ri[j], i);
+        widen(rdy[j], dy);
+        if constexpr (GATE) {
+            float ga[VEC];
+            widen(rga[j], ga);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) dy[c] *= ga[c];
+        }
+        const bool in = whole || (int64_t)hr + j < left;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            float er, ei, w;
+            const float sr = sigm(r[c], er), si = sigm(i[c], ei);
+            float s = k[c] * sr;
+            a[j][c] = decay(s, w);
+            s = fminf(s, 1e4f);                                // a is 0 there
+            const float inv = __builtin_amdgcn_rsqf(w);
+            const bool still = w < 1.17549435e-38f;            // a gate that lets nothing in or out
+            float m = still ? 0.0f : w * inv;
+            const float q = still ? 0.0f : s * inv;
+            const float ix = si * x[c];
+            u[j][c] = a[j][c] * ix * q;
+            if constexpr (RESET) {
+                if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; u[j][c] = 0.0f; s = 0.0f; }
+            }
+            b[j][c] = m * ix;
+            mi[j][c] = m * si;
+            oi[j][c] = one_minus(si, ei);
+            orr[j][c] = one_minus(sr, er);
+            sw[j][c] = s;
+            up[j][c] = dy[c];
+            if (!in) { a[j][c] = 1.0f; b[j][c] = 0.0f; up[j][c] = 0.0f; }
+            H[c] = behind<RESET>(a[j][c], b[j][c], H[c]);
+            P[c] = both<RESET>(P[c], a[j][c]);
+        }
+    }
+    // what flows out of the stream towards the past, of what flows in at its end
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) G[c] = 0.0f;
+#pragma unroll
+    for (int j = TT - 1; j >= 0; --j)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float g = up[j][c] + G[c];
+            G[c] = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * g;
+        }
+    // the states: from the kept one, in the chunk alone
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) sh.map[2 * wave + half][l + c] = make_float2(P[c], H[c]);
+    const int64_t bd = (int64_t)at.b * p.dim + ch;
+    if (wave == 0 && lane < kRow) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            sh.start[l + c] = chunk == 0 ? (p.h0 ? p.h0[bd + c] : 0.0f) : p.keep[((int64_t)at.b * p.kept + chunk) * p.dim + ch + c];
+    }
+    __syncthreads();
+    float h[VEC];
+    stream_start<VEC, RESET, false>(sh, wave, half, l, h);
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) sh.map[2 * wave + half][l + c] = make_float2(P[c], G[c]);
+    __syncthreads();
+    if (wave == 0) {
+        float d[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) d[c] = p.dh_last ? p.dh_last[bd + c] : 0.0f;
+        join_chunks<VEC, RESET, true>(p, sh, at, d, lane, ch, ok);
+    }
+    const uint32_t off = (hr * (uint32_t)p.dim + (uint32_t)ch) * (uint32_t)sizeof(T);
+    const int64_t step = p.dim * (int64_t)sizeof(T), base = row0 * step;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        float dg[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            // a reset reads nothing of the state before it: its s and u are 0
+            const float t = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * fmaf(-sw[j][c], h[c], u[j][c]);
+            h[c] = behind<RESET>(a[j][c], b[j][c], h[c]);
+            sw[j][c] = t;
+            b[j][c] *= oi[j][c];
+        }
+        if constexpr (GATE) {
+            float dy[VEC];
+            widen(rdy[j], dy);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) dg[c] = dy[c] * h[c];
+            R o;
+            narrow(dg, o);
+            if (ok && (whole || (int64_t)hr + j < left))
+                *reinterpret_cast<R *>(static_cast<char *>(p.dgate) + base + j * step + off) = o;
+        }
+    }
+    __syncthreads();
+    float c_in[VEC], dl[VEC];
+    stream_start<VEC, RESET, true>(sh, wave, half, l, c_in);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) dl[c] = 0.0f;
+#pragma unroll
+    for (int j = TT - 1; j >= 0; --j) {
+        const bool in = whole || (int64_t)hr + j < left;
+        float vx[VEC], vr[VEC], vi[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            const float g = up[j][c] + c_in[c];
+            c_in[c] = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * g;
+            vx[c] = g * mi[j][c];
+            vi[c] = g * b[j][c];
+            const float t = g * sw[j][c];
+            vr[c] = t * orr[j][c];
+            dl[c] += in ? t : 0.0f;
+        }
+        R ox, orv, oiv;
+        narrow(vx, ox);
+        narrow(vr, orv);
+        narrow(vi, oiv);
+        if (ok && in) {
+            const int64_t o = base + j * step;
+            *reinterpret_cast<R *>(static_cast<char *>(p.dx) + o + off) = ox;
+            *reinterpret_cast<R *>(static_cast<char *>(p.drg) + o + off) = orv;
+            *reinterpret_cast<R *>(static_cast<char *>(p.dig) + o + off) = oiv;
+        }
+    }
+    if (p.dh0 && chunk == 0 && wave == 0 && half == 0 && ok) stf<VEC>(p.dh0 + bd, c_in);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) sum[2 * wave + half][l + c] = dl[c];
+    __syncthreads();
+    if (threadIdx.x < kRow * VEC && at.c0 + (int64_t)threadIdx.x < p.dim) {
+        float v = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kStreams; ++s) v += sum[s][threadIdx.x];
+        p.part[((int64_t)at.b * p.chunks + chunk) * p.dim + at.c0 + threadIdx.x] = v;
+    }
+}
+
+// dlam from the chunks' sums, in 64 bits and a fixed order: 16 channels by 64 runs of rows
+constexpr int kSumCols = 16, kSumRuns = 64;
+__global__ __launch_bounds__(kSumCols * kSumRuns) void glr_sum_kernel(const float *part, int64_t n, int64_t dim,
+                                                                     const float *lam, float *dlam) {
+    __shared__ double s[kSumRuns][kSumCols];
+    const int l = threadIdx.x % kSumCols, run = threadIdx.x / kSumCols;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + l;
+    double v = 0.0;
+    if (c < dim)
+        for (int64_t k = run; k < n; k += kSumRuns) v += part[k * dim + c];
+    s[run][l] = v;
+    for (int o = kSumRuns / 2; o >= 1; o >>= 1) {
+        __syncthreads();
+        if (run < o) s[run][l] += s[run + o][l];
+    }
+    if (run == 0 && c < dim) {
+        // sigmoid(lam) / softplus(lam), 1 towards minus infinity
+        const float x = lam[c], e = expf(-fabsf(x)), sig = (x >= 0.0f ? 1.0f : e) / (1.0f + e), sp = soft_plus(x);
+        dlam[c] = (float)(s[0][l] * (sp < 1e-30f ? 1.0 : (double)sig / (double)sp));
+    }
+}
+
+// Counter to 0, what chunks publish to "not there"
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint4 *at, int64_t n) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t v = k < 16 ? 0u : kNone;
+    if (k < n) at[k] = uint4{v, v, v, v};
+}
+
+// One token. A lane takes VEC channels of `rows` batch rows, so that softplus(lam) is formed once for them.
+template <typename T, int VEC>
+__global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p, const float *h, float *h_out, int rows_per) {
+    typedef typename Raw<T, VEC>::type R;
+    const int64_t ch = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
+    if (ch >= p.dim) return;
+    float k[VEC];
+    ldf<VEC>(p.lam + ch, k);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) k[c] = p.rate * soft_plus(k[c]);
+    const int64_t b1 = min((int64_t)(blockIdx.y + 1) * rows_per, (int64_t)p.batch);
+    for (int64_t b = (int64_t)blockIdx.y * rows_per; b < b1; ++b) {
+        const T *px = static_cast<const T *>(p.x), *pr = static_cast<const T *>(p.rg), *pi = static_cast<const T *>(p.ig);
+        float x[VEC], r[VEC], i[VEC], g[VEC], s0[VEC], v[VEC];
+        widen(*reinterpret_cast<const R *>(px + b * p.xs + ch), x);
+        widen(*reinterpret_cast<const R *>(pr + b * p.rs + ch), r);
+        widen(*reinterpret_cast<const R *>(pi + b * p.is + ch), i);
+        if (p.gate) widen(*reinterpret_cast<const R *>(static_cast<const T *>(p.gate) + b * p.gs + ch), g);
+        ldf<VEC>(h + b * p.dim + ch, s0);
+        const bool first = p.reset && p.reset[b];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            float e, w;
+            const float a = decay(k[c] * sigm(r[c], e), w);
+            const float ix = sigm(i[c], e) * x[c];
+            s0[c] = first ? ix : fmaf(a, s0[c], __builtin_amdgcn_sqrtf(w) * ix);
+            v[c] = p.gate ? s0[c] * g[c] : s0[c];
+        }
+        stf<VEC>(h_out + b * p.dim + ch, s0);
+        R o;
+        narrow(v, o);
+        *reinterpret_cast<R *>(static_cast<T *>(p.y) + b * p.dim + ch) = o;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launching
+
+int fwd_tokens(int dtype) { return dtype == SSM_BF16 ? 16 * kStreams : 8 * kStreams; }
+int64_t chunks_of(int64_t L, int tokens) { return (L + tokens - 1) / tokens; }
+
+// Where what chunks publish lies in a workspace: the counter, the maps, the states
+struct Layout {
+    size_t keep, part, sync, map, state, total;
+};
+
+// What both directions publish shares one place: the larger of the two, the backward's
+Layout layout(const ssm_glr_desc &d, bool bwd) {
+    const size_t bd = (size_t)d.batch * (size_t)d.dim;
+    const size_t kept = (size_t)chunks_of(d.seqlen, kKeep), n = bwd ? kept : (size_t)chunks_of(d.seqlen, fwd_tokens(d.dtype));
+    Layout l{};
+    if (bwd) {
+        l.part = align256(kept * bd * 4);
+        l.sync = l.part + align256(kept * bd * 4);
+    }
+    l.map = l.sync + 256;
+    l.state = l.map + align256(n * bd * 8);
+    l.total = n > 1 ? l.state + align256(n * bd * 4) : l.sync;
+    return l;
+}
+
+int64_t tiles_of(int64_t dim, int vec) { return (dim + kRow * vec - 1) / (kRow * vec); }
+
+size_t esize(int t) { return t == SSM_BF16 ? 2 : 4; }
+
+int check(const ssm_glr_desc *desc) {
+    if (desc == nullptr) return SSM_ERR_NULL;
+    const ssm_glr_desc &d = *desc;
+    if (d.batch < 0 || d.seqlen < 0 || d.dim < 1 || d.dim > kMaxStride) return SSM_ERR_SHAPE;
+    int64_t n = 0, m;
+    const int64_t strides[] = {d.x_stride, d.rgate_stride, d.igate_stride, d.gate_stride};
+    for (int64_t s : strides) {
+        if (s < 0 || (s != 0 && s < d.dim) || s > kMaxStride) return SSM_ERR_SHAPE;
+        n = std::max(n, s);
+    }
+    if (!mul_ok(d.batch, d.seqlen, &m) || !mul_ok(m, std::max(n, d.dim), &n) || n > INT64_MAX / 64) return SSM_ERR_SHAPE;
+    if (d.batch > INT32_MAX || d.seqlen > ((int64_t)1 << 37)) return SSM_ERR_SHAPE;
+    if (d.dtype != SSM_F32 && d.dtype != SSM_BF16) return SSM_ERR_DTYPE;
+    if (!(d.rate >= 0.0f) || d.rate > 3e38f) return SSM_ERR_UNSUPPORTED;
+    // every launch below 2^32 work items, with the narrowest pieces
+    if (!mul_ok(d.batch, tiles_of(d.dim, 1), &n) || !mul_ok(n, std::max<int64_t>(1, chunks_of(d.seqlen, kKeep)), &n) ||
+        !grid_ok(n, kThreads))
+        return SSM_ERR_SHAPE;
+    int64_t cells;
+    if (!mul_ok(d.batch * d.dim, chunks_of(d.seqlen, kKeep), &cells) || !grid_ok(cells / 256 + 64, 256)) return SSM_ERR_SHAPE;
+    return SSM_OK;
+}
+
+int64_t stride_of(int64_t s, int64_t dim) { return s ? s : dim; }
+int64_t span(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? (rows - 1) * stride + width : 0; }
+
+GlrParams params_of(const ssm_glr_desc &d) {
+    GlrParams p{};
+    p.L = d.seqlen;
+    p.dim = d.dim;
+    p.batch = (int)d.batch;
+    p.xs = stride_of(d.x_stride, d.dim);
+    p.rs = stride_of(d.rgate_stride, d.dim);
+    p.is = stride_of(d.igate_stride, d.dim);
+    p.gs = stride_of(d.gate_stride, d.dim);
+    p.rate = d.rate;
+    p.kept = (int)chunks_of(d.seqlen, kKeep);
+    return p;
+}
+
+// Whether lanes move two channels at a time
+bool pairs(const ssm_glr_desc &d, const GlrParams &p, const void *const *ptr, int n) {
+    if (d.dim % 2 || p.xs % 2 || p.rs % 2 || p.is % 2 || (p.gate && p.gs % 2)) return false;
+    for (int k = 0; k < n; ++k)
+        if (ptr[k] && !aligned(ptr[k], 2 * esize(d.dtype))) return false;
+    return true;
+}
+
+hipError_t set_sync(GlrParams &p, char *ws, const Layout &l, int64_t chunks, hipStream_t st) {
+    p.chunks = (int)chunks;
+    if (chunks <= 1) return hipSuccess;
+    p.ticket = reinterpret_cast<uint32_t *>(ws + l.sync);
+    p.map = reinterpret_cast<unsigned long long *>(ws + l.map);
+    p.state = reinterpret_cast<uint32_t *>(ws + l.state);
+    const int64_t n = (int64_t)(l.total - l.sync) / 16;
+    hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
+                       reinterpret_cast<uint4 *>(ws + l.sync), n);
+    return hipGetLastError();
+}
+
+template <typename T, int VEC, int TT> void launch_fwd(const GlrParams &p, unsigned blocks, hipStream_t st) {
+    if (p.reset) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, TT, true>), dim3(blocks), dim3(kThreads), 0, st, p);
+    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, TT, false>), dim3(blocks), dim3(kThreads), 0, st, p);
+}
+
+int run_fwd(const ssm_glr_desc &d, GlrParams &p, bool two, char *ws, const Layout &l, hipStream_t st) {
+    if (set_sync(p, ws, l, chunks_of(d.seqlen, fwd_tokens(d.dtype)), st) != hipSuccess) return SSM_ERR_HIP;
+    p.tiles = (int)tiles_of(d.dim, two ? 2 : 1);
+    const unsigned blocks = (unsigned)((int64_t)p.tiles * p.batch * p.chunks);
+    if (d.dtype == SSM_BF16) two ? launch_fwd<uint16_t, 2, 16>(p, blocks, st) : launch_fwd<uint16_t, 1, 16>(p, blocks, st);
+    else two ? launch_fwd<float, 2, 8>(p, blocks, st) : launch_fwd<float, 1, 8>(p, blocks, st);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+template <typename T, int VEC> void launch_bwd(const GlrParams &p, unsigned blocks, hipStream_t st) {
+#define GLR_CASE(RESET, GATE) \
+    hipLaunchKernelGGL((glr_bwd_kernel<T, VEC, RESET, GATE>), dim3(blocks), dim3(kThreads), 0, st, p)
+    if (p.reset) {
+        if (p.gate) GLR_CASE(true, true);
+        else GLR_CASE(true, false);
+    } else {
+        if (p.gate) GLR_CASE(false, true);
+        else GLR_CASE(false, false);
+    }
+#undef GLR_CASE
+}
+
+// No tokens: the last state is the first, and the gradients of what no token reads are 0
+__global__ __launch_bounds__(256) void glr_pass_kernel(const float *from, float *to, int64_t n, float *zero, int64_t m) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (to && k < n) to[k] = from ? from[k] : 0.0f;
+    if (zero && k < m) zero[k] = 0.0f;
+}
+
+int pass_state(const float *from, float *to, int64_t n, float *zero, int64_t m, hipStream_t st) {
+    const int64_t blocks = (std::max(to ? n : 0, zero ? m : 0) + 255) / 256;
+    if (blocks == 0) return SSM_OK;
+    if (!grid_ok(blocks, 256)) return SSM_ERR_SHAPE;
+    hipLaunchKernelGGL(glr_pass_kernel, dim3((unsigned)blocks), dim3(256), 0, st, from, to, n, zero, m);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+struct Inputs {
+    const void *x, *rg, *ig, *gate;
+    const float *lam, *h0;
+    const uint8_t *reset;
+};
+
+// Ranges of what both directions read
+int inputs_of(const ssm_glr_desc &d, const GlrParams &p, const Inputs &in, Range *r) {
+    const int64_t rows = d.batch * d.seqlen, e = (int64_t)esize(d.dtype);
+    r[0] = range_of(in.x, span(rows, p.xs, d.dim) * e);
+    r[1] = range_of(in.rg, span(rows, p.rs, d.dim) * e);
+    r[2] = range_of(in.ig, span(rows, p.is, d.dim) * e);
+    r[3] = range_of(in.gate, span(rows, p.gs, d.dim) * e);
+    r[4] = range_of(in.lam, d.dim * 4);
+    r[5] = range_of(in.reset, rows);
+    r[6] = range_of(in.h0, d.batch * d.dim * 4);
+    return 7;
+}
+
+bool same(Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; }
+
+int forward(const ssm_glr_desc *desc, const Inputs &in, void *y, float *h_last, void *workspace, size_t bytes, bool save,
+            hipStream_t st) {
+    if (const int rc = check(desc)) return rc;
+    const ssm_glr_desc &d = *desc;
+    const int64_t bd = d.batch * d.dim, rows = d.batch * d.seqlen;
+    if (!aligned(in.h0, 4) || !aligned(h_last, 4)) return SSM_ERR_ALIGN;
+    const Range rl = range_of(h_last, bd * 4), r0 = range_of(in.h0, bd * 4);
+    if (overlaps(rl, r0) && !same(rl, r0)) return SSM_ERR_ALIAS;
+    if (bd == 0) return SSM_OK;
+    if (d.seqlen == 0) return h_last == in.h0 ? SSM_OK : pass_state(in.h0, h_last, bd, nullptr, 0, st);
+    if (!in.x || !in.rg || !in.ig || !in.lam || !y) return SSM_ERR_NULL;
+    const size_t e = esize(d.dtype);
+    if (!aligned(in.x, e) || !aligned(in.rg, e) || !aligned(in.ig, e) || !aligned(in.gate, e) || !aligned(in.lam, 4) ||
+        !aligned(y, e))
+        return SSM_ERR_ALIGN;
+    const Layout l = layout(d, save);
+    if (l.total && (!workspace || bytes < l.total)) return SSM_ERR_WORKSPACE;
+    if (l.total && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
+    GlrParams p = params_of(d);
+    Range r[8];
+    const int n = inputs_of(d, p, in, r);
+    const Range ry = range_of(y, rows * d.dim * (int64_t)e), ws = range_of(workspace, (int64_t)l.total);
+    for (int k = 0; k < n; ++k)
+        if (overlaps(ry, r[k]) || overlaps(ws, r[k]) || (k < 6 && overlaps(rl, r[k]))) return SSM_ERR_ALIAS;
+    if (overlaps(ry, rl) || overlaps(ws, ry) || overlaps(ws, rl)) return SSM_ERR_ALIAS;
+    p.x = in.x; p.rg = in.rg; p.ig = in.ig; p.gate = in.gate; p.lam = in.lam; p.h0 = in.h0; p.reset = in.reset;
+    p.y = y;
+    p.h_last = h_last;
+    char *w = static_cast<char *>(workspace);
+    if (save) p.keep = reinterpret_cast<float *>(w + l.keep);
+    const void *ptr[] = {in.x, in.rg, in.ig, in.gate, y};
+    return run_fwd(d, p, pairs(d, p, ptr, 5), w, l, st);
+}
+
+int backward(const ssm_glr_desc *desc, const Inputs &in, const void *dy, const float *dh_last, void *dx, void *drg, void *dig,
+             void *dgate, float *dlam, float *dh0, void *workspace, size_t bytes, bool saved, hipStream_t st) {
+    if (const int rc = check(desc)) return rc;
+    const ssm_glr_desc &d = *desc;
+    const int64_t bd = d.batch * d.dim, rows = d.batch * d.seqlen;
+    if (!dlam) return SSM_ERR_NULL;
+    if (!aligned(dlam, 4) || !aligned(dh0, 4) || !aligned(dh_last, 4) || !aligned(in.h0, 4)) return SSM_ERR_ALIGN;
+    const Range rdl = range_of(dlam, d.dim * 4), rd0 = range_of(dh0, bd * 4), rdh = range_of(dh_last, bd * 4);
+    if ((overlaps(rd0, rdh) && !same(rd0, rdh)) || overlaps(rdl, rd0) || overlaps(rdl, rdh)) return SSM_ERR_ALIAS;
+    if (rows == 0) return pass_state(dh_last, dh0 == dh_last ? nullptr : dh0, bd, dlam, d.dim, st);
+    if (!in.x || !in.rg || !in.ig || !in.lam || !dy || !dx || !drg || !dig || (in.gate && !dgate)) return SSM_ERR_NULL;
+    const size_t e = esize(d.dtype);
+    const void *typed[] = {in.x, in.rg, in.ig, in.gate, dy, dx, drg, dig, in.gate ? dgate : nullptr};
+    for (const void *q : typed)
+        if (!aligned(q, e)) return SSM_ERR_ALIGN;
+    if (!aligned(in.lam, 4)) return SSM_ERR_ALIGN;
+    const Layout l = layout(d, true);
+    if (!workspace || bytes < l.total) return SSM_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SSM_ERR_ALIGN;
+    GlrParams p = params_of(d);
+    Range r[10];
+    int n = inputs_of(d, p, in, r);
+    const int64_t full = rows * d.dim * (int64_t)e;
+    r[n++] = range_of(dy, full);
+    r[n++] = rdh;
+    const Range ws = range_of(workspace, (int64_t)l.total);
+    const Range out[] = {range_of(dx, full), range_of(drg, full), range_of(dig, full), range_of(dgate, in.gate ? full : 0), rdl, rd0};
+    for (int k = 0; k < 6; ++k) {
+        for (int j = 0; j < n; ++j)
+            if (overlaps(out[k], r[j]) && !(k == 5 && j == n - 1)) return SSM_ERR_ALIAS;
+        for (int j = 0; j < k; ++j)
+            if (overlaps(out[k], out[j])) return SSM_ERR_ALIAS;
+        if (overlaps(out[k], ws)) return SSM_ERR_ALIAS;
+    }
+    for (int j = 0; j < n; ++j)
+        if (overlaps(ws, r[j])) return SSM_ERR_ALIAS;
+    p.x = in.x; p.rg = in.rg; p.ig = in.ig; p.gate = in.gate; p.lam = in.lam; p.h0 = in.h0; p.reset = in.reset;
+    char *w = static_cast<char *>(workspace);
+    p.keep = reinterpret_cast<float *>(w + l.keep);
+    const bool two = pairs(d, p, typed, 9);
+    if (!saved) {
+        const int rc = run_fwd(d, p, two, w, l, st);
+        if (rc != SSM_OK) return rc;
+        p.ticket = nullptr;
+    }
+    p.dy = dy; p.dh_last = dh_last; p.dx = dx; p.drg = drg; p.dig = dig; p.dgate = dgate; p.dh0 = dh0;
+    p.part = reinterpret_cast<float *>(w + l.part);
+    if (set_sync(p, w, l, chunks_of(d.seqlen, kKeep), st) != hipSuccess) return SSM_ERR_HIP;
+    p.tiles = (int)tiles_of(d.dim, two ? 2 : 1);
+    const unsigned blocks = (unsigned)((int64_t)p.tiles * p.batch * p.chunks);
+    if (d.dtype == SSM_BF16) two ? launch_bwd<uint16_t, 2>(p, blocks, st) : launch_bwd<uint16_t, 1>(p, blocks, st);
+    else two ? launch_bwd<float, 2>(p, blocks, st) : launch_bwd<float, 1>(p, blocks, st);
+    if (hipGetLastError() != hipSuccess) return SSM_ERR_HIP;
+    hipLaunchKernelGGL(glr_sum_kernel, dim3((unsigned)((d.dim + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumRuns), 0, st,
+                       p.part, (int64_t)p.batch * p.chunks, d.dim, in.lam, dlam);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" size_t ssm_glr_workspace_size(const ssm_glr_desc *desc) {
+    if (check(desc) != SSM_OK || desc->batch == 0 || desc->seqlen == 0) return 0;
+    return layout(*desc, false).total;
+}
+
+extern "C" size_t ssm_glr_bwd_workspace_size(const ssm_glr_desc *desc) {
+    if (check(desc) != SSM_OK || desc->batch == 0 || desc->seqlen == 0) return 0;
+    return layout(*desc, true).total;
+}
+
+extern "C" int ssm_glr_fwd(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                           const float *h0, const void *gate, const uint8_t *reset, void *y, float *h_last, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+    return forward(desc, Inputs{x, rgate, igate, gate, lam, h0, reset}, y, h_last, workspace, workspace_bytes, false, stream);
+}
+
+extern "C" int ssm_glr_fwd_save(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                                const float *h0, const void *gate, const uint8_t *reset, void *y, float *h_last,
+                                void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    return forward(desc, Inputs{x, rgate, igate, gate, lam, h0, reset}, y, h_last, workspace, workspace_bytes, true, stream);
+}
+
+extern "C" int ssm_glr_bwd(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                           const float *h0, const void *gate, const uint8_t *reset, const void *dy, const float *dh_last,
+                           void *dx, void *drgate, void *digate, void *dgate, float *dlam, float *dh0, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+    return backward(desc, Inputs{x, rgate, igate, gate, lam, h0, reset}, dy, dh_last, dx, drgate, digate, dgate, dlam, dh0,
+                    workspace, workspace_bytes, false, stream);
+}
+
+extern "C" int ssm_glr_bwd_saved(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
+                                 const float *h0, const void *gate, const uint8_t *reset, const void *dy,
+                                 const float *dh_last, void *dx, void *drgate, void *digate, void *dgate, float *dlam,
+                                 float *dh0, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    return backward(desc, Inputs{x, rgate, igate, gate, lam, h0, reset}, dy, dh_last, dx, drgate, digate, dgate, dlam, dh0,
+                    workspace, workspace_bytes, true, stream);
+}
+
+extern "C" int ssm_glr_state_update(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate,
+                                    const float *lam, const void *gate, const uint8_t *reset, const float *h, float *h_out,
+                                    void *y, hipStream_t stream) {
+    if (const int rc = check(desc)) return rc;
+    const ssm_glr_desc &d = *desc;
+    if (d.seqlen != 1) return SSM_ERR_SHAPE;
+    if (d.batch == 0) return SSM_OK;
+    if (!x || !rgate || !igate || !lam || !h || !h_out || !y) return SSM_ERR_NULL;
+    const size_t e = esize(d.dtype);
+    const void *typed[] = {x, rgate, igate, gate, y};
+    for (const void *q : typed)
+        if (!aligned(q, e)) return SSM_ERR_ALIGN;
+    if (!aligned(lam, 4) || !aligned(h, 4) || !aligned(h_out, 4)) return SSM_ERR_ALIGN;
+    GlrParams p = params_of(d);
+    Range r[8];
+    const int n = inputs_of(d, p, Inputs{x, rgate, igate, gate, lam, h, reset}, r);
+    const Range ry = range_of(y, d.batch * d.dim * (int64_t)e), ro = range_of(h_out, d.batch * d.dim * 4);
+    for (int k = 0; k < n; ++k)
+        if (overlaps(ry, r[k]) || (overlaps(ro, r[k]) && !(k == 6 && same(ro, r[k])))) return SSM_ERR_ALIAS;
+    if (overlaps(ry, ro)) return SSM_ERR_ALIAS;
+    p.x = x; p.rg = rgate; p.ig = igate; p.gate = gate; p.lam = lam; p.reset = reset;
+    p.y = y;
+    const bool two = pairs(d, p, typed, 5);
+    const int64_t bx = (d.dim + 256 * (two ? 2 : 1) - 1) / (256 * (two ? 2 : 1));
+    // rows to a lane: as many as leave four workgroups to a CU
+    int rows_per = 1;
+    while (rows_per < 16 && bx * ((d.batch + 2 * rows_per - 1) / (2 * rows_per)) >= 1024) rows_per *= 2;
+    while ((d.batch + rows_per - 1) / rows_per > 65535) rows_per *= 2;
+    const dim3 grid((unsigned)bx, (unsigned)((d.batch + rows_per - 1) / rows_per));
+    if (d.dtype == SSM_BF16) {
+        if (two) hipLaunchKernelGGL((glr_step_kernel<uint16_t, 2>), grid, dim3(256), 0, stream, p, h, h_out, rows_per);
+        else hipLaunchKernelGGL((glr_step_kernel<uint16_t, 1>), grid, dim3(256), 0, stream, p, h, h_out, rows_per);
+    } else {
+        if (two) hipLaunchKernelGGL((glr_step_kernel<float, 2>), grid, dim3(256), 0, stream, p, h, h_out, rows_per);
+        else hipLaunchKernelGGL((glr_step_kernel<float, 1>), grid, dim3(256), 0, stream, p, h, h_out, rows_per);
+    }
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
