@@ -679,6 +679,35 @@ int ssm_glr_state_update(const ssm_glr_desc *desc, const void *x, const void *rg
                          const float *lam, const void *gate, const uint8_t *reset, const float *h, float *h_out,
                          void *y, hipStream_t stream);
 
+/*
+ * The norm over all gradients of a model, and their clipping by it:
+ *
+ *   norm = sqrt(sum over tensors and elements of g^2)   squares and sums in 64 bits
+ *   g   <- g * min(1, max_norm / (norm + eps))          factor and product in fp32, rounded once
+ *
+ * A norm of infinity makes finite gradients 0, one of NaN makes all of them NaN.
+ *   count     tensors, 0..2^20; every array below is a HOST array of so many values
+ *   grads     device pointers of dense tensors, their element's alignment
+ *   out       the same for what is written: grads[k] itself, or apart from everything
+ *   sizes     elements, 0..2^35; pointers of empty tensors are not looked at
+ *   dtypes    SSM_F32 or SSM_BF16, one for each
+ *   norm      one fp32 on the device, written; ssm_grad_scale reads it, for a norm
+ *             over more tensors than these (those of other GPUs)
+ *   workspace ssm_grad_workspace_size(count) bytes, 256-byte aligned
+ * What is written overlaps nothing else; the same gradient twice in one list is
+ * refused (SSM_ERR_ALIAS) where it is written and counts twice in ssm_grad_norm. The
+ * host arrays are not read after the call returns. Results do not depend on timing;
+ * tensors go 128 to a launch.
+ */
+size_t ssm_grad_workspace_size(int64_t count);
+int ssm_grad_norm(int64_t count, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                  float *norm, void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ssm_grad_clip(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes,
+                  const int32_t *dtypes, float max_norm, float eps, float *norm,
+                  void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ssm_grad_scale(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes,
+                   const int32_t *dtypes, const float *norm, float max_norm, float eps, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *ssm_status_string(int status);
 

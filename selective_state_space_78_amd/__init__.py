@@ -10,7 +10,7 @@ Names follow the C ABI: ``ssm_scan_fwd``, ``ssm_scan_fwd_noalloc``, ``ssm_scan_w
 ``ssm_scan_plan``, ``ssm_scan_bwd``, ``ssm_state_update``, ``ssm_ssd_fwd``,
 ``ssm_gdr_fwd``, ``ssm_gdr_bwd``, ``ssm_gdr_state_update``, ``ssm_prenorm_fwd``,
 ``ssm_gated_norm_fwd``, ``ssm_glr_fwd``, ``ssm_glr_bwd``, ``ssm_glr_state_update``,
-``ssm_status_string``.
+``ssm_grad_norm``, ``ssm_grad_clip``, ``ssm_status_string``.
 
 ``stream`` runs a call on a stream other than the current one. The caller orders the
 two where inputs or results cross; what the call allocates comes out of that stream's
@@ -37,7 +37,8 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_workspace_size_t
            "ssm_gdr_fwd_save", "ssm_gdr_bwd", "ssm_gdr_bwd_saved", "ssm_gdr_state_update", "ssm_prenorm_fwd",
            "ssm_prenorm_bwd", "ssm_prenorm_bwd_workspace_size", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
            "ssm_gated_norm_bwd_workspace_size", "ssm_glr_workspace_size", "ssm_glr_bwd_workspace_size", "ssm_glr_fwd",
-           "ssm_glr_fwd_save", "ssm_glr_bwd", "ssm_glr_bwd_saved", "ssm_glr_state_update", "ssm_status_string")
+           "ssm_glr_fwd_save", "ssm_glr_bwd", "ssm_glr_bwd_saved", "ssm_glr_state_update", "ssm_grad_workspace_size", "ssm_grad_norm",
+           "ssm_grad_clip", "ssm_grad_scale", "ssm_status_string")
 
 # Fixed scratch of ssm_scan_fwd_noalloc per GPU (SSM_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -160,6 +161,14 @@ def lib() -> ctypes.CDLL:
                                ("ssm_glr_bwd", [pl] + [vp] * 16 + [sz, vp]),
                                ("ssm_glr_bwd_saved", [pl] + [vp] * 16 + [sz, vp]),
                                ("ssm_glr_state_update", [pl] + [vp] * 10)):
+                getattr(L, name).argtypes = args
+                getattr(L, name).restype = ctypes.c_int
+            f32 = ctypes.c_float
+            L.ssm_grad_workspace_size.argtypes = [i64]
+            L.ssm_grad_workspace_size.restype = sz
+            for name, args in (("ssm_grad_norm", [i64, vp, vp, vp, vp, vp, sz, vp]),
+                               ("ssm_grad_clip", [i64, vp, vp, vp, vp, f32, f32, vp, vp, sz, vp]),
+                               ("ssm_grad_scale", [i64, vp, vp, vp, vp, vp, f32, f32, vp])):
                 getattr(L, name).argtypes = args
                 getattr(L, name).restype = ctypes.c_int
             L.ssm_status_string.argtypes = [ctypes.c_int]
@@ -1091,3 +1100,93 @@ def ssm_glr_state_update(x, rgate, igate, lam, h, y=None, h_out=None, gate=None,
     if rc != 0:
         raise SsmError(rc, "ssm_glr_state_update")
     return y
+
+
+def _grad_list(grads, out, device=None):
+    """(count, pointers, outputs' pointers, sizes, types, device) of gradients, those
+    that are None left out; host arrays for one call."""
+    import torch
+    grads = list(grads)
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out has %d tensors, there are %d gradients" % (len(out), len(grads)))
+        out = [o for o, g in zip(out, grads) if g is not None]
+    grads = [g for g in grads if g is not None]
+    codes = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+    if device is None:
+        if not grads:
+            raise ValueError("no gradients, and so no device: give the norm")
+        device = grads[0].device
+    try:
+        types = [codes[g.dtype] for g in grads]
+    except KeyError as e:
+        raise TypeError("gradients must be bfloat16 or float32, got %s" % e.args[0]) from None
+    for k, g in enumerate(grads):
+        if not g.is_contiguous():
+            raise ValueError("gradient %d must be contiguous" % k)
+        if g.device != device:
+            raise ValueError("gradient %d is on %s, expected %s" % (k, g.device, device))
+    n = len(grads)
+    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    outs = ptrs
+    if out is not None:
+        for k, (o, g) in enumerate(zip(out, grads)):
+            if o is not g and (o is None or o.shape != g.shape or o.dtype != g.dtype or o.device != device or
+                               not o.is_contiguous()):
+                raise ValueError("out %d must be a contiguous tensor like its gradient" % k)
+        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    return n, ptrs, outs, (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*types), device
+
+
+def _norm_tensor(norm, device, stream):
+    import torch
+    if norm is None:
+        return _empty((), torch.float32, device, stream)
+    if norm.numel() != 1 or norm.dtype != torch.float32 or norm.device != device:
+        raise ValueError("norm must be one float32 on %s" % device)
+    return norm
+
+
+def ssm_grad_workspace_size(count) -> int:
+    """Workspace bytes of ssm_grad_norm and ssm_grad_clip for so many tensors."""
+    return int(lib().ssm_grad_workspace_size(int(count)))
+
+
+def ssm_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The norm over all gradients, sqrt(sum g^2), squares and sums in 64 bits.
+    grads: contiguous bfloat16 or float32 tensors of one GPU; None among them is left
+    out. Returns a float32 tensor of no dimensions (``norm`` if given)."""
+    n, ptrs, _, sizes, types, dev = _grad_list(grads, None, None if norm is None else norm.device)
+    norm = _norm_tensor(norm, dev, stream)
+    workspace, ws_bytes = _workspace(workspace, ssm_grad_workspace_size(n), dev, "ssm_grad_norm", stream)
+    rc = _on(dev, lib().ssm_grad_norm, n, ptrs, sizes, types, _ptr(norm), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_grad_norm")
+    return norm
+
+
+def ssm_grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, stream=None):
+    """Clips gradients by the norm over all of them:
+    g <- g min(1, max_norm / (norm + eps)), in place, or written to ``out`` (a tensor
+    for each gradient). grads as ssm_grad_norm, each tensor once. Returns the norm
+    before the clipping."""
+    n, ptrs, outs, sizes, types, dev = _grad_list(grads, out, None if norm is None else norm.device)
+    norm = _norm_tensor(norm, dev, stream)
+    workspace, ws_bytes = _workspace(workspace, ssm_grad_workspace_size(n), dev, "ssm_grad_clip", stream)
+    rc = _on(dev, lib().ssm_grad_clip, n, ptrs, outs, sizes, types, float(max_norm), float(eps), _ptr(norm),
+             _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_grad_clip")
+    return norm
+
+
+def ssm_grad_scale(grads, norm, max_norm, eps=1e-6, out=None, stream=None):
+    """The scaling of ssm_grad_clip by a given ``norm`` (one float32 on the GPU), as
+    where it is taken over the gradients of several GPUs."""
+    n, ptrs, outs, sizes, types, dev = _grad_list(grads, out, norm.device)
+    _norm_tensor(norm, dev, stream)
+    rc = _on(dev, lib().ssm_grad_scale, n, ptrs, outs, sizes, types, _ptr(norm), float(max_norm), float(eps),
+             _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_grad_scale")
