@@ -680,6 +680,68 @@ int ssm_glr_state_update(const ssm_glr_desc *desc, const void *x, const void *rg
                          void *y, hipStream_t stream);
 
 /*
+ * A projection: a matrix product with what follows it. Per row (token) and group,
+ *
+ *   pre = x W^T + bias,   y = act(pre) + residual
+ *
+ * groups 1 is a linear layer, more a block-diagonal one (the gates of a recurrence).
+ * bf16 products are summed in fp32 on the matrix cores, fp32 ones are full fp32; bias,
+ * activation and residual are applied to the fp32 sums, and y and pre are rounded once.
+ * gelu is the form z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3)).
+ *
+ * Up to 8 rows the forward reads the weight once without tiles. Results do not depend
+ * on timing, nor on other rows' values; they may differ by rounding between numbers of
+ * rows. Sizes that need 2^32 work items in a launch are refused (SSM_ERR_SHAPE).
+ */
+typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1, SSM_ACT_GELU = 2, SSM_ACT_SIGMOID = 3 } ssm_activation;
+
+typedef struct {
+    int64_t rows;            /* 0..2^31 - 1 */
+    int64_t groups;          /* >= 1 */
+    int64_t in, out;         /* values of a group in x and in y, >= 1; groups times either < 2^22 */
+    int32_t dtype;           /* of x, weight, pre and their gradients */
+    int32_t y_dtype;         /* of residual, y, dy: dtype, or SSM_F32 */
+    int32_t activation;      /* ssm_activation */
+    int32_t reserved;        /* 0 */
+    int64_t x_stride;        /* elements from row to row of x, < 2^22; 0: groups * in */
+} ssm_proj_desc;
+
+/*
+ *   x         (rows, groups, in)        dtype
+ *   weight    (groups, out, in)         dtype
+ *   bias      (groups, out) fp32, or NULL
+ *   residual  (rows, groups, out)       y_dtype, or NULL
+ *   pre       (rows, groups, out)       dtype, written, or NULL (not wanted)
+ *   y         (rows, groups, out)       y_dtype, written; may equal residual exactly
+ *   workspace ssm_proj_workspace_size(desc) bytes, 256-byte aligned; its contents on
+ *             entry do not matter
+ * Pointers need their element's alignment only (16-byte aligned rows move faster).
+ * Other overlaps of outputs are refused.
+ */
+size_t ssm_proj_workspace_size(const ssm_proj_desc *desc);
+int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void *weight, const float *bias,
+                 const void *residual, void *pre, void *y, void *workspace, size_t workspace_bytes,
+                 hipStream_t stream);
+
+/*
+ * Gradients of sum dy . y (that of the residual is dy).
+ *   dy        (rows, groups, out)  y_dtype, dense
+ *   pre       what the forward wrote; read with an activation only
+ *   dpre      (rows, groups, out)  dtype, written: dy act'(pre), rounded; required with an
+ *             activation and where dy is not of dtype, else unused (dy serves)
+ *   dx        (rows, groups, in)   dtype, dense, written, or NULL (not wanted): that of dpre as stored
+ *   dweight   (groups, out, in)    dtype, written, or NULL: that of dpre as stored
+ *   dbias     (groups, out) fp32, written, or NULL: the sum of dpre before its rounding
+ *   x is read for dweight, weight for dx; each may be NULL without
+ *   workspace ssm_proj_bwd_workspace_size(desc) bytes, 256-byte aligned
+ * Sums over rows are taken in a fixed order. rows == 0 writes dweight = 0, dbias = 0.
+ */
+size_t ssm_proj_bwd_workspace_size(const ssm_proj_desc *desc);
+int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const void *x, const void *weight, const void *pre,
+                 void *dpre, void *dx, void *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                 hipStream_t stream);
+
+/*
  * The norm over all gradients of a model, and their clipping by it:
  *
  *   norm = sqrt(sum over tensors and elements of g^2)   squares and sums in 64 bits

@@ -10,7 +10,7 @@ Names follow the C ABI: ``ssm_scan_fwd``, ``ssm_scan_fwd_noalloc``, ``ssm_scan_w
 ``ssm_scan_plan``, ``ssm_scan_bwd``, ``ssm_state_update``, ``ssm_ssd_fwd``,
 ``ssm_gdr_fwd``, ``ssm_gdr_bwd``, ``ssm_gdr_state_update``, ``ssm_prenorm_fwd``,
 ``ssm_gated_norm_fwd``, ``ssm_glr_fwd``, ``ssm_glr_bwd``, ``ssm_glr_state_update``,
-``ssm_grad_norm``, ``ssm_grad_clip``, ``ssm_status_string``.
+``ssm_proj_fwd``, ``ssm_proj_bwd``, ``ssm_grad_norm``, ``ssm_grad_clip``, ``ssm_status_string``.
 
 ``stream`` runs a call on a stream other than the current one. The caller orders the
 two where inputs or results cross; what the call allocates comes out of that stream's
@@ -28,6 +28,7 @@ LIBRARY = os.path.join(PKG, "libssm_scan.so")
 SSM_F32, SSM_BF16 = 0, 1
 SSM_DISC_EULER, SSM_DISC_ZOH = 0, 1
 _DISC = {"euler": SSM_DISC_EULER, "zoh": SSM_DISC_ZOH}
+_ACT = {None: 0, "silu": 1, "gelu": 2, "sigmoid": 3}
 
 # Every symbol include/ssm_scan.h declares.
 EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_workspace_size_tuned",
@@ -38,7 +39,8 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_workspace_size_t
            "ssm_prenorm_bwd", "ssm_prenorm_bwd_workspace_size", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
            "ssm_gated_norm_bwd_workspace_size", "ssm_glr_workspace_size", "ssm_glr_bwd_workspace_size", "ssm_glr_fwd",
            "ssm_glr_fwd_save", "ssm_glr_bwd", "ssm_glr_bwd_saved", "ssm_glr_state_update", "ssm_grad_workspace_size", "ssm_grad_norm",
-           "ssm_grad_clip", "ssm_grad_scale", "ssm_status_string")
+           "ssm_grad_clip", "ssm_grad_scale", "ssm_proj_workspace_size", "ssm_proj_fwd", "ssm_proj_bwd_workspace_size",
+           "ssm_proj_bwd", "ssm_status_string")
 
 # Fixed scratch of ssm_scan_fwd_noalloc per GPU (SSM_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -83,6 +85,12 @@ class GlrDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("rate", ctypes.c_float), ("x_stride", ctypes.c_int64),
                 ("rgate_stride", ctypes.c_int64), ("igate_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64)]
+
+
+class ProjDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("in_", ctypes.c_int64), ("out", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_stride", ctypes.c_int64)]
 
 
 class ScanTuning(ctypes.Structure):
@@ -141,10 +149,11 @@ def lib() -> ctypes.CDLL:
             L.ssm_ssd_state_update.argtypes = [ctypes.POINTER(SsdDesc)] + [vp] * 10
             L.ssm_ssd_state_update.restype = ctypes.c_int
             pg, pp, pn = ctypes.POINTER(GdrDesc), ctypes.POINTER(PrenormDesc), ctypes.POINTER(GatedNormDesc)
-            pl = ctypes.POINTER(GlrDesc)
+            pl, pj = ctypes.POINTER(GlrDesc), ctypes.POINTER(ProjDesc)
             for name, d in (("ssm_gdr_workspace_size", pg), ("ssm_gdr_bwd_workspace_size", pg),
                             ("ssm_prenorm_bwd_workspace_size", pp), ("ssm_gated_norm_bwd_workspace_size", pn),
-                            ("ssm_glr_workspace_size", pl), ("ssm_glr_bwd_workspace_size", pl)):
+                            ("ssm_glr_workspace_size", pl), ("ssm_glr_bwd_workspace_size", pl),
+                            ("ssm_proj_workspace_size", pj), ("ssm_proj_bwd_workspace_size", pj)):
                 getattr(L, name).argtypes = [d]
                 getattr(L, name).restype = sz
             for name, args in (("ssm_gdr_fwd", [pg] + [vp] * 10 + [sz, vp]),
@@ -160,7 +169,9 @@ def lib() -> ctypes.CDLL:
                                ("ssm_glr_fwd_save", [pl] + [vp] * 10 + [sz, vp]),
                                ("ssm_glr_bwd", [pl] + [vp] * 16 + [sz, vp]),
                                ("ssm_glr_bwd_saved", [pl] + [vp] * 16 + [sz, vp]),
-                               ("ssm_glr_state_update", [pl] + [vp] * 10)):
+                               ("ssm_glr_state_update", [pl] + [vp] * 10),
+                               ("ssm_proj_fwd", [pj] + [vp] * 7 + [sz, vp]),
+                               ("ssm_proj_bwd", [pj] + [vp] * 9 + [sz, vp])):
                 getattr(L, name).argtypes = args
                 getattr(L, name).restype = ctypes.c_int
             f32 = ctypes.c_float
@@ -1190,3 +1201,107 @@ def ssm_grad_scale(grads, norm, max_norm, eps=1e-6, out=None, stream=None):
              _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_grad_scale")
+
+
+def _proj_desc(x, weight, y_dtype, activation):
+    """The descriptor, and the shapes of y and of the bias."""
+    import torch
+    code, dev = _dtype_code(x), x.device
+    if activation not in _ACT:
+        raise ValueError("activation must be None, silu, gelu or sigmoid, got %r" % (activation,))
+    if weight.dim() not in (2, 3):
+        raise ValueError("weight must be (out, in) or (groups, out, in)")
+    grouped = weight.dim() == 3
+    G, (N, K) = weight.shape[0] if grouped else 1, weight.shape[-2:]
+    tail = (G, K) if grouped else (K,)
+    if x.dim() < len(tail):
+        raise ValueError("x must be (..., %s)" % ("groups, in" if grouped else "in"))
+    lead = tuple(x.shape[:x.dim() - len(tail)])
+    xs = _row_stride(x, "x", lead, tail, x.dtype, dev)
+    _check(weight, "weight", dtype=x.dtype, device=dev)
+    if y_dtype not in (x.dtype, torch.float32):
+        raise TypeError("residual, y and dy must be float32 or of x's dtype, got %s" % y_dtype)
+    rows = 1
+    for n in lead:
+        rows *= n
+    head = (G, N) if grouped else (N,)
+    return ProjDesc(rows, G, K, N, code, SSM_F32 if y_dtype == torch.float32 else SSM_BF16, _ACT[activation], 0, xs), lead + head, head
+
+
+def ssm_proj_workspace_size(rows, in_features, out_features, groups=1, dtype=SSM_BF16) -> int:
+    """Workspace bytes of ssm_proj_fwd."""
+    return int(lib().ssm_proj_workspace_size(ctypes.byref(ProjDesc(rows, groups, in_features, out_features, dtype, dtype))))
+
+
+def ssm_proj_bwd_workspace_size(rows, in_features, out_features, groups=1, dtype=SSM_BF16) -> int:
+    """Workspace bytes of ssm_proj_bwd."""
+    return int(lib().ssm_proj_bwd_workspace_size(ctypes.byref(ProjDesc(rows, groups, in_features, out_features, dtype, dtype))))
+
+
+def ssm_proj_fwd(x, weight, bias=None, activation=None, residual=None, y=None, workspace=None, stream=None, _pre=None,
+                 _save=False):
+    """A projection with what follows it, on device tensors:
+    y = act(x W^T + bias) + residual.
+
+    x: (..., in) bfloat16 or float32 (rows evenly spaced) with weight (out, in) of the
+    same dtype, or, block-diagonal, x (..., groups, in) with weight (groups, out, in);
+    bias: (out,) or (groups, out) float32; activation: None, "silu", "gelu" (the tanh
+    form) or "sigmoid"; residual: y's shape, of x's dtype or float32. y has the
+    residual's dtype (x's without one), is allocated when not given and may be the
+    residual itself. Returns y.
+    """
+    import torch
+    yt = x.dtype if residual is None else residual.dtype
+    desc, shape, head = _proj_desc(x, weight, yt, activation)
+    dev = x.device
+    _check(bias, "bias", head, torch.float32, dev)
+    _check(residual, "residual", shape, yt, dev)
+    if y is None:
+        y = _empty(shape, yt, dev, stream)
+    if _save and _pre is None:
+        _pre = _empty(shape, x.dtype, dev, stream)
+    _check(y, "y", shape, yt, dev)
+    _check(_pre, "pre", shape, x.dtype, dev)
+    L_ = lib()
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_proj_workspace_size(ctypes.byref(desc)), dev, "ssm_proj_fwd", stream)
+    rc = _on(dev, L_.ssm_proj_fwd, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(_pre), _ptr(y),
+             _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_proj_fwd")
+    return (y, _pre) if _save else y
+
+
+def ssm_proj_fwd_save(x, weight, bias=None, activation=None, residual=None, y=None, pre=None, workspace=None, stream=None):
+    """ssm_proj_fwd that also keeps pre = x W^T + bias, in x's dtype, which
+    ssm_proj_bwd reads with an activation. Returns (y, pre)."""
+    return ssm_proj_fwd(x, weight, bias, activation, residual, y, workspace, stream, pre, _save=True)
+
+
+def ssm_proj_bwd(dy, x, weight, pre=None, activation=None, want_dx=True, want_dweight=True, want_dbias=False, out=None,
+                 workspace=None, stream=None):
+    """Backward of ssm_proj_fwd (the residual's gradient is dy). dy: y's shape, of x's
+    dtype or float32; pre: what ssm_proj_fwd_save kept, needed with an activation.
+    Returns a dict with dpre = dy act'(pre) (x's dtype; dy itself where it is that), dx,
+    dweight (of the inputs' shapes and dtypes) and dbias (float32), None where not
+    wanted. dx and dweight are the products of dpre as stored, dbias is summed before
+    the rounding. ``out`` may hold preallocated outputs."""
+    import torch
+    desc, shape, head = _proj_desc(x, weight, dy.dtype, activation)
+    dev = x.device
+    _check(dy, "dy", shape, dy.dtype, dev)
+    if activation is not None and pre is None:
+        raise ValueError("the gradient of an activation needs pre")
+    _check(pre if activation is not None else None, "pre", shape, x.dtype, dev)
+    made = activation is not None or dy.dtype != x.dtype
+    get = _outputs(out, dev, stream)
+    g = dict(dpre=get("dpre", shape, x.dtype) if made else dy, dx=get("dx", tuple(x.shape), x.dtype, want_dx),
+             dweight=get("dweight", tuple(weight.shape), x.dtype, want_dweight),
+             dbias=get("dbias", head, torch.float32, want_dbias))
+    L_ = lib()
+    workspace, ws_bytes = _workspace(workspace, L_.ssm_proj_bwd_workspace_size(ctypes.byref(desc)), dev, "ssm_proj_bwd", stream)
+    rc = _on(dev, L_.ssm_proj_bwd, ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(weight),
+             _ptr(pre if activation is not None else None), _ptr(g["dpre"] if made else None), _ptr(g["dx"]),
+             _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_proj_bwd")
+    return g

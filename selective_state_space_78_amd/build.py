@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 UNITS = ("ssm_scan.hip", "scan_bf16_euler.hip", "scan_bf16_zoh.hip", "scan_bf16_euler_u32.hip",
          "scan_bf16_zoh_u32.hip", "scan_f32_euler.hip", "scan_f32_zoh.hip",
          "bwd_bf16_euler.hip", "bwd_bf16_zoh.hip", "bwd_f32_euler.hip", "bwd_f32_zoh.hip",
-         "ssd_euler.hip", "ssd_zoh.hip", "gdr.hip", "gdr_n64.hip", "gdr_n128.hip", "norm.hip", "glr.hip", "grad.hip")
+         "ssd_euler.hip", "ssd_zoh.hip", "gdr.hip", "gdr_n64.hip", "gdr_n128.hip", "norm.hip", "glr.hip", "grad.hip", "proj.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libssm_scan.so")
 ARCH = "gfx950"

@@ -1,0 +1,405 @@
+// The projections' C entries, their launches and the first pass of the backward
+// (include/ssm_scan.h states them; proj_kernels.hpp has the products).
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssm_scan.h"
+#include "abi_util.hpp"
+#include "proj_kernels.hpp"
+#include "scan_kernels.hpp"
+
+namespace {
+
+using namespace ssm_detail;
+
+constexpr int64_t kMaxWidth = ((int64_t)1 << 22) - 1;   // of a row: a tile's lane offsets stay in 32 bits
+constexpr int kCus = 256;
+
+size_t esize(int t) { return t == SSM_BF16 ? 2 : 4; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------------------------
+// dpre = dy act'(pre), and its sums over rows. A workgroup takes 64 lanes' columns
+// of a slab of rows, four rows at a time; the slabs' sums are added by proj_sum_kernel.
+
+__device__ __forceinline__ float act_grad(float z, int act) {
+    const float u = act == kActGelu ? kGeluK * fmaf(0.044715f * z * z, z, z) : z;
+    const float e = __builtin_amdgcn_exp2f(u * -1.4426950408889634f), s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float r = e > 1.0f ? 1.0f - s : e * s;          // 1 - s to its own digits
+    if (act == kActSilu) return s * fmaf(z, r, 1.0f);
+    if (act == kActGelu) return fmaf(z * s * r, kGeluK * fmaf(3.0f * 0.044715f * z, z, 1.0f), s);
+    return act == kActSigmoid ? s * r : 1.0f;
+}
+
+struct DpreParams {
+    const void *dy, *pre;
+    void *dpre;                 // NULL: not written
+    float *part;                // (slab, columns), or NULL
+    int64_t rows, cols, per;    // rows of a slab
+    int act;
+};
+
+template <typename T, typename D, int VEC> __global__ __launch_bounds__(256) void proj_dpre_kernel(DpreParams a) {
+    __shared__ float sum[4][64 * VEC];
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = ((int64_t)blockIdx.x * 64 + l) * VEC;
+    const int64_t r1 = min((int64_t)(blockIdx.y + 1) * a.per, a.rows);
+    float s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[e] = 0.0f;
+    if (c < a.cols) {
+#pragma unroll 4
+        for (int64_t r = (int64_t)blockIdx.y * a.per + w; r < r1; r += 4) {
+            const int64_t at = r * a.cols + c;
+            float d[VEC], z[VEC];
+            if constexpr (VEC == 4) proj_load4<D>(a.dy, at, d);
+            else d[0] = proj_load1<D>(a.dy, at);
+            if (a.act != kActNone) {
+                if constexpr (VEC == 4) proj_load4<T>(a.pre, at, z);
+                else z[0] = proj_load1<T>(a.pre, at);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) d[e] *= act_grad(z[e], a.act);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[e] += d[e];
+            if (a.dpre) {
+                if constexpr (VEC == 4) proj_store4<T>(a.dpre, at, d);
+                else proj_store1<T>(a.dpre, at, d[0]);
+            }
+        }
+    }
+    if (a.part == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[w][l * VEC + e] = s[e];
+    __syncthreads();
+    for (int k = threadIdx.x; k < 64 * VEC; k += 256) {
+        const int64_t col = (int64_t)blockIdx.x * 64 * VEC + k;
+        if (col < a.cols) a.part[(int64_t)blockIdx.y * a.cols + col] = (sum[0][k] + sum[1][k]) + (sum[2][k] + sum[3][k]);
+    }
+}
+
+// 16 columns by 64 runs of slabs, in 64 bits
+constexpr int kSumCols = 16, kSumRuns = 64;
+__global__ __launch_bounds__(kSumCols * kSumRuns) void proj_sum_kernel(const float *part, int64_t slabs, int64_t cols, float *out) {
+    __shared__ double s[kSumRuns][kSumCols];
+    const int l = threadIdx.x % kSumCols, run = threadIdx.x / kSumCols;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + l;
+    double v = 0.0;
+    if (c < cols)
+        for (int64_t k = run; k < slabs; k += kSumRuns) v += part[k * cols + c];
+    s[run][l] = v;
+    for (int o = kSumRuns / 2; o >= 1; o >>= 1) {
+        __syncthreads();
+        if (run < o) s[run][l] += s[run + o][l];
+    }
+    if (run == 0 && c < cols) out[c] = (float)s[0][l];
+}
+
+__global__ __launch_bounds__(256) void proj_zero_kernel(void *p, int64_t bytes) {
+    const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+    if (k < bytes) *reinterpret_cast<uint16_t *>(static_cast<char *>(p) + k) = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Products: which tile, how many splits
+
+struct Tiling {
+    int tile;         // 256, 128 or 64: its sides
+    int64_t splits;
+};
+
+// The time of a product of J x I outputs over R, in units of one CU's steps. A step of
+// 128 bytes of r takes a CU kStep; workgroups in excess of what the CUs hold at once
+// come in rounds.
+Tiling plan_for(int64_t I, int64_t J, int64_t R, int64_t groups, int dtype) {
+    const int64_t every = ceil_div(R, dtype == SSM_BF16 ? 64 : 32);
+    struct { int side, hold; double step, fixed; } kinds[] = {{256, 1, 4.0, 10.0}, {128, 2, 2.4, 8.0}, {64, 4, 1.8, 6.0}};
+    Tiling best{128, 1};
+    double least = 1e300;
+    for (const auto &k : kinds) {
+        const int64_t tiles = ceil_div(I, k.side) * ceil_div(J, k.side) * groups;
+        for (int64_t s = 1; s <= 64 && s <= every; s = s < 4 ? s + 1 : s + s / 2) {
+            if (s > 1 && (tiles >= 2 * kCus * k.hold || every / s < 2)) break;
+            const double rounds = (double)ceil_div(tiles * s, kCus * k.hold);
+            double t = rounds * ((double)ceil_div(every, s) * k.step + k.fixed);
+            // the sums written and read, and a launch
+            if (s > 1) t += 30.0 + (double)I * J * groups * (8.0 * s + 4.0) / 2e6;
+            if (t < least) {
+                least = t;
+                best = Tiling{k.side, s};
+            }
+        }
+    }
+    return best;
+}
+
+int64_t part_bytes(int64_t I, int64_t J, int64_t groups, const Tiling &pl) {
+    return pl.splits > 1 ? (int64_t)align256((size_t)(pl.splits * groups * J * I * 4)) : 0;
+}
+
+constexpr int kFew = 8;     // rows up to which the forward reads the weight once, without tiles
+
+template <typename T, bool TP, bool TQ, bool FAST>
+hipError_t launch_tiles(ProjParams &a, int tile, hipStream_t st) {
+    a.ti = (int)ceil_div(a.I, tile);
+    a.tj = (int)ceil_div(a.J, tile);
+    const unsigned blocks = (unsigned)((int64_t)a.ti * a.tj * a.groups * a.splits);
+    if constexpr (FAST) {
+        if (tile == 256) hipLaunchKernelGGL((proj_kernel<T, TP, TQ, 256, 256, true>), dim3(blocks), dim3(512), 0, st, a);
+        else if (tile == 128) hipLaunchKernelGGL((proj_kernel<T, TP, TQ, 128, 128, true>), dim3(blocks), dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((proj_kernel<T, TP, TQ, 64, 64, true>), dim3(blocks), dim3(256), 0, st, a);
+    } else {
+        hipLaunchKernelGGL((proj_kernel<T, TP, TQ, 64, 64, false>), dim3(blocks), dim3(256), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, bool TP, bool TQ> hipError_t product(ProjParams &a, Tiling pl, int dtype, hipStream_t st) {
+    const int each = 16 / (int)sizeof(T);
+    const int64_t per16 = each;
+    // whether pieces of 16 bytes lie whole in rows (columns) and on 16-byte addresses
+    const bool fast = aligned(a.p, 16) && aligned(a.q, 16) && a.ldp % per16 == 0 && a.ldq % per16 == 0 &&
+                      (a.groups == 1 || (a.gp % per16 == 0 && a.gq % per16 == 0)) && (TP ? a.I : a.R) % per16 == 0 &&
+                      (TQ ? a.J : a.R) % per16 == 0;
+    a.splits = (int)pl.splits;
+    a.steps = (int)ceil_div(ceil_div(a.R, 128 / (int64_t)sizeof(T)), pl.splits);
+    const hipError_t e = fast ? launch_tiles<T, TP, TQ, true>(a, pl.tile, st) : launch_tiles<T, TP, TQ, false>(a, 64, st);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t n = (int64_t)a.groups * a.J * ceil_div(a.I, 4);
+    hipLaunchKernelGGL((proj_join_kernel<T>), dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t few(const ProjParams &a, hipStream_t st) {
+    const int64_t each = 16 / (int64_t)sizeof(T);
+    const bool fast = aligned(a.p, 16) && aligned(a.q, 16) && a.R % each == 0 && a.ldq % each == 0 &&
+                      (a.groups == 1 || a.gq % each == 0);
+    const unsigned blocks = (unsigned)ceil_div(a.groups * a.I, 8);
+#define PROJ_FEW(M)                                                                                             \
+    if (a.J <= M) {                                                                                             \
+        if (fast) hipLaunchKernelGGL((proj_few_kernel<T, M, true>), dim3(blocks), dim3(256), 0, st, a);         \
+        else hipLaunchKernelGGL((proj_few_kernel<T, M, false>), dim3(blocks), dim3(256), 0, st, a);             \
+        return hipGetLastError();                                                                               \
+    }
+    PROJ_FEW(1) PROJ_FEW(2) PROJ_FEW(4) PROJ_FEW(8)
+#undef PROJ_FEW
+    return hipErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------------------
+// Checks
+
+bool type_ok(int t) { return t == SSM_F32 || t == SSM_BF16; }
+
+int check(const ssm_proj_desc *desc) {
+    if (desc == nullptr) return SSM_ERR_NULL;
+    const ssm_proj_desc &d = *desc;
+    if (d.rows < 0 || d.groups < 1 || d.in < 1 || d.out < 1 || d.x_stride < 0) return SSM_ERR_SHAPE;
+    int64_t ki, ko, n;
+    if (!mul_ok(d.groups, d.in, &ki) || !mul_ok(d.groups, d.out, &ko) || ki > kMaxWidth || ko > kMaxWidth ||
+        d.x_stride > kMaxWidth || (d.x_stride != 0 && d.x_stride < ki) || d.rows > INT32_MAX)
+        return SSM_ERR_SHAPE;
+    if (!type_ok(d.dtype) || !type_ok(d.y_dtype)) return SSM_ERR_DTYPE;
+    if (d.y_dtype != d.dtype && d.y_dtype != SSM_F32) return SSM_ERR_UNSUPPORTED;
+    if (d.activation < SSM_ACT_NONE || d.activation > SSM_ACT_SIGMOID || d.reserved != 0) return SSM_ERR_UNSUPPORTED;
+    // the smallest tiles of every product in the largest number of splits, and the joining pass, below 2^32 work items
+    if (!mul_ok(d.rows, std::max(ki, ko), &n) || n > ((int64_t)1 << 38)) return SSM_ERR_SHAPE;
+    const int64_t ti = ceil_div(d.in, 64), to = ceil_div(d.out, 64), tr = ceil_div(d.rows, 64);
+    if (!grid_ok(std::max(tr * std::max(ti, to), ti * to) * d.groups, 256 * 2) ||
+        !grid_ok(ceil_div(std::max(std::max(d.rows * ki, d.rows * ko), d.in * ko), 1024) * 4 + 1, 256))
+        return SSM_ERR_SHAPE;
+    return SSM_OK;
+}
+
+int64_t span(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? (rows - 1) * stride + width : 0; }
+
+struct BackPlan {
+    Tiling dx, dw;
+    int64_t slabs, per;         // of dpre's pass
+    int64_t sums, total;        // bytes: the slabs' sums; all
+};
+
+BackPlan back_plan(const ssm_proj_desc &d) {
+    BackPlan b;
+    b.dx = plan_for(d.in, d.rows, d.out, d.groups, d.dtype);
+    b.dw = plan_for(d.in, d.out, d.rows, d.groups, d.dtype);
+    // enough slabs for four workgroups to a CU, of 16 rows at least
+    const int64_t cols = d.groups * d.out, blocks = ceil_div(cols, 256);
+    b.slabs = std::max<int64_t>(1, std::min(ceil_div(d.rows, 16), ceil_div(4 * kCus, blocks)));
+    b.per = ceil_div(d.rows, b.slabs);
+    b.slabs = ceil_div(d.rows, b.per);
+    b.sums = (int64_t)align256((size_t)(b.slabs * cols * 4));
+    b.total = b.sums + std::max(part_bytes(d.in, d.rows, d.groups, b.dx), part_bytes(d.in, d.out, d.groups, b.dw));
+    return b;
+}
+
+template <typename T, typename D> hipError_t dpre_pass(const DpreParams &a, int64_t slabs, bool four, hipStream_t st) {
+    if (four)
+        hipLaunchKernelGGL((proj_dpre_kernel<T, D, 4>), dim3((unsigned)ceil_div(a.cols, 256), (unsigned)slabs), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((proj_dpre_kernel<T, D, 1>), dim3((unsigned)ceil_div(a.cols, 64), (unsigned)slabs), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+int zero(void *p, int64_t bytes, hipStream_t st) {
+    if (p == nullptr || bytes == 0) return SSM_OK;
+    hipLaunchKernelGGL(proj_zero_kernel, dim3((unsigned)ceil_div(bytes, 512)), dim3(256), 0, st, p, bytes);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
+
+}  // namespace
+
+extern "C" size_t ssm_proj_workspace_size(const ssm_proj_desc *desc) {
+    if (check(desc) != SSM_OK || desc->rows <= kFew) return 0;
+    const ssm_proj_desc &d = *desc;
+    return (size_t)part_bytes(d.out, d.rows, d.groups, plan_for(d.out, d.rows, d.in, d.groups, d.dtype));
+}
+
+extern "C" size_t ssm_proj_bwd_workspace_size(const ssm_proj_desc *desc) {
+    if (check(desc) != SSM_OK || desc->rows == 0) return 0;
+    return (size_t)back_plan(*desc).total;
+}
+
+extern "C" int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void *weight, const float *bias, const void *residual,
+                            void *pre, void *y, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (const int rc = check(desc)) return rc;
+    const ssm_proj_desc &d = *desc;
+    if (d.rows == 0) return SSM_OK;
+    if (!x || !weight || !y) return SSM_ERR_NULL;
+    const size_t e = esize(d.dtype), ey = esize(d.y_dtype);
+    if (!aligned(x, e) || !aligned(weight, e) || !aligned(pre, e) || !aligned(bias, 4) || !aligned(residual, ey) || !aligned(y, ey))
+        return SSM_ERR_ALIGN;
+    const int64_t xs = d.x_stride ? d.x_stride : d.groups * d.in, n = d.rows * d.groups * d.out;
+    const Tiling pl = plan_for(d.out, d.rows, d.in, d.groups, d.dtype);
+    const int64_t need = d.rows <= kFew ? 0 : part_bytes(d.out, d.rows, d.groups, pl);
+    if (need && (!workspace || workspace_bytes < (size_t)need)) return SSM_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
+    const Range in[] = {range_of(x, span(d.rows, xs, d.groups * d.in) * e), range_of(weight, d.groups * d.in * d.out * e),
+                        range_of(bias, d.groups * d.out * 4), range_of(residual, n * ey)};
+    const Range ry = range_of(y, n * ey), rp = range_of(pre, n * e), ws = range_of(workspace, need);
+    for (int k = 0; k < 4; ++k) {
+        const bool same = k == 3 && in[k].lo == ry.lo;      // a residual updated in place
+        if ((overlaps(ry, in[k]) && !same) || overlaps(rp, in[k]) || overlaps(ws, in[k])) return SSM_ERR_ALIAS;
+    }
+    if (overlaps(ry, rp) || overlaps(ws, ry) || overlaps(ws, rp)) return SSM_ERR_ALIAS;
+    ProjParams a{};
+    a.p = weight;
+    a.q = x;
+    a.ldp = d.in;
+    a.ldq = xs;
+    a.gp = d.in * d.out;
+    a.gq = d.in;
+    a.I = d.out;
+    a.J = d.rows;
+    a.R = d.in;
+    a.bias = bias;
+    a.res = residual;
+    a.pre = pre;
+    a.out = y;
+    a.ldo = d.groups * d.out;
+    a.go = d.out;
+    a.part = static_cast<float *>(workspace);
+    a.groups = (int)d.groups;
+    a.splits = 1;
+    a.act = d.activation;
+    a.wide = d.y_dtype == SSM_F32;
+    a.four = d.out % 4 == 0 && aligned(y, 4 * ey) && aligned(residual, 4 * ey) && aligned(pre, 4 * e);
+    if (d.rows <= kFew) return status(d.dtype == SSM_BF16 ? few<uint16_t>(a, stream) : few<float>(a, stream));
+    return status(d.dtype == SSM_BF16 ? product<uint16_t, false, false>(a, pl, d.dtype, stream)
+                                      : product<float, false, false>(a, pl, d.dtype, stream));
+}
+
+extern "C" int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const void *x, const void *weight, const void *pre,
+                            void *dpre, void *dx, void *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+    if (const int rc = check(desc)) return rc;
+    const ssm_proj_desc &d = *desc;
+    const size_t e = esize(d.dtype), ey = esize(d.y_dtype);
+    const int64_t ko = d.groups * d.out, ki = d.groups * d.in, wn = d.groups * d.in * d.out;
+    if (!aligned(dweight, e) || !aligned(dbias, 4)) return SSM_ERR_ALIGN;
+    if (d.rows == 0) {
+        const Range rw = range_of(dweight, wn * e), rb = range_of(dbias, ko * 4);
+        if (overlaps(rw, rb)) return SSM_ERR_ALIAS;
+        const int rc = zero(dweight, wn * (int64_t)e, stream);
+        return rc != SSM_OK ? rc : zero(dbias, ko * 4, stream);
+    }
+    const bool act = d.activation != SSM_ACT_NONE, made = act || d.y_dtype != d.dtype;
+    if (!dy || (act && !pre) || (made && !dpre) || (dx && !weight) || (dweight && !x)) return SSM_ERR_NULL;
+    if (!aligned(dy, ey) || (act && !aligned(pre, e)) || (made && !aligned(dpre, e)) || !aligned(dx, e) || !aligned(x, e) ||
+        !aligned(weight, e))
+        return SSM_ERR_ALIGN;
+    const BackPlan b = back_plan(d);
+    if (b.total && (!workspace || workspace_bytes < (size_t)b.total)) return SSM_ERR_WORKSPACE;
+    if (b.total && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
+    const int64_t xs = d.x_stride ? d.x_stride : ki;
+    const Range ws = range_of(workspace, b.total);
+    const Range in[] = {range_of(dy, d.rows * ko * ey), range_of(act ? pre : nullptr, d.rows * ko * e),
+                        range_of(dweight ? x : nullptr, span(d.rows, xs, ki) * e), range_of(dx ? weight : nullptr, wn * e), ws};
+    const Range out[] = {range_of(made ? dpre : nullptr, d.rows * ko * e), range_of(dx, d.rows * ki * e),
+                         range_of(dweight, wn * e), range_of(dbias, ko * 4)};
+    for (int k = 0; k < 4; ++k) {
+        for (int j = 0; j < 5; ++j)
+            if (overlaps(out[k], in[j])) return SSM_ERR_ALIAS;
+        for (int j = 0; j < k; ++j)
+            if (overlaps(out[k], out[j])) return SSM_ERR_ALIAS;
+    }
+    for (int j = 0; j < 4; ++j)
+        if (overlaps(ws, in[j])) return SSM_ERR_ALIAS;
+    const bool bf = d.dtype == SSM_BF16;
+    float *sums = static_cast<float *>(workspace), *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + b.sums);
+    if (made || dbias) {
+        DpreParams q{dy, act ? pre : nullptr, made ? dpre : nullptr, dbias ? sums : nullptr, d.rows, ko, b.per, d.activation};
+        const bool four = ko % 4 == 0 && aligned(dy, 4 * ey) && (!act || aligned(pre, 4 * e)) && (!made || aligned(dpre, 4 * e));
+        const hipError_t r = !bf                   ? dpre_pass<float, float>(q, b.slabs, four, stream)
+                             : d.y_dtype == SSM_F32 ? dpre_pass<uint16_t, float>(q, b.slabs, four, stream)
+                                                    : dpre_pass<uint16_t, uint16_t>(q, b.slabs, four, stream);
+        if (r != hipSuccess) return SSM_ERR_HIP;
+        if (dbias) {
+            hipLaunchKernelGGL(proj_sum_kernel, dim3((unsigned)ceil_div(ko, kSumCols)), dim3(kSumCols * kSumRuns), 0, stream, sums,
+                               b.slabs, ko, dbias);
+            if (hipGetLastError() != hipSuccess) return SSM_ERR_HIP;
+        }
+    }
+    const void *dz = made ? dpre : dy;
+    ProjParams a{};
+    a.groups = (int)d.groups;
+    a.part = part;
+    a.q = dz;
+    a.ldq = ko;
+    a.gq = d.out;
+    a.wide = !bf;
+    if (dx) {
+        a.p = weight;
+        a.ldp = d.in;
+        a.gp = d.in * d.out;
+        a.I = d.in;
+        a.J = d.rows;
+        a.R = d.out;
+        a.out = dx;
+        a.ldo = ki;
+        a.go = d.in;
+        a.four = d.in % 4 == 0 && aligned(dx, 4 * e);
+        const hipError_t r = bf ? product<uint16_t, true, false>(a, b.dx, d.dtype, stream) : product<float, true, false>(a, b.dx, d.dtype, stream);
+        if (r != hipSuccess) return SSM_ERR_HIP;
+    }
+    if (dweight) {
+        a.p = x;
+        a.ldp = xs;
+        a.gp = d.in;
+        a.I = d.in;
+        a.J = d.out;
+        a.R = d.rows;
+        a.out = dweight;
+        a.ldo = d.in;
+        a.go = d.in * d.out;
+        a.four = d.in % 4 == 0 && aligned(dweight, 4 * e);
+        const hipError_t r = bf ? product<uint16_t, true, true>(a, b.dw, d.dtype, stream) : product<float, true, true>(a, b.dw, d.dtype, stream);
+        if (r != hipSuccess) return SSM_ERR_HIP;
+    }
+    return SSM_OK;
+}
