@@ -402,6 +402,10 @@ def _own_glr(s, c):
         return dict(y=y, h_last=h_last)
     y, h_last, saved = ssm.ssm_glr_fwd_save(*ins, h0=s["h0"], **opts)
     g = ssm.ssm_glr_bwd_saved(*ins, s["dy"], saved, h0=s["h0"], dh_last=s["dh_last"], want_dh0=s["h0"] is not None, **opts)
+    if s["gate"] is None and s["dy"].dtype == torch.float32:
+        # the plain form adds dh_last to the last token's dy where it is kept: a further pass on the same state goes
+        # on from there, on both sides
+        s["dy"][:, -1] += s["dh_last"]
     out = dict(y=y, h_last=h_last)
     out.update({n: v for n, v in g.items() if v is not None})
     return out
