@@ -166,7 +166,7 @@ template <typename T, bool TP, bool TQ> hipError_t product(ProjParams &a, Tiling
                       (TQ ? a.J : a.R) % per16 == 0;
     a.splits = (int)pl.splits;
     a.steps = (int)ceil_div(ceil_div(a.R, 128 / (int64_t)sizeof(T)), pl.splits);
-    const hipError_t e = fast ? launch_tiles<T, TP, TQ, true>(a, pl.tile, st) : launch_tiles<T, TP, TQ, false>(a, 64, st);
+    const hipError_t e = fast ? launch_tiles<T, TP, TQ, true>(a, a.four ? pl.tile : 64, st) : launch_tiles<T, TP, TQ, false>(a, 64, st);
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t n = (int64_t)a.groups * a.J * ceil_div(a.I, 4);
     hipLaunchKernelGGL((proj_join_kernel<T>), dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st, a);

@@ -84,19 +84,16 @@ template <typename T> __device__ __forceinline__ void proj_load4(const void *bas
     }
 }
 
-// Sums of columns i..i+3 (those below I) of output row j, finished and stored
-template <typename T>
+// pre of columns i..i+3 of output row j (with FOUR all below I, moved as one), finished and stored
+template <typename T, bool FOUR>
 __device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t j, int64_t i, float (&v)[4]) {
-    if (a.bias) {
-        const float *b = a.bias + g * a.I + i;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += i + e < a.I ? b[e] : 0.0f;
-    }
     const int64_t at = g * a.go + j * a.ldo + i;
-    if (a.four) {
+    if constexpr (FOUR) {
         if (a.pre) proj_store4<T>(a.pre, at, v);
+        if (a.act != kActNone) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = proj_act(v[e], a.act);
+            for (int e = 0; e < 4; ++e) v[e] = proj_act(v[e], a.act);
+        }
         if (a.res) {
             float r[4];
             if (a.wide) proj_load4<float>(a.res, at, r);
@@ -106,16 +103,33 @@ __device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t 
         }
         if (a.wide) proj_store4<float>(a.out, at, v);
         else proj_store4<T>(a.out, at, v);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (i + e >= a.I) break;
-        if (a.pre) proj_store1<T>(a.pre, at + e, v[e]);
-        float y = proj_act(v[e], a.act);
-        if (a.res) y += a.wide ? proj_load1<float>(a.res, at + e) : proj_load1<T>(a.res, at + e);
-        if (a.wide) proj_store1<float>(a.out, at + e, y);
-        else proj_store1<T>(a.out, at + e, y);
+        for (int e = 0; e < 4; ++e) {
+            if (i + e < a.I) {
+                if (a.pre) proj_store1<T>(a.pre, at + e, v[e]);
+                float y = proj_act(v[e], a.act);
+                if (a.res) y += a.wide ? proj_load1<float>(a.res, at + e) : proj_load1<T>(a.res, at + e);
+                if (a.wide) proj_store1<float>(a.out, at + e, y);
+                else proj_store1<T>(a.out, at + e, y);
+            }
+        }
+    }
+}
+
+// The bias of columns i..i+3
+__device__ __forceinline__ void proj_bias(const ProjParams &a, int g, int64_t i, float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = a.bias && i + e < a.I ? a.bias[g * a.I + i + e] : 0.0f;
+}
+
+template <bool FOUR> __device__ __forceinline__ void proj_keep(float *o, int64_t left, const float (&v)[4]) {
+    if constexpr (FOUR) {
+        *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (c < left) o[c] = v[c];
     }
 }
 
@@ -165,39 +179,37 @@ template <typename T, bool TURNED, int B, int W, bool FAST> struct ProjTile {
         }
     }
 
-    // Step s (values r0 = s kStep of R) into LDS
-    __device__ __forceinline__ void load(char *lds, int64_t s, int64_t R, int wave, int lane) const {
+    // Step s (values of r from s kStep), all of it inside the operand, straight into LDS
+    __device__ __forceinline__ void load(char *lds, int64_t s, int wave) const {
+        const char *b = base + s * kStep * (TURNED ? ld : 1) * (int64_t)sizeof(T);
+        // every lane's offset is inside the operand: the buffer's own bound is all that 32 bits reach
+        const __amdgpu_buffer_rsrc_t r = ssd_buffer(b, 0xffffffffu);
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (proj_lds *)(lds + (wave * kLoads + n) * 1024), 16, (int)off[n], 0, 0, 0);
+    }
+
+    // Any step, values past the last r as zeros
+    __device__ __forceinline__ void load_any(char *lds, int64_t s, int64_t R, int wave, int lane) const {
         const int64_t r0 = s * kStep;
         const char *b = base + (TURNED ? r0 * ld : r0) * (int64_t)sizeof(T);
-        if constexpr (FAST) {
-            if (r0 + kStep <= R) {
 #pragma unroll
-                for (int n = 0; n < kLoads; ++n)
-                    __builtin_amdgcn_global_load_lds((proj_glb *)(b + off[n]), (proj_lds *)(lds + (wave * kLoads + n) * 1024), 16, 0, 0);
+        for (int n = 0; n < kLoads; ++n) {
+            const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n) * kEach;
+            uint4 w = uint4{0, 0, 0, 0};
+            if constexpr (FAST) {
+                // a piece is on one side of the end whole
+                if (r0 + (TURNED ? row : c) < R) w = *reinterpret_cast<const uint4 *>(b + off[n]);
             } else {
-                // pieces past the last r are zeros (a piece is on one side whole)
-#pragma unroll
-                for (int n = 0; n < kLoads; ++n) {
-                    const int64_t r = r0 + (TURNED ? row_of(wave, lane, n) : piece_of(wave, lane, n) * kEach);
-                    uint4 v = uint4{0, 0, 0, 0};
-                    if (r < R) v = *reinterpret_cast<const uint4 *>(b + off[n]);
-                    *reinterpret_cast<uint4 *>(lds + ((wave * kLoads + n) * 64 + lane) * 16) = v;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int n = 0; n < kLoads; ++n) {
-                const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n) * kEach;
                 T v[kEach];
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {
                     const bool in = TURNED ? r0 + row < R && c + e < left : r0 + c + e < R && row < left;
                     v[e] = in ? *reinterpret_cast<const T *>(b + ((int64_t)row * ld + c + e) * (int64_t)sizeof(T)) : T(0);
                 }
-                uint4 w;
                 __builtin_memcpy(&w, v, 16);
-                *reinterpret_cast<uint4 *>(lds + ((wave * kLoads + n) * 64 + lane) * 16) = w;
             }
+            *reinterpret_cast<uint4 *>(lds + ((wave * kLoads + n) * 64 + lane) * 16) = w;
         }
     }
 
@@ -241,6 +253,7 @@ template <typename T, bool TP, bool TQ, int BI, int BJ, bool FAST>
 __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(ProjParams a) {
     typedef ProjShape<BI, BJ> S;
     constexpr int FI = S::kWI / 16, FJ = S::kWJ / 16;
+    constexpr bool FOUR = BI > 64;      // outputs that do not move in fours get the smallest tile
     typedef ProjTile<T, TP, BI, S::kWaves, FAST> TileP;
     typedef ProjTile<T, TQ, BJ, S::kWaves, FAST> TileQ;
     // two objects, so that the compiler knows a load into one from a read of the other
@@ -273,10 +286,17 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
 #pragma unroll
         for (int e = 0; e < FI; ++e) acc[f][e] = ssd_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+    auto load_any = [&](char *to, int64_t s) {
+        tp.load_any(to, s, a.R, wave, lane);
+        tq.load_any(to + TileP::kBytes, s, a.R, wave, lane);
+    };
     auto load = [&](char *to, int64_t s) {
-        if (s >= s1) return;
-        tp.load(to, s, a.R, wave, lane);
-        tq.load(to + TileP::kBytes, s, a.R, wave, lane);
+        if constexpr (FAST) {
+            tp.load(to, s, wave);
+            tq.load(to + TileP::kBytes, s, wave);
+        } else {
+            load_any(to, s);
+        }
     };
     auto multiply = [&](const char *from) {
 #pragma unroll
@@ -290,44 +310,64 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
             for (int f = 0; f < FJ; ++f)
 #pragma unroll
                 for (int e = 0; e < FI; ++e) proj_mul<T>(p[e], q[f], acc[f][e]);
+            // one half's fragments in registers at a time
+            if constexpr (BI == 256) __builtin_amdgcn_sched_barrier(0);
         }
     };
-    load(one, s0);
-    __syncthreads();
-    for (int64_t s = s0; s < s1; s += 2) {
-        load(two, s + 1);
-        multiply(one);
+    // A ragged last step, and one more where the whole ones are odd in number, go first
+    // and by themselves; the rest in pairs, each step loaded while the one before is multiplied.
+    const int64_t s2 = max(s0, min(s1, a.R / TileP::kStep));
+    const int odd = (int)((s2 - s0) & 1), alone = odd + (s1 > s2);
+    for (int k = 0; k < alone; ++k) {
+        load_any(two, odd && k == alone - 1 ? s0 : s1 - 1);
         __syncthreads();
-        if (s + 1 >= s1) break;
-        load(one, s + 2);
         multiply(two);
         __syncthreads();
     }
-
-    const int64_t jl = j0 + wj + (lane & 15), il = i0 + wi + 4 * (lane >> 4);
-#pragma unroll
-    for (int f = 0; f < FJ; ++f) {
-        const int64_t j = jl + 16 * f;
-        if (j >= a.J) break;
-#pragma unroll
-        for (int e = 0; e < FI; ++e) {
-            const int64_t i = il + 16 * e;
-            if (i >= a.I) break;
-            float v[4] = {acc[f][e][0], acc[f][e][1], acc[f][e][2], acc[f][e][3]};
-            if (a.splits == 1) {
-                proj_finish<T>(a, g, j, i, v);
-            } else {
-                float *o = a.part + (((int64_t)split * a.groups + g) * a.J + j) * a.I + i;
-                if ((a.I & 3) == 0) {
-                    *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (i + c < a.I) o[c] = v[c];
-                }
-            }
+    int64_t s = s0 + odd;
+    if (s < s2) {
+        load(one, s);
+        __syncthreads();
+        for (; s < s2; s += 2) {
+            load(two, s + 1);
+            multiply(one);
+            __syncthreads();
+            if (s + 2 < s2) load(one, s + 2);
+            multiply(two);
+            __syncthreads();
         }
     }
+
+    const int64_t jl = j0 + wj + (lane & 15), il = i0 + wi + 4 * (lane >> 4);
+    if (a.splits > 1) {
+        float *sums = a.part + ((int64_t)split * a.groups + g) * a.J * a.I;
+#pragma unroll
+        for (int f = 0; f < FJ; ++f)
+#pragma unroll
+            for (int e = 0; e < FI; ++e) {
+                const int64_t j = jl + 16 * f, i = il + 16 * e;
+                const float v[4] = {acc[f][e][0], acc[f][e][1], acc[f][e][2], acc[f][e][3]};
+                if (j < a.J && i < a.I) proj_keep<FOUR>(sums + j * a.I + i, a.I - i, v);
+            }
+        return;
+    }
+    float bias[FI][4];
+#pragma unroll
+    for (int e = 0; e < FI; ++e) proj_bias(a, g, il + 16 * e, bias[e]);
+#pragma unroll
+    for (int f = 0; f < FJ; ++f)
+#pragma unroll
+        for (int e = 0; e < FI; ++e) {
+            const int64_t j = jl + 16 * f, i = il + 16 * e;
+            float v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = acc[f][e][c] + bias[e][c];
+            if (j < a.J && i < a.I) {
+                if constexpr (FOUR) proj_finish<T, true>(a, g, j, i, v);
+                else if (a.four) proj_finish<T, true>(a, g, j, i, v);
+                else proj_finish<T, false>(a, g, j, i, v);
+            }
+        }
 }
 
 // Splits added in order, and finished: 4 columns of a row to a lane
@@ -348,7 +388,12 @@ template <typename T> __global__ __launch_bounds__(256) void proj_join_kernel(Pr
             for (int e = 0; e < 4; ++e) v[e] += i + e < a.I ? p[e] : 0.0f;
         }
     }
-    proj_finish<T>(a, (int)g, j, i, v);
+    float b[4];
+    proj_bias(a, (int)g, i, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += b[e];
+    if (a.four) proj_finish<T, true>(a, (int)g, j, i, v);
+    else proj_finish<T, false>(a, (int)g, j, i, v);
 }
 
 // A few rows (up to MJ): the weight is read once, 16 bytes a lane along r (one value
