@@ -16,7 +16,7 @@ namespace {
 using namespace ssm_detail;
 
 constexpr int64_t kMaxWidth = ((int64_t)1 << 22) - 1;   // of a row: a tile's lane offsets stay in 32 bits
-constexpr int kCus = 256;
+constexpr int kCus = 256, kMostSplits = 64;
 
 size_t esize(int t) { return t == SSM_BF16 ? 2 : 4; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -107,29 +107,38 @@ __global__ __launch_bounds__(256) void proj_zero_kernel(void *p, int64_t bytes) 
 // Products: which tile, how many splits
 
 struct Tiling {
-    int tile;         // 256, 128 or 64: its sides
-    int64_t splits;
+    int tile;         // 256, 128 or 64: a tile's sides
+    int64_t splits, steps;      // steps of r to a split
 };
 
-// The time of a product of J x I outputs over R, in units of one CU's steps. A step of
-// 128 bytes of r takes a CU kStep; workgroups in excess of what the CUs hold at once
-// come in rounds.
+// The time of a product of J x I outputs over R, in us, from how many workgroups a CU
+// gets: it holds `hold` of a tile at once, and a step of 128 bytes of r takes it
+// step[k] with k + 1 of them, next to `fixed` for a workgroup's first loads and its
+// output. Splits add their sums' traffic and a launch. Measured (bf16, us, tiles of 256
+// / 128 / 64, one split): 16384 x 2048 -> 4096 236 / 270 / 369; 8192 x 768 -> 1536 30.5
+// / 34.5 / 36.7; 2048 x 2048 -> 2048 39 (2 splits 41) / 31.5 / 27.7; 512 x 2048 -> 2048
+// 24 with 128, 12.7 with 64, 18.6 with 64 in two splits; fp32 8192 x 768 -> 1536 197 / 162 / 163.
 Tiling plan_for(int64_t I, int64_t J, int64_t R, int64_t groups, int dtype) {
+    struct Kind { int side, hold; double step[4], fixed; };
+    static const Kind narrow[] = {{256, 1, {1.75}, 8.0}, {128, 2, {0.75, 1.0}, 4.0}, {64, 4, {0.3, 0.42, 0.58, 0.74}, 2.5}};
+    static const Kind wide[] = {{256, 1, {7.3}, 12.0}, {128, 2, {2.2, 4.1}, 5.0}, {64, 4, {0.9, 1.2, 1.6, 2.1}, 2.5}};
     const int64_t every = ceil_div(R, dtype == SSM_BF16 ? 64 : 32);
-    struct { int side, hold; double step, fixed; } kinds[] = {{256, 1, 4.0, 10.0}, {128, 2, 2.4, 8.0}, {64, 4, 1.8, 6.0}};
-    Tiling best{128, 1};
+    Tiling best{128, 1, every};
     double least = 1e300;
-    for (const auto &k : kinds) {
+    for (const Kind &k : dtype == SSM_BF16 ? narrow : wide) {
         const int64_t tiles = ceil_div(I, k.side) * ceil_div(J, k.side) * groups;
-        for (int64_t s = 1; s <= 64 && s <= every; s = s < 4 ? s + 1 : s + s / 2) {
-            if (s > 1 && (tiles >= 2 * kCus * k.hold || every / s < 2)) break;
-            const double rounds = (double)ceil_div(tiles * s, kCus * k.hold);
-            double t = rounds * ((double)ceil_div(every, s) * k.step + k.fixed);
-            // the sums written and read, and a launch
-            if (s > 1) t += 30.0 + (double)I * J * groups * (8.0 * s + 4.0) / 2e6;
+        for (int64_t s = 1; s <= kMostSplits && s <= every; s = s < 4 ? s + 1 : s + s / 2) {
+            if (s > 1 && tiles * s > 4 * kCus * k.hold) break;
+            // an even number of steps to a split: they go in pairs
+            const int64_t each = s == 1 ? every : 2 * ceil_div(every, 2 * s), splits = ceil_div(every, each);
+            const double steps = (double)each;
+            const int64_t on = ceil_div(tiles * splits, kCus), rest = on % k.hold;
+            double t = (double)(on / k.hold) * (steps * k.step[k.hold - 1] + k.fixed);
+            if (rest) t += steps * k.step[rest - 1] + k.fixed;
+            if (splits > 1) t += 3.5 + (double)I * J * groups * (8.0 * splits + 4.0) / 4.5e6;
             if (t < least) {
                 least = t;
-                best = Tiling{k.side, s};
+                best = Tiling{k.side, splits, each};
             }
         }
     }
@@ -158,30 +167,26 @@ hipError_t launch_tiles(ProjParams &a, int tile, hipStream_t st) {
 }
 
 template <typename T, bool TP, bool TQ> hipError_t product(ProjParams &a, Tiling pl, int dtype, hipStream_t st) {
-    const int each = 16 / (int)sizeof(T);
-    const int64_t per16 = each;
+    const int64_t each = 16 / (int64_t)sizeof(T);
     // whether pieces of 16 bytes lie whole in rows (columns) and on 16-byte addresses
-    const bool fast = aligned(a.p, 16) && aligned(a.q, 16) && a.ldp % per16 == 0 && a.ldq % per16 == 0 &&
-                      (a.groups == 1 || (a.gp % per16 == 0 && a.gq % per16 == 0)) && (TP ? a.I : a.R) % per16 == 0 &&
-                      (TQ ? a.J : a.R) % per16 == 0;
+    const bool fast = aligned(a.p, 16) && aligned(a.q, 16) && a.ldp % each == 0 && a.ldq % each == 0 &&
+                      (a.groups == 1 || (a.gp % each == 0 && a.gq % each == 0)) && (TP ? a.I : a.R) % each == 0 &&
+                      (TQ ? a.J : a.R) % each == 0;
     a.splits = (int)pl.splits;
-    a.steps = (int)ceil_div(ceil_div(a.R, 128 / (int64_t)sizeof(T)), pl.splits);
-    const hipError_t e = fast ? launch_tiles<T, TP, TQ, true>(a, a.four ? pl.tile : 64, st) : launch_tiles<T, TP, TQ, false>(a, 64, st);
+    a.steps = (int)pl.steps;
+    const hipError_t e = fast ? launch_tiles<T, TP, TQ, true>(a, pl.tile, st) : launch_tiles<T, TP, TQ, false>(a, 64, st);
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t n = (int64_t)a.groups * a.J * ceil_div(a.I, 4);
-    hipLaunchKernelGGL((proj_join_kernel<T>), dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st, a);
+    const int64_t n = (int64_t)a.groups * a.J * a.I;
+    if (a.eight) hipLaunchKernelGGL((proj_join_kernel<T, 8>), dim3((unsigned)ceil_div(n / 8, 256)), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((proj_join_kernel<T, 1>), dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 template <typename T> hipError_t few(const ProjParams &a, hipStream_t st) {
-    const int64_t each = 16 / (int64_t)sizeof(T);
-    const bool fast = aligned(a.p, 16) && aligned(a.q, 16) && a.R % each == 0 && a.ldq % each == 0 &&
-                      (a.groups == 1 || a.gq % each == 0);
     const unsigned blocks = (unsigned)ceil_div(a.groups * a.I, 8);
 #define PROJ_FEW(M)                                                                                             \
     if (a.J <= M) {                                                                                             \
-        if (fast) hipLaunchKernelGGL((proj_few_kernel<T, M, true>), dim3(blocks), dim3(256), 0, st, a);         \
-        else hipLaunchKernelGGL((proj_few_kernel<T, M, false>), dim3(blocks), dim3(256), 0, st, a);             \
+        hipLaunchKernelGGL((proj_few_kernel<T, M>), dim3(blocks), dim3(256), 0, st, a);                         \
         return hipGetLastError();                                                                               \
     }
     PROJ_FEW(1) PROJ_FEW(2) PROJ_FEW(4) PROJ_FEW(8)
@@ -209,7 +214,7 @@ int check(const ssm_proj_desc *desc) {
     if (!mul_ok(d.rows, std::max(ki, ko), &n) || n > ((int64_t)1 << 38)) return SSM_ERR_SHAPE;
     const int64_t ti = ceil_div(d.in, 64), to = ceil_div(d.out, 64), tr = ceil_div(d.rows, 64);
     if (!grid_ok(std::max(tr * std::max(ti, to), ti * to) * d.groups, 256 * 2) ||
-        !grid_ok(ceil_div(std::max(std::max(d.rows * ki, d.rows * ko), d.in * ko), 1024) * 4 + 1, 256))
+        !grid_ok(ceil_div(std::max(std::max(d.rows * ki, d.rows * ko), d.in * ko), 256), 256))
         return SSM_ERR_SHAPE;
     return SSM_OK;
 }
@@ -308,7 +313,7 @@ extern "C" int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void
     a.splits = 1;
     a.act = d.activation;
     a.wide = d.y_dtype == SSM_F32;
-    a.four = d.out % 4 == 0 && aligned(y, 4 * ey) && aligned(residual, 4 * ey) && aligned(pre, 4 * e);
+    a.eight = d.out % 8 == 0 && aligned(y, 16) && aligned(residual, 16) && aligned(pre, 16);
     if (d.rows <= kFew) return status(d.dtype == SSM_BF16 ? few<uint16_t>(a, stream) : few<float>(a, stream));
     return status(d.dtype == SSM_BF16 ? product<uint16_t, false, false>(a, pl, d.dtype, stream)
                                       : product<float, false, false>(a, pl, d.dtype, stream));
@@ -383,7 +388,7 @@ extern "C" int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const voi
         a.out = dx;
         a.ldo = ki;
         a.go = d.in;
-        a.four = d.in % 4 == 0 && aligned(dx, 4 * e);
+        a.eight = d.in % 8 == 0 && aligned(dx, 16);
         const hipError_t r = bf ? product<uint16_t, true, false>(a, b.dx, d.dtype, stream) : product<float, true, false>(a, b.dx, d.dtype, stream);
         if (r != hipSuccess) return SSM_ERR_HIP;
     }
@@ -397,7 +402,7 @@ extern "C" int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const voi
         a.out = dweight;
         a.ldo = d.in;
         a.go = d.in * d.out;
-        a.four = d.in % 4 == 0 && aligned(dweight, 4 * e);
+        a.eight = d.in % 8 == 0 && aligned(dweight, 16);
         const hipError_t r = bf ? product<uint16_t, true, true>(a, b.dw, d.dtype, stream) : product<float, true, true>(a, b.dw, d.dtype, stream);
         if (r != hipSuccess) return SSM_ERR_HIP;
     }

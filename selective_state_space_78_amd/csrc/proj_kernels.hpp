@@ -16,8 +16,10 @@
 // read with the transposing LDS reads. bf16 products use the 16x16x32 instruction, fp32 ones
 // 16x16x4: full precision, four to a 16-byte piece.
 //
-// P is the instruction's first operand, so a lane holds 4 consecutive values of an output
-// row: bias, activation and residual are applied there, and stores are 8 or 16 bytes.
+// The sums then go through LDS, each wave's by itself, to lanes of 8 consecutive values of
+// an output row: bias, activation and residual are applied there, in fp32, and rows leave
+// in 16-byte stores of whole lines (stored from the accumulators, 8 bytes a lane over 16
+// rows, an output of 16384 x 4096 took 85 us instead of 40).
 //
 // Where tiles are few the reduction is split over workgroups: each writes its fp32 sums,
 // and a second kernel adds them in order and finishes as the first would.
@@ -40,7 +42,7 @@ struct ProjParams {
     int64_t ldo, go;            // elements from output row to row, from group to group
     float *part;                // splits > 1: (split, group, J, I)
     int ti, tj, groups, splits, steps;   // tiles; steps of r to a split
-    int act, wide, four;        // wide: the output is fp32; four: groups of 4 columns move as one
+    int act, wide, eight;       // wide: the output is fp32; eight: groups of 8 columns lie on 16-byte addresses
 };
 
 __device__ __forceinline__ float proj_sigmoid(float v) {
@@ -84,53 +86,59 @@ template <typename T> __device__ __forceinline__ void proj_load4(const void *bas
     }
 }
 
-// pre of columns i..i+3 of output row j (with FOUR all below I, moved as one), finished and stored
-template <typename T, bool FOUR>
-__device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t j, int64_t i, float (&v)[4]) {
-    const int64_t at = g * a.go + j * a.ldo + i;
-    if constexpr (FOUR) {
-        if (a.pre) proj_store4<T>(a.pre, at, v);
-        if (a.act != kActNone) {
+template <typename T, int N> __device__ __forceinline__ void proj_store(void *base, int64_t at, const float (&v)[N]) {
+    if constexpr (N == 1) {
+        proj_store1<T>(base, at, v[0]);
+    } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = proj_act(v[e], a.act);
+        for (int e = 0; e < N; e += sizeof(T) == 2 ? 8 : 4) {
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(base) + at) =
+                    uint4{ssd_pack(v[0], v[1]), ssd_pack(v[2], v[3]), ssd_pack(v[4], v[5]), ssd_pack(v[6], v[7])};
+            else
+                *reinterpret_cast<float4 *>(static_cast<T *>(base) + at + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
-        if (a.res) {
+    }
+}
+template <typename T, int N> __device__ __forceinline__ void proj_load(const void *base, int64_t at, float (&v)[N]) {
+    if constexpr (N == 1) {
+        v[0] = proj_load1<T>(base, at);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
             float r[4];
-            if (a.wide) proj_load4<float>(a.res, at, r);
-            else proj_load4<T>(a.res, at, r);
+            proj_load4<T>(base, at + e, r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += r[e];
-        }
-        if (a.wide) proj_store4<float>(a.out, at, v);
-        else proj_store4<T>(a.out, at, v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (i + e < a.I) {
-                if (a.pre) proj_store1<T>(a.pre, at + e, v[e]);
-                float y = proj_act(v[e], a.act);
-                if (a.res) y += a.wide ? proj_load1<float>(a.res, at + e) : proj_load1<T>(a.res, at + e);
-                if (a.wide) proj_store1<float>(a.out, at + e, y);
-                else proj_store1<T>(a.out, at + e, y);
-            }
+            for (int c = 0; c < 4; ++c) v[e + c] = r[c];
         }
     }
 }
 
-// The bias of columns i..i+3
-__device__ __forceinline__ void proj_bias(const ProjParams &a, int g, int64_t i, float (&v)[4]) {
+// The sums of N columns from i of output row j (1, or 8 on 16-byte addresses), finished and stored
+template <typename T, int N>
+__device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t j, int64_t i, const float (&bias)[N], float (&v)[N]) {
+    const int64_t at = g * a.go + j * a.ldo + i;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = a.bias && i + e < a.I ? a.bias[g * a.I + i + e] : 0.0f;
+    for (int e = 0; e < N; ++e) v[e] += bias[e];
+    if (a.pre) proj_store<T, N>(a.pre, at, v);
+    if (a.act != kActNone) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = proj_act(v[e], a.act);
+    }
+    if (a.res) {
+        float r[N];
+        if (a.wide) proj_load<float, N>(a.res, at, r);
+        else proj_load<T, N>(a.res, at, r);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += r[e];
+    }
+    if (a.wide) proj_store<float, N>(a.out, at, v);
+    else proj_store<T, N>(a.out, at, v);
 }
 
-template <bool FOUR> __device__ __forceinline__ void proj_keep(float *o, int64_t left, const float (&v)[4]) {
-    if constexpr (FOUR) {
-        *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+template <int N> __device__ __forceinline__ void proj_bias(const ProjParams &a, int g, int64_t i, float (&v)[N]) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (c < left) o[c] = v[c];
-    }
+    for (int e = 0; e < N; ++e) v[e] = a.bias && i + e < a.I ? a.bias[g * a.I + i + e] : 0.0f;
 }
 
 typedef __attribute__((address_space(3))) void proj_lds;
@@ -189,28 +197,36 @@ template <typename T, bool TURNED, int B, int W, bool FAST> struct ProjTile {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (proj_lds *)(lds + (wave * kLoads + n) * 1024), 16, (int)off[n], 0, 0, 0);
     }
 
-    // Any step, values past the last r as zeros
-    __device__ __forceinline__ void load_any(char *lds, int64_t s, int64_t R, int wave, int lane) const {
+    // Any step, into registers: values past the last r, or past the operand, are zeros.
+    // Pieces inside are read at whatever address they have.
+    __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int64_t s, int64_t R, int wave, int lane) const {
         const int64_t r0 = s * kStep;
         const char *b = base + (TURNED ? r0 * ld : r0) * (int64_t)sizeof(T);
 #pragma unroll
         for (int n = 0; n < kLoads; ++n) {
             const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n) * kEach;
-            uint4 w = uint4{0, 0, 0, 0};
+            v[n] = uint4{0, 0, 0, 0};
             if constexpr (FAST) {
                 // a piece is on one side of the end whole
-                if (r0 + (TURNED ? row : c) < R) w = *reinterpret_cast<const uint4 *>(b + off[n]);
+                if (r0 + (TURNED ? row : c) < R) v[n] = *reinterpret_cast<const uint4 *>(b + off[n]);
             } else {
-                T v[kEach];
+                const char *at = b + ((int64_t)row * ld + c) * (int64_t)sizeof(T);
+                const int64_t in = TURNED ? (r0 + row < R ? left - c : 0) : (row < left ? R - r0 - c : 0);   // values of the piece
+                if (in >= kEach) {
+                    __builtin_memcpy(&v[n], at, 16);
+                } else if (in > 0) {
+                    T w[kEach];
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const bool in = TURNED ? r0 + row < R && c + e < left : r0 + c + e < R && row < left;
-                    v[e] = in ? *reinterpret_cast<const T *>(b + ((int64_t)row * ld + c + e) * (int64_t)sizeof(T)) : T(0);
+                    for (int e = 0; e < kEach; ++e) w[e] = e < in ? reinterpret_cast<const T *>(at)[e] : T(0);
+                    __builtin_memcpy(&v[n], w, 16);
                 }
-                __builtin_memcpy(&w, v, 16);
             }
-            *reinterpret_cast<uint4 *>(lds + ((wave * kLoads + n) * 64 + lane) * 16) = w;
         }
+    }
+
+    __device__ __forceinline__ void put(char *lds, const uint4 (&v)[kLoads], int wave, int lane) const {
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) *reinterpret_cast<uint4 *>(lds + ((wave * kLoads + n) * 64 + lane) * 16) = v[n];
     }
 
     // Fragment of the 16 rows (columns) from `at`, of the step's half h: r running over
@@ -253,12 +269,11 @@ template <typename T, bool TP, bool TQ, int BI, int BJ, bool FAST>
 __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(ProjParams a) {
     typedef ProjShape<BI, BJ> S;
     constexpr int FI = S::kWI / 16, FJ = S::kWJ / 16;
-    constexpr bool FOUR = BI > 64;      // outputs that do not move in fours get the smallest tile
     typedef ProjTile<T, TP, BI, S::kWaves, FAST> TileP;
     typedef ProjTile<T, TQ, BJ, S::kWaves, FAST> TileQ;
     // two objects, so that the compiler knows a load into one from a read of the other
     __shared__ __attribute__((aligned(1024))) char one[TileP::kBytes + TileQ::kBytes];
-    __shared__ __attribute__((aligned(1024))) char two[TileP::kBytes + TileQ::kBytes];
+    __shared__ __attribute__((aligned(1024))) char two[FAST ? TileP::kBytes + TileQ::kBytes : 16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
 
     // Workgroups go to the 8 XCDs in turn: each gets a run of consecutive tiles, 8 rows of tiles deep
@@ -286,17 +301,18 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
 #pragma unroll
         for (int e = 0; e < FI; ++e) acc[f][e] = ssd_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto load_any = [&](char *to, int64_t s) {
-        tp.load_any(to, s, a.R, wave, lane);
-        tq.load_any(to + TileP::kBytes, s, a.R, wave, lane);
+    uint4 vp[TileP::kLoads], vq[TileQ::kLoads];
+    auto fetch = [&](int64_t s) {
+        tp.fetch(vp, s, a.R, wave, lane);
+        tq.fetch(vq, s, a.R, wave, lane);
+    };
+    auto put = [&](char *to) {
+        tp.put(to, vp, wave, lane);
+        tq.put(to + TileP::kBytes, vq, wave, lane);
     };
     auto load = [&](char *to, int64_t s) {
-        if constexpr (FAST) {
-            tp.load(to, s, wave);
-            tq.load(to + TileP::kBytes, s, wave);
-        } else {
-            load_any(to, s);
-        }
+        tp.load(to, s, wave);
+        tq.load(to + TileP::kBytes, s, wave);
     };
     auto multiply = [&](const char *from) {
 #pragma unroll
@@ -314,93 +330,129 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
             if constexpr (BI == 256) __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // A ragged last step, and one more where the whole ones are odd in number, go first
-    // and by themselves; the rest in pairs, each step loaded while the one before is multiplied.
-    const int64_t s2 = max(s0, min(s1, a.R / TileP::kStep));
-    const int odd = (int)((s2 - s0) & 1), alone = odd + (s1 > s2);
-    for (int k = 0; k < alone; ++k) {
-        load_any(two, odd && k == alone - 1 ? s0 : s1 - 1);
-        __syncthreads();
-        multiply(two);
-        __syncthreads();
-    }
-    int64_t s = s0 + odd;
-    if (s < s2) {
-        load(one, s);
-        __syncthreads();
-        for (; s < s2; s += 2) {
-            load(two, s + 1);
-            multiply(one);
+    if constexpr (FAST) {
+        // A ragged last step, and one more where the whole ones are odd in number, go first and by
+        // themselves; the rest in pairs, each step loaded while the one before is multiplied.
+        const int64_t s2 = max(s0, min(s1, a.R / TileP::kStep));
+        const int odd = (int)((s2 - s0) & 1), alone = odd + (s1 > s2);
+        for (int k = 0; k < alone; ++k) {
+            fetch(odd && k == alone - 1 ? s0 : s1 - 1);
+            put(two);
             __syncthreads();
-            if (s + 2 < s2) load(one, s + 2);
             multiply(two);
             __syncthreads();
         }
+        int64_t s = s0 + odd;
+        if (s < s2) {
+            load(one, s);
+            __syncthreads();
+            for (; s < s2; s += 2) {
+                load(two, s + 1);
+                multiply(one);
+                __syncthreads();
+                if (s + 2 < s2) load(one, s + 2);
+                multiply(two);
+                __syncthreads();
+            }
+        }
+    } else if (s0 < s1) {
+        // through registers: the next step is on its way while this one is multiplied
+        fetch(s0);
+        for (int64_t s = s0; s < s1; ++s) {
+            put(one);
+            __syncthreads();
+            if (s + 1 < s1) fetch(s + 1);
+            multiply(one);
+            __syncthreads();
+        }
     }
 
-    const int64_t jl = j0 + wj + (lane & 15), il = i0 + wi + 4 * (lane >> 4);
-    if (a.splits > 1) {
-        float *sums = a.part + ((int64_t)split * a.groups + g) * a.J * a.I;
+    // A wave's sums in parts of RJ rows: rows of WI floats, their 16-byte pieces laid out by an
+    // exclusive or with the row's low bits.
+    constexpr int WI = S::kWI, RJ = S::kWJ > 64 ? 64 : S::kWJ, kPart = RJ * WI * 4;
+    constexpr int kIn = (TileP::kBytes + TileQ::kBytes) / kPart;      // waves that fit the first object
+    static_assert(kIn >= S::kWaves || (FAST && 2 * kIn >= S::kWaves));
+    char *mine = kIn >= S::kWaves || wave < kIn ? one + wave * kPart : two + (wave - kIn) * kPart;
+    float *sums = a.splits > 1 ? a.part + ((int64_t)split * a.groups + g) * a.J * a.I : nullptr;
 #pragma unroll
-        for (int f = 0; f < FJ; ++f)
+    for (int part = 0; part < S::kWJ / RJ; ++part) {
+        const int64_t jp = j0 + wj + part * RJ;
+#pragma unroll
+        for (int f = 0; f < RJ / 16; ++f)
 #pragma unroll
             for (int e = 0; e < FI; ++e) {
-                const int64_t j = jl + 16 * f, i = il + 16 * e;
-                const float v[4] = {acc[f][e][0], acc[f][e][1], acc[f][e][2], acc[f][e][3]};
-                if (j < a.J && i < a.I) proj_keep<FOUR>(sums + j * a.I + i, a.I - i, v);
+                const int row = 16 * f + (lane & 15), c = 4 * e + (lane >> 4);
+                const ssd_f32x4 &v = acc[part * (RJ / 16) + f][e];
+                *reinterpret_cast<float4 *>(mine + row * (WI * 4) + ((c ^ (row & 7)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
             }
-        return;
-    }
-    float bias[FI][4];
-#pragma unroll
-    for (int e = 0; e < FI; ++e) proj_bias(a, g, il + 16 * e, bias[e]);
-#pragma unroll
-    for (int f = 0; f < FJ; ++f)
-#pragma unroll
-        for (int e = 0; e < FI; ++e) {
-            const int64_t j = jl + 16 * f, i = il + 16 * e;
-            float v[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = acc[f][e][c] + bias[e][c];
-            if (j < a.J && i < a.I) {
-                if constexpr (FOUR) proj_finish<T, true>(a, g, j, i, v);
-                else if (a.four) proj_finish<T, true>(a, g, j, i, v);
-                else proj_finish<T, false>(a, g, j, i, v);
+        __builtin_amdgcn_wave_barrier();
+        if (a.eight) {
+            constexpr int kAcross = WI / 8, kRows = 64 / kAcross;     // lanes to a row, rows at a time
+            const int c = 2 * (lane % kAcross), r0 = lane / kAcross;
+            const int64_t i = i0 + wi + 4 * c;
+            float bias[8];
+            proj_bias<8>(a, g, i, bias);
+#pragma unroll 2
+            for (int n = 0; n < RJ; n += kRows) {
+                const int row = n + r0;
+                const char *at = mine + row * (WI * 4);
+                const float4 x = *reinterpret_cast<const float4 *>(at + ((c ^ (row & 7)) << 4));
+                const float4 y = *reinterpret_cast<const float4 *>(at + (((c + 1) ^ (row & 7)) << 4));
+                float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                const int64_t j = jp + row;
+                if (j < a.J && i < a.I) {
+                    if (sums) proj_store<float, 8>(sums, j * a.I + i, v);
+                    else proj_finish<T, 8>(a, g, j, i, bias, v);
+                }
+            }
+        } else {
+            constexpr int kRows = 64 / WI;
+            const int c = lane % WI;
+            const int64_t i = i0 + wi + c;
+            float bias[1];
+            proj_bias<1>(a, g, i, bias);
+#pragma unroll 2
+            for (int n = 0; n < RJ; n += kRows) {
+                const int row = n + lane / WI;
+                float v[1] = {*reinterpret_cast<const float *>(mine + row * (WI * 4) + (((c >> 2) ^ (row & 7)) << 4) + (c & 3) * 4)};
+                const int64_t j = jp + row;
+                if (j < a.J && i < a.I) {
+                    if (sums) sums[j * a.I + i] = v[0];
+                    else proj_finish<T, 1>(a, g, j, i, bias, v);
+                }
             }
         }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
-// Splits added in order, and finished: 4 columns of a row to a lane
-template <typename T> __global__ __launch_bounds__(256) void proj_join_kernel(ProjParams a) {
-    const uint32_t cols = (uint32_t)((a.I + 3) / 4);
+// Splits added in order, and finished: 8 columns of a row to a lane, or one
+template <typename T, int N> __global__ __launch_bounds__(256) void proj_join_kernel(ProjParams a) {
+    const uint32_t cols = (uint32_t)(a.I / N);
     const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x, row = k / cols;
     if (row >= (int64_t)a.groups * a.J) return;
-    const int64_t i = (k - row * cols) * 4, g = row / a.J, j = row - g * a.J;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t i = (k - row * cols) * N, g = row / a.J, j = row - g * a.J;
+    float v[N], bias[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = 0.0f;
     const int64_t step = (int64_t)a.groups * a.J * a.I;
     const float *p = a.part + row * a.I + i;
+#pragma unroll 4
     for (int s = 0; s < a.splits; ++s, p += step) {
-        if ((a.I & 3) == 0) {
-            const float4 r = *reinterpret_cast<const float4 *>(p);
-            v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
-        } else {
+        float r[N];
+        proj_load<float, N>(p, 0, r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += i + e < a.I ? p[e] : 0.0f;
-        }
+        for (int e = 0; e < N; ++e) v[e] += r[e];
     }
-    float b[4];
-    proj_bias(a, (int)g, i, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += b[e];
-    if (a.four) proj_finish<T, true>(a, (int)g, j, i, v);
-    else proj_finish<T, false>(a, (int)g, j, i, v);
+    proj_bias<N>(a, (int)g, i, bias);
+    proj_finish<T, N>(a, (int)g, j, i, bias, v);
 }
 
-// A few rows (up to MJ): the weight is read once, 16 bytes a lane along r (one value
-// where rows are not aligned), two of its rows to a wave; the products are ordinary
-// fp32 ones. Bound by the weight's bytes.
-template <typename T, int MJ, bool FAST> __global__ __launch_bounds__(256) void proj_few_kernel(ProjParams a) {
-    constexpr int E = FAST ? 16 / (int)sizeof(T) : 1, NI = 2;
+// A few rows (up to MJ): the weight is read once, 16 bytes a lane along r (at any
+// address), two of its rows to a wave; the products are ordinary fp32 ones. Bound by
+// the weight's bytes.
+template <typename T, int MJ> __global__ __launch_bounds__(256) void proj_few_kernel(ProjParams a) {
+    constexpr int E = 16 / (int)sizeof(T), NI = 2;
     const int lane = threadIdx.x & 63;
     const int64_t total = a.groups * a.I;
     const int64_t n0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * NI;
@@ -415,24 +467,23 @@ template <typename T, int MJ, bool FAST> __global__ __launch_bounds__(256) void 
 #pragma unroll
         for (int m = 0; m < MJ; ++m) acc[n][m] = 0.0f;
     }
+    const bool apart = x[1] != x[0];        // the wave's two rows lie in two groups
     auto get = [](const T *p, float (&v)[E]) {
-        if constexpr (!FAST) {
-            v[0] = proj_load1<T>(p, 0);
-        } else if constexpr (sizeof(T) == 2) {
-            const uint4 r = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+        uint32_t u[4];
+        __builtin_memcpy(u, p, 16);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 2) {
                 v[2 * e] = __uint_as_float(u[e] << 16);
                 v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            } else {
+                v[e] = __uint_as_float(u[e]);
             }
-        } else {
-            const float4 r = *reinterpret_cast<const float4 *>(p);
-            v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
         }
     };
+    const int64_t whole = a.R / E * E;
 #pragma unroll 4
-    for (int64_t r = (int64_t)lane * E; r < a.R; r += 64 * E) {
+    for (int64_t r = (int64_t)lane * E; r < whole; r += 64 * E) {
         float wv[NI][E];
 #pragma unroll
         for (int n = 0; n < NI; ++n) get(w[n] + r, wv[n]);
@@ -443,11 +494,19 @@ template <typename T, int MJ, bool FAST> __global__ __launch_bounds__(256) void 
             get(x[0] + m * a.ldq + r, xv);
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
-                // the wave's two rows lie in two groups only where one ends
-                if (n > 0 && x[n] != x[0]) get(x[n] + m * a.ldq + r, xv);
+                if (n > 0 && apart) get(x[n] + m * a.ldq + r, xv);
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[n][m] = fmaf(wv[n][e], xv[e], acc[n][m]);
             }
+        }
+    }
+    if (whole + lane < a.R) {
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const float wv = proj_load1<T>(w[n], whole + lane);
+#pragma unroll
+            for (int m = 0; m < MJ; ++m)
+                if (m < a.J) acc[n][m] = fmaf(wv, proj_load1<T>(x[n], m * a.ldq + whole + lane), acc[n][m]);
         }
     }
 #pragma unroll
