@@ -21,7 +21,7 @@
 // relaxed device-scope atomics: no fence, no cache write-back.
 //
 // Backward: g_t = dy_t gate_t + a_{t+1} g_{t+1}, by the same maps from the end, with
-// the states recomputed from the ones that the forward kept every 128 tokens. With
+// the states recomputed from the ones that the forward kept every 64 tokens. With
 // w = a (a i x s / m - s h_{t-1}):  dx = g m i, digate = g m i x (1 - i), drgate =
 // g w (1 - r), dlam = sigmoid(lam) / softplus(lam) sum g w. s / m goes to 0 with s,
 // so an open recurrence gate (a = 1) has gradients.
@@ -43,12 +43,18 @@
 #include "matrix_ops.hpp"
 #include "scan_kernels.hpp"
 
+// Products and sums are fused where fmaf says so and nowhere else: every form of a kernel
+// (single channels, pairs) then rounds alike
+#pragma clang fp contract(off)
+
 namespace {
 
 using namespace ssm_detail;
 
-constexpr int kThreads = 512, kStreams = 16, kRow = 32;   // lanes to a token's row of a tile
-constexpr int kKeep = 128;                                // tokens from one kept state to the next
+constexpr int kRow = 32;                                  // lanes to a token's row of a tile
+constexpr int kFwdStreams = 16, kBwdStreams = 8;          // to a workgroup, of kRow lanes each
+constexpr int kBwdTokens = 8;                             // of a stream
+constexpr int kKeep = kBwdStreams * kBwdTokens;           // tokens from one kept state to the next
 constexpr int kBack = 8;                                  // chunks that are looked back over
 constexpr int64_t kMaxStride = (1 << 24) - 1;             // lane offsets stay in 32 bits
 constexpr float kLog2e = 1.4426950408889634f;
@@ -106,18 +112,41 @@ __device__ __forceinline__ float sigm(float v, float &e) {
 // 1 - sigmoid to its own digits
 __device__ __forceinline__ float one_minus(float sig, float e) { return e > 1.0f ? 1.0f - sig : e * sig; }
 
-// a = exp(-s) and 1 - a^2, s >= 0. 1 - a = s - s^2 / 2 + ..., fitted up to s = 1/2 to 1.5e-9 of itself.
-__device__ __forceinline__ float decay(float s, float &w) {
+// a = exp(-s) and w = 1 - a^2, 0 <= s < 1/2: 1 - a = s - s^2 / 2 + ..., fitted to 1.5e-9 of itself
+__device__ __forceinline__ float decay_near(float s, float &w) {
     float q = fmaf(s, -0.0011259224265813828f, 0.008193295449018478f);
     q = fmaf(s, q, -0.04163204878568649f);
     q = fmaf(s, q, 0.16666288673877716f);
     q = fmaf(s, q, -0.49999985098838806f);
-    const float near = fmaf(s, s * q, s), ex = __builtin_amdgcn_exp2f(s * -kLog2e);
-    const bool small = s < 0.5f;
-    const float em = small ? near : 1.0f - ex, a = small ? 1.0f - near : ex;
+    const float em = fmaf(s, s * q, s), a = 1.0f - em;
     w = fmaf(em, a, em);
     return a;
 }
+
+// The same for s beyond (and NaN)
+__device__ __forceinline__ void decay_far(float s, float &a, float &w) {
+    const float ex = __builtin_amdgcn_exp2f(s * -kLog2e), em = 1.0f - ex;
+    if (!(s < 0.5f)) {
+        a = ex;
+        w = fmaf(em, ex, em);
+    }
+}
+
+// Whether every rate of the wave keeps s below 1/2 (decays that last more than 1.6 tokens
+// with the gate open, as trained and initial ones do): the exponential is then left out.
+template <int VEC> __device__ __forceinline__ bool all_near(const float (&k)[VEC]) {
+    bool y = true;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) y = y && k[c] < 0.5f;
+    return __all(y);
+}
+
+// Has the compiler form v at this point
+__device__ __forceinline__ void here(float &v) { asm volatile("" : "+v"(v)); }
+
+// Has the compiler take what was read as it is from here on, not what was formed of it
+__device__ __forceinline__ void again(uint32_t &v) { asm volatile("" : "+v"(v)); }
+template <typename R> __device__ __forceinline__ void again(R &) {}   // other types take no fewer registers
 
 __device__ __forceinline__ bool is_reset(float P) { return __float_as_uint(P) == 0x80000000u; }
 
@@ -147,8 +176,9 @@ template <typename W> __device__ __forceinline__ void post(W *p, W v) {
 }
 
 // Streams' maps of a chunk, and the state before it
-template <int VEC> struct Shared {
-    float2 map[kStreams][kRow * VEC];
+template <int VEC, int NS> struct Shared {
+    float2 map[NS][kRow * VEC];
+    float2 back[kBack][64];      // a lane's own
     float start[kRow * VEC];
     float rate[kRow * VEC];
     uint32_t tile;
@@ -160,7 +190,7 @@ struct Place {
     int64_t c0;       // first channel
 };
 
-template <int VEC> __device__ __forceinline__ Place place(const GlrParams &p, Shared<VEC> &sh) {
+template <int VEC, int NS> __device__ __forceinline__ Place place(const GlrParams &p, Shared<VEC, NS> &sh) {
     uint32_t t = blockIdx.x;
     if (p.ticket) {
         if (threadIdx.x == 0) sh.tile = atomicAdd(p.ticket, 1u);
@@ -176,100 +206,63 @@ template <int VEC> __device__ __forceinline__ Place place(const GlrParams &p, Sh
     return q;
 }
 
-// Wave 0: the chunk's map from its streams', in order of the direction; the state
-// before the chunk by looking back; the state behind it published. `first` is the
-// state before the sequence. All 64 lanes take part, the upper half as copies.
-template <int VEC, bool RESET, bool REV>
-__device__ __forceinline__ void join_chunks(const GlrParams &p, Shared<VEC> &sh, const Place &at, const float (&first)[VEC],
-                                            int lane, int64_t ch, bool ok) {
-    const int l = (lane & (kRow - 1)) * VEC;
-    const bool write = ok && lane < kRow;
-    float P[VEC], H[VEC], h[VEC];
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) { P[c] = 1.0f; H[c] = 0.0f; }
-    const bool last = at.k == p.chunks - 1;
+// Wave 0, a channel to a lane: the chunk's map from its streams', in order of the
+// direction; the state before the chunk by looking back; the state behind it published.
+// `first` is the state before the sequence (NULL: 0). Lanes past the channels go along
+// with the last one.
+template <bool RESET, bool REV, int VEC, int NS>
+__device__ __forceinline__ void join_chunks(const GlrParams &p, Shared<VEC, NS> &sh, const Place &at, const float *first, int lane) {
+    const int l = lane < kRow * VEC ? lane : kRow * VEC - 1;
+    const int64_t ch = min(at.c0 + l, p.dim - 1);
+    const bool write = at.c0 + lane < p.dim && lane < kRow * VEC, last = at.k == p.chunks - 1;
+    float P = 1.0f, H = 0.0f, h = 0.0f;
     if (!last) {
 #pragma unroll 4
-        for (int s = 0; s < kStreams; ++s)
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                const float2 m = sh.map[REV ? kStreams - 1 - s : s][l + c];
-                H[c] = behind<RESET>(m.x, m.y, H[c]);
-                P[c] = both<RESET>(P[c], m.x);
-            }
+        for (int s = 0; s < NS; ++s) {
+            const float2 m = sh.map[REV ? NS - 1 - s : s][l];
+            H = behind<RESET>(m.x, m.y, H);
+            P = both<RESET>(P, m.x);
+        }
     }
     const int64_t row = (int64_t)p.batch * p.dim;
     const int64_t mine = ((int64_t)at.k * p.batch + at.b) * p.dim + ch;
     if (at.k == 0) {
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) h[c] = first[c];
+        if (first) h = first[(int64_t)at.b * p.dim + ch];
     } else {
-        float bp[kBack][VEC], bh[kBack][VEC];
-        int found = -1;
         bool published = last;
-#pragma unroll
-        for (int w = 0; w < kBack; ++w) {
-            if (found >= 0) continue;
-            const int64_t there = mine - (w + 1) * row;      // not reached before chunk 0, whose state comes first
-            for (;;) {
-                uint32_t s[VEC];
-                bool has = true;
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    s[c] = peek(p.state + there + c);
-                    has = has && s[c] != kNone;
-                }
-                if (__all(has)) {
-#pragma unroll
-                    for (int c = 0; c < VEC; ++c) h[c] = __uint_as_float(s[c]);
-                    found = w;
-                    break;
-                }
-                if (!published) {
-                    if (write)
-#pragma unroll
-                        for (int c = 0; c < VEC; ++c)
-                            post(p.map + mine + c, (unsigned long long)word_of(P[c]) | ((unsigned long long)word_of(H[c]) << 32));
-                    published = true;
-                }
-                // chunk 0 publishes no map: its state is all that there is to wait for
-                if (w < kBack - 1 && at.k - 1 - w > 0) {
-                    unsigned long long m[VEC];
-                    has = true;
-#pragma unroll
-                    for (int c = 0; c < VEC; ++c) {
-                        m[c] = peek(p.map + there + c);
-                        has = has && m[c] != ~0ull;
-                    }
-                    if (__all(has)) {
-#pragma unroll
-                        for (int c = 0; c < VEC; ++c) {
-                            bp[w][c] = __uint_as_float((uint32_t)m[c]);
-                            bh[w][c] = __uint_as_float((uint32_t)(m[c] >> 32));
-                        }
-                        break;
-                    }
-                }
-                __builtin_amdgcn_s_sleep(1);
+        int w = 0;                            // chunks back whose maps lie in sh.back
+        int64_t there = mine - row;           // not reached before chunk 0, whose state comes first
+        for (;;) {
+            const uint32_t s = peek(p.state + there);
+            if (__all(s != kNone)) {
+                h = __uint_as_float(s);
+                break;
             }
+            if (!published) {
+                if (write) post(p.map + mine, (unsigned long long)word_of(P) | ((unsigned long long)word_of(H) << 32));
+                published = true;
+            }
+            // chunk 0 publishes no map: its state is all that there is to wait for
+            if (w < kBack && at.k - 1 - w > 0) {
+                const unsigned long long m = peek(p.map + there);
+                if (__all(m != ~0ull)) {
+                    sh.back[w][lane] = make_float2(__uint_as_float((uint32_t)m), __uint_as_float((uint32_t)(m >> 32)));
+                    there -= row;
+                    ++w;
+                    continue;
+                }
+            }
+            __builtin_amdgcn_s_sleep(1);
         }
-#pragma unroll
-        for (int w = kBack - 1; w >= 0; --w)
-            if (w < found)
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(bp[w][c], bh[w][c], h[c]);
+        while (--w >= 0) h = behind<RESET>(sh.back[w][lane].x, sh.back[w][lane].y, h);
     }
-    if (!last && write)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) post(p.state + mine + c, word_of(behind<RESET>(P[c], H[c], h[c])));
-    if (lane < kRow)
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) sh.start[l + c] = h[c];
+    if (!last && write) post(p.state + mine, word_of(behind<RESET>(P, H, h)));
+    if (lane < kRow * VEC) sh.start[lane] = h;
 }
 
 // The state before a stream, in order of the direction
-template <int VEC, bool RESET, bool REV>
-__device__ __forceinline__ void stream_start(const Shared<VEC> &sh, int wave, int half, int l, float (&h)[VEC]) {
+template <bool RESET, bool REV, int VEC, int NS>
+__device__ __forceinline__ void stream_start(const Shared<VEC, NS> &sh, int wave, int half, int l, float (&h)[VEC]) {
 #pragma unroll
     for (int c = 0; c < VEC; ++c) h[c] = sh.start[l + c];
     if constexpr (!REV) {
@@ -282,7 +275,7 @@ __device__ __forceinline__ void stream_start(const Shared<VEC> &sh, int wave, in
             h[c] = half ? v : h[c];
         }
     } else {
-        for (int s = kStreams - 1; s > 2 * wave + 1; --s)
+        for (int s = NS - 1; s > 2 * wave + 1; --s)
 #pragma unroll
             for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(sh.map[s][l + c].x, sh.map[s][l + c].y, h[c]);
 #pragma unroll
@@ -293,33 +286,50 @@ __device__ __forceinline__ void stream_start(const Shared<VEC> &sh, int wave, in
     }
 }
 
-// One token's piece of a lane. Whole chunks: a base that is the same for the wave and
-// a lane offset of 32 bits; in the last, ragged one rows past the end read the last row.
-template <typename R, int TT>
-__device__ __forceinline__ void rows(const void *base, int64_t row0, int64_t stride, uint32_t half_rows, int64_t ch, int esz,
-                                     bool whole, int64_t left, R (&out)[TT]) {
-    const char *b = static_cast<const char *>(base) + row0 * stride * esz;
-    if (whole) {
-        const uint32_t off = (half_rows * (uint32_t)stride + (uint32_t)ch) * (uint32_t)esz;
-        const int64_t step = stride * esz;
+template <typename R> __device__ __forceinline__ R bload(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
+    if constexpr (sizeof(R) == 2) return __builtin_bit_cast(R, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane_off, (int)off, 0));
+    else if constexpr (sizeof(R) == 4) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, 0));
+    else return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_off, (int)off, 0));
+}
+template <typename R> __device__ __forceinline__ void bstore(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off, R v) {
+    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, (int)lane_off, (int)off, 0);
+    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, (int)lane_off, (int)off, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(ssd_u32x2, v), r, (int)lane_off, (int)off, 0);
+}
+
+// A wave's rows of one tensor, from its first token's: a lane offset that stays, and the
+// token's own, which is the same for the wave (a scalar register: no address arithmetic in
+// the lanes). Offsets reach 32 rows: below 2^31 bytes. In the last, ragged chunk, rows past
+// the end read the last row.
+struct Rows {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t off, step;
+
+    __device__ __forceinline__ Rows(const void *base, int64_t row0, int64_t stride, uint32_t half_rows, int64_t ch, int esz)
+        : r(ssd_buffer(static_cast<const char *>(base) + row0 * stride * esz, 0xffffffffu)),
+          off((half_rows * (uint32_t)stride + (uint32_t)ch) * (uint32_t)esz), step((uint32_t)stride * (uint32_t)esz) {}
+
+    template <typename R, int TT> __device__ __forceinline__ void load(bool whole, uint32_t half_rows, int64_t left, R (&out)[TT]) const {
+        if (whole) {
 #pragma unroll
-        for (int j = 0; j < TT; ++j) out[j] = *reinterpret_cast<const R *>(b + j * step + off);
-    } else {
+            for (int j = 0; j < TT; ++j) out[j] = bload<R>(r, off, j * step);
+        } else {
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const int64_t r = min((int64_t)half_rows + j, left - 1);
-            out[j] = *reinterpret_cast<const R *>(b + (r * stride + ch) * esz);
+            for (int j = 0; j < TT; ++j) {
+                const uint32_t back = (uint32_t)max((int64_t)0, (int64_t)half_rows + j - (left - 1));   // rows past the last
+                out[j] = bload<R>(r, off + (j - back) * step, 0);
+            }
         }
     }
-}
+};
 
 // Forward: TT tokens to a stream. y NULL: the kept states and h_last alone.
 template <typename T, int VEC, int TT, bool RESET>
-__global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
+__global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParams p) {
     typedef typename Raw<T, VEC>::type R;
-    constexpr int CT = kStreams * TT;
-    __shared__ Shared<VEC> sh;
-    const Place at = place<VEC>(p, sh);
+    constexpr int CT = kFwdStreams * TT;
+    __shared__ Shared<VEC, kFwdStreams> sh;
+    const Place at = place(p, sh);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
     const int l = (lane & (kRow - 1)) * VEC;
     const bool ok = at.c0 + l < p.dim;
@@ -332,9 +342,9 @@ __global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
     const uint32_t hr = half * TT;
 
     R rx[TT], rr[TT], ri[TT];
-    rows<R, TT>(p.rg, row0, p.rs, hr, ch, sizeof(T), whole, lf, rr);
-    rows<R, TT>(p.ig, row0, p.is, hr, ch, sizeof(T), whole, lf, ri);
-    rows<R, TT>(p.x, row0, p.xs, hr, ch, sizeof(T), whole, lf, rx);
+    Rows(p.rg, row0, p.rs, hr, ch, sizeof(T)).load(whole, hr, lf, rr);
+    Rows(p.ig, row0, p.is, hr, ch, sizeof(T)).load(whole, hr, lf, ri);
+    Rows(p.x, row0, p.xs, hr, ch, sizeof(T)).load(whole, hr, lf, rx);
     if (threadIdx.x < kRow * VEC) sh.rate[threadIdx.x] = p.rate * soft_plus(p.lam[min(at.c0 + (int64_t)threadIdx.x, p.dim - 1)]);
     __syncthreads();
     float k[VEC];
@@ -348,43 +358,59 @@ __global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
         }
     }
     float a[TT][VEC], b[TT][VEC], P[VEC], H[VEC];
+    const bool near = all_near<VEC>(k);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) { P[c] = 1.0f; H[c] = 0.0f; }
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        float x[VEC], r[VEC], i[VEC];
-        widen(rx[j], x);
-        widen(rr[j], r);
-        widen(ri[j], i);
-        const bool in = whole || (int64_t)hr + j < left;
+    for (int j0 = 0; j0 < TT; j0 += 2) {
+        float s[2][VEC], w[2][VEC];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            float e, w;
-            const float s = k[c] * sigm(r[c], e);
-            a[j][c] = decay(s, w);
-            float m = __builtin_amdgcn_sqrtf(w);
-            if constexpr (RESET) {
-                if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; }
+        for (int n = 0; n < 2; ++n) {
+            float r[VEC];
+            widen(rr[j0 + n], r);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float e;
+                s[n][c] = k[c] * sigm(r[c], e);
+                a[j0 + n][c] = decay_near(s[n][c], w[n][c]);
             }
-            b[j][c] = m * sigm(i[c], e) * x[c];
-            if (!in) { a[j][c] = 1.0f; b[j][c] = 0.0f; }
-            H[c] = behind<RESET>(a[j][c], b[j][c], H[c]);
-            P[c] = both<RESET>(P[c], a[j][c]);
         }
+        if (!near) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) decay_far(s[n][c], a[j0 + n][c], w[n][c]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j = j0 + n;
+            float x[VEC], i[VEC];
+            widen(rx[j], x);
+            widen(ri[j], i);
+            const bool in = whole || (int64_t)hr + j < left;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float e, m = __builtin_amdgcn_sqrtf(w[n][c]);
+                if constexpr (RESET) {
+                    if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; }
+                }
+                b[j][c] = m * sigm(i[c], e) * x[c];
+                if (!in) { a[j][c] = 1.0f; b[j][c] = 0.0f; }
+                H[c] = behind<RESET>(a[j][c], b[j][c], H[c]);
+                P[c] = both<RESET>(P[c], a[j][c]);
+            }
+        }
+        // a few tokens' chains at a time: all of them at once do not fit the registers
+        __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) sh.map[2 * wave + half][l + c] = make_float2(P[c], H[c]);
     __syncthreads();
     const int64_t bd = (int64_t)at.b * p.dim + ch;
-    if (wave == 0) {
-        float h0[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) h0[c] = p.h0 ? p.h0[bd + c] : 0.0f;
-        join_chunks<VEC, RESET, false>(p, sh, at, h0, lane, ch, ok);
-    }
+    if (wave == 0) join_chunks<RESET, false>(p, sh, at, p.h0, lane);
     __syncthreads();
     float h[VEC];
-    stream_start<VEC, RESET, false>(sh, wave, half, l, h);
+    stream_start<RESET, false>(sh, wave, half, l, h);
     if (!ok) return;
     if (p.keep) {
         const int64_t t = t0 + hr;
@@ -392,10 +418,8 @@ __global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
     }
     if (p.y) {
         R rg[TT];
-        if (p.gate) rows<R, TT>(p.gate, row0, p.gs, hr, ch, sizeof(T), whole, lf, rg);
-        char *out = static_cast<char *>(p.y) + row0 * p.dim * (int64_t)sizeof(T);
-        const uint32_t off = (hr * (uint32_t)p.dim + (uint32_t)ch) * (uint32_t)sizeof(T);
-        const int64_t step = p.dim * (int64_t)sizeof(T);
+        if (p.gate) Rows(p.gate, row0, p.gs, hr, ch, sizeof(T)).load(whole, hr, lf, rg);
+        const Rows out(p.y, row0, p.dim, hr, ch, sizeof(T));
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
             float v[VEC];
@@ -409,7 +433,7 @@ __global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
             }
             R o;
             narrow(v, o);
-            if (whole || (int64_t)hr + j < left) *reinterpret_cast<R *>(out + j * step + off) = o;
+            if (whole || (int64_t)hr + j < left) bstore<R>(out.r, out.off, j * out.step, o);
         }
     } else {
 #pragma unroll
@@ -418,19 +442,17 @@ __global__ __launch_bounds__(kThreads, 4) void glr_fwd_kernel(GlrParams p) {
             for (int c = 0; c < VEC; ++c) h[c] = behind<RESET>(a[j][c], b[j][c], h[c]);
     }
     // tokens past the end leave the state as it is
-    if (p.h_last && at.k == p.chunks - 1 && 2 * wave + half == kStreams - 1) stf<VEC>(p.h_last + bd, h);
+    if (p.h_last && at.k == p.chunks - 1 && 2 * wave + half == kFwdStreams - 1) stf<VEC>(p.h_last + bd, h);
 }
 
 // Backward: chunks of kKeep tokens from the end.
-constexpr int kBT = kKeep / kStreams;
-
 template <typename T, int VEC, bool RESET, bool GATE>
-__global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
+__global__ __launch_bounds__(kBwdStreams * kRow, 3) void glr_bwd_kernel(GlrParams p) {
     typedef typename Raw<T, VEC>::type R;
-    constexpr int TT = kBT, CT = kStreams * TT;
-    __shared__ Shared<VEC> sh;
-    __shared__ float sum[kStreams][kRow * VEC];
-    const Place at = place<VEC>(p, sh);
+    constexpr int TT = kBwdTokens, CT = kKeep;
+    __shared__ Shared<VEC, kBwdStreams> sh;
+    __shared__ float sum[kBwdStreams][kRow * VEC];
+    const Place at = place(p, sh);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, half = lane >> 5;
     const int l = (lane & (kRow - 1)) * VEC;
     const int chunk = p.chunks - 1 - at.k;
@@ -444,11 +466,11 @@ __global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
     const uint32_t hr = half * TT;
 
     R rx[TT], rr[TT], ri[TT], rdy[TT], rga[TT];
-    rows<R, TT>(p.rg, row0, p.rs, hr, ch, sizeof(T), whole, lf, rr);
-    rows<R, TT>(p.ig, row0, p.is, hr, ch, sizeof(T), whole, lf, ri);
-    rows<R, TT>(p.x, row0, p.xs, hr, ch, sizeof(T), whole, lf, rx);
-    rows<R, TT>(p.dy, row0, p.dim, hr, ch, sizeof(T), whole, lf, rdy);
-    if constexpr (GATE) rows<R, TT>(p.gate, row0, p.gs, hr, ch, sizeof(T), whole, lf, rga);
+    Rows(p.rg, row0, p.rs, hr, ch, sizeof(T)).load(whole, hr, lf, rr);
+    Rows(p.ig, row0, p.is, hr, ch, sizeof(T)).load(whole, hr, lf, ri);
+    Rows(p.x, row0, p.xs, hr, ch, sizeof(T)).load(whole, hr, lf, rx);
+    Rows(p.dy, row0, p.dim, hr, ch, sizeof(T)).load(whole, hr, lf, rdy);
+    if constexpr (GATE) Rows(p.gate, row0, p.gs, hr, ch, sizeof(T)).load(whole, hr, lf, rga);
     if (threadIdx.x < kRow * VEC) sh.rate[threadIdx.x] = p.rate * soft_plus(p.lam[min(at.c0 + (int64_t)threadIdx.x, p.dim - 1)]);
     __syncthreads();
     float k[VEC];
@@ -461,62 +483,96 @@ __global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
             first |= (p.reset[row0 + r] ? 1u : 0u) << j;
         }
     }
-    // per token: a; b, then g's factor of digate; m i; 1 - i; 1 - r; s, then w; a i x s / m; dy gate
-    float a[TT][VEC], b[TT][VEC], mi[TT][VEC], oi[TT][VEC], orr[TT][VEC], sw[TT][VEC], u[TT][VEC], up[TT][VEC];
+    // Per token, beside x, dy and the gate as they were read: a; m i; 1 - i, then g's factor of
+    // digate; 1 - r; s, then w; a i x s / m. b = m i x and dy gate are formed again at each use.
+    float a[TT][VEC], mi[TT][VEC], oi[TT][VEC], orr[TT][VEC], sw[TT][VEC], u[TT][VEC];
+    auto input = [&](int j, float (&b)[VEC]) {
+        widen(rx[j], b);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) b[c] *= mi[j][c];
+    };
+    auto incoming = [&](int j, const float (&from)[VEC], float (&g)[VEC]) {       // dy gate + from
+        float dy[VEC], ga[VEC];
+        widen(rdy[j], dy);
+        if constexpr (GATE) widen(rga[j], ga);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) g[c] = GATE ? fmaf(dy[c], ga[c], from[c]) : dy[c] + from[c];
+    };
     float P[VEC], H[VEC], G[VEC];
+    const bool near = all_near<VEC>(k);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) { P[c] = 1.0f; H[c] = 0.0f; }
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-        float x[VEC], r[VEC], i[VEC], dy[VEC];
-        widen(rx[j], x);
+        float x[VEC], r[VEC], i[VEC], sr[VEC], er[VEC], w[VEC], b[VEC];
         widen(rr[j], r);
-        widen(ri[j], i);
-        widen(rdy[j], dy);
-        if constexpr (GATE) {
-            float ga[VEC];
-            widen(rga[j], ga);
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) dy[c] *= ga[c];
-        }
-        const bool in = whole || (int64_t)hr + j < left;
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
-            float er, ei, w;
-            const float sr = sigm(r[c], er), si = sigm(i[c], ei);
-            float s = k[c] * sr;
-            a[j][c] = decay(s, w);
-            s = fminf(s, 1e4f);                                // a is 0 there
-            const float inv = __builtin_amdgcn_rsqf(w);
-            const bool still = w < 1.17549435e-38f;            // a gate that lets nothing in or out
-            float m = still ? 0.0f : w * inv;
-            const float q = still ? 0.0f : s * inv;
-            const float ix = si * x[c];
-            u[j][c] = a[j][c] * ix * q;
-            if constexpr (RESET) {
-                if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; u[j][c] = 0.0f; s = 0.0f; }
+            sr[c] = sigm(r[c], er[c]);
+            sw[j][c] = k[c] * sr[c];
+            a[j][c] = decay_near(sw[j][c], w[c]);
+        }
+        if (!near) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                decay_far(sw[j][c], a[j][c], w[c]);
+                sw[j][c] = fminf(sw[j][c], 1e4f);          // a is 0 there
             }
-            b[j][c] = m * ix;
+        }
+        const bool in = whole || (int64_t)hr + j < left;
+        if (!in) {
+            rx[j] = R{};
+            rdy[j] = R{};
+            if constexpr (GATE) rga[j] = R{};
+        }
+        widen(rx[j], x);
+        widen(ri[j], i);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            float ei;
+            const float si = sigm(i[c], ei), inv = __builtin_amdgcn_rsqf(w[c]);
+            const bool still = w[c] < 1.17549435e-38f;     // a gate that lets nothing in or out
+            float m = still ? 0.0f : w[c] * inv;
+            const float q = still ? 0.0f : sw[j][c] * inv;
+            u[j][c] = a[j][c] * (si * x[c]) * q;
+            if constexpr (RESET) {
+                if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; u[j][c] = 0.0f; sw[j][c] = 0.0f; }
+            }
             mi[j][c] = m * si;
             oi[j][c] = one_minus(si, ei);
-            orr[j][c] = one_minus(sr, er);
-            sw[j][c] = s;
-            up[j][c] = dy[c];
-            if (!in) { a[j][c] = 1.0f; b[j][c] = 0.0f; up[j][c] = 0.0f; }
-            H[c] = behind<RESET>(a[j][c], b[j][c], H[c]);
+            orr[j][c] = one_minus(sr[c], er[c]);
+            if (!in) { a[j][c] = 1.0f; mi[j][c] = 0.0f; }
+            // formed here: put off to where it is used, each would keep two values alive instead of one
+            here(oi[j][c]);
+            here(orr[j][c]);
+            here(u[j][c]);
+            here(mi[j][c]);
+        }
+        input(j, b);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            H[c] = behind<RESET>(a[j][c], b[c], H[c]);
             P[c] = both<RESET>(P[c], a[j][c]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
     // what flows out of the stream towards the past, of what flows in at its end
 #pragma unroll
+    for (int j = 0; j < TT; ++j) again(rx[j]);
+#pragma unroll
     for (int c = 0; c < VEC; ++c) G[c] = 0.0f;
 #pragma unroll
-    for (int j = TT - 1; j >= 0; --j)
+    for (int j = TT - 1; j >= 0; --j) {
+        float g[VEC];
+        incoming(j, G, g);
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            const float g = up[j][c] + G[c];
-            G[c] = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * g;
-        }
+        for (int c = 0; c < VEC; ++c) G[c] = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * g[c];
+    }
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        again(rdy[j]);
+        if constexpr (GATE) again(rga[j]);
+    }
     // the states: from the kept one, in the chunk alone
 #pragma unroll
     for (int c = 0; c < VEC; ++c) sh.map[2 * wave + half][l + c] = make_float2(P[c], H[c]);
@@ -528,29 +584,24 @@ __global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
     }
     __syncthreads();
     float h[VEC];
-    stream_start<VEC, RESET, false>(sh, wave, half, l, h);
+    stream_start<RESET, false>(sh, wave, half, l, h);
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < VEC; ++c) sh.map[2 * wave + half][l + c] = make_float2(P[c], G[c]);
     __syncthreads();
-    if (wave == 0) {
-        float d[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) d[c] = p.dh_last ? p.dh_last[bd + c] : 0.0f;
-        join_chunks<VEC, RESET, true>(p, sh, at, d, lane, ch, ok);
-    }
-    const uint32_t off = (hr * (uint32_t)p.dim + (uint32_t)ch) * (uint32_t)sizeof(T);
-    const int64_t step = p.dim * (int64_t)sizeof(T), base = row0 * step;
+    if (wave == 0) join_chunks<RESET, true>(p, sh, at, p.dh_last, lane);
+    const Rows outg(GATE ? p.dgate : p.dx, row0, p.dim, hr, ch, sizeof(T));
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
-        float dg[VEC];
+        float dg[VEC], b[VEC];
+        input(j, b);
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
             // a reset reads nothing of the state before it: its s and u are 0
             const float t = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * fmaf(-sw[j][c], h[c], u[j][c]);
-            h[c] = behind<RESET>(a[j][c], b[j][c], h[c]);
+            h[c] = behind<RESET>(a[j][c], b[c], h[c]);
             sw[j][c] = t;
-            b[j][c] *= oi[j][c];
+            oi[j][c] *= b[c];
         }
         if constexpr (GATE) {
             float dy[VEC];
@@ -559,26 +610,27 @@ __global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
             for (int c = 0; c < VEC; ++c) dg[c] = dy[c] * h[c];
             R o;
             narrow(dg, o);
-            if (ok && (whole || (int64_t)hr + j < left))
-                *reinterpret_cast<R *>(static_cast<char *>(p.dgate) + base + j * step + off) = o;
+            if (ok && (whole || (int64_t)hr + j < left)) bstore<R>(outg.r, outg.off, j * outg.step, o);
         }
     }
     __syncthreads();
+    const Rows outx(p.dx, row0, p.dim, hr, ch, sizeof(T)), outr(p.drg, row0, p.dim, hr, ch, sizeof(T)),
+        outi(p.dig, row0, p.dim, hr, ch, sizeof(T));
     float c_in[VEC], dl[VEC];
-    stream_start<VEC, RESET, true>(sh, wave, half, l, c_in);
+    stream_start<RESET, true>(sh, wave, half, l, c_in);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) dl[c] = 0.0f;
 #pragma unroll
     for (int j = TT - 1; j >= 0; --j) {
         const bool in = whole || (int64_t)hr + j < left;
-        float vx[VEC], vr[VEC], vi[VEC];
+        float vx[VEC], vr[VEC], vi[VEC], g[VEC];
+        incoming(j, c_in, g);
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
-            const float g = up[j][c] + c_in[c];
-            c_in[c] = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * g;
-            vx[c] = g * mi[j][c];
-            vi[c] = g * b[j][c];
-            const float t = g * sw[j][c];
+            c_in[c] = RESET && is_reset(a[j][c]) ? 0.0f : a[j][c] * g[c];
+            vx[c] = g[c] * mi[j][c];
+            vi[c] = g[c] * oi[j][c];
+            const float t = g[c] * sw[j][c];
             vr[c] = t * orr[j][c];
             dl[c] += in ? t : 0.0f;
         }
@@ -587,10 +639,9 @@ __global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
         narrow(vr, orv);
         narrow(vi, oiv);
         if (ok && in) {
-            const int64_t o = base + j * step;
-            *reinterpret_cast<R *>(static_cast<char *>(p.dx) + o + off) = ox;
-            *reinterpret_cast<R *>(static_cast<char *>(p.drg) + o + off) = orv;
-            *reinterpret_cast<R *>(static_cast<char *>(p.dig) + o + off) = oiv;
+            bstore<R>(outx.r, outx.off, j * outx.step, ox);
+            bstore<R>(outr.r, outr.off, j * outx.step, orv);
+            bstore<R>(outi.r, outi.off, j * outx.step, oiv);
         }
     }
     if (p.dh0 && chunk == 0 && wave == 0 && half == 0 && ok) stf<VEC>(p.dh0 + bd, c_in);
@@ -600,7 +651,7 @@ __global__ __launch_bounds__(kThreads, 2) void glr_bwd_kernel(GlrParams p) {
     if (threadIdx.x < kRow * VEC && at.c0 + (int64_t)threadIdx.x < p.dim) {
         float v = 0.0f;
 #pragma unroll
-        for (int s = 0; s < kStreams; ++s) v += sum[s][threadIdx.x];
+        for (int s = 0; s < kBwdStreams; ++s) v += sum[s][threadIdx.x];
         p.part[((int64_t)at.b * p.chunks + chunk) * p.dim + at.c0 + threadIdx.x] = v;
     }
 }
@@ -657,7 +708,9 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p, const float 
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
             float e, w;
-            const float a = decay(k[c] * sigm(r[c], e), w);
+            const float s = k[c] * sigm(r[c], e);
+            float a = decay_near(s, w);
+            decay_far(s, a, w);
             const float ix = sigm(i[c], e) * x[c];
             s0[c] = first ? ix : fmaf(a, s0[c], __builtin_amdgcn_sqrtf(w) * ix);
             v[c] = p.gate ? s0[c] * g[c] : s0[c];
@@ -672,27 +725,34 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p, const float 
 // ---------------------------------------------------------------------------
 // Launching
 
-int fwd_tokens(int dtype) { return dtype == SSM_BF16 ? 16 * kStreams : 8 * kStreams; }
+// Tokens to a stream of the forward: 16 halve what joining chunks costs (8 x 8192 x 4096 bf16
+// 437 us, with 8 464), where they fit the registers: not in fp32, nor with resets (4 x 4096 x
+// 2048 bf16 160 us, with 8 98)
+int fwd_tokens(int dtype, bool reset) { return (dtype == SSM_BF16 && !reset ? 16 : 8) * kFwdStreams; }
 int64_t chunks_of(int64_t L, int tokens) { return (L + tokens - 1) / tokens; }
 
-// Where what chunks publish lies in a workspace: the counter, the maps, the states
+// A workspace: the backward's kept states and sums, then what chunks publish: the
+// counter, the maps, the states
 struct Layout {
-    size_t keep, part, sync, map, state, total;
+    size_t part, sync, map, state, total;
 };
 
-// What both directions publish shares one place: the larger of the two, the backward's
-Layout layout(const ssm_glr_desc &d, bool bwd) {
+Layout layout(const ssm_glr_desc &d, bool bwd, int64_t chunks) {
     const size_t bd = (size_t)d.batch * (size_t)d.dim;
-    const size_t kept = (size_t)chunks_of(d.seqlen, kKeep), n = bwd ? kept : (size_t)chunks_of(d.seqlen, fwd_tokens(d.dtype));
     Layout l{};
     if (bwd) {
-        l.part = align256(kept * bd * 4);
-        l.sync = l.part + align256(kept * bd * 4);
+        l.part = align256((size_t)chunks_of(d.seqlen, kKeep) * bd * 4);
+        l.sync = 2 * l.part;
     }
     l.map = l.sync + 256;
-    l.state = l.map + align256(n * bd * 8);
-    l.total = n > 1 ? l.state + align256(n * bd * 4) : l.sync;
+    l.state = l.map + align256((size_t)chunks * bd * 8);
+    l.total = chunks > 1 ? l.state + align256((size_t)chunks * bd * 4) : l.sync;
     return l;
+}
+
+// Bytes that any call with this descriptor needs
+size_t bytes_of(const ssm_glr_desc &d, bool bwd) {
+    return layout(d, bwd, chunks_of(d.seqlen, bwd ? kKeep : fwd_tokens(d.dtype, true))).total;
 }
 
 int64_t tiles_of(int64_t dim, int vec) { return (dim + kRow * vec - 1) / (kRow * vec); }
@@ -715,7 +775,7 @@ int check(const ssm_glr_desc *desc) {
     if (!(d.rate >= 0.0f) || d.rate > 3e38f) return SSM_ERR_UNSUPPORTED;
     // every launch below 2^32 work items, with the narrowest pieces
     if (!mul_ok(d.batch, tiles_of(d.dim, 1), &n) || !mul_ok(n, std::max<int64_t>(1, chunks_of(d.seqlen, kKeep)), &n) ||
-        !grid_ok(n, kThreads))
+        !grid_ok(n, kFwdStreams * kRow))
         return SSM_ERR_SHAPE;
     int64_t cells;
     if (!mul_ok(d.batch * d.dim, chunks_of(d.seqlen, kKeep), &cells) || !grid_ok(cells / 256 + 64, 256)) return SSM_ERR_SHAPE;
@@ -747,9 +807,11 @@ bool pairs(const ssm_glr_desc &d, const GlrParams &p, const void *const *ptr, in
     return true;
 }
 
-hipError_t set_sync(GlrParams &p, char *ws, const Layout &l, int64_t chunks, hipStream_t st) {
+hipError_t set_sync(const ssm_glr_desc &d, GlrParams &p, char *ws, bool bwd, int64_t chunks, hipStream_t st) {
     p.chunks = (int)chunks;
+    p.ticket = nullptr;
     if (chunks <= 1) return hipSuccess;
+    const Layout l = layout(d, bwd, chunks);
     p.ticket = reinterpret_cast<uint32_t *>(ws + l.sync);
     p.map = reinterpret_cast<unsigned long long *>(ws + l.map);
     p.state = reinterpret_cast<uint32_t *>(ws + l.state);
@@ -760,12 +822,13 @@ hipError_t set_sync(GlrParams &p, char *ws, const Layout &l, int64_t chunks, hip
 }
 
 template <typename T, int VEC, int TT> void launch_fwd(const GlrParams &p, unsigned blocks, hipStream_t st) {
-    if (p.reset) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, TT, true>), dim3(blocks), dim3(kThreads), 0, st, p);
-    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, TT, false>), dim3(blocks), dim3(kThreads), 0, st, p);
+    if (p.reset) hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, 8, true>), dim3(blocks), dim3(kFwdStreams * kRow), 0, st, p);
+    else hipLaunchKernelGGL((glr_fwd_kernel<T, VEC, TT, false>), dim3(blocks), dim3(kFwdStreams * kRow), 0, st, p);
 }
 
-int run_fwd(const ssm_glr_desc &d, GlrParams &p, bool two, char *ws, const Layout &l, hipStream_t st) {
-    if (set_sync(p, ws, l, chunks_of(d.seqlen, fwd_tokens(d.dtype)), st) != hipSuccess) return SSM_ERR_HIP;
+int run_fwd(const ssm_glr_desc &d, GlrParams &p, bool two, char *ws, bool save, hipStream_t st) {
+    const int64_t chunks = chunks_of(d.seqlen, fwd_tokens(d.dtype, p.reset != nullptr));
+    if (set_sync(d, p, ws, save, chunks, st) != hipSuccess) return SSM_ERR_HIP;
     p.tiles = (int)tiles_of(d.dim, two ? 2 : 1);
     const unsigned blocks = (unsigned)((int64_t)p.tiles * p.batch * p.chunks);
     if (d.dtype == SSM_BF16) two ? launch_fwd<uint16_t, 2, 16>(p, blocks, st) : launch_fwd<uint16_t, 1, 16>(p, blocks, st);
@@ -775,7 +838,7 @@ int run_fwd(const ssm_glr_desc &d, GlrParams &p, bool two, char *ws, const Layou
 
 template <typename T, int VEC> void launch_bwd(const GlrParams &p, unsigned blocks, hipStream_t st) {
 #define GLR_CASE(RESET, GATE) \
-    hipLaunchKernelGGL((glr_bwd_kernel<T, VEC, RESET, GATE>), dim3(blocks), dim3(kThreads), 0, st, p)
+    hipLaunchKernelGGL((glr_bwd_kernel<T, VEC, RESET, GATE>), dim3(blocks), dim3(kBwdStreams * kRow), 0, st, p)
     if (p.reset) {
         if (p.gate) GLR_CASE(true, true);
         else GLR_CASE(true, false);
@@ -837,13 +900,13 @@ int forward(const ssm_glr_desc *desc, const Inputs &in, void *y, float *h_last, 
     if (!aligned(in.x, e) || !aligned(in.rg, e) || !aligned(in.ig, e) || !aligned(in.gate, e) || !aligned(in.lam, 4) ||
         !aligned(y, e))
         return SSM_ERR_ALIGN;
-    const Layout l = layout(d, save);
-    if (l.total && (!workspace || bytes < l.total)) return SSM_ERR_WORKSPACE;
-    if (l.total && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
+    const size_t need = bytes_of(d, save);
+    if (need && (!workspace || bytes < need)) return SSM_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
     GlrParams p = params_of(d);
     Range r[8];
     const int n = inputs_of(d, p, in, r);
-    const Range ry = range_of(y, rows * d.dim * (int64_t)e), ws = range_of(workspace, (int64_t)l.total);
+    const Range ry = range_of(y, rows * d.dim * (int64_t)e), ws = range_of(workspace, (int64_t)need);
     for (int k = 0; k < n; ++k)
         if (overlaps(ry, r[k]) || overlaps(ws, r[k]) || (k < 6 && overlaps(rl, r[k]))) return SSM_ERR_ALIAS;
     if (overlaps(ry, rl) || overlaps(ws, ry) || overlaps(ws, rl)) return SSM_ERR_ALIAS;
@@ -851,9 +914,9 @@ int forward(const ssm_glr_desc *desc, const Inputs &in, void *y, float *h_last, 
     p.y = y;
     p.h_last = h_last;
     char *w = static_cast<char *>(workspace);
-    if (save) p.keep = reinterpret_cast<float *>(w + l.keep);
+    if (save) p.keep = reinterpret_cast<float *>(w);
     const void *ptr[] = {in.x, in.rg, in.ig, in.gate, y};
-    return run_fwd(d, p, pairs(d, p, ptr, 5), w, l, st);
+    return run_fwd(d, p, pairs(d, p, ptr, 5), w, save, st);
 }
 
 int backward(const ssm_glr_desc *desc, const Inputs &in, const void *dy, const float *dh_last, void *dx, void *drg, void *dig,
@@ -872,8 +935,8 @@ int backward(const ssm_glr_desc *desc, const Inputs &in, const void *dy, const f
     for (const void *q : typed)
         if (!aligned(q, e)) return SSM_ERR_ALIGN;
     if (!aligned(in.lam, 4)) return SSM_ERR_ALIGN;
-    const Layout l = layout(d, true);
-    if (!workspace || bytes < l.total) return SSM_ERR_WORKSPACE;
+    const size_t need = bytes_of(d, true);
+    if (!workspace || bytes < need) return SSM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SSM_ERR_ALIGN;
     GlrParams p = params_of(d);
     Range r[10];
@@ -881,7 +944,7 @@ int backward(const ssm_glr_desc *desc, const Inputs &in, const void *dy, const f
     const int64_t full = rows * d.dim * (int64_t)e;
     r[n++] = range_of(dy, full);
     r[n++] = rdh;
-    const Range ws = range_of(workspace, (int64_t)l.total);
+    const Range ws = range_of(workspace, (int64_t)need);
     const Range out[] = {range_of(dx, full), range_of(drg, full), range_of(dig, full), range_of(dgate, in.gate ? full : 0), rdl, rd0};
     for (int k = 0; k < 6; ++k) {
         for (int j = 0; j < n; ++j)
@@ -894,16 +957,16 @@ int backward(const ssm_glr_desc *desc, const Inputs &in, const void *dy, const f
         if (overlaps(ws, r[j])) return SSM_ERR_ALIAS;
     p.x = in.x; p.rg = in.rg; p.ig = in.ig; p.gate = in.gate; p.lam = in.lam; p.h0 = in.h0; p.reset = in.reset;
     char *w = static_cast<char *>(workspace);
-    p.keep = reinterpret_cast<float *>(w + l.keep);
+    p.keep = reinterpret_cast<float *>(w);
     const bool two = pairs(d, p, typed, 9);
     if (!saved) {
-        const int rc = run_fwd(d, p, two, w, l, st);
+        const int rc = run_fwd(d, p, two, w, true, st);
         if (rc != SSM_OK) return rc;
-        p.ticket = nullptr;
     }
     p.dy = dy; p.dh_last = dh_last; p.dx = dx; p.drg = drg; p.dig = dig; p.dgate = dgate; p.dh0 = dh0;
-    p.part = reinterpret_cast<float *>(w + l.part);
-    if (set_sync(p, w, l, chunks_of(d.seqlen, kKeep), st) != hipSuccess) return SSM_ERR_HIP;
+    const int64_t chunks = chunks_of(d.seqlen, kKeep);
+    p.part = reinterpret_cast<float *>(w + layout(d, true, chunks).part);
+    if (set_sync(d, p, w, true, chunks, st) != hipSuccess) return SSM_ERR_HIP;
     p.tiles = (int)tiles_of(d.dim, two ? 2 : 1);
     const unsigned blocks = (unsigned)((int64_t)p.tiles * p.batch * p.chunks);
     if (d.dtype == SSM_BF16) two ? launch_bwd<uint16_t, 2>(p, blocks, st) : launch_bwd<uint16_t, 1>(p, blocks, st);
@@ -918,12 +981,12 @@ int backward(const ssm_glr_desc *desc, const Inputs &in, const void *dy, const f
 
 extern "C" size_t ssm_glr_workspace_size(const ssm_glr_desc *desc) {
     if (check(desc) != SSM_OK || desc->batch == 0 || desc->seqlen == 0) return 0;
-    return layout(*desc, false).total;
+    return bytes_of(*desc, false);
 }
 
 extern "C" size_t ssm_glr_bwd_workspace_size(const ssm_glr_desc *desc) {
     if (check(desc) != SSM_OK || desc->batch == 0 || desc->seqlen == 0) return 0;
-    return layout(*desc, true).total;
+    return bytes_of(*desc, true);
 }
 
 extern "C" int ssm_glr_fwd(const ssm_glr_desc *desc, const void *x, const void *rgate, const void *igate, const float *lam,
