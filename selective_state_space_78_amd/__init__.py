@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(PKG, "libssm_scan.so")
@@ -1102,10 +1103,12 @@ def ssm_glr_state_update(x, rgate, igate, lam, h, y=None, h_out=None, gate=None,
     _check(h, "h", x.shape, torch.float32, dev)
     if h_out is None:
         h_out = h
-    _check(h_out, "h_out", x.shape, torch.float32, dev)
+    else:
+        _check(h_out, "h_out", x.shape, torch.float32, dev)
     if y is None:
         y = _empty(x.shape, x.dtype, dev, stream)
-    _check(y, "y", x.shape, x.dtype, dev)
+    else:
+        _check(y, "y", x.shape, x.dtype, dev)
     rc = _on(dev, lib().ssm_glr_state_update, ctypes.byref(desc), _ptr(x), _ptr(rgate), _ptr(igate), _ptr(lam), _ptr(gate),
              _ptr(reset), _ptr(h), _ptr(h_out), _ptr(y), _stream(stream, dev))
     if rc != 0:
@@ -1115,7 +1118,9 @@ def ssm_glr_state_update(x, rgate, igate, lam, h, y=None, h_out=None, gate=None,
 
 def _grad_list(grads, out, device=None):
     """(count, pointers, outputs' pointers, sizes, types, device) of gradients, those
-    that are None left out; host arrays for one call."""
+    that are None left out; the middle four are arrays for one call (_at gives their addresses). Hundreds of tensors are looked at
+    in every training step: one question to all of them at a time, which one it was
+    only when the answer is no."""
     import torch
     grads = list(grads)
     if out is not None:
@@ -1124,30 +1129,38 @@ def _grad_list(grads, out, device=None):
             raise ValueError("out has %d tensors, there are %d gradients" % (len(out), len(grads)))
         out = [o for o, g in zip(out, grads) if g is not None]
     grads = [g for g in grads if g is not None]
-    codes = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
     if device is None:
         if not grads:
             raise ValueError("no gradients, and so no device: give the norm")
         device = grads[0].device
+    index = -1 if device.type != "cuda" else torch.cuda.current_device() if device.index is None else device.index
+    codes = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+    kinds = [g.dtype for g in grads]
     try:
-        types = [codes[g.dtype] for g in grads]
+        types = [codes[t] for t in kinds]
     except KeyError as e:
         raise TypeError("gradients must be bfloat16 or float32, got %s" % e.args[0]) from None
-    for k, g in enumerate(grads):
-        if not g.is_contiguous():
-            raise ValueError("gradient %d must be contiguous" % k)
-        if g.device != device:
-            raise ValueError("gradient %d is on %s, expected %s" % (k, g.device, device))
-    n = len(grads)
-    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    n, sizes = len(grads), [g.numel() for g in grads]
+    for what, tensors in (("gradient", grads), ("out", out)):
+        if tensors is None:
+            continue
+        if any([t is None for t in tensors]):
+            raise ValueError("%s %d is missing" % (what, [t is None for t in tensors].index(True)))
+        if not all([t.is_contiguous() for t in tensors]):
+            raise ValueError("%s %d must be contiguous" % (what, [t.is_contiguous() for t in tensors].index(False)))
+        if any([t.get_device() != index for t in tensors]):
+            raise ValueError("%s %d is not on %s" % (what, [t.get_device() != index for t in tensors].index(True), device))
+    ptrs = array("Q", [g.data_ptr() for g in grads])
     outs = ptrs
     if out is not None:
-        for k, (o, g) in enumerate(zip(out, grads)):
-            if o is not g and (o is None or o.shape != g.shape or o.dtype != g.dtype or o.device != device or
-                               not o.is_contiguous()):
-                raise ValueError("out %d must be a contiguous tensor like its gradient" % k)
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
-    return n, ptrs, outs, (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*types), device
+        if [o.dtype for o in out] != kinds or [o.numel() for o in out] != sizes:
+            raise ValueError("every out must have its gradient's type and size")
+        outs = array("Q", [o.data_ptr() for o in out])
+    return n, ptrs, outs, array("q", sizes), array("i", types), device
+
+
+def _at(values):
+    return values.buffer_info()[0]
 
 
 def _norm_tensor(norm, device, stream):
@@ -1171,7 +1184,7 @@ def ssm_grad_norm(grads, norm=None, workspace=None, stream=None):
     n, ptrs, _, sizes, types, dev = _grad_list(grads, None, None if norm is None else norm.device)
     norm = _norm_tensor(norm, dev, stream)
     workspace, ws_bytes = _workspace(workspace, ssm_grad_workspace_size(n), dev, "ssm_grad_norm", stream)
-    rc = _on(dev, lib().ssm_grad_norm, n, ptrs, sizes, types, _ptr(norm), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    rc = _on(dev, lib().ssm_grad_norm, n, _at(ptrs), _at(sizes), _at(types), _ptr(norm), _ptr(workspace), ws_bytes, _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_grad_norm")
     return norm
@@ -1185,7 +1198,7 @@ def ssm_grad_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None
     n, ptrs, outs, sizes, types, dev = _grad_list(grads, out, None if norm is None else norm.device)
     norm = _norm_tensor(norm, dev, stream)
     workspace, ws_bytes = _workspace(workspace, ssm_grad_workspace_size(n), dev, "ssm_grad_clip", stream)
-    rc = _on(dev, lib().ssm_grad_clip, n, ptrs, outs, sizes, types, float(max_norm), float(eps), _ptr(norm),
+    rc = _on(dev, lib().ssm_grad_clip, n, _at(ptrs), _at(outs), _at(sizes), _at(types), float(max_norm), float(eps), _ptr(norm),
              _ptr(workspace), ws_bytes, _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_grad_clip")
@@ -1197,7 +1210,7 @@ def ssm_grad_scale(grads, norm, max_norm, eps=1e-6, out=None, stream=None):
     where it is taken over the gradients of several GPUs."""
     n, ptrs, outs, sizes, types, dev = _grad_list(grads, out, norm.device)
     _norm_tensor(norm, dev, stream)
-    rc = _on(dev, lib().ssm_grad_scale, n, ptrs, outs, sizes, types, _ptr(norm), float(max_norm), float(eps),
+    rc = _on(dev, lib().ssm_grad_scale, n, _at(ptrs), _at(outs), _at(sizes), _at(types), _ptr(norm), float(max_norm), float(eps),
              _stream(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_grad_scale")
@@ -1258,10 +1271,12 @@ def ssm_proj_fwd(x, weight, bias=None, activation=None, residual=None, y=None, w
     _check(residual, "residual", shape, yt, dev)
     if y is None:
         y = _empty(shape, yt, dev, stream)
+    else:
+        _check(y, "y", shape, yt, dev)
     if _save and _pre is None:
         _pre = _empty(shape, x.dtype, dev, stream)
-    _check(y, "y", shape, yt, dev)
-    _check(_pre, "pre", shape, x.dtype, dev)
+    else:
+        _check(_pre, "pre", shape, x.dtype, dev)
     L_ = lib()
     workspace, ws_bytes = _workspace(workspace, L_.ssm_proj_workspace_size(ctypes.byref(desc)), dev, "ssm_proj_fwd", stream)
     rc = _on(dev, L_.ssm_proj_fwd, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(_pre), _ptr(y),

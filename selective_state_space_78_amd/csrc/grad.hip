@@ -11,8 +11,10 @@
 // Squares are taken and added in 64 bits: no gradient overflows or vanishes in its
 // square, and the order of sums, fixed here, matters to no digit of the fp32 norm. Each workgroup
 // leaves one partial sum; those of the scaling add all of them, in the same order,
-// instead of waiting for a launch that does. They walk their run backwards, so what
-// the sum read last is read first, out of the cache.
+// instead of waiting for a launch that does (beyond one launch's worth a launch does, or
+// every workgroup would read as much again in sums). They ask for their first elements before
+// they add, and walk launches and runs backwards: what the sum read last is read first,
+// out of the cache.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -100,17 +102,18 @@ template <typename T> __device__ __forceinline__ void words(const uint4 &r, floa
 
 // One piece: elements [e0, e1) of a tensor, e0 a multiple of kPiece. Their 16-byte
 // words are those of the elements from `head` on; what is left over on both sides
-// goes one by one. SCALE writes in * coef to out, else squares are added to sum.
-template <typename T, bool SCALE>
-__device__ __forceinline__ void piece(const T *in, T *out, int64_t n, int64_t e0, float coef, double &sum) {
+// goes one by one. SCALE writes in * factor() to out (asked for once the reads are under
+// way), else squares are added to sum.
+template <typename T, bool SCALE, typename F>
+__device__ __forceinline__ void piece(const T *in, T *out, int64_t n, int64_t e0, F factor, double &sum) {
     typedef Words<T> W;
     const int64_t e1 = min(e0 + kPiece, n);
     const int64_t head = head_of<T>(in, SCALE ? out : in, n);
     // first and behind the last whole word in [e0, e1)
     int64_t w0 = e0 <= head ? head : head + (e0 - head + W::kEach - 1) / W::kEach * W::kEach;
     w0 = min(w0, e1);
-    const int64_t nw = (e1 - w0) / W::kEach;
-    const int64_t w1 = w0 + nw * W::kEach;
+    const int nw = (int)((e1 - w0) / W::kEach);
+    const int64_t w1 = w0 + (int64_t)nw * W::kEach;
     const uint4 *src = reinterpret_cast<const uint4 *>(in + w0);
     uint4 r[W::kIter];
 #pragma unroll
@@ -118,6 +121,9 @@ __device__ __forceinline__ void piece(const T *in, T *out, int64_t n, int64_t e0
         const int at = k * kThreads + (int)threadIdx.x;
         if (at < nw) r[k] = src[at];
     }
+    const float coef = SCALE ? factor() : 0.0f;
+    // in place, a factor of 1 leaves what is there
+    if (SCALE && coef == 1.0f && in == out) return;
 #pragma unroll
     for (int k = 0; k < W::kIter; ++k) {
         const int at = k * kThreads + (int)threadIdx.x;
@@ -139,16 +145,13 @@ __device__ __forceinline__ void piece(const T *in, T *out, int64_t n, int64_t e0
             for (int e = 0; e < W::kEach; ++e) sum = fma((double)v[e], (double)v[e], sum);
         }
     }
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-        if (e >= w0 && e < w1) {
-            // on to the elements behind the words
-            e += (w1 - e + kThreads - 1) / kThreads * kThreads - kThreads;
-            continue;
-        }
+    auto one = [&](int64_t e) {
         const float v = value<T>(in + e);
         if constexpr (SCALE) put<T>(out + e, v * coef);
         else sum = fma((double)v, (double)v, sum);
-    }
+    };
+    for (int64_t e = e0 + threadIdx.x; e < w0; e += kThreads) one(e);
+    for (int64_t e = w1 + threadIdx.x; e < e1; e += kThreads) one(e);
 }
 
 // The sum over a workgroup's threads, to all of them
@@ -171,8 +174,9 @@ __global__ __launch_bounds__(kThreads) void grad_square_kernel(Table t, double *
     for (uint32_t p = p0; p < p1; ++p) {
         while (p >= t.first[k + 1]) ++k;
         const int64_t e0 = (int64_t)(p - t.first[k]) * kPiece;
-        if (is_wide(t, k)) piece<float, false>(static_cast<const float *>(t.in[k]), nullptr, t.n[k], e0, 0.0f, sum);
-        else piece<uint16_t, false>(static_cast<const uint16_t *>(t.in[k]), nullptr, t.n[k], e0, 0.0f, sum);
+        auto none = [] { return 0.0f; };
+        if (is_wide(t, k)) piece<float, false>(static_cast<const float *>(t.in[k]), nullptr, t.n[k], e0, none, sum);
+        else piece<uint16_t, false>(static_cast<const uint16_t *>(t.in[k]), nullptr, t.n[k], e0, none, sum);
     }
     sum = wg_sum(sum, s);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
@@ -185,20 +189,31 @@ __device__ __forceinline__ double total(const double *part, int n, double *s) {
     return wg_sum(v, s);
 }
 
-__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double *part, int n, float *norm) {
+// The norm, and the sum again where `sum` is given
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double *part, int n, float *norm, double *sum) {
     __shared__ double s[kThreads / 64];
-    const double v = sqrt(total(part, n, s));
-    if (threadIdx.x == 0) *norm = (float)v;
+    const double v = total(part, n, s);
+    if (threadIdx.x != 0) return;
+    *norm = (float)sqrt(v);
+    if (sum) *sum = v;
 }
 
-// parts > 0: the norm is formed from the partial sums, and written by the first launch; else it is read
+// parts > 0: the norm is formed from the partial sums, and written where `write` is set; else it is read
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Table t, const double *part, int parts, float *norm, int write,
                                                               float max_norm, float eps) {
     __shared__ double s[kThreads / 64];
-    const double v = parts > 0 ? sqrt(total(part, parts, s)) : (double)*norm;
-    if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-    const double c = (double)max_norm / (v + (double)eps);
-    const float coef = c >= 1.0 ? 1.0f : (float)c;      // NaN stays
+    bool known = false;
+    float coef = 0.0f;
+    auto factor = [&] {
+        if (!known) {
+            known = true;
+            const double v = parts > 0 ? sqrt(total(part, parts, s)) : (double)*norm;
+            if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
+            const double c = (double)max_norm / (v + (double)eps);
+            coef = c >= 1.0 ? 1.0f : (float)c;      // NaN stays
+        }
+        return coef;
+    };
     uint32_t p0, p1;
     run_of(t, p0, p1);
     if (p0 >= p1) return;
@@ -206,13 +221,11 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Table t, const dou
     int k = find(t, p1 - 1);
     for (uint32_t p = p1; p-- > p0;) {
         while (p < t.first[k]) --k;
-        // in place, a factor of 1 leaves what is there
-        if (coef == 1.0f && t.in[k] == t.out[k]) continue;
         const int64_t e0 = (int64_t)(p - t.first[k]) * kPiece;
         if (is_wide(t, k))
-            piece<float, true>(static_cast<const float *>(t.in[k]), static_cast<float *>(t.out[k]), t.n[k], e0, coef, none);
+            piece<float, true>(static_cast<const float *>(t.in[k]), static_cast<float *>(t.out[k]), t.n[k], e0, factor, none);
         else
-            piece<uint16_t, true>(static_cast<const uint16_t *>(t.in[k]), static_cast<uint16_t *>(t.out[k]), t.n[k], e0, coef, none);
+            piece<uint16_t, true>(static_cast<const uint16_t *>(t.in[k]), static_cast<uint16_t *>(t.out[k]), t.n[k], e0, factor, none);
     }
 }
 
@@ -229,7 +242,7 @@ struct List {
 
 size_t esize(int t) { return t == SSM_BF16 ? 2 : 4; }
 int64_t launches(int64_t count) { return (count + kPer - 1) / kPer; }
-int64_t part_bytes(int64_t count) { return launches(count) * kWgs * (int64_t)sizeof(double); }
+int64_t part_bytes(int64_t count) { return launches(count) * kWgs * (int64_t)sizeof(double) + (count ? 256 : 0); }   // and the sum
 
 int check(const List &l) {
     if (l.count < 0 || l.count > (1 << 20)) return SSM_ERR_SHAPE;
@@ -321,10 +334,9 @@ int squares(const List &l, double *part, int &parts, hipStream_t st) {
     return SSM_OK;
 }
 
-int scale(const List &l, const double *part, int parts, float *norm, float max_norm, float eps, hipStream_t st) {
+int scale(const List &l, const double *part, int parts, float *norm, bool write, float max_norm, float eps, hipStream_t st) {
     Table t;
-    bool write = parts > 0;
-    for (int64_t k = 0; k < launches(l.count); ++k) {
+    for (int64_t k = launches(l.count) - 1; k >= 0; --k) {
         const unsigned wgs = table(l, k, t);
         if (wgs == 0) continue;
         hipLaunchKernelGGL(grad_scale_kernel, dim3(wgs), dim3(kThreads), 0, st, t, part, parts, norm, (int)write, max_norm, eps);
@@ -334,8 +346,8 @@ int scale(const List &l, const double *part, int parts, float *norm, float max_n
     return SSM_OK;
 }
 
-int norm_of(const double *part, int parts, float *norm, hipStream_t st) {
-    hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kThreads), 0, st, part, parts, norm);
+int norm_of(const double *part, int parts, float *norm, double *sum, hipStream_t st) {
+    hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kThreads), 0, st, part, parts, norm, sum);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
@@ -359,7 +371,7 @@ extern "C" int ssm_grad_norm(int64_t count, const void *const *grads, const int6
     if (const int rc = clashes(l, range_of(norm, 4), range_of(workspace, need))) return rc;
     int parts = 0;
     if (const int rc = squares(l, static_cast<double *>(workspace), parts, stream)) return rc;
-    return norm_of(static_cast<double *>(workspace), parts, norm, stream);
+    return norm_of(static_cast<double *>(workspace), parts, norm, nullptr, stream);
 }
 
 extern "C" int ssm_grad_clip(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes,
@@ -378,8 +390,11 @@ extern "C" int ssm_grad_clip(int64_t count, const void *const *grads, void *cons
     double *part = static_cast<double *>(workspace);
     int parts = 0;
     if (const int rc = squares(l, part, parts, stream)) return rc;
-    if (parts == 0) return norm_of(part, 0, norm, stream);
-    return scale(l, part, parts, norm, max_norm, eps, stream);
+    if (parts == 0) return norm_of(part, 0, norm, nullptr, stream);
+    if (parts <= kWgs) return scale(l, part, parts, norm, true, max_norm, eps, stream);
+    double *sum = part + parts;
+    if (const int rc = norm_of(part, parts, norm, sum, stream)) return rc;
+    return scale(l, sum, 1, norm, false, max_norm, eps, stream);
 }
 
 extern "C" int ssm_grad_scale(int64_t count, const void *const *grads, void *const *out, const int64_t *sizes,
@@ -391,5 +406,5 @@ extern "C" int ssm_grad_scale(int64_t count, const void *const *grads, void *con
     if (!norm) return SSM_ERR_NULL;
     if (!aligned(norm, 4)) return SSM_ERR_ALIGN;
     if (const int rc = clashes(l, range_of(norm, 4), Range{0, 0})) return rc;
-    return scale(l, nullptr, 0, const_cast<float *>(norm), max_norm, eps, stream);
+    return scale(l, nullptr, 0, const_cast<float *>(norm), false, max_norm, eps, stream);
 }
