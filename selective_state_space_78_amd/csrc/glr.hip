@@ -56,6 +56,10 @@ constexpr int kFwdStreams = 16, kBwdStreams = 8;          // to a workgroup, of 
 constexpr int kBwdTokens = 8;                             // of a stream
 constexpr int kKeep = kBwdStreams * kBwdTokens;           // tokens from one kept state to the next
 constexpr int kBack = 8;                                  // chunks that are looked back over
+// Bytes of one tensor beyond which reads and writes go past the cache: half of it (8 x 8192 x 4096
+// bf16 441 -> 417 us, 131072 x 5120 1116 -> 1083 us; the training pass on 4 x 2048 x 1536, which
+// stays in it, 100 -> 106 us)
+constexpr int64_t kCached = (int64_t)128 << 20;
 constexpr int64_t kMaxStride = (1 << 24) - 1;             // lane offsets stay in 32 bits
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -70,7 +74,7 @@ struct GlrParams {
     uint32_t *state;             // (chunk, batch, dim) the state behind a chunk
     uint32_t *ticket;            // NULL with one chunk
     int64_t L, dim, xs, rs, is, gs;
-    int batch, chunks, tiles, kept;
+    int batch, chunks, tiles, kept, past;
     float rate;
 };
 
@@ -286,15 +290,18 @@ __device__ __forceinline__ void stream_start(const Shared<VEC, NS> &sh, int wave
     }
 }
 
-template <typename R> __device__ __forceinline__ R bload(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
-    if constexpr (sizeof(R) == 2) return __builtin_bit_cast(R, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane_off, (int)off, 0));
-    else if constexpr (sizeof(R) == 4) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, 0));
-    else return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_off, (int)off, 0));
+// PAST: past the cache, which the tensor does not fit
+template <bool PAST, typename R> __device__ __forceinline__ R bload(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
+    constexpr int aux = PAST ? 2 : 0;
+    if constexpr (sizeof(R) == 2) return __builtin_bit_cast(R, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane_off, (int)off, aux));
+    else if constexpr (sizeof(R) == 4) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_off, (int)off, aux));
+    else return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_off, (int)off, aux));
 }
-template <typename R> __device__ __forceinline__ void bstore(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off, R v) {
-    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, (int)lane_off, (int)off, 0);
-    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, (int)lane_off, (int)off, 0);
-    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(ssd_u32x2, v), r, (int)lane_off, (int)off, 0);
+template <bool PAST, typename R> __device__ __forceinline__ void bstore(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off, R v) {
+    constexpr int aux = PAST ? 2 : 0;
+    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, (int)lane_off, (int)off, aux);
+    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, (int)lane_off, (int)off, aux);
+    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(ssd_u32x2, v), r, (int)lane_off, (int)off, aux);
 }
 
 // A wave's rows of one tensor, from its first token's: a lane offset that stays, and the
@@ -309,17 +316,26 @@ struct Rows {
         : r(ssd_buffer(static_cast<const char *>(base) + row0 * stride * esz, 0xffffffffu)),
           off((half_rows * (uint32_t)stride + (uint32_t)ch) * (uint32_t)esz), step((uint32_t)stride * (uint32_t)esz) {}
 
-    template <typename R, int TT> __device__ __forceinline__ void load(bool whole, uint32_t half_rows, int64_t left, R (&out)[TT]) const {
-        if (whole) {
+    template <typename R, int TT>
+    __device__ __forceinline__ void load(bool whole, bool past, uint32_t half_rows, int64_t left, R (&out)[TT]) const {
+        if (whole && past) {
 #pragma unroll
-            for (int j = 0; j < TT; ++j) out[j] = bload<R>(r, off, j * step);
+            for (int j = 0; j < TT; ++j) out[j] = bload<true, R>(r, off, j * step);
+        } else if (whole) {
+#pragma unroll
+            for (int j = 0; j < TT; ++j) out[j] = bload<false, R>(r, off, j * step);
         } else {
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
                 const uint32_t back = (uint32_t)max((int64_t)0, (int64_t)half_rows + j - (left - 1));   // rows past the last
-                out[j] = bload<R>(r, off + (j - back) * step, 0);
+                out[j] = bload<false, R>(r, off + (j - back) * step, 0);
             }
         }
+    }
+
+    template <typename R> __device__ __forceinline__ void store(bool past, int j, R v) const {
+        if (past) bstore<true, R>(r, off, j * step, v);
+        else bstore<false, R>(r, off, j * step, v);
     }
 };
 
@@ -342,9 +358,9 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
     const uint32_t hr = half * TT;
 
     R rx[TT], rr[TT], ri[TT];
-    Rows(p.rg, row0, p.rs, hr, ch, sizeof(T)).load(whole, hr, lf, rr);
-    Rows(p.ig, row0, p.is, hr, ch, sizeof(T)).load(whole, hr, lf, ri);
-    Rows(p.x, row0, p.xs, hr, ch, sizeof(T)).load(whole, hr, lf, rx);
+    Rows(p.rg, row0, p.rs, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rr);
+    Rows(p.ig, row0, p.is, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, ri);
+    Rows(p.x, row0, p.xs, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rx);
     if (threadIdx.x < kRow * VEC) sh.rate[threadIdx.x] = p.rate * soft_plus(p.lam[min(at.c0 + (int64_t)threadIdx.x, p.dim - 1)]);
     __syncthreads();
     float k[VEC];
@@ -418,7 +434,7 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
     }
     if (p.y) {
         R rg[TT];
-        if (p.gate) Rows(p.gate, row0, p.gs, hr, ch, sizeof(T)).load(whole, hr, lf, rg);
+        if (p.gate) Rows(p.gate, row0, p.gs, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rg);
         const Rows out(p.y, row0, p.dim, hr, ch, sizeof(T));
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
@@ -433,7 +449,7 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
             }
             R o;
             narrow(v, o);
-            if (whole || (int64_t)hr + j < left) bstore<R>(out.r, out.off, j * out.step, o);
+            if (whole || (int64_t)hr + j < left) out.store(p.past != 0, j, o);
         }
     } else {
 #pragma unroll
@@ -466,11 +482,11 @@ __global__ __launch_bounds__(kBwdStreams * kRow, 3) void glr_bwd_kernel(GlrParam
     const uint32_t hr = half * TT;
 
     R rx[TT], rr[TT], ri[TT], rdy[TT], rga[TT];
-    Rows(p.rg, row0, p.rs, hr, ch, sizeof(T)).load(whole, hr, lf, rr);
-    Rows(p.ig, row0, p.is, hr, ch, sizeof(T)).load(whole, hr, lf, ri);
-    Rows(p.x, row0, p.xs, hr, ch, sizeof(T)).load(whole, hr, lf, rx);
-    Rows(p.dy, row0, p.dim, hr, ch, sizeof(T)).load(whole, hr, lf, rdy);
-    if constexpr (GATE) Rows(p.gate, row0, p.gs, hr, ch, sizeof(T)).load(whole, hr, lf, rga);
+    Rows(p.rg, row0, p.rs, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rr);
+    Rows(p.ig, row0, p.is, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, ri);
+    Rows(p.x, row0, p.xs, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rx);
+    Rows(p.dy, row0, p.dim, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rdy);
+    if constexpr (GATE) Rows(p.gate, row0, p.gs, hr, ch, sizeof(T)).load(whole, p.past != 0, hr, lf, rga);
     if (threadIdx.x < kRow * VEC) sh.rate[threadIdx.x] = p.rate * soft_plus(p.lam[min(at.c0 + (int64_t)threadIdx.x, p.dim - 1)]);
     __syncthreads();
     float k[VEC];
@@ -610,7 +626,7 @@ __global__ __launch_bounds__(kBwdStreams * kRow, 3) void glr_bwd_kernel(GlrParam
             for (int c = 0; c < VEC; ++c) dg[c] = dy[c] * h[c];
             R o;
             narrow(dg, o);
-            if (ok && (whole || (int64_t)hr + j < left)) bstore<R>(outg.r, outg.off, j * outg.step, o);
+            if (ok && (whole || (int64_t)hr + j < left)) outg.store(p.past != 0, j, o);
         }
     }
     __syncthreads();
@@ -639,9 +655,9 @@ __global__ __launch_bounds__(kBwdStreams * kRow, 3) void glr_bwd_kernel(GlrParam
         narrow(vr, orv);
         narrow(vi, oiv);
         if (ok && in) {
-            bstore<R>(outx.r, outx.off, j * outx.step, ox);
-            bstore<R>(outr.r, outr.off, j * outx.step, orv);
-            bstore<R>(outi.r, outi.off, j * outx.step, oiv);
+            outx.store(p.past != 0, j, ox);
+            outr.store(p.past != 0, j, orv);
+            outi.store(p.past != 0, j, oiv);
         }
     }
     if (p.dh0 && chunk == 0 && wave == 0 && half == 0 && ok) stf<VEC>(p.dh0 + bd, c_in);
@@ -796,6 +812,7 @@ GlrParams params_of(const ssm_glr_desc &d) {
     p.gs = stride_of(d.gate_stride, d.dim);
     p.rate = d.rate;
     p.kept = (int)chunks_of(d.seqlen, kKeep);
+    p.past = d.batch * d.seqlen * d.dim * (int64_t)esize(d.dtype) > kCached;
     return p;
 }
 
