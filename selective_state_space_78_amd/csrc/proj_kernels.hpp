@@ -53,7 +53,11 @@ constexpr float kGeluK = 1.5957691216057308f;   // 2 sqrt(2 / pi): z (1 + tanh(u
 
 __device__ __forceinline__ float proj_act(float z, int act) {
     if (act == kActSilu) return z * proj_sigmoid(z);
-    if (act == kActGelu) return z * proj_sigmoid(kGeluK * fmaf(0.044715f * z * z, z, z));
+    if (act == kActGelu) {
+        // the sigmoid's exponent -kGeluK log2(e) (z + 0.044715 z^3) from folded constants
+        constexpr float c = kGeluK * -1.4426950408889634f;
+        return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(z * z, c * 0.044715f, c)));
+    }
     return act == kActSigmoid ? proj_sigmoid(z) : z;
 }
 
@@ -260,6 +264,14 @@ template <typename T> __device__ __forceinline__ void proj_mul(const uint4 &p, c
     }
 }
 
+// A barrier behind which every wave's loads into LDS are there: a wave waits for its own
+// first. (The compiler waits where a wave itself reads what it loaded, which may be behind
+// the barrier, where others' are read too.)
+__device__ __forceinline__ void proj_arrived() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt 0; the other counters as they are
+    __syncthreads();
+}
+
 template <int BI, int BJ> struct ProjShape {
     static constexpr int kWI = BI == 256 ? 64 : BI / 2, kWJ = BJ / 2;     // a wave's part of the tile
     static constexpr int kWaves = (BI / kWI) * (BJ / kWJ);
@@ -345,14 +357,17 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
         int64_t s = s0 + odd;
         if (s < s2) {
             load(one, s);
-            __syncthreads();
-            for (; s < s2; s += 2) {
-                load(two, s + 1);
+            load(two, s + 1);
+            proj_arrived();
+            for (;; s += 2) {
                 multiply(one);
-                __syncthreads();
-                if (s + 2 < s2) load(one, s + 2);
+                proj_arrived();
+                const bool more = s + 2 < s2;
+                if (more) load(one, s + 2);
                 multiply(two);
-                __syncthreads();
+                proj_arrived();
+                if (!more) break;
+                load(two, s + 3);
             }
         }
     } else if (s0 < s1) {
