@@ -233,20 +233,31 @@ template <typename T, bool TURNED, int B, int W, bool FAST> struct ProjTile {
         for (int n = 0; n < kLoads; ++n) *reinterpret_cast<uint4 *>(lds + ((wave * kLoads + n) * 64 + lane) * 16) = v[n];
     }
 
-    // Fragment of the 16 rows (columns) from `at`, of the step's half h: r running over
-    // 4 groups of kEach values, one to each 16 lanes
-    static __device__ __forceinline__ uint4 read(const char *lds, int at, int h, int lane) {
+    // Where a lane's part of a wave's first fragment lies (the fragment's 16 rows or columns
+    // begin at `at`, a multiple of all that the wave's fragments span). Fragment f and the step's
+    // half h are told apart by an exclusive or and an addition of constants.
+    static __device__ __forceinline__ uint32_t place(int at, int lane) {
         const int s = lane & 15, g = lane >> 4;
         if constexpr (!TURNED) {
-            return *reinterpret_cast<const uint4 *>(lds + (at + s) * 128 + (((4 * h + g) ^ (s & 7)) << 4));
+            return (uint32_t)((at + s) * 128 + ((g ^ (s & 7)) << 4));
         } else if constexpr (sizeof(T) == 2) {
-            const int row = 32 * h + 8 * g + (s >> 2);
-            const int c = swap(at / 8 + ((s >> 1) & 1), row);
-            const uint16_t *p = reinterpret_cast<const uint16_t *>(lds + row * (B * 2) + c * 16 + (s & 1) * 8);
+            const int row = 8 * g + (s >> 2);
+            return (uint32_t)(row * (B * 2) + swap(at / 8 + ((s >> 1) & 1), row) * 16 + (s & 1) * 8);
+        } else {
+            const int row = 4 * g;
+            return (uint32_t)(row * (B * 4) + swap((at + s) >> 2, row) * 16 + (s & 3) * 4);
+        }
+    }
+
+    // Fragment f: r running over 4 groups of kEach values, one to each 16 lanes
+    static __device__ __forceinline__ uint4 read(const char *lds, uint32_t place, int f, int h) {
+        if constexpr (!TURNED) {
+            return *reinterpret_cast<const uint4 *>(lds + (place ^ (uint32_t)(h * 64)) + f * 2048);
+        } else if constexpr (sizeof(T) == 2) {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(lds + (place ^ (uint32_t)(f * 32)) + h * (64 * B));
             return __builtin_bit_cast(uint4, ssd_ld_tr2(p, p + 4 * B));
         } else {
-            const int row = 16 * h + 4 * g;
-            const char *p = lds + row * (B * 4) + swap((at + s) >> 2, row) * 16 + (s & 3) * 4;
+            const char *p = lds + (place ^ (uint32_t)(f * 64)) + h * (64 * B);
             return uint4{*reinterpret_cast<const uint32_t *>(p), *reinterpret_cast<const uint32_t *>(p + B * 4),
                          *reinterpret_cast<const uint32_t *>(p + B * 8), *reinterpret_cast<const uint32_t *>(p + B * 12)};
         }
@@ -304,6 +315,7 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
     tp.start(static_cast<const T *>(a.p) + g * a.gp, i0, a.I, a.ldp, wave, lane);
     tq.start(static_cast<const T *>(a.q) + g * a.gq, j0, a.J, a.ldq, wave, lane);
     const int wi = wave % (BI / S::kWI) * S::kWI, wj = wave / (BI / S::kWI) * S::kWJ;
+    const uint32_t place_p = TileP::place(wi, lane), place_q = TileQ::place(wj, lane);
     const int64_t every = (a.R + TileP::kStep - 1) / TileP::kStep;
     const int64_t s0 = (int64_t)split * a.steps, s1 = min(s0 + a.steps, every);
 
@@ -331,15 +343,16 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
         for (int h = 0; h < 2; ++h) {
             uint4 p[FI], q[FJ];
 #pragma unroll
-            for (int e = 0; e < FI; ++e) p[e] = TileP::read(from, wi + 16 * e, h, lane);
+            for (int e = 0; e < FI; ++e) p[e] = TileP::read(from, place_p, e, h);
 #pragma unroll
-            for (int f = 0; f < FJ; ++f) q[f] = TileQ::read(from + TileP::kBytes, wj + 16 * f, h, lane);
+            for (int f = 0; f < FJ; ++f) q[f] = TileQ::read(from + TileP::kBytes, place_q, f, h);
 #pragma unroll
             for (int f = 0; f < FJ; ++f)
 #pragma unroll
                 for (int e = 0; e < FI; ++e) proj_mul<T>(p[e], q[f], acc[f][e]);
-            // one half's fragments in registers at a time
-            if constexpr (BI == 256) __builtin_amdgcn_sched_barrier(0);
+            // both operands turned: one half's fragments in registers at a time, or they spill (8192^3: 0.83 ms,
+            // without 1.29; with one turned or none the halves overlap and gain 2%)
+            if constexpr (BI == 256 && TP && TQ && sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
         }
     };
     if constexpr (FAST) {
