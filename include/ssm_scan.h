@@ -3,7 +3,9 @@
  *
  * The library computes the Mamba selective scan (S6) forward pass, its
  * backward, its one-token decode step, the Mamba-2 SSD layer, the gated delta
- * rule (forward, backward, decode step) and the norms around such a mixer with
+ * rule (forward, backward, decode step), the norms around such a mixer, the gated
+ * linear recurrence (forward, backward, decode step), the projections around these
+ * (with bias, activation and residual) and the clipping of a model's gradients with
  * hand-written HIP kernels. Every pointer that
  * names tensor data is a DEVICE pointer owned by the caller; the library
  * allocates and frees nothing. Work is enqueued asynchronously on the given
@@ -599,10 +601,12 @@ int ssm_gated_norm_bwd(const ssm_gated_norm_desc *desc, const void *dy, const vo
  * y. Any other NaN or infinity makes NaN or infinite what depends on it by the
  * formulas; tokens of the same run of 8 or 16 behind which it stands, other channels
  * and other batch rows keep their values.
- * A row takes one workgroup of 512 work items per 64 channels (32 where channels or
- * addresses do not allow two at a time) and chunk of 128 or 256 tokens; sizes that
- * need 2^32 work items in a launch, counted for the smaller pieces, are refused
- * (SSM_ERR_SHAPE) before the first.
+ * A row takes one workgroup per 64 channels (32 where channels or addresses do not
+ * allow two at a time) and chunk: of 512 work items for 128 or 256 tokens forward, of
+ * 256 for 64 tokens backward. Sizes that need 2^32 work items in a launch, counted for
+ * the smaller pieces, are refused (SSM_ERR_SHAPE) before the first.
+ * Workgroups wait for one another through the workspace: it serves one call at a time,
+ * and calls on two streams need one each.
  */
 typedef struct {
     int64_t batch;     /* >= 0 */
@@ -647,7 +651,7 @@ int ssm_glr_fwd(const ssm_glr_desc *desc, const void *x, const void *rgate, cons
  *   dh0       (batch, dim) fp32, written, or NULL (not wanted); may equal dh_last exactly
  *   workspace ssm_glr_bwd_workspace_size(desc) bytes, 256-byte aligned
  * ssm_glr_fwd_save is ssm_glr_fwd (same results) that leaves in `workspace`
- * (ssm_glr_bwd_workspace_size bytes) the state before every 128 tokens, which
+ * (ssm_glr_bwd_workspace_size bytes) the state before every 64 tokens, which
  * ssm_glr_bwd would first recompute; ssm_glr_bwd_saved is ssm_glr_bwd reading them
  * there. It must receive the workspace of an ssm_glr_fwd_save call with the same
  * descriptor and inputs; nothing checks this. It clobbers the workspace's other

@@ -14,6 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 # translation units: the ABI (+ decode), one scan unit and one backward unit per
 # element type and discretisation (bf16 scans also one reading u in fp32),
+# then one for each of the other operators (the gated delta rule's by state size),
 # compiled in parallel and linked into one shared object
 UNITS = ("ssm_scan.hip", "scan_bf16_euler.hip", "scan_bf16_zoh.hip", "scan_bf16_euler_u32.hip",
          "scan_bf16_zoh_u32.hip", "scan_f32_euler.hip", "scan_f32_zoh.hip",

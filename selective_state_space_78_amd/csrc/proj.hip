@@ -115,12 +115,15 @@ struct Tiling {
 // gets: it holds `hold` of a tile at once, and a step of 128 bytes of r takes it
 // step[k] with k + 1 of them, next to `fixed` for a workgroup's first loads and its
 // output. Splits add their sums' traffic and a launch. Measured (bf16, us, tiles of 256
-// / 128 / 64, one split): 16384 x 2048 -> 4096 236 / 270 / 369; 8192 x 768 -> 1536 30.5
-// / 34.5 / 36.7; 2048 x 2048 -> 2048 39 (2 splits 41) / 31.5 / 27.7; 512 x 2048 -> 2048
-// 24 with 128, 12.7 with 64, 18.6 with 64 in two splits; fp32 8192 x 768 -> 1536 197 / 162 / 163.
+// / 128 / 64, one split): 16384 x 2048 -> 4096 233 / 263 / 355; 8192 x 768 -> 1536 28.1
+// / 29.2 / 33.3; 16384 x 64 -> 4096 43.8 / 47.5 / 49.8; 2048 x 2048 -> 2048 46 (2 splits
+// 41) / 27.4 / 27.2; 8192 x 12 groups of 128 -> 128 26.3 / 16.5 / 15.1; 2048 x 768 -> 1536
+// 23.8 / 12.6 / 10.5; 512 x 2048 -> 2048 44 / 21.7 / 12.0 (2 splits 32 / 20.6 / 16.5);
+// dweight of 8192 x 768 -> 1536 175 / 92 / 63, in 8 splits 43 / 35 / -; fp32 8192 x 768 ->
+// 1536 187 / 145 / 143.
 Tiling plan_for(int64_t I, int64_t J, int64_t R, int64_t groups, int dtype) {
     struct Kind { int side, hold; double step[4], fixed; };
-    static const Kind narrow[] = {{256, 1, {1.75}, 8.0}, {128, 2, {0.75, 1.0}, 4.0}, {64, 4, {0.3, 0.42, 0.58, 0.74}, 2.5}};
+    static const Kind narrow[] = {{256, 1, {1.75}, 8.0}, {128, 2, {0.75, 1.0}, 4.0}, {64, 4, {0.3, 0.42, 0.58, 0.74}, 2.3}};
     static const Kind wide[] = {{256, 1, {7.3}, 12.0}, {128, 2, {2.2, 4.1}, 5.0}, {64, 4, {0.9, 1.2, 1.6, 2.1}, 2.5}};
     const int64_t every = ceil_div(R, dtype == SSM_BF16 ? 64 : 32);
     Tiling best{128, 1, every};
