@@ -215,8 +215,8 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Table t, const dou
             known = true;
             const double v = parts > 0 ? sqrt(total(part, parts, s)) : (double)*norm;
             if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-            const double c = (double)max_norm / (v + (double)eps);
-            coef = c >= 1.0 ? 1.0f : (float)c;      // NaN stays
+            const double d = v + (double)eps, c = (double)max_norm / d;
+            coef = c >= 1.0 || d == 0.0 ? 1.0f : (float)c;      // NaN stays
         }
         return coef;
     };

@@ -120,6 +120,17 @@ def test_nothing(env):
     assert float(ssm.ssm_grad_norm([torch.ones(4, device="cuda")] * 4)) == 4
 
 
+def test_norm_of_zero(env):
+    """Zeros stay zeros, also where the formula's quotient would be 0 / 0."""
+    torch, ssm = env
+    for max_norm, eps in ((1.0, 1e-6), (1.0, 0.0), (0.0, 1e-6), (0.0, 0.0)):
+        g = [torch.zeros(70000, device="cuda"), torch.zeros(5, device="cuda").bfloat16()]
+        out = [torch.ones_like(t) for t in g]
+        norm = ssm.ssm_grad_clip(g, max_norm, eps=eps, out=out)
+        torch.cuda.synchronize()
+        assert float(norm) == 0 and not any(bool(t.any()) for t in out), (max_norm, eps)
+
+
 def test_captured(env):
     """In a graph, replayed on new gradients with eager work between."""
     torch, ssm = env
