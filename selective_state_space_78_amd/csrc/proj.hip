@@ -17,6 +17,10 @@ using namespace ssm_detail;
 
 constexpr int64_t kMaxWidth = ((int64_t)1 << 22) - 1;   // of a row: a tile's lane offsets stay in 32 bits
 constexpr int kCus = 256, kMostSplits = 64;
+// Bytes of a 16-bit output beyond which it goes past the cache. A product and one that reads its
+// output: 65536 x 1024 -> 2048 (268 MB) 540 -> 494 us, 16384 x 2048 -> 4096 (134 MB) 463 -> 430;
+// 16384 x 2560 -> 2560 (84 MB) 405 -> 417. fp32 gains nowhere (16384 x 768 -> 2048, 134 MB, 729 -> 738).
+constexpr int64_t kCached = (int64_t)100 << 20;
 
 size_t esize(int t) { return t == SSM_BF16 ? 2 : 4; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -177,6 +181,7 @@ template <typename T, bool TP, bool TQ> hipError_t product(ProjParams &a, Tiling
                       (TQ ? a.J : a.R) % each == 0;
     a.splits = (int)pl.splits;
     a.steps = (int)pl.steps;
+    a.past = !a.wide && a.groups * a.J * a.I * 2 > kCached;
     const hipError_t e = fast ? launch_tiles<T, TP, TQ, true>(a, pl.tile, st) : launch_tiles<T, TP, TQ, false>(a, 64, st);
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t n = (int64_t)a.groups * a.J * a.I;

@@ -21,10 +21,10 @@
 // in 16-byte stores of whole lines (16384 x 2048 -> 4096 writing pre as well 239 us; stored
 // from the accumulators, 8 bytes a lane over 16 rows, 329).
 //
-// Bound by the matrix cores at the large sizes: 8192^3 in bf16 takes 798 us (1377 TFLOP/s),
-// 71 % of its cycles with products running, the rest at the steps' barriers; fp32 4096^3
-// 930 us (148 TFLOP/s). Four waves of 128 x 128 instead of eight of 128 x 64 halve what is
-// read from LDS and read a step ahead, and came to 841; four buffers of 64 bytes of r to 832.
+// Bound by the matrix cores at the large sizes: 8192^3 in bf16 takes 766 us (1435 TFLOP/s),
+// products running in 71 % of its cycles, the rest at the steps' barriers; fp32 4096^3 930 us
+// (148 TFLOP/s). Four waves of 128 x 128 instead of eight of 128 x 64 halve what is read from
+// LDS, and read a step ahead: 841 us where this took 798; with four buffers of 64 bytes of r 832.
 //
 // Where tiles are few the reduction is split over workgroups: each writes its fp32 sums,
 // and a second kernel adds them in order and finishes as the first would.
@@ -48,6 +48,7 @@ struct ProjParams {
     float *part;                // splits > 1: (split, group, J, I)
     int ti, tj, groups, splits, steps;   // tiles; steps of r to a split
     int act, wide, eight;       // wide: the output is fp32; eight: groups of 8 columns lie on 16-byte addresses
+    int past;                   // the output goes past the cache
 };
 
 __device__ __forceinline__ float proj_sigmoid(float v) {
@@ -95,18 +96,21 @@ template <typename T> __device__ __forceinline__ void proj_load4(const void *bas
     }
 }
 
-template <typename T, int N> __device__ __forceinline__ void proj_store(void *base, int64_t at, const float (&v)[N]) {
+// PAST: past the cache
+template <bool PAST> __device__ __forceinline__ void proj_put(void *to, uint4 v) {
+    if constexpr (PAST) __builtin_nontemporal_store(__builtin_bit_cast(ssd_u32x4, v), static_cast<ssd_u32x4 *>(to));
+    else *static_cast<uint4 *>(to) = v;
+}
+template <typename T, int N, bool PAST = false> __device__ __forceinline__ void proj_store(void *base, int64_t at, const float (&v)[N]) {
+    T *o = static_cast<T *>(base) + at;
     if constexpr (N == 1) {
         proj_store1<T>(base, at, v[0]);
+    } else if constexpr (sizeof(T) == 2) {
+        proj_put<PAST>(o, uint4{ssd_pack(v[0], v[1]), ssd_pack(v[2], v[3]), ssd_pack(v[4], v[5]), ssd_pack(v[6], v[7])});
     } else {
 #pragma unroll
-        for (int e = 0; e < N; e += sizeof(T) == 2 ? 8 : 4) {
-            if constexpr (sizeof(T) == 2)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(base) + at) =
-                    uint4{ssd_pack(v[0], v[1]), ssd_pack(v[2], v[3]), ssd_pack(v[4], v[5]), ssd_pack(v[6], v[7])};
-            else
-                *reinterpret_cast<float4 *>(static_cast<T *>(base) + at + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        }
+        for (int e = 0; e < N; e += 4)
+            proj_put<PAST>(o + e, uint4{__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]), __float_as_uint(v[e + 3])});
     }
 }
 template <typename T, int N> __device__ __forceinline__ void proj_load(const void *base, int64_t at, float (&v)[N]) {
@@ -129,7 +133,7 @@ __device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t 
     const int64_t at = g * a.go + j * a.ldo + i;
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] += bias[e];
-    if (a.pre) proj_store<T, N>(a.pre, at, v);
+    if (a.pre) proj_store<T, N, true>(a.pre, at, v);       // nothing reads it before the backward
     if (a.act != kActNone) {
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = proj_act(v[e], a.act);
@@ -142,6 +146,7 @@ __device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t 
         for (int e = 0; e < N; ++e) v[e] += r[e];
     }
     if (a.wide) proj_store<float, N>(a.out, at, v);
+    else if (a.past) proj_store<T, N, true>(a.out, at, v);
     else proj_store<T, N>(a.out, at, v);
 }
 
@@ -151,7 +156,6 @@ template <int N> __device__ __forceinline__ void proj_bias(const ProjParams &a, 
 }
 
 typedef __attribute__((address_space(3))) void proj_lds;
-typedef const __attribute__((address_space(1))) void proj_glb;
 
 // One operand's tile of B rows (kept) or columns (turned), W waves
 template <typename T, bool TURNED, int B, int W, bool FAST> struct ProjTile {
