@@ -964,15 +964,16 @@ def ssm_gated_norm_bwd(dy, x, z, weight, eps=1e-5, gate_first=False, out=None, w
 
 def _outputs(out, device, stream):
     """get(name, shape, dtype, wanted): the preallocated output of that name, or a new one."""
-    o = dict(out or {})
+    given = out or {}
 
     def get(name, shape, dtype, wanted=True):
         if not wanted:
             return None
-        if o.get(name) is None:
-            o[name] = _empty(shape, dtype, device, stream)
-        _check(o[name], name, shape, dtype, device)
-        return o[name]
+        t = given.get(name)
+        if t is None:
+            return _empty(shape, dtype, device, stream)
+        _check(t, name, shape, dtype, device)
+        return t
     return get
 
 
@@ -1022,11 +1023,13 @@ def ssm_glr_fwd(x, rgate, igate, lam, h0=None, gate=None, reset=None, rate=8.0, 
     dev, f32 = x.device, torch.float32
     _check(h0, "h0", (batch, dim), f32, dev)
     if y is None:
-        y = _empty((batch, L, dim), x.dtype, dev, stream)
-    if h_last is None and want_h_last:
+        y = _empty(x.shape, x.dtype, dev, stream)
+    else:
+        _check(y, "y", x.shape, x.dtype, dev)
+    if h_last is not None:
+        _check(h_last, "h_last", (batch, dim), f32, dev)
+    elif want_h_last:
         h_last = _empty((batch, dim), f32, dev, stream)
-    _check(y, "y", (batch, L, dim), x.dtype, dev)
-    _check(h_last, "h_last", (batch, dim), f32, dev)
     L_ = lib()
     name = "ssm_glr_fwd_save" if _save else "ssm_glr_fwd"
     size = L_.ssm_glr_bwd_workspace_size if _save else L_.ssm_glr_workspace_size
@@ -1060,14 +1063,15 @@ def ssm_glr_bwd(x, rgate, igate, lam, dy, h0=None, dh_last=None, gate=None, rese
     if x.dim() != 3:
         raise ValueError("x must be (batch, L, dim)")
     desc = _glr_desc(x, rgate, igate, lam, gate, reset, rate)
-    batch, L, dim = x.shape
+    shape = x.shape
+    batch, _, dim = shape
     dev, t, f32 = x.device, x.dtype, torch.float32
     _check(h0, "h0", (batch, dim), f32, dev)
-    _check(dy, "dy", (batch, L, dim), t, dev)
+    _check(dy, "dy", shape, t, dev)
     _check(dh_last, "dh_last", (batch, dim), f32, dev)
     get = _outputs(out, dev, stream)
-    g = dict(dx=get("dx", (batch, L, dim), t), drgate=get("drgate", (batch, L, dim), t),
-             digate=get("digate", (batch, L, dim), t), dgate=get("dgate", (batch, L, dim), t, gate is not None),
+    g = dict(dx=get("dx", shape, t), drgate=get("drgate", shape, t), digate=get("digate", shape, t),
+             dgate=get("dgate", shape, t, gate is not None),
              dlam=get("dlam", (dim,), f32), dh0=get("dh0", (batch, dim), f32, want_dh0))
     L_ = lib()
     name = "ssm_glr_bwd_saved" if _saved else "ssm_glr_bwd"

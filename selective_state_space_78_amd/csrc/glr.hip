@@ -466,7 +466,7 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
 
 // Backward: chunks of kKeep tokens from the end, the states before a lane's tokens recomputed into
 // registers. 4 x 2048 x 1536 in bf16 with a gate 59 us, 230 MB at 3.9 TB/s: the arithmetic of two
-// sigmoids, the decay and four gradients (117 instructions to a value, 38 us of them at 2.4 GHz)
+// sigmoids, the decay and four gradients (80 instructions to a value, 26 us of issue at 2.4 GHz)
 // stands beside the memory. Three workgroups a CU, two where pairs of fp32 and a gate would spill
 // (training on 4 x 2048 x 1536 165 us, with three 176; without a gate 132 either way).
 template <typename T, int VEC, bool RESET, bool GATE>
