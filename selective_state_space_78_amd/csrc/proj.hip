@@ -29,10 +29,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // dpre = dy act'(pre), and its sums over rows. A workgroup takes 64 lanes' columns
 // of a slab of rows, four rows at a time; the slabs' sums are added by proj_sum_kernel.
 
+// Beyond 100 the slopes are at their ends, 0 and 1: there z's powers, which the vanishing
+// 1 - s or s stands before, are taken at 100 and do not overflow.
 __device__ __forceinline__ float act_grad(float z, int act) {
     const float u = act == kActGelu ? kGeluK * fmaf(0.044715f * z * z, z, z) : z;
     const float e = __builtin_amdgcn_exp2f(u * -1.4426950408889634f), s = __builtin_amdgcn_rcpf(1.0f + e);
     const float r = e > 1.0f ? 1.0f - s : e * s;          // 1 - s to its own digits
+    z = fminf(fmaxf(z, -100.0f), 100.0f);                 // NaN is in s
     if (act == kActSilu) return s * fmaf(z, r, 1.0f);
     if (act == kActGelu) return fmaf(z * s * r, kGeluK * fmaf(3.0f * 0.044715f * z, z, 1.0f), s);
     return act == kActSigmoid ? s * r : 1.0f;

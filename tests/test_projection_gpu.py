@@ -207,6 +207,33 @@ def test_rows_keep_apart(env):
         assert torch.equal(bad, clean)
 
 
+@pytest.mark.parametrize("shape", [(16500, 1, 40, 4104), (16500, 1, 4104, 40), (13100, 2, 24, 2056)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_outputs_beyond_the_cache(env, shape):
+    """y or dx of more than 100 MiB in 16 bits, with a residual and pre."""
+    torch, ssm = env
+    whole(env, *shape, torch.bfloat16, res=torch.bfloat16)
+    s = make(torch, *shape, torch.bfloat16, torch.bfloat16)
+    y = ssm.ssm_proj_fwd(s["x"], s["weight"], residual=s["residual"])
+    ssm.ssm_proj_fwd(s["x"], s["weight"], residual=s["residual"], y=s["residual"])
+    torch.cuda.synchronize()
+    assert torch.equal(y, s["residual"])
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_slopes_at_their_ends(env, dtype):
+    """Where the activations are straight their gradients are 0 and 1, whatever z's square; NaN stays."""
+    torch, ssm = env
+    t = getattr(torch, dtype)
+    z = torch.tensor([300.0, 1e10, 1e20, 3e38, float("inf"), float("nan")], device="cuda").to(t)
+    z = torch.cat([z, -z]).view(1, 12)
+    x, w, dy = torch.ones(1, 4, device="cuda").to(t), torch.ones(12, 4, device="cuda").to(t), torch.full_like(z, 2.0)
+    for act, up in (("silu", 2.0), ("gelu", 2.0), ("sigmoid", 0.0)):
+        d = ssm.ssm_proj_bwd(dy, x, w, pre=z, activation=act)["dpre"][0].float()
+        torch.cuda.synchronize()
+        assert (d[:5] == up).all() and (d[6:11] == 0).all() and d[5].isnan() and d[11].isnan(), (act, d)
+
+
 def test_empty(env):
     torch, ssm = env
     x, w = torch.zeros(0, 8, device="cuda"), torch.ones(4, 8, device="cuda")
