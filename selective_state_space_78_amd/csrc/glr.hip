@@ -61,7 +61,7 @@ constexpr int kBack = 8;                                  // chunks that are loo
 // stays in it, 100 -> 106 us)
 constexpr int64_t kCached = (int64_t)128 << 20;
 constexpr int64_t kMaxStride = (1 << 24) - 1;             // lane offsets stay in 32 bits
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.92596299e-8f;   // and its next digits
 
 struct GlrParams {
     const void *x, *rg, *ig, *gate, *dy;
@@ -108,9 +108,17 @@ template <int VEC> __device__ __forceinline__ void stf(float *p, const float (&v
 
 __device__ __forceinline__ float soft_plus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))) + (v != v ? v : 0.0f); }
 
-// sigmoid; e = exp(-v) (infinite where the sigmoid is 0)
-__device__ __forceinline__ float sigm(float v, float &e) {
-    e = __builtin_amdgcn_exp2f(v * -kLog2e);
+// sigmoid; e = exp(-v) (infinite where the sigmoid is 0). With fp32 gates the exponent is taken
+// to twice fp32's digits, as its rounding leaves e off by |v| half steps: a few at any v then.
+// Where gates have 16 bits, which tell them to 2^-9, it is rounded (8 x 8192 x 4096 425 us, in
+// full 457; fp32 takes the same time either way).
+template <typename T> __device__ __forceinline__ float sigm(float v, float &e) {
+    const float t = v * -kLog2e;
+    e = __builtin_amdgcn_exp2f(t);
+    if constexpr (sizeof(T) == 4) {
+        const float low = fmaf(v, -kLog2eLow, fmaf(v, -kLog2e, -t));
+        e *= fmaf(__builtin_amdgcn_fmed3f(low, -1.0f, 1.0f), 0.69314718f, 1.0f);      // infinities stay
+    }
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
 // 1 - sigmoid to its own digits
@@ -390,7 +398,7 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
                 float e;
-                s[n][c] = k[c] * sigm(r[c], e);
+                s[n][c] = k[c] * sigm<T>(r[c], e);
                 a[j0 + n][c] = decay_near(s[n][c], w[n][c]);
             }
         }
@@ -413,7 +421,7 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
                 if constexpr (RESET) {
                     if ((first >> j) & 1) { a[j][c] = -0.0f; m = 1.0f; }
                 }
-                b[j][c] = m * sigm(i[c], e) * x[c];
+                b[j][c] = m * sigm<T>(i[c], e) * x[c];
                 if (!in) { a[j][c] = 1.0f; b[j][c] = 0.0f; }
                 H[c] = behind<RESET>(a[j][c], b[j][c], H[c]);
                 P[c] = both<RESET>(P[c], a[j][c]);
@@ -531,7 +539,7 @@ __global__ __launch_bounds__(kBwdStreams * kRow, sizeof(T) * VEC == 8 && GATE ? 
         widen(rr[j], r);
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
-            sr[c] = sigm(r[c], er[c]);
+            sr[c] = sigm<T>(r[c], er[c]);
             sw[j][c] = k[c] * sr[c];
             a[j][c] = decay_near(sw[j][c], w[c]);
         }
@@ -553,7 +561,7 @@ __global__ __launch_bounds__(kBwdStreams * kRow, sizeof(T) * VEC == 8 && GATE ? 
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
             float ei;
-            const float si = sigm(i[c], ei), inv = __builtin_amdgcn_rsqf(w[c]);
+            const float si = sigm<T>(i[c], ei), inv = __builtin_amdgcn_rsqf(w[c]);
             const bool still = w[c] < 1.17549435e-38f;     // a gate that lets nothing in or out
             float m = still ? 0.0f : w[c] * inv;
             const float q = still ? 0.0f : sw[j][c] * inv;
@@ -732,10 +740,10 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p, const float 
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
             float e, w;
-            const float s = k[c] * sigm(r[c], e);
+            const float s = k[c] * sigm<T>(r[c], e);
             float a = decay_near(s, w);
             decay_far(s, a, w);
-            const float ix = sigm(i[c], e) * x[c];
+            const float ix = sigm<T>(i[c], e) * x[c];
             s0[c] = first ? ix : fmaf(a, s0[c], __builtin_amdgcn_sqrtf(w) * ix);
             v[c] = p.gate ? s0[c] * g[c] : s0[c];
         }

@@ -31,9 +31,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Beyond 100 the slopes are at their ends, 0 and 1: there z's powers, which the vanishing
 // 1 - s or s stands before, are taken at 100 and do not overflow.
-__device__ __forceinline__ float act_grad(float z, int act) {
-    const float u = act == kActGelu ? kGeluK * fmaf(0.044715f * z * z, z, z) : z;
-    const float e = __builtin_amdgcn_exp2f(u * -1.4426950408889634f), s = __builtin_amdgcn_rcpf(1.0f + e);
+template <typename T> __device__ __forceinline__ float act_grad(float z, int act) {
+    float e;
+    const float s = proj_gate<T>(z, act, e);
     const float r = e > 1.0f ? 1.0f - s : e * s;          // 1 - s to its own digits
     z = fminf(fmaxf(z, -100.0f), 100.0f);                 // NaN is in s
     if (act == kActSilu) return s * fmaf(z, r, 1.0f);
@@ -68,7 +68,7 @@ template <typename T, typename D, int VEC> __global__ __launch_bounds__(256) voi
                 if constexpr (VEC == 4) proj_load4<T>(a.pre, at, z);
                 else z[0] = proj_load1<T>(a.pre, at);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) d[e] *= act_grad(z[e], a.act);
+                for (int e = 0; e < VEC; ++e) d[e] *= act_grad<T>(z[e], a.act);
             }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[e] += d[e];

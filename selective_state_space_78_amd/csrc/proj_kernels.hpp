@@ -51,20 +51,42 @@ struct ProjParams {
     int past;                   // the output goes past the cache
 };
 
-__device__ __forceinline__ float proj_sigmoid(float v) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+constexpr float kGeluK = 1.5957691216057308f;   // 2 sqrt(2 / pi): z (1 + tanh(u)) / 2 = z sigmoid(2 u)
+constexpr double kGelu1 = -1.5957691216057308 * 1.4426950408889634, kGelu3 = kGelu1 * 0.044715;   // of z and z^3, as a power of 2
+
+// The sigmoid that the activation multiplies z by (or is): of z, for gelu of 2 sqrt(2 / pi)
+// (z + 0.044715 z^3); e is the exponential of its negative argument. Rounding the argument
+// leaves e off by as many half steps as the argument is large. T of 16 bits rounds more than
+// that; of fp32 the argument is taken to twice its digits, and 1 + e scaled so that its
+// reciprocal stays a normal number up to e's overflow: a few half steps at any z.
+template <typename T> __device__ __forceinline__ float proj_gate(float z, int act, float &e) {
+#pragma clang fp contract(off)      // what a product rounds away is added once
+    constexpr float c = -1.4426950408889634f;
+    if constexpr (sizeof(T) == 2) {
+        e = __builtin_amdgcn_exp2f(z * (act == kActGelu ? fmaf(z * z, (float)kGelu3, (float)kGelu1) : c));
+        return __builtin_amdgcn_rcpf(1.0f + e);
+    } else {
+        float t, low;
+        if (act == kActGelu) {
+            constexpr float c1 = (float)kGelu1, d1 = (float)(kGelu1 - c1), c3 = (float)kGelu3, d3 = (float)(kGelu3 - c3);
+            const float q = z * z, w = z * q, wl = fmaf(z, q, -w) + z * fmaf(z, z, -q);
+            const float a = z * c1, b = w * c3, bb = (t = a + b) - a;
+            low = ((a - (t - bb)) + (b - bb)) + fmaf(z, d1, fmaf(z, c1, -a)) + fmaf(wl, c3, fmaf(w, d3, fmaf(w, c3, -b)));
+        } else {
+            t = z * c;
+            low = fmaf(z, -1.92596299e-8f, fmaf(z, c, -t));
+        }
+        e = __builtin_amdgcn_exp2f(t) * fmaf(__builtin_amdgcn_fmed3f(low, -1.0f, 1.0f), 0.69314718f, 1.0f);   // infinities stay
+        constexpr float kScale = 1.0f / 256.0f;
+        return __builtin_amdgcn_rcpf(fmaf(e, kScale, kScale)) * kScale;
+    }
 }
 
-constexpr float kGeluK = 1.5957691216057308f;   // 2 sqrt(2 / pi): z (1 + tanh(u)) / 2 = z sigmoid(2 u)
-
-__device__ __forceinline__ float proj_act(float z, int act) {
-    if (act == kActSilu) return z * proj_sigmoid(z);
-    if (act == kActGelu) {
-        // the sigmoid's exponent -kGeluK log2(e) (z + 0.044715 z^3) from folded constants
-        constexpr float c = kGeluK * -1.4426950408889634f;
-        return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * fmaf(z * z, c * 0.044715f, c)));
-    }
-    return act == kActSigmoid ? proj_sigmoid(z) : z;
+template <typename T> __device__ __forceinline__ float proj_act(float z, int act) {
+    float e;
+    if (act == kActNone) return z;
+    const float s = proj_gate<T>(z, act, e);
+    return act == kActSigmoid ? s : z * s;
 }
 
 template <typename T> __device__ __forceinline__ void proj_store4(void *base, int64_t at, const float (&v)[4]) {
@@ -136,7 +158,7 @@ __device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t 
     if (a.pre) proj_store<T, N, true>(a.pre, at, v);       // nothing reads it before the backward
     if (a.act != kActNone) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = proj_act(v[e], a.act);
+        for (int e = 0; e < N; ++e) v[e] = proj_act<T>(v[e], a.act);
     }
     if (a.res) {
         float r[N];
@@ -564,7 +586,7 @@ template <typename T, int MJ> __global__ __launch_bounds__(256) void proj_few_ke
     if (a.bias) v += a.bias[n0 + n];
     const int64_t at = g * a.go + m * a.ldo + i;
     if (a.pre) proj_store1<T>(a.pre, at, v);
-    v = proj_act(v, a.act);
+    v = proj_act<T>(v, a.act);
     if (a.res) v += a.wide ? proj_load1<float>(a.res, at) : proj_load1<T>(a.res, at);
     if (a.wide) proj_store1<float>(a.out, at, v);
     else proj_store1<T>(a.out, at, v);

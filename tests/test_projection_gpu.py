@@ -234,6 +234,33 @@ def test_slopes_at_their_ends(env, dtype):
         assert (d[:5] == up).all() and (d[6:11] == 0).all() and d[5].isnan() and d[11].isnan(), (act, d)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid"])
+def test_tails_in_fp32(env, act):
+    """fp32 activations and their gradients against their own size, to values of 1e-37. The argument is known
+    to twice fp32's digits; exp2 and the reciprocal 2 u each, three products or sums u each, z's product u: 10 u.
+    A gradient's terms have one such factor or two, and three products: 24 u of their sizes."""
+    torch, ssm = env
+    z = torch.linspace(-9.9, 9.9, 4096, device="cuda") if act == "gelu" else torch.linspace(-86, 86, 4096, device="cuda")
+    w = z.view(-1, 1)
+    z64 = z.double().cpu().numpy()
+    want = block.activation(z64, act)
+    sg = block.sigmoid(block.GELU_K * (z64 + 0.044715 * z64 ** 3) if act == "gelu" else z64)
+    r = block.sigmoid(-block.GELU_K * (z64 + 0.044715 * z64 ** 3) if act == "gelu" else -z64)
+    slope = block.GELU_K * (1 + 3 * 0.044715 * z64 * z64) if act == "gelu" else 1.0
+    # from 1 - s itself, where the oracle's difference has no digits left
+    grad = sg * r if act == "sigmoid" else sg + z64 * sg * r * slope
+    terms = sg * r if act == "sigmoid" else sg + np.abs(z64) * sg * r * slope
+    for rows in (1, 20):
+        x = torch.ones(rows, 1, device="cuda")
+        y, pre = ssm.ssm_proj_fwd_save(x, w, activation=act)
+        d = ssm.ssm_proj_bwd(torch.ones_like(y), x, w, pre=pre, activation=act, want_dx=False, want_dweight=False)["dpre"]
+        torch.cuda.synchronize()
+        assert torch.equal(pre[-1], z)
+        off, doff = np.abs(y[-1].double().cpu().numpy() - want), np.abs(d[-1].double().cpu().numpy() - grad)
+        say("tails", act, rows, float((off / np.abs(want).clip(1e-300)).max() / U), float((doff / terms).max() / U))
+        assert (off <= 10 * U * np.abs(want)).all() and (doff <= 24 * U * terms).all()
+
+
 def test_empty(env):
     torch, ssm = env
     x, w = torch.zeros(0, 8, device="cuda"), torch.ones(4, 8, device="cuda")

@@ -268,6 +268,25 @@ def test_extreme_gates(env):
     assert np.allclose(np64(got["y"]), y, rtol=1e-5, atol=1e-5) and np.allclose(np64(got["dx"]), g["dx"], rtol=1e-5, atol=1e-5)
 
 
+def test_input_gates_in_fp32(env):
+    """Where every token starts a sequence y = sigmoid(igate) x: against its own size, to values of 1e-37. The gate's
+    exponent is known to twice fp32's digits; exp2 and the reciprocal 2 u each, four products or sums u each: 10 u."""
+    torch, ssm = env
+    gate = torch.linspace(-86, 86, 4096, device="cuda")
+    for D in (64, 1):
+        i = gate.view(1, -1, D)
+        x = torch.linspace(0.5, 2, 4096, device="cuda").view_as(i)
+        reset = torch.ones(i.shape[:2], dtype=torch.bool, device="cuda")
+        y, _ = ssm.ssm_glr_fwd(x, x, i, torch.zeros(D, device="cuda"), reset=reset)
+        step = ssm.ssm_glr_state_update(x[:, 3], x[:, 3], i[:, 3], torch.zeros(D, device="cuda"), torch.ones(1, D, device="cuda"),
+                                        reset=reset[:, 3])
+        torch.cuda.synchronize()
+        want = block.sigmoid(np64(i)) * np64(x)
+        off = np.abs(np64(y) - want) / want
+        say("input gates", D, float(off.max() / U))
+        assert off.max() <= 10 * U and torch.equal(step, y[:, 3])
+
+
 def test_empty(env):
     torch, ssm = env
     z = lambda *s: torch.zeros(s, device="cuda")
