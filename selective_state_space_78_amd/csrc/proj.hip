@@ -106,8 +106,8 @@ __global__ __launch_bounds__(kSumCols * kSumRuns) void proj_sum_kernel(const flo
 }
 
 __global__ __launch_bounds__(256) void proj_zero_kernel(void *p, int64_t bytes) {
-    const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
-    if (k < bytes) *reinterpret_cast<uint16_t *>(static_cast<char *>(p) + k) = 0;
+    for (int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2; k < bytes; k += (int64_t)gridDim.x * 512)
+        *reinterpret_cast<uint16_t *>(static_cast<char *>(p) + k) = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -262,7 +262,7 @@ template <typename T, typename D> hipError_t dpre_pass(const DpreParams &a, int6
 
 int zero(void *p, int64_t bytes, hipStream_t st) {
     if (p == nullptr || bytes == 0) return SSM_OK;
-    hipLaunchKernelGGL(proj_zero_kernel, dim3((unsigned)ceil_div(bytes, 512)), dim3(256), 0, st, p, bytes);
+    hipLaunchKernelGGL(proj_zero_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(bytes, 512), 1 << 20)), dim3(256), 0, st, p, bytes);
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
