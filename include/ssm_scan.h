@@ -693,7 +693,7 @@ int ssm_glr_state_update(const ssm_glr_desc *desc, const void *x, const void *rg
  * activation and residual are applied to the fp32 sums, and y and pre are rounded once.
  * gelu is the form z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3)).
  *
- * Up to 8 rows the forward reads the weight once without tiles. Results do not depend
+ * Up to 16 rows the forward reads the weight once without tiles. Results do not depend
  * on timing, nor on other rows' values; they may differ by rounding between numbers of
  * rows. Sizes that need 2^32 work items in a launch are refused (SSM_ERR_SHAPE).
  */

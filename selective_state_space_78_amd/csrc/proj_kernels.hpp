@@ -30,6 +30,8 @@
 // and a second kernel adds them in order and finishes as the first would.
 #pragma once
 
+#include <type_traits>
+
 #include "matrix_ops.hpp"
 
 namespace ssm_detail {
@@ -507,24 +509,23 @@ template <typename T, int N> __global__ __launch_bounds__(256) void proj_join_ke
     proj_finish<T, N>(a, (int)g, j, i, bias, v);
 }
 
-// A few rows (up to MJ): the weight is read once, 16 bytes a lane along r (at any
-// address), two of its rows to a wave; the products are ordinary fp32 ones. Bound by
-// the weight's bytes.
-template <typename T, int MJ> __global__ __launch_bounds__(256) void proj_few_kernel(ProjParams a) {
+// One row: the weight is read once, 16 bytes a lane along r at any address, two of its rows to
+// a wave; the products are ordinary fp32 ones. Bound by the weight's bytes (4096 -> 4096 in bf16
+// 6.1 us, 5.5 TB/s; by the matrix instructions of the next kernel 7.0).
+template <typename T> __global__ __launch_bounds__(256) void proj_one_row_kernel(ProjParams a) {
     constexpr int E = 16 / (int)sizeof(T), NI = 2;
     const int lane = threadIdx.x & 63;
     const int64_t total = a.groups * a.I;
     const int64_t n0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * NI;
     if (n0 >= total) return;
-    float acc[NI][MJ];
+    float acc[NI];
     const T *w[NI], *x[NI];
 #pragma unroll
     for (int n = 0; n < NI; ++n) {
         const int64_t i = min(n0 + n, total - 1), g = i / a.I;
         w[n] = static_cast<const T *>(a.p) + g * a.gp + (i - g * a.I) * a.ldp;
         x[n] = static_cast<const T *>(a.q) + g * a.gq;
-#pragma unroll
-        for (int m = 0; m < MJ; ++m) acc[n][m] = 0.0f;
+        acc[n] = 0.0f;
     }
     const bool apart = x[1] != x[0];        // the wave's two rows lie in two groups
     auto get = [](const T *p, float (&v)[E]) {
@@ -543,53 +544,94 @@ template <typename T, int MJ> __global__ __launch_bounds__(256) void proj_few_ke
     const int64_t whole = a.R / E * E;
 #pragma unroll 4
     for (int64_t r = (int64_t)lane * E; r < whole; r += 64 * E) {
-        float wv[NI][E];
+        float wv[NI][E], xv[E];
 #pragma unroll
         for (int n = 0; n < NI; ++n) get(w[n] + r, wv[n]);
+        get(x[0] + r, xv);
 #pragma unroll
-        for (int m = 0; m < MJ; ++m) {
-            if (m >= a.J) break;
-            float xv[E];
-            get(x[0] + m * a.ldq + r, xv);
+        for (int n = 0; n < NI; ++n) {
+            if (n > 0 && apart) get(x[n] + r, xv);
 #pragma unroll
-            for (int n = 0; n < NI; ++n) {
-                if (n > 0 && apart) get(x[n] + m * a.ldq + r, xv);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[n][m] = fmaf(wv[n][e], xv[e], acc[n][m]);
-            }
+            for (int e = 0; e < E; ++e) acc[n] = fmaf(wv[n][e], xv[e], acc[n]);
         }
     }
     if (whole + lane < a.R) {
 #pragma unroll
-        for (int n = 0; n < NI; ++n) {
-            const float wv = proj_load1<T>(w[n], whole + lane);
-#pragma unroll
-            for (int m = 0; m < MJ; ++m)
-                if (m < a.J) acc[n][m] = fmaf(wv, proj_load1<T>(x[n], m * a.ldq + whole + lane), acc[n][m]);
-        }
+        for (int n = 0; n < NI; ++n) acc[n] = fmaf(proj_load1<T>(w[n], whole + lane), proj_load1<T>(x[n], whole + lane), acc[n]);
     }
 #pragma unroll
     for (int n = 0; n < NI; ++n)
 #pragma unroll
-        for (int m = 0; m < MJ; ++m)
+        for (int o = 1; o < 64; o <<= 1) acc[n] += __shfl_xor(acc[n], o);
+    if (lane >= NI || n0 + lane >= total) return;
+    const int64_t g = (n0 + lane) / a.I, i = n0 + lane - g * a.I;
+    float v[1] = {lane == 0 ? acc[0] : acc[1]}, bias[1];
+    proj_bias<1>(a, (int)g, i, bias);
+    proj_finish<T, 1>(a, (int)g, 0, i, bias, v);
+}
+
+// Up to 16 rows: the weight is read once, straight into the matrix instructions' registers,
+// 16 bytes a lane along r at any address. A workgroup takes 16 of its rows, the waves share r
+// in runs of pairs of steps (whole lines); their sums are added in LDS in order. Bound by the
+// weight's bytes, then by x, which every workgroup reads (8 rows 4096 -> 4096 in bf16 8.3 us, 16
+// rows 9.6; in tiles 10.6; 8 rows 768 -> 1536 3.3 us, in tiles 5.7; with 16 waves 8.3 and 6.7).
+template <typename T, int W> __global__ __launch_bounds__(W * 64) void proj_few_rows_kernel(ProjParams a) {
+    constexpr int E = 16 / (int)sizeof(T), kStep = 4 * E;
+    __shared__ float4 sum[W][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, s = lane & 15, q = lane >> 4;
+    const uint32_t g = blockIdx.x / (uint32_t)a.ti;
+    const int64_t i0 = (int64_t)(blockIdx.x - g * (uint32_t)a.ti) * 16;
+    // rows past the last read it again; their products are not stored
+    const T *w = static_cast<const T *>(a.p) + g * a.gp + min(i0 + s, a.I - 1) * a.ldp + q * E;
+    const T *x = static_cast<const T *>(a.q) + g * a.gq + min((int64_t)s, a.J - 1) * a.ldq + q * E;
+    const int64_t steps = a.R / kStep, each = (steps + 2 * W - 1) / (2 * W) * 2;
+    const int64_t k0 = min(wave * each, steps), k1 = min(k0 + each, steps);
+    ssd_f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    auto get = [](const T *p) {
+        uint4 v;
+        __builtin_memcpy(&v, p, 16);
+        return v;
+    };
+    int64_t k = k0;
+    auto run = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        if (k + N > k1) return;
+        uint4 vw[N], vx[N];
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) acc[n][m] += __shfl_xor(acc[n][m], o);
-    // one output to a lane
-    float v = 0.0f;
+        for (int n = 0; n < N; ++n) vw[n] = get(w + (k + n) * kStep);
 #pragma unroll
-    for (int n = 0; n < NI; ++n)
+        for (int n = 0; n < N; ++n) vx[n] = get(x + (k + n) * kStep);
 #pragma unroll
-        for (int m = 0; m < MJ; ++m) v = lane == n * MJ + m ? acc[n][m] : v;
-    const int n = lane / MJ, m = lane % MJ;
-    if (n >= NI || m >= a.J || n0 + n >= total) return;
-    const int64_t g = (n0 + n) / a.I, i = n0 + n - g * a.I;
-    if (a.bias) v += a.bias[n0 + n];
-    const int64_t at = g * a.go + m * a.ldo + i;
-    if (a.pre) proj_store1<T>(a.pre, at, v);
-    v = proj_act<T>(v, a.act);
-    if (a.res) v += a.wide ? proj_load1<float>(a.res, at) : proj_load1<T>(a.res, at);
-    if (a.wide) proj_store1<float>(a.out, at, v);
-    else proj_store1<T>(a.out, at, v);
+        for (int n = 0; n < N; ++n) proj_mul<T>(vw[n], vx[n], acc);
+        k += N;
+    };
+    while (k + 8 <= k1) run(std::integral_constant<int, 8>());
+    run(std::integral_constant<int, 4>());
+    run(std::integral_constant<int, 2>());
+    run(std::integral_constant<int, 1>());
+    if (wave == W - 1 && steps * kStep < a.R) {
+        const int64_t at = steps * kStep, in = a.R - at - q * E;      // values of the lane's piece
+        T tw[E], tx[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            tw[e] = e < in ? w[at + e] : T(0);
+            tx[e] = e < in ? x[at + e] : T(0);
+        }
+        uint4 vw, vx;
+        __builtin_memcpy(&vw, tw, 16);
+        __builtin_memcpy(&vx, tx, 16);
+        proj_mul<T>(vw, vx, acc);
+    }
+    sum[wave][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (threadIdx.x >= 256) return;
+    const int i = threadIdx.x & 15, j = threadIdx.x >> 4;
+    if (j >= a.J || i0 + i >= a.I) return;
+    float v[1] = {0.0f}, bias[1];
+#pragma unroll
+    for (int n = 0; n < W; ++n) v[0] += reinterpret_cast<const float *>(&sum[n][(i >> 2) * 16 + j])[i & 3];
+    proj_bias<1>(a, (int)g, i0 + i, bias);
+    proj_finish<T, 1>(a, (int)g, j, i0 + i, bias, v);
 }
 
 }  // namespace ssm_detail

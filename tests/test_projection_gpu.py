@@ -137,6 +137,28 @@ def test_shapes(env, shape, dtype):
     whole(env, *shape, t, act=ACTS[k % 4], bias=k % 3 != 0, res=(None, t, torch.float32)[k % 3], strided=k % 2 == 1)
 
 
+# up to 16 rows: one or more groups, reductions of no step, some waves' steps, runs of every length and a rest
+FEW = [(1, 7, 40, 5), (1, 3, 1000, 33), (1, 1, 4097, 70), (2, 4, 64, 16), (2, 1, 4100, 72), (3, 1, 1, 3), (4, 1, 31, 8), (7, 3, 33, 17),
+       (8, 1, 520, 250), (12, 2, 700, 40), (15, 1, 4160, 24), (16, 1, 128, 4100), (16, 1, 6200, 33), (17, 1, 128, 24)]
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shape", FEW, ids=lambda s: "x".join(map(str, s)))
+def test_few_rows(env, shape, dtype):
+    torch, ssm = env
+    t = getattr(torch, dtype)
+    k = FEW.index(shape)
+    whole(env, *shape, t, act=ACTS[k % 4], bias=k % 2 == 0, res=(None, t, torch.float32)[k % 3], strided=k % 2 == 1)
+    # the same values at addresses that only their element's size divides
+    s = make(torch, *shape, t)
+    off = lambda v: torch.cat([v.new_zeros(1), v.reshape(-1)])[1:].view(v.shape)
+    y = ssm.ssm_proj_fwd(s["x"], s["weight"], bias=s["bias"])
+    z = ssm.ssm_proj_fwd(off(s["x"]), off(s["weight"]), bias=s["bias"])
+    torch.cuda.synchronize()
+    if shape[0] <= 16:
+        assert torch.equal(y, z)
+
+
 # every tile with ragged ends, reductions long enough to be split
 LARGE = [(4100, 1, 136, 2056), (2056, 1, 1032, 2064), (4096, 1, 512, 4096), (300, 1, 4096, 512), (40, 1, 4096, 72),
          (9000, 1, 128, 128), (6000, 4, 64, 64)]
