@@ -510,8 +510,9 @@ template <typename T, int N> __global__ __launch_bounds__(256) void proj_join_ke
 }
 
 // One row: the weight is read once, 16 bytes a lane along r at any address, two of its rows to
-// a wave; the products are ordinary fp32 ones. Bound by the weight's bytes (4096 -> 4096 in bf16
-// 6.1 us, 5.5 TB/s; by the matrix instructions of the next kernel 7.0).
+// a wave, four pieces of each on their way at once (one after another 6.0 us); the products are
+// ordinary fp32 ones. Bound by the weight's bytes (4096 -> 4096 in bf16 5.0 us, out of the cache;
+// by the matrix instructions of the next kernel 7.0, 768 -> 1536 3.2 either way).
 template <typename T> __global__ __launch_bounds__(256) void proj_one_row_kernel(ProjParams a) {
     constexpr int E = 16 / (int)sizeof(T), NI = 2;
     const int lane = threadIdx.x & 63;
@@ -528,9 +529,13 @@ template <typename T> __global__ __launch_bounds__(256) void proj_one_row_kernel
         acc[n] = 0.0f;
     }
     const bool apart = x[1] != x[0];        // the wave's two rows lie in two groups
-    auto get = [](const T *p, float (&v)[E]) {
-        uint32_t u[4];
-        __builtin_memcpy(u, p, 16);
+    auto get = [](const T *p) {
+        uint4 v;
+        __builtin_memcpy(&v, p, 16);
+        return v;
+    };
+    auto wide = [](const uint4 &r, float (&v)[E]) {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if constexpr (sizeof(T) == 2) {
@@ -542,19 +547,39 @@ template <typename T> __global__ __launch_bounds__(256) void proj_one_row_kernel
         }
     };
     const int64_t whole = a.R / E * E;
-#pragma unroll 4
-    for (int64_t r = (int64_t)lane * E; r < whole; r += 64 * E) {
-        float wv[NI][E], xv[E];
+    int64_t r = (int64_t)lane * E;
+    // N pieces on their way at once
+    auto run = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        uint4 vw[N][NI], vx[N], vo[N];
 #pragma unroll
-        for (int n = 0; n < NI; ++n) get(w[n] + r, wv[n]);
-        get(x[0] + r, xv);
+        for (int k = 0; k < N; ++k) {
 #pragma unroll
-        for (int n = 0; n < NI; ++n) {
-            if (n > 0 && apart) get(x[n] + r, xv);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[n] = fmaf(wv[n][e], xv[e], acc[n]);
+            for (int n = 0; n < NI; ++n) vw[k][n] = get(w[n] + r + k * 64 * E);
+            vx[k] = get(x[0] + r + k * 64 * E);
+            vo[k] = vx[k];
         }
-    }
+        if (apart) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) vo[k] = get(x[1] + r + k * 64 * E);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float w0[E], w1[E], x0[E], x1[E];
+            wide(vw[k][0], w0);
+            wide(vw[k][1], w1);
+            wide(vx[k], x0);
+            wide(vo[k], x1);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                acc[0] = fmaf(w0[e], x0[e], acc[0]);
+                acc[1] = fmaf(w1[e], x1[e], acc[1]);
+            }
+        }
+        r += N * 64 * E;
+    };
+    while (r + 3 * 64 * E < whole) run(std::integral_constant<int, 4>());
+    while (r < whole) run(std::integral_constant<int, 1>());
     if (whole + lane < a.R) {
 #pragma unroll
         for (int n = 0; n < NI; ++n) acc[n] = fmaf(proj_load1<T>(w[n], whole + lane), proj_load1<T>(x[n], whole + lane), acc[n]);
