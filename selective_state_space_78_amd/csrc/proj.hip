@@ -31,14 +31,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Beyond 100 the slopes are at their ends, 0 and 1: there z's powers, which the vanishing
 // 1 - s or s stands before, are taken at 100 and do not overflow.
-template <typename T> __device__ __forceinline__ float act_grad(float z, int act) {
+template <typename T, int ACT> __device__ __forceinline__ float act_grad(float z) {
     float e;
-    const float s = proj_gate<T>(z, act, e);
+    const float s = proj_gate<T, ACT>(z, e);
     const float r = e > 1.0f ? 1.0f - s : e * s;          // 1 - s to its own digits
-    z = fminf(fmaxf(z, -100.0f), 100.0f);                 // NaN is in s
-    if (act == kActSilu) return s * fmaf(z, r, 1.0f);
-    if (act == kActGelu) return fmaf(z * s * r, kGeluK * fmaf(3.0f * 0.044715f * z, z, 1.0f), s);
-    return act == kActSigmoid ? s * r : 1.0f;
+    z = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f);      // NaN is in s
+    if constexpr (ACT == kActSilu) return s * fmaf(z, r, 1.0f);
+    if constexpr (ACT == kActGelu) return fmaf(z * s * r, kGeluK * fmaf(3.0f * 0.044715f * z, z, 1.0f), s);
+    return s * r;
 }
 
 struct DpreParams {
@@ -67,8 +67,10 @@ template <typename T, typename D, int VEC> __global__ __launch_bounds__(256) voi
             if (a.act != kActNone) {
                 if constexpr (VEC == 4) proj_load4<T>(a.pre, at, z);
                 else z[0] = proj_load1<T>(a.pre, at);
+                proj_with(a.act, [&](auto act) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) d[e] *= act_grad<T>(z[e], a.act);
+                    for (int e = 0; e < VEC; ++e) d[e] *= act_grad<T, decltype(act)::value>(z[e]);
+                });
             }
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[e] += d[e];

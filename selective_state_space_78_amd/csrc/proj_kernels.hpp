@@ -61,15 +61,15 @@ constexpr double kGelu1 = -1.5957691216057308 * 1.4426950408889634, kGelu3 = kGe
 // leaves e off by as many half steps as the argument is large. T of 16 bits rounds more than
 // that; of fp32 the argument is taken to twice its digits, and 1 + e scaled so that its
 // reciprocal stays a normal number up to e's overflow: a few half steps at any z.
-template <typename T> __device__ __forceinline__ float proj_gate(float z, int act, float &e) {
+template <typename T, int ACT> __device__ __forceinline__ float proj_gate(float z, float &e) {
 #pragma clang fp contract(off)      // what a product rounds away is added once
     constexpr float c = -1.4426950408889634f;
     if constexpr (sizeof(T) == 2) {
-        e = __builtin_amdgcn_exp2f(z * (act == kActGelu ? fmaf(z * z, (float)kGelu3, (float)kGelu1) : c));
+        e = __builtin_amdgcn_exp2f(z * (ACT == kActGelu ? fmaf(z * z, (float)kGelu3, (float)kGelu1) : c));
         return __builtin_amdgcn_rcpf(1.0f + e);
     } else {
         float t, low;
-        if (act == kActGelu) {
+        if constexpr (ACT == kActGelu) {
             constexpr float c1 = (float)kGelu1, d1 = (float)(kGelu1 - c1), c3 = (float)kGelu3, d3 = (float)(kGelu3 - c3);
             const float q = z * z, w = z * q, wl = fmaf(z, q, -w) + z * fmaf(z, z, -q);
             const float a = z * c1, b = w * c3, bb = (t = a + b) - a;
@@ -84,11 +84,22 @@ template <typename T> __device__ __forceinline__ float proj_gate(float z, int ac
     }
 }
 
-template <typename T> __device__ __forceinline__ float proj_act(float z, int act) {
-    float e;
-    if (act == kActNone) return z;
-    const float s = proj_gate<T>(z, act, e);
-    return act == kActSigmoid ? s : z * s;
+// f(activation as a constant): one branch for all values that it is done for
+template <typename F> __device__ __forceinline__ void proj_with(int act, F f) {
+    if (act == kActSilu) f(std::integral_constant<int, kActSilu>());
+    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>());
+    else if (act == kActSigmoid) f(std::integral_constant<int, kActSigmoid>());
+}
+
+template <typename T, int N> __device__ __forceinline__ void proj_act(float (&v)[N], int act) {
+    proj_with(act, [&](auto a) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float e;
+            const float s = proj_gate<T, decltype(a)::value>(v[n], e);
+            v[n] = decltype(a)::value == kActSigmoid ? s : v[n] * s;
+        }
+    });
 }
 
 template <typename T> __device__ __forceinline__ void proj_store4(void *base, int64_t at, const float (&v)[4]) {
@@ -158,10 +169,7 @@ __device__ __forceinline__ void proj_finish(const ProjParams &a, int g, int64_t 
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] += bias[e];
     if (a.pre) proj_store<T, N, true>(a.pre, at, v);       // nothing reads it before the backward
-    if (a.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = proj_act<T>(v[e], a.act);
-    }
+    proj_act<T, N>(v, a.act);
     if (a.res) {
         float r[N];
         if (a.wide) proj_load<float, N>(a.res, at, r);
