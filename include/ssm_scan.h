@@ -719,7 +719,7 @@ typedef struct {
  *   y         (rows, groups, out)       y_dtype, written; may equal residual exactly
  *   workspace ssm_proj_workspace_size(desc) bytes, 256-byte aligned; its contents on
  *             entry do not matter
- * Pointers need their element's alignment only (16-byte aligned rows move faster).
+ * Pointers need their element's alignment only (rows of whole 4-byte words move faster).
  * Other overlaps of outputs are refused.
  */
 size_t ssm_proj_workspace_size(const ssm_proj_desc *desc);

@@ -223,9 +223,10 @@ template <typename T, bool TURNED, int B, int W, bool FAST> struct ProjTile {
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
                 const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n);
-                // rows and columns past the operand's read its last ones; their products are not stored
+                // rows and columns past the operand's read its last ones, and a piece that its end cuts
+                // reads on into the next row (the last row's step comes by fetch); their products are not stored
                 if constexpr (TURNED)
-                    off[n] = (uint32_t)(row * ld + min((int64_t)c * kEach, left - kEach)) * (uint32_t)sizeof(T);
+                    off[n] = (uint32_t)(row * ld + min((int64_t)c * kEach, (left - 1) / kEach * kEach)) * (uint32_t)sizeof(T);
                 else
                     off[n] = (uint32_t)(min((int64_t)row, left - 1) * ld + c * kEach) * (uint32_t)sizeof(T);
             }
@@ -242,19 +243,36 @@ template <typename T, bool TURNED, int B, int W, bool FAST> struct ProjTile {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (proj_lds *)(lds + (wave * kLoads + n) * 1024), 16, (int)off[n], 0, 0, 0);
     }
 
-    // Any step, into registers: values past the last r, or past the operand, are zeros.
-    // Pieces inside are read at whatever address they have.
+    // The value of 16 bytes without its first ones, which its last take the place of, zeros behind
+    static __device__ __forceinline__ uint4 moved(const uint4 &v, int bytes) {
+        const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+        const int by = bytes * 8;
+        const uint64_t l = by >= 64 ? hi >> (by - 64) : by == 0 ? lo : lo >> by | hi << (64 - by), h = by >= 64 ? 0 : hi >> by;
+        return uint4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+    }
+
+    // Any step, into registers: values past the last r are zeros, and so are whole pieces past the
+    // operand. Pieces inside are read at whatever address they have.
     __device__ __forceinline__ void fetch(uint4 (&v)[kLoads], int64_t s, int64_t R, int wave, int lane) const {
         const int64_t r0 = s * kStep;
         const char *b = base + (TURNED ? r0 * ld : r0) * (int64_t)sizeof(T);
+        if constexpr (FAST) {
+            // a piece that the end cuts is read as the 16 bytes before the end, and moved down
+            const int64_t end = TURNED ? left : R - r0;
+            const int rest = (int)((TURNED ? left : R) % kEach), back = rest ? (kEach - rest) * (int)sizeof(T) : 0;
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n) * kEach;
-            v[n] = uint4{0, 0, 0, 0};
-            if constexpr (FAST) {
-                // a piece is on one side of the end whole
-                if (r0 + (TURNED ? row : c) < R) v[n] = *reinterpret_cast<const uint4 *>(b + off[n]);
-            } else {
+            for (int n = 0; n < kLoads; ++n) {
+                const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n) * kEach;
+                v[n] = uint4{0, 0, 0, 0};
+                const bool any = c < end && (!TURNED || r0 + row < R), part = c + kEach > end;
+                if (any) __builtin_memcpy(&v[n], b + off[n] - (part ? back : 0), 16);
+                if (rest) v[n] = part ? moved(v[n], back) : v[n];
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) {
+                const int row = row_of(wave, lane, n), c = piece_of(wave, lane, n) * kEach;
+                v[n] = uint4{0, 0, 0, 0};
                 const char *at = b + ((int64_t)row * ld + c) * (int64_t)sizeof(T);
                 const int64_t in = TURNED ? (r0 + row < R ? left - c : 0) : (row < left ? R - r0 - c : 0);   // values of the piece
                 if (in >= kEach) {
@@ -399,12 +417,18 @@ __global__ __launch_bounds__((ProjShape<BI, BJ>::kWaves * 64)) void proj_kernel(
     if constexpr (FAST) {
         // A ragged last step, and one more where the whole ones are odd in number, go first and by
         // themselves; the rest in pairs, each step loaded while the one before is multiplied.
-        const int64_t s2 = max(s0, min(s1, a.R / TileP::kStep));
+        const bool cut = (TP && a.I % TileP::kEach) || (TQ && a.J % TileQ::kEach);
+        const int64_t s2 = max(s0, min(s1, (cut ? a.R - 1 : a.R) / TileP::kStep));
         const int odd = (int)((s2 - s0) & 1), alone = odd + (s1 > s2);
         for (int k = 0; k < alone; ++k) {
-            fetch(odd && k == alone - 1 ? s0 : s1 - 1);
-            put(two);
-            __syncthreads();
+            if (odd && k == alone - 1) {
+                load(two, s0);
+                proj_arrived();
+            } else {
+                fetch(s1 - 1);
+                put(two);
+                __syncthreads();
+            }
             multiply(two);
             __syncthreads();
         }

@@ -171,6 +171,20 @@ def test_large(env, shape, dtype):
     whole(env, *shape, getattr(torch, dtype), act="silu", res=torch.float32)
 
 
+# rows of whole 4-byte words and no whole 16-byte piece: every tile, steps that the end of r or of a row cuts, alone,
+# before pairs and in splits; rows of one piece and of less
+WORDS = [(4100, 1, 138, 2058), (2050, 1, 1030, 2062), (300, 3, 204, 518), (128, 1, 66, 130), (64, 1, 10, 12), (65, 1, 130, 66),
+         (30, 1, 6, 70), (33, 2, 64, 10), (90, 1, 4098, 100), (9000, 1, 100, 202), (192, 1, 12, 14), (4097, 1, 514, 4098)]
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("shape", WORDS, ids=lambda s: "x".join(map(str, s)))
+def test_rows_of_words(env, shape, dtype):
+    torch, _ = env
+    k = WORDS.index(shape)
+    whole(env, *shape, getattr(torch, dtype), bias=k % 2 == 0, res=(None, torch.float32)[k % 2], strided=k % 3 == 1)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("res", [None, "bfloat16", "float32"])
 def test_epilogues(env, act, res):
@@ -227,6 +241,21 @@ def test_rows_keep_apart(env):
         assert bool(bad[rows // 2].isnan().all())
         bad[rows // 2] = clean[rows // 2]
         assert torch.equal(bad, clean)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_nothing_past_a_cut_out_row(env, dtype):
+    """NaN behind a cut-out row of whole words, which pieces read on into, reaches no product."""
+    torch, ssm = env
+    t = getattr(torch, dtype)
+    for rows, K, N in ((200, 34, 70), (128, 70, 130), (65, 10, 12), (4097, 138, 258)):
+        s = make(torch, rows, 1, K, N, t)
+        wide = torch.full((rows, K + 6), float("nan"), device="cuda").to(t)
+        wide[:, :K] = s["x"]
+        y, g = ssm.ssm_proj_fwd(wide[:, :K], s["weight"]), ssm.ssm_proj_bwd(s["dy"], wide[:, :K], s["weight"])
+        want, ref = ssm.ssm_proj_fwd(s["x"], s["weight"]), ssm.ssm_proj_bwd(s["dy"], s["x"], s["weight"])
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(g["dweight"], ref["dweight"]) and torch.equal(g["dx"], ref["dx"])
 
 
 @pytest.mark.parametrize("shape", [(16500, 1, 40, 4104), (16500, 1, 4104, 40), (13100, 2, 24, 2056)],
