@@ -21,7 +21,7 @@
 // in 16-byte stores of whole lines (16384 x 2048 -> 4096 writing pre as well 239 us; stored
 // from the accumulators, 8 bytes a lane over 16 rows, 329).
 //
-// Bound by the matrix cores at the large sizes: 8192^3 in bf16 takes 766 us (1435 TFLOP/s),
+// Bound by the matrix cores at the large sizes: 8192^3 in bf16 takes 753 us (1460 TFLOP/s),
 // products running in 71 % of its cycles, the rest at the steps' barriers; fp32 4096^3 930 us
 // (148 TFLOP/s). Four waves of 128 x 128 instead of eight of 128 x 64 halve what is read from
 // LDS, and read a step ahead: 841 us where this took 798; with four buffers of 64 bytes of r 832.
