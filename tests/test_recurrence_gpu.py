@@ -287,6 +287,27 @@ def test_input_gates_in_fp32(env):
         assert off.max() <= 10 * U and torch.equal(step, y[:, 3])
 
 
+@pytest.mark.parametrize("B,D", [(200000, 8), (70001, 33)])
+def test_more_batch_rows_than_a_grid_is_high(env, B, D):
+    """Rows keep to themselves: a large batch gives what its parts give, to the bit."""
+    torch, ssm = env
+    s = inputs(torch, B, 2, D, torch.float32, h0=True)
+    cut = lambda v, r: v if v is None or v.shape[0] != B else v[r]
+    ins = ("x", "rgate", "igate")
+    whole = outputs(ssm, s)
+    h = s["h0"].clone()
+    y = ssm.ssm_glr_state_update(*(s[k][:, 0].contiguous() for k in ins), s["lam"], h)
+    for r in (slice(0, 1000), slice(B - 1000, B)):
+        part = {k: cut(v, r) for k, v in s.items()}
+        got = outputs(ssm, part)
+        h1 = part["h0"].clone()
+        y1 = ssm.ssm_glr_state_update(*(part[k][:, 0].contiguous() for k in ins), s["lam"], h1)
+        torch.cuda.synchronize()
+        assert torch.equal(y[r], y1) and torch.equal(h[r], h1)
+        for k, v in got.items():
+            assert k == "dlam" or v is None or torch.equal(whole[k][r], v), k
+
+
 def test_empty(env):
     torch, ssm = env
     z = lambda *s: torch.zeros(s, device="cuda")
