@@ -693,9 +693,9 @@ int ssm_glr_state_update(const ssm_glr_desc *desc, const void *x, const void *rg
  * activation and residual are applied to the fp32 sums, and y and pre are rounded once.
  * gelu is the form z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3)).
  *
- * Up to 16 rows the forward reads the weight once without tiles. Results do not depend
- * on timing, nor on other rows' values; they may differ by rounding between numbers of
- * rows. Sizes that need 2^32 work items in a launch are refused (SSM_ERR_SHAPE).
+ * Up to 16 rows the forward reads the weight once without tiles, unless its rows are
+ * long. Results do not depend on timing, nor on other rows' values; they may differ by
+ * rounding between numbers of rows. Sizes that need 2^32 work items in a launch are refused (SSM_ERR_SHAPE).
  */
 typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1, SSM_ACT_GELU = 2, SSM_ACT_SIGMOID = 3 } ssm_activation;
 

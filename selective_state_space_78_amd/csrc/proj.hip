@@ -118,6 +118,7 @@ __global__ __launch_bounds__(256) void proj_zero_kernel(void *p, int64_t bytes) 
 struct Tiling {
     int tile;         // 256, 128 or 64: a tile's sides
     int64_t splits, steps;      // steps of r to a split
+    double us;        // as planned
 };
 
 // The time of a product of J x I outputs over R, in us, from how many workgroups a CU
@@ -135,8 +136,7 @@ Tiling plan_for(int64_t I, int64_t J, int64_t R, int64_t groups, int dtype) {
     static const Kind narrow[] = {{256, 1, {1.75}, 8.0}, {128, 2, {0.75, 1.0}, 4.0}, {64, 4, {0.3, 0.42, 0.58, 0.74}, 2.3}};
     static const Kind wide[] = {{256, 1, {7.3}, 12.0}, {128, 2, {2.2, 4.1}, 5.0}, {64, 4, {0.9, 1.2, 1.6, 2.1}, 2.5}};
     const int64_t every = ceil_div(R, dtype == SSM_BF16 ? 64 : 32);
-    Tiling best{128, 1, every};
-    double least = 1e300;
+    Tiling best{128, 1, every, 1e300};
     for (const Kind &k : dtype == SSM_BF16 ? narrow : wide) {
         const int64_t tiles = ceil_div(I, k.side) * ceil_div(J, k.side) * groups;
         for (int64_t s = 1; s <= kMostSplits && s <= every; s = s < 4 ? s + 1 : s + s / 2) {
@@ -148,10 +148,7 @@ Tiling plan_for(int64_t I, int64_t J, int64_t R, int64_t groups, int dtype) {
             double t = (double)(on / k.hold) * (steps * k.step[k.hold - 1] + k.fixed);
             if (rest) t += steps * k.step[rest - 1] + k.fixed;
             if (splits > 1) t += 3.5 + (double)I * J * groups * (8.0 * splits + 4.0) / 4.5e6;
-            if (t < least) {
-                least = t;
-                best = Tiling{k.side, splits, each};
-            }
+            if (t < best.us) best = Tiling{k.side, splits, each, t};
         }
     }
     return best;
@@ -161,7 +158,19 @@ int64_t part_bytes(int64_t I, int64_t J, int64_t groups, const Tiling &pl) {
     return pl.splits > 1 ? (int64_t)align256((size_t)(pl.splits * groups * J * I * 4)) : 0;
 }
 
-constexpr int kFew = 16;    // rows up to which the forward reads the weight once, without tiles (5120 -> 2560: 11.0 us, in tiles 10.7)
+constexpr int kFew = 16;    // rows that the forward can take without tiles, reading the weight once
+
+// Whether it does: where the weight's rows are so long that the waves of a workgroup are longer at
+// theirs than split tiles take. By the weight's rows in KB and workgroups a CU; measured in us
+// without tiles / with: one row 4096 -> 2048 4.3 / 8.3, 65536 -> 16 19.3 / 12.5; 8 rows 4096 -> 4096
+// 8.3 / 10.5, 8192 -> 256 13.3 / 8.7, 65536 -> 256 92 / 18.5; fp32 4096 -> 4096 14.2 / 23.8, 8192 -> 512 24.7 / 11.7.
+bool without_tiles(const ssm_proj_desc &d, const Tiling &pl) {
+    if (d.rows > kFew) return false;
+    const double kb = (double)d.in * (d.dtype == SSM_BF16 ? 2 : 4) / 1024;
+    const int64_t each = d.rows == 1 ? 32 : 16;      // outputs that share a CU's pace
+    const double turns = (double)ceil_div(d.groups * ceil_div(d.out, each), kCus);
+    return (d.rows == 1 ? 2.7 + kb * 0.13 * turns : 2.0 + kb * (0.535 + 0.02 * (double)d.rows) * turns) <= pl.us;
+}
 
 template <typename T, bool TP, bool TQ, bool FAST>
 hipError_t launch_tiles(ProjParams &a, int tile, hipStream_t st) {
@@ -273,9 +282,10 @@ int status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 }  // namespace
 
 extern "C" size_t ssm_proj_workspace_size(const ssm_proj_desc *desc) {
-    if (check(desc) != SSM_OK || desc->rows <= kFew) return 0;
+    if (check(desc) != SSM_OK || desc->rows == 0) return 0;
     const ssm_proj_desc &d = *desc;
-    return (size_t)part_bytes(d.out, d.rows, d.groups, plan_for(d.out, d.rows, d.in, d.groups, d.dtype));
+    const Tiling pl = plan_for(d.out, d.rows, d.in, d.groups, d.dtype);
+    return without_tiles(d, pl) ? 0 : (size_t)part_bytes(d.out, d.rows, d.groups, pl);
 }
 
 extern "C" size_t ssm_proj_bwd_workspace_size(const ssm_proj_desc *desc) {
@@ -294,7 +304,8 @@ extern "C" int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void
         return SSM_ERR_ALIGN;
     const int64_t xs = d.x_stride ? d.x_stride : d.groups * d.in, n = d.rows * d.groups * d.out;
     const Tiling pl = plan_for(d.out, d.rows, d.in, d.groups, d.dtype);
-    const int64_t need = d.rows <= kFew ? 0 : part_bytes(d.out, d.rows, d.groups, pl);
+    const bool few_rows = without_tiles(d, pl);
+    const int64_t need = few_rows ? 0 : part_bytes(d.out, d.rows, d.groups, pl);
     if (need && (!workspace || workspace_bytes < (size_t)need)) return SSM_ERR_WORKSPACE;
     if (need && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
     const Range in[] = {range_of(x, span(d.rows, xs, d.groups * d.in) * e), range_of(weight, d.groups * d.in * d.out * e),
@@ -327,7 +338,7 @@ extern "C" int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void
     a.act = d.activation;
     a.wide = d.y_dtype == SSM_F32;
     a.eight = d.out % 8 == 0 && aligned(y, 16) && aligned(residual, 16) && aligned(pre, 16);
-    if (d.rows <= kFew) return status(d.dtype == SSM_BF16 ? few<uint16_t>(a, stream) : few<float>(a, stream));
+    if (few_rows) return status(d.dtype == SSM_BF16 ? few<uint16_t>(a, stream) : few<float>(a, stream));
     return status(d.dtype == SSM_BF16 ? product<uint16_t, false, false>(a, pl, d.dtype, stream)
                                       : product<float, false, false>(a, pl, d.dtype, stream));
 }

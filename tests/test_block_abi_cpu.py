@@ -152,7 +152,11 @@ def test_proj_overlaps_and_workspace(L):
     size = L.ssm_proj_workspace_size(ctypes.byref(long))
     assert size > 0 and call(L.ssm_proj_fwd, long, P_FWD, ws_bytes=size - 1) == EWS
     assert call(L.ssm_proj_fwd, long, P_FWD, y=20 * GB) == EALIAS
-    assert L.ssm_proj_workspace_size(ctypes.byref(proj(rows=8, k=1 << 16))) == 0
+    # few rows: without tiles, unless the weight's rows are long
+    few, more = proj(rows=8, k=1 << 12, n=1 << 12), proj(rows=8, k=1 << 16, n=64)
+    assert L.ssm_proj_workspace_size(ctypes.byref(few)) == 0
+    size = L.ssm_proj_workspace_size(ctypes.byref(more))
+    assert size > 0 and call(L.ssm_proj_fwd, more, P_FWD, ws_bytes=size - 1) == EWS
     assert call(L.ssm_proj_fwd, proj(rows=0), P_FWD) == OK
 
 
