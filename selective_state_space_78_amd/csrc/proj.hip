@@ -160,16 +160,17 @@ int64_t part_bytes(int64_t I, int64_t J, int64_t groups, const Tiling &pl) {
 
 constexpr int kFew = 16;    // rows that the forward can take without tiles, reading the weight once
 
-// Whether it does: where the weight's rows are so long that the waves of a workgroup are longer at
-// theirs than split tiles take. By the weight's rows in KB and workgroups a CU; measured in us
+// Whether it does: not where the weight's rows are so long that the waves of a workgroup are longer
+// at theirs than split tiles take. By the weight's rows in KB and workgroups a CU; measured in us
 // without tiles / with: one row 4096 -> 2048 4.3 / 8.3, 65536 -> 16 19.3 / 12.5; 8 rows 4096 -> 4096
-// 8.3 / 10.5, 8192 -> 256 13.3 / 8.7, 65536 -> 256 92 / 18.5; fp32 4096 -> 4096 14.2 / 23.8, 8192 -> 512 24.7 / 11.7.
+// 5.9 / 10.5, 8192 -> 1024 7.8 / 10.4, 16384 -> 512 13.0 / 9.3, 65536 -> 256 50 / 18.5; fp32 4096 -> 4096
+// 14.5 / 23.8, 8192 -> 512 15.0 / 11.7.
 bool without_tiles(const ssm_proj_desc &d, const Tiling &pl) {
     if (d.rows > kFew) return false;
     const double kb = (double)d.in * (d.dtype == SSM_BF16 ? 2 : 4) / 1024;
     const int64_t each = d.rows == 1 ? 32 : 16;      // outputs that share a CU's pace
     const double turns = (double)ceil_div(d.groups * ceil_div(d.out, each), kCus);
-    return (d.rows == 1 ? 2.7 + kb * 0.13 * turns : 2.0 + kb * (0.535 + 0.02 * (double)d.rows) * turns) <= pl.us;
+    return (d.rows == 1 ? 2.7 + kb * 0.13 * turns : 2.3 + kb * 0.35 * turns) <= pl.us;
 }
 
 template <typename T, bool TP, bool TQ, bool FAST>

@@ -629,9 +629,11 @@ template <typename T> __global__ __launch_bounds__(256) void proj_one_row_kernel
 
 // Up to 16 rows: the weight is read once, straight into the matrix instructions' registers,
 // 16 bytes a lane along r at any address. A workgroup takes 16 of its rows, the waves share r
-// in runs of pairs of steps (whole lines); their sums are added in LDS in order. Bound by the
-// weight's bytes, then by x, which every workgroup reads (8 rows 4096 -> 4096 in bf16 8.3 us, 16
-// rows 9.6; in tiles 10.6; 8 rows 768 -> 1536 3.3 us, in tiles 5.7; with 16 waves 8.3 and 6.7).
+// in runs of pairs of steps (whole lines); their sums are added in LDS in order. Lanes read four
+// to a row, next to one another, and hand over to the lane that the instruction has the piece in
+// (read there directly, neighbouring lanes in different rows, loads pass one lane at a time: 8 rows
+// 4096 -> 4096 in bf16 8.3 us, 16 rows 9.6; so 5.9 and 6.3; in tiles 10.6; 8 rows 768 -> 1536 2.9 us,
+// in tiles 5.7; fp32 4096 -> 4096 14.5 us, 2 rows read directly 12.2, 16 rows 16.8).
 template <typename T, int W> __global__ __launch_bounds__(W * 64) void proj_few_rows_kernel(ProjParams a) {
     constexpr int E = 16 / (int)sizeof(T), kStep = 4 * E;
     __shared__ float4 sum[W][64];
@@ -644,10 +646,18 @@ template <typename T, int W> __global__ __launch_bounds__(W * 64) void proj_few_
     const int64_t steps = a.R / kStep, each = (steps + 2 * W - 1) / (2 * W) * 2;
     const int64_t k0 = min(wave * each, steps), k1 = min(k0 + each, steps);
     ssd_f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    // the lane that read what this lane multiplies, and what this lane reads
+    const int back = (lane & 15) * 16 + (lane >> 4) * 4;
+    const T *wl = static_cast<const T *>(a.p) + g * a.gp + min(i0 + (lane >> 2), a.I - 1) * a.ldp + (lane & 3) * E;
+    const T *xl = static_cast<const T *>(a.q) + g * a.gq + min((int64_t)(lane >> 2), a.J - 1) * a.ldq + (lane & 3) * E;
     auto get = [](const T *p) {
         uint4 v;
         __builtin_memcpy(&v, p, 16);
         return v;
+    };
+    auto turned = [&](const uint4 &v) {
+        return uint4{(uint32_t)__builtin_amdgcn_ds_bpermute(back, (int)v.x), (uint32_t)__builtin_amdgcn_ds_bpermute(back, (int)v.y),
+                     (uint32_t)__builtin_amdgcn_ds_bpermute(back, (int)v.z), (uint32_t)__builtin_amdgcn_ds_bpermute(back, (int)v.w)};
     };
     int64_t k = k0;
     auto run = [&](auto count) {
@@ -655,11 +665,11 @@ template <typename T, int W> __global__ __launch_bounds__(W * 64) void proj_few_
         if (k + N > k1) return;
         uint4 vw[N], vx[N];
 #pragma unroll
-        for (int n = 0; n < N; ++n) vw[n] = get(w + (k + n) * kStep);
+        for (int n = 0; n < N; ++n) vw[n] = get(wl + (k + n) * kStep);
 #pragma unroll
-        for (int n = 0; n < N; ++n) vx[n] = get(x + (k + n) * kStep);
+        for (int n = 0; n < N; ++n) vx[n] = get(xl + (k + n) * kStep);
 #pragma unroll
-        for (int n = 0; n < N; ++n) proj_mul<T>(vw[n], vx[n], acc);
+        for (int n = 0; n < N; ++n) proj_mul<T>(turned(vw[n]), turned(vx[n]), acc);
         k += N;
     };
     while (k + 8 <= k1) run(std::integral_constant<int, 8>());
