@@ -191,7 +191,7 @@ hipError_t launch_tiles(ProjParams &a, int tile, hipStream_t st) {
 template <typename T, bool TP, bool TQ> hipError_t product(ProjParams &a, Tiling pl, int dtype, hipStream_t st) {
     const int64_t each = 16 / (int64_t)sizeof(T);
     // whether pieces of 16 bytes lie on 4-byte addresses, and rows hold one at least; others go through
-    // registers (8192 x 772 -> 1536 in bf16 35 us, through registers 73; 8192 x 767 -> 1535, which must, 87)
+    // registers (8192 x 772 -> 1536 in bf16 35 us, through registers 73)
     auto dwords = [&](const void *p, int64_t ld, int64_t g, int64_t n) {
         return aligned(p, 4) && ld * (int64_t)sizeof(T) % 4 == 0 && (a.groups == 1 || g * (int64_t)sizeof(T) % 4 == 0) && n >= each;
     };
@@ -244,10 +244,76 @@ int check(const ssm_proj_desc *desc) {
 
 int64_t span(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? (rows - 1) * stride + width : 0; }
 
+// Rows of an odd number of 16-bit values begin between 4-byte words, from where nothing goes
+// straight into LDS. Such operands are first copied, their rows padded to whole pieces, where the
+// product is long enough for that: a launch and twice the bytes against its planned time again, at
+// least (gradients of 7447 x 155 -> 3200 through registers 171 us, with copies 64; 8192 x 767 -> 1535
+// 87 and 68, its gradients 98 and 105 and 58 each).
+int64_t padded(int64_t width) { return ceil_div(width, 8) * 8; }
+
+bool worth_copies(const Tiling &pl, int64_t bytes) { return pl.us > 6.0 + (double)bytes / 2.0e6; }
+
+// One 16-byte piece of the copy to a lane; pieces lie row by row, group by group
+__global__ __launch_bounds__(256) void proj_pad_kernel(const uint16_t *from, uint4 *to, uint32_t pieces, int width, uint32_t groups,
+                                                       int64_t ld, int64_t group) {
+    const uint32_t k = blockIdx.x * 256 + threadIdx.x;
+    if (k >= pieces) return;
+    const uint32_t across = (uint32_t)(width + 7) / 8, line = k / across, row = line / groups, g = line - row * groups;
+    const int c = (int)(k - line * across) * 8, in = width - c;
+    const uint16_t *at = from + row * ld + g * group + c;
+    uint4 v{0, 0, 0, 0};
+    if (in >= 8) {
+        __builtin_memcpy(&v, at, 16);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = e < in ? at[e] : 0;
+        v = uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+    }
+    to[k] = v;
+}
+
+hipError_t pad(const void *from, char *to, int64_t rows, int64_t width, int64_t groups, int64_t ld, int64_t group, hipStream_t st) {
+    const int64_t pieces = rows * groups * (padded(width) / 8);
+    hipLaunchKernelGGL(proj_pad_kernel, dim3((unsigned)ceil_div(pieces, 256)), dim3(256), 0, st, static_cast<const uint16_t *>(from),
+                       reinterpret_cast<uint4 *>(to), (uint32_t)pieces, (int)width, (uint32_t)groups, ld, group);
+    return hipGetLastError();
+}
+
+int64_t copy_bytes(int64_t rows, int64_t groups, int64_t width) { return (int64_t)align256((size_t)(rows * groups * padded(width) * 2)); }
+
+// Bytes of the operands' copies, 0 for one that is read where it is
+struct Copies {
+    int64_t w, x, dz;
+};
+
+bool odd_x(const ssm_proj_desc &d) { return d.dtype == SSM_BF16 && (d.in % 2 || d.x_stride % 2); }
+bool odd_in(const ssm_proj_desc &d) { return d.dtype == SSM_BF16 && d.in % 2; }
+bool odd_out(const ssm_proj_desc &d) { return d.dtype == SSM_BF16 && d.out % 2; }
+
+struct ForwardPlan {
+    Tiling tiles;
+    bool few;
+    Copies copies;
+    int64_t part, total;        // bytes: splits' sums; all
+};
+
+ForwardPlan forward_plan(const ssm_proj_desc &d) {
+    ForwardPlan f{plan_for(d.out, d.rows, d.in, d.groups, d.dtype), false, {0, 0, 0}, 0, 0};
+    f.few = without_tiles(d, f.tiles);
+    if (f.few) return f;
+    f.part = part_bytes(d.out, d.rows, d.groups, f.tiles);
+    Copies c{odd_in(d) ? copy_bytes(d.groups * d.out, 1, d.in) : 0, odd_x(d) ? copy_bytes(d.rows, d.groups, d.in) : 0, 0};
+    if (worth_copies(f.tiles, c.w + c.x)) f.copies = c;
+    f.total = f.part + f.copies.w + f.copies.x;
+    return f;
+}
+
 struct BackPlan {
     Tiling dx, dw;
     int64_t slabs, per;         // of dpre's pass
-    int64_t sums, total;        // bytes: the slabs' sums; all
+    Copies copies;
+    int64_t sums, part, total;  // bytes: the slabs' sums; splits' sums; all
 };
 
 BackPlan back_plan(const ssm_proj_desc &d) {
@@ -260,7 +326,14 @@ BackPlan back_plan(const ssm_proj_desc &d) {
     b.per = ceil_div(d.rows, b.slabs);
     b.slabs = ceil_div(d.rows, b.per);
     b.sums = (int64_t)align256((size_t)(b.slabs * cols * 4));
-    b.total = b.sums + std::max(part_bytes(d.in, d.rows, d.groups, b.dx), part_bytes(d.in, d.out, d.groups, b.dw));
+    b.part = std::max(part_bytes(d.in, d.rows, d.groups, b.dx), part_bytes(d.in, d.out, d.groups, b.dw));
+    const Copies c{odd_in(d) ? copy_bytes(d.groups * d.out, 1, d.in) : 0, odd_x(d) ? copy_bytes(d.rows, d.groups, d.in) : 0,
+                   odd_out(d) ? copy_bytes(d.rows, d.groups, d.out) : 0};
+    const bool dx = worth_copies(b.dx, c.w + c.dz), dw = worth_copies(b.dw, c.x + c.dz);
+    b.copies = Copies{dx ? c.w : 0, dw ? c.x : 0, dx && dw ? c.dz : 0};
+    // dz is copied for both products or for none: one that goes without leaves the other's no use
+    if (c.dz && !b.copies.dz) b.copies = Copies{0, 0, 0};
+    b.total = b.sums + b.part + b.copies.w + b.copies.x + b.copies.dz;
     return b;
 }
 
@@ -285,8 +358,7 @@ int status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 extern "C" size_t ssm_proj_workspace_size(const ssm_proj_desc *desc) {
     if (check(desc) != SSM_OK || desc->rows == 0) return 0;
     const ssm_proj_desc &d = *desc;
-    const Tiling pl = plan_for(d.out, d.rows, d.in, d.groups, d.dtype);
-    return without_tiles(d, pl) ? 0 : (size_t)part_bytes(d.out, d.rows, d.groups, pl);
+    return (size_t)forward_plan(d).total;
 }
 
 extern "C" size_t ssm_proj_bwd_workspace_size(const ssm_proj_desc *desc) {
@@ -304,9 +376,8 @@ extern "C" int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void
     if (!aligned(x, e) || !aligned(weight, e) || !aligned(pre, e) || !aligned(bias, 4) || !aligned(residual, ey) || !aligned(y, ey))
         return SSM_ERR_ALIGN;
     const int64_t xs = d.x_stride ? d.x_stride : d.groups * d.in, n = d.rows * d.groups * d.out;
-    const Tiling pl = plan_for(d.out, d.rows, d.in, d.groups, d.dtype);
-    const bool few_rows = without_tiles(d, pl);
-    const int64_t need = few_rows ? 0 : part_bytes(d.out, d.rows, d.groups, pl);
+    const ForwardPlan f = forward_plan(d);
+    const int64_t need = f.total;
     if (need && (!workspace || workspace_bytes < (size_t)need)) return SSM_ERR_WORKSPACE;
     if (need && !aligned(workspace, 256)) return SSM_ERR_ALIGN;
     const Range in[] = {range_of(x, span(d.rows, xs, d.groups * d.in) * e), range_of(weight, d.groups * d.in * d.out * e),
@@ -339,9 +410,23 @@ extern "C" int ssm_proj_fwd(const ssm_proj_desc *desc, const void *x, const void
     a.act = d.activation;
     a.wide = d.y_dtype == SSM_F32;
     a.eight = d.out % 8 == 0 && aligned(y, 16) && aligned(residual, 16) && aligned(pre, 16);
-    if (few_rows) return status(d.dtype == SSM_BF16 ? few<uint16_t>(a, stream) : few<float>(a, stream));
-    return status(d.dtype == SSM_BF16 ? product<uint16_t, false, false>(a, pl, d.dtype, stream)
-                                      : product<float, false, false>(a, pl, d.dtype, stream));
+    if (f.few) return status(d.dtype == SSM_BF16 ? few<uint16_t>(a, stream) : few<float>(a, stream));
+    char *copy = static_cast<char *>(workspace) + f.part;
+    if (f.copies.w) {
+        if (pad(weight, copy, d.groups * d.out, d.in, 1, d.in, 0, stream) != hipSuccess) return SSM_ERR_HIP;
+        a.p = copy;
+        a.ldp = padded(d.in);
+        a.gp = d.out * a.ldp;
+        copy += f.copies.w;
+    }
+    if (f.copies.x) {
+        if (pad(x, copy, d.rows, d.in, d.groups, xs, d.in, stream) != hipSuccess) return SSM_ERR_HIP;
+        a.q = copy;
+        a.gq = padded(d.in);
+        a.ldq = d.groups * a.gq;
+    }
+    return status(d.dtype == SSM_BF16 ? product<uint16_t, false, false>(a, f.tiles, d.dtype, stream)
+                                      : product<float, false, false>(a, f.tiles, d.dtype, stream));
 }
 
 extern "C" int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const void *x, const void *weight, const void *pre,
@@ -403,10 +488,24 @@ extern "C" int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const voi
     a.ldq = ko;
     a.gq = d.out;
     a.wide = !bf;
+    char *copy = reinterpret_cast<char *>(part) + b.part;
+    if (b.copies.dz && (dx || dweight)) {
+        if (pad(dz, copy, d.rows, d.out, d.groups, ko, d.out, stream) != hipSuccess) return SSM_ERR_HIP;
+        a.q = copy;
+        a.gq = padded(d.out);
+        a.ldq = d.groups * a.gq;
+        copy += b.copies.dz;
+    }
     if (dx) {
         a.p = weight;
         a.ldp = d.in;
         a.gp = d.in * d.out;
+        if (b.copies.w) {
+            if (pad(weight, copy, d.groups * d.out, d.in, 1, d.in, 0, stream) != hipSuccess) return SSM_ERR_HIP;
+            a.p = copy;
+            a.ldp = padded(d.in);
+            a.gp = d.out * a.ldp;
+        }
         a.I = d.in;
         a.J = d.rows;
         a.R = d.out;
@@ -421,6 +520,13 @@ extern "C" int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const voi
         a.p = x;
         a.ldp = xs;
         a.gp = d.in;
+        if (b.copies.x) {
+            copy += b.copies.w;
+            if (pad(x, copy, d.rows, d.in, d.groups, xs, d.in, stream) != hipSuccess) return SSM_ERR_HIP;
+            a.p = copy;
+            a.gp = padded(d.in);
+            a.ldp = d.groups * a.gp;
+        }
         a.I = d.in;
         a.J = d.out;
         a.R = d.rows;

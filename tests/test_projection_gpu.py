@@ -186,6 +186,35 @@ def test_rows_of_words(env, shape, dtype):
     whole(env, *shape, getattr(torch, dtype), bias=k % 2 == 0, res=(None, torch.float32)[k % 2], strided=k % 3 == 1)
 
 
+# rows of an odd number of 16-bit values, long enough that they are copied first: one side, both, groups
+ODD = [(4100, 1, 139, 2058), (4100, 1, 1032, 1031), (2050, 1, 1031, 2061), (4096, 3, 135, 1033), (6000, 2, 257, 515)]
+
+
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("shape", ODD, ids=lambda s: "x".join(map(str, s)))
+def test_odd_rows(env, shape, strided):
+    torch, ssm = env
+    rows, G, K, N = shape
+    assert ssm.ssm_proj_bwd_workspace_size(rows, K, N, G) > 2 * rows * G * min(K, N)
+    whole(env, *shape, torch.bfloat16, res=torch.float32, strided=strided)
+
+
+def test_rows_an_odd_way_apart(env):
+    """x of even width cut out of odd rows, and memory whose first value lies between two words."""
+    torch, ssm = env
+    for rows, K, N in ((4100, 1032, 1030), (3000, 1031, 1033)):
+        s = make(torch, rows, 1, K, N, torch.bfloat16)
+        flat = torch.full((rows * (K + 7) + 1,), float("nan"), device="cuda", dtype=torch.bfloat16)
+        odd = dict(s, x=flat[1:].view(rows, K + 7)[:, :K])
+        odd["x"].copy_(s["x"])
+        show = {}
+        y = ssm.ssm_proj_fwd(odd["x"], s["weight"], bias=s["bias"])
+        g = ssm.ssm_proj_bwd(s["dy"], odd["x"], s["weight"], want_dbias=True)
+        torch.cuda.synchronize()
+        forward_check(torch, dict(odd, residual=None), 1, None, y, None, show)
+        backward_check(torch, odd, 1, None, g, show)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("res", [None, "bfloat16", "float32"])
 def test_epilogues(env, act, res):
