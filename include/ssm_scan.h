@@ -751,8 +751,10 @@ int ssm_proj_bwd(const ssm_proj_desc *desc, const void *dy, const void *x, const
  *   norm = sqrt(sum over tensors and elements of g^2)   squares and sums in 64 bits
  *   g   <- g * min(1, max_norm / (norm + eps))          factor and product in fp32, rounded once
  *
- * A norm of infinity makes finite gradients 0, one of NaN makes all of them NaN; one of
- * 0 leaves them, also without eps.
+ * A norm of infinity, which one beyond fp32's range is too, makes finite gradients 0, one
+ * of NaN makes all of them NaN; one of 0 leaves them, also without eps. ssm_grad_clip's factor
+ * comes from the norm in 64 bits, ssm_grad_scale's from the one in fp32 that it is given: they
+ * may differ by its rounding.
  *   count     tensors, 0..2^20; every array below is a HOST array of so many values
  *   grads     device pointers of dense tensors, their element's alignment
  *   out       the same for what is written: grads[k] itself, or apart from everything

@@ -213,8 +213,10 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(Table t, const dou
     auto factor = [&] {
         if (!known) {
             known = true;
-            const double v = parts > 0 ? sqrt(total(part, parts, s)) : (double)*norm;
-            if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
+            double v = parts > 0 ? sqrt(total(part, parts, s)) : (double)*norm;
+            const float shown = (float)v;
+            if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = shown;
+            if (isinf(shown)) v = shown;      // beyond fp32 it is infinity, as the caller is told
             const double d = v + (double)eps, c = (double)max_norm / d;
             coef = c >= 1.0 || d == 0.0 ? 1.0f : (float)c;      // NaN stays
         }

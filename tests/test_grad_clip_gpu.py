@@ -110,6 +110,34 @@ def test_sizes_of_values(env):
     assert bool(norm.isnan()) and bool(g[1].isnan().all())
 
 
+def test_norm_beyond_fp32(env):
+    """Finite gradients whose norm is beyond fp32: it is infinity, and they become 0, by either route; one just inside
+    leaves what the formula says."""
+    torch, ssm = env
+    full = lambda n, v, t: torch.full((n,), v, device="cuda", dtype=t)
+    # a few workgroups' sums, some hundred, those of two launches, and so many that a launch of its own adds them
+    for sizes in ([2, 1], [3_000_000, 5], [100] * 130, [80_000] * 130):
+        for t in (torch.float32, torch.bfloat16):
+            grads = [full(n, 3e38, t) for n in sizes]
+            out = [torch.ones_like(g) for g in grads]
+            norm = ssm.ssm_grad_clip(grads, 1.0, out=out)
+            same = [g.clone() for g in grads]
+            alone = ssm.ssm_grad_norm(same)
+            ssm.ssm_grad_scale(same, alone, 1.0)
+            ssm.ssm_grad_clip(grads, 1.0)
+            torch.cuda.synchronize()
+            assert float(norm) == float("inf") == float(alone)
+            for g, o, k in zip(grads, out, same):
+                assert not bool(g.any()) and not bool(o.any()) and not bool(k.any()), (sizes, t)
+    grads = [full(1, 2e38, torch.float32) for _ in range(2)]
+    ref, want = block.clip([np64(g) for g in grads], 1e30)
+    norm = ssm.ssm_grad_clip(grads, 1e30)
+    torch.cuda.synchronize()
+    assert abs(float(norm) - ref) <= 1.01 * U * ref
+    for g, w in zip(grads, want):
+        assert (np.abs(np64(g) - w) <= 3 * U * np.abs(w)).all()
+
+
 def test_nothing(env):
     torch, ssm = env
     e = torch.zeros(0, device="cuda")
