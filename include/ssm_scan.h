@@ -718,7 +718,9 @@ typedef struct {
  *   pre       (rows, groups, out)       dtype, written, or NULL (not wanted)
  *   y         (rows, groups, out)       y_dtype, written; may equal residual exactly
  *   workspace ssm_proj_workspace_size(desc) bytes, 256-byte aligned; its contents on
- *             entry do not matter
+ *             entry do not matter. The size goes with x_stride too, and fewer rows may
+ *             need more (a product of few tiles is split): one workspace for several
+ *             descriptors, here or in the backward, has the largest of their sizes
  * Pointers need their element's alignment only (rows of whole 4-byte words move faster).
  * Other overlaps of outputs are refused.
  */

@@ -1245,14 +1245,22 @@ def _proj_desc(x, weight, y_dtype, activation):
     return ProjDesc(rows, G, K, N, code, SSM_F32 if y_dtype == torch.float32 else SSM_BF16, _ACT[activation], 0, xs), lead + head, head
 
 
-def ssm_proj_workspace_size(rows, in_features, out_features, groups=1, dtype=SSM_BF16) -> int:
-    """Workspace bytes of ssm_proj_fwd."""
-    return int(lib().ssm_proj_workspace_size(ctypes.byref(ProjDesc(rows, groups, in_features, out_features, dtype, dtype))))
+def _proj_size(size, rows, in_features, out_features, groups, dtype, x_stride):
+    # x whose rows are an odd number of values apart may be copied, though its width is even: both are asked
+    strides = ((groups * in_features) | 1, 0) if x_stride is None else (x_stride,)
+    return max(int(size(ctypes.byref(ProjDesc(rows, groups, in_features, out_features, dtype, dtype, 0, 0, xs)))) for xs in strides)
 
 
-def ssm_proj_bwd_workspace_size(rows, in_features, out_features, groups=1, dtype=SSM_BF16) -> int:
-    """Workspace bytes of ssm_proj_bwd."""
-    return int(lib().ssm_proj_bwd_workspace_size(ctypes.byref(ProjDesc(rows, groups, in_features, out_features, dtype, dtype))))
+def ssm_proj_workspace_size(rows, in_features, out_features, groups=1, dtype=SSM_BF16, x_stride=None) -> int:
+    """Workspace bytes of ssm_proj_fwd: for any x, or for one whose rows are ``x_stride``
+    elements apart (0: dense). Fewer rows may need more than these: what serves several
+    numbers of rows is the largest of their sizes."""
+    return _proj_size(lib().ssm_proj_workspace_size, rows, in_features, out_features, groups, dtype, x_stride)
+
+
+def ssm_proj_bwd_workspace_size(rows, in_features, out_features, groups=1, dtype=SSM_BF16, x_stride=None) -> int:
+    """Workspace bytes of ssm_proj_bwd; arguments as ssm_proj_workspace_size."""
+    return _proj_size(lib().ssm_proj_bwd_workspace_size, rows, in_features, out_features, groups, dtype, x_stride)
 
 
 def ssm_proj_fwd(x, weight, bias=None, activation=None, residual=None, y=None, workspace=None, stream=None, _pre=None,

@@ -160,6 +160,32 @@ def test_proj_overlaps_and_workspace(L):
     assert call(L.ssm_proj_fwd, proj(rows=0), P_FWD) == OK
 
 
+def test_proj_sizes_serve_any_stride(L, world):
+    """The binding's sizes without a stride serve x of any, those with one are that descriptor's. A call whose outputs
+    overlap gets past the check of its workspace and no further."""
+    grown = 0
+    for rows, g, k, n in ((4100, 1, 1032, 1030), (4100, 1, 1032, 1031), (4100, 1, 1031, 1030), (4096, 2, 258, 516), (300, 1, 1032, 1030),
+                          (8, 1, 4096, 4096), (100000, 1, 6, 4096), (16384, 2, 257, 515)):
+        for dtype in (ssm.SSM_BF16, ssm.SSM_F32):
+            fwd, bwd = ssm.ssm_proj_workspace_size(rows, k, n, g, dtype), ssm.ssm_proj_bwd_workspace_size(rows, k, n, g, dtype)
+            for xs in (0, g * k, g * k + 1, g * k + 6, g * k + 7):
+                d = proj(rows, g, k, n, dtype, dtype, xs=xs)
+                one, two = L.ssm_proj_workspace_size(ctypes.byref(d)), L.ssm_proj_bwd_workspace_size(ctypes.byref(d))
+                assert one <= fwd and two <= bwd, (rows, g, k, n, xs)
+                assert one == ssm.ssm_proj_workspace_size(rows, k, n, g, dtype, x_stride=xs)
+                assert two == ssm.ssm_proj_bwd_workspace_size(rows, k, n, g, dtype, x_stride=xs)
+                grown += one < fwd
+                far = dict(zip(P_FWD, (k * GB << 10 for k in (1, 2, 3, 4, 5, 6))))
+                assert call(L.ssm_proj_fwd, d, P_FWD, ws=1 << 50, ws_bytes=fwd, **dict(far, y=far["x"])) == EALIAS
+                back = dict(zip(P_BWD, (k * GB << 10 for k in range(1, 9))))
+                assert call(L.ssm_proj_bwd, d, P_BWD, ws=1 << 50, ws_bytes=bwd, **dict(back, dx=back["x"])) == EALIAS
+    assert grown
+    x, w = z(4100, 1039, dtype=BF)[:, :1032], z(1030, 1032, dtype=BF)
+    room = lambda n: torch.zeros(n, dtype=torch.uint8)
+    ssm.ssm_proj_fwd(x, w, workspace=room(ssm.ssm_proj_workspace_size(4100, 1032, 1030)))
+    ssm.ssm_proj_bwd(z(4100, 1030, dtype=BF), x, w, workspace=room(ssm.ssm_proj_bwd_workspace_size(4100, 1032, 1030)))
+
+
 # ---------------------------------------------------------------- the clipping
 def arrays(n, at=1, size=1000, dtype=ssm.SSM_F32):
     return (array("Q", [(at + k) * GB for k in range(n)]), array("q", [size] * n), array("i", [dtype] * n))

@@ -215,6 +215,24 @@ def test_rows_an_odd_way_apart(env):
         backward_check(torch, odd, 1, None, g, show)
 
 
+def test_workspace_of_the_size_said(env):
+    """The size that is said without a stride serves x cut out of rows of an odd and an even number of values."""
+    torch, ssm = env
+    for rows, K, N in ((4100, 1032, 1030), (4100, 1032, 1031)):
+        s = make(torch, rows, 1, K, N, torch.bfloat16)
+        fwd = torch.empty(ssm.ssm_proj_workspace_size(rows, K, N), dtype=torch.uint8, device="cuda")
+        bwd = torch.empty(ssm.ssm_proj_bwd_workspace_size(rows, K, N), dtype=torch.uint8, device="cuda")
+        for wide in (K, K + 7, K + 8):
+            x = torch.full((rows, wide), float("nan"), device="cuda", dtype=torch.bfloat16)[:, :K]
+            x.copy_(s["x"])
+            show = {}
+            y = ssm.ssm_proj_fwd(x, s["weight"], bias=s["bias"], workspace=fwd)
+            g = ssm.ssm_proj_bwd(s["dy"], x, s["weight"], want_dbias=True, workspace=bwd)
+            torch.cuda.synchronize()
+            forward_check(torch, dict(s, x=x, residual=None), 1, None, y, None, show)
+            backward_check(torch, dict(s, x=x), 1, None, g, show)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("res", [None, "bfloat16", "float32"])
 def test_epilogues(env, act, res):
