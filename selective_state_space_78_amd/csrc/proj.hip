@@ -248,10 +248,12 @@ int64_t span(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? (r
 // straight into LDS. Such operands are first copied, their rows padded to whole pieces, where the
 // product is long enough for that: a launch and twice the bytes against its planned time again, at
 // least (gradients of 7447 x 155 -> 3200 through registers 171 us, with copies 64; 8192 x 767 -> 1535
-// 87 and 68, its gradients 98 and 105 and 58 each).
+// 87 and 68, its gradients 98 and 105 and 58 each). Rows of less than a piece go through registers
+// padded or not, and are left where they are: `row` is the shorter one of a product's operands
+// (50000 x 5 -> 515 forward 47.6 us, with copies 52.4; both gradients of 200000 x 7 -> 2048 496, with 507).
 int64_t padded(int64_t width) { return ceil_div(width, 8) * 8; }
 
-bool worth_copies(const Tiling &pl, int64_t bytes) { return pl.us > 6.0 + (double)bytes / 2.0e6; }
+bool worth_copies(const Tiling &pl, int64_t row, int64_t bytes) { return row >= 8 && pl.us > 6.0 + (double)bytes / 2.0e6; }
 
 // One 16-byte piece of the copy to a lane; pieces lie row by row, group by group
 __global__ __launch_bounds__(256) void proj_pad_kernel(const uint16_t *from, uint4 *to, uint32_t pieces, int width, uint32_t groups,
@@ -304,7 +306,7 @@ ForwardPlan forward_plan(const ssm_proj_desc &d) {
     if (f.few) return f;
     f.part = part_bytes(d.out, d.rows, d.groups, f.tiles);
     Copies c{odd_in(d) ? copy_bytes(d.groups * d.out, 1, d.in) : 0, odd_x(d) ? copy_bytes(d.rows, d.groups, d.in) : 0, 0};
-    if (worth_copies(f.tiles, c.w + c.x)) f.copies = c;
+    if (worth_copies(f.tiles, d.in, c.w + c.x)) f.copies = c;
     f.total = f.part + f.copies.w + f.copies.x;
     return f;
 }
@@ -329,7 +331,8 @@ BackPlan back_plan(const ssm_proj_desc &d) {
     b.part = std::max(part_bytes(d.in, d.rows, d.groups, b.dx), part_bytes(d.in, d.out, d.groups, b.dw));
     const Copies c{odd_in(d) ? copy_bytes(d.groups * d.out, 1, d.in) : 0, odd_x(d) ? copy_bytes(d.rows, d.groups, d.in) : 0,
                    odd_out(d) ? copy_bytes(d.rows, d.groups, d.out) : 0};
-    const bool dx = worth_copies(b.dx, c.w + c.dz), dw = worth_copies(b.dw, c.x + c.dz);
+    const int64_t row = std::min(d.in, d.out);
+    const bool dx = worth_copies(b.dx, row, c.w + c.dz), dw = worth_copies(b.dw, row, c.x + c.dz);
     b.copies = Copies{dx ? c.w : 0, dw ? c.x : 0, dx && dw ? c.dz : 0};
     // dz is copied for both products or for none: one that goes without leaves the other's no use
     if (c.dz && !b.copies.dz) b.copies = Copies{0, 0, 0};

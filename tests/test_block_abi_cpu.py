@@ -186,6 +186,23 @@ def test_proj_sizes_serve_any_stride(L, world):
     ssm.ssm_proj_bwd(z(4100, 1030, dtype=BF), x, w, workspace=room(ssm.ssm_proj_bwd_workspace_size(4100, 1032, 1030)))
 
 
+def test_proj_copies_where_they_help(L):
+    """Rows shorter than one 16-byte piece go through registers, padded or not: nothing of such a product is copied."""
+    fwd = lambda *a, **k: L.ssm_proj_workspace_size(ctypes.byref(proj(*a, **k)))
+    bwd = lambda *a, **k: L.ssm_proj_bwd_workspace_size(ctypes.byref(proj(*a, **k)))
+    for rows, n in ((100000, 4096), (200000, 2048)):
+        for k in (1, 3, 5, 7):
+            assert fwd(rows, 1, k, n) == 0, (rows, k, n)
+            # no more than the slabs' and the splits' sums, which its even neighbour has as well
+            assert bwd(rows, 1, k, n) <= bwd(rows, 1, k + 1, n), (rows, k, n)
+        assert fwd(rows, 1, 6, n, xs=9) == 0 and bwd(rows, 1, 6, n, xs=9) == bwd(rows, 1, 6, n)
+    for k in (512, 4096):
+        for n in (1, 3, 5, 7):
+            assert bwd(50000, 1, k, n) <= bwd(50000, 1, k, n + 1), (k, n)
+    # rows of a piece and more are copied
+    assert fwd(100000, 1, 9, 4096) > 100000 * 32 and bwd(50000, 1, 513, 515) > 50000 * 2 * 1040
+
+
 # ---------------------------------------------------------------- the clipping
 def arrays(n, at=1, size=1000, dtype=ssm.SSM_F32):
     return (array("Q", [(at + k) * GB for k in range(n)]), array("q", [size] * n), array("i", [dtype] * n))

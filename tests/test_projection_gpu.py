@@ -233,6 +233,16 @@ def test_workspace_of_the_size_said(env):
             backward_check(torch, dict(s, x=x), 1, None, g, show)
 
 
+# rows shorter than one 16-byte piece, of an odd number of values, in long products
+SHORT = [(20000, 1, 7, 515), (20000, 3, 5, 257), (20000, 1, 515, 7), (50000, 1, 3, 1024)]
+
+
+@pytest.mark.parametrize("shape", SHORT, ids=lambda s: "x".join(map(str, s)))
+def test_short_odd_rows(env, shape):
+    torch, _ = env
+    whole(env, *shape, torch.bfloat16, act="silu", strided=SHORT.index(shape) % 2 == 1)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("res", [None, "bfloat16", "float32"])
 def test_epilogues(env, act, res):
