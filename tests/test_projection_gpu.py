@@ -215,6 +215,27 @@ def test_rows_an_odd_way_apart(env):
         backward_check(torch, odd, 1, None, g, show)
 
 
+def padded_bytes(rows, G, K, N):
+    """Of the backward's copies of weight, x and dpre with rows padded to 16 bytes."""
+    up, wide = lambda n: -(-n // 256) * 256, lambda n: -(-n // 8) * 8 * 2
+    return up(G * N * wide(K)) + up(rows * G * wide(K)) + up(rows * G * wide(N))
+
+
+# groups of odd rows on both sides, whose weight, x and dpre are all copied in the backward
+ODD_GROUPS = [(16384, 2, 257, 515), (8192, 3, 515, 1033), (12000, 2, 515, 517)]
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("shape", ODD_GROUPS, ids=lambda s: "x".join(map(str, s)))
+def test_odd_rows_of_groups(env, shape, act):
+    torch, ssm = env
+    rows, G, K, N = shape
+    # the next even widths have the same tiles and splits, and no copies
+    more = ssm.ssm_proj_bwd_workspace_size(rows, K, N, G) - ssm.ssm_proj_bwd_workspace_size(rows, K + 1, N + 1, G, x_stride=0)
+    assert 0.99 * padded_bytes(*shape) < more <= padded_bytes(*shape)
+    whole(env, *shape, torch.bfloat16, act=act, res=None if act else torch.float32, strided=act is None)
+
+
 def test_workspace_of_the_size_said(env):
     """The size that is said without a stride serves x cut out of rows of an odd and an even number of values."""
     torch, ssm = env
