@@ -57,8 +57,8 @@ constexpr int kBwdTokens = 8;                             // of a stream
 constexpr int kKeep = kBwdStreams * kBwdTokens;           // tokens from one kept state to the next
 constexpr int kBack = 8;                                  // chunks that are looked back over
 // Bytes of one tensor beyond which reads and writes go past the cache: half of it (8 x 8192 x 4096
-// bf16 441 -> 417 us, 131072 x 5120 1116 -> 1083 us; the training pass on 4 x 2048 x 1536, which
-// stays in it, 100 -> 106 us)
+// bf16 436 -> 415 us, 131072 x 5120 1134 -> 1097 us; the training pass on 4 x 2048 x 1536, which
+// stays in it, 100 -> 109 us)
 constexpr int64_t kCached = (int64_t)128 << 20;
 constexpr int64_t kMaxStride = (1 << 24) - 1;             // lane offsets stay in 32 bits
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = 1.92596299e-8f;   // and its next digits
@@ -110,8 +110,8 @@ __device__ __forceinline__ float soft_plus(float v) { return fmaxf(v, 0.0f) + lo
 
 // sigmoid; e = exp(-v) (infinite where the sigmoid is 0). With fp32 gates the exponent is taken
 // to twice fp32's digits, as its rounding leaves e off by |v| half steps: a few at any v then.
-// Where gates have 16 bits, which tell them to 2^-9, it is rounded (8 x 8192 x 4096 425 us, in
-// full 457; fp32 takes the same time either way).
+// Where gates have 16 bits, which tell them to 2^-9, it is rounded (8 x 8192 x 4096 415 us, in
+// full 448; fp32 takes the same time either way).
 template <typename T> __device__ __forceinline__ float sigm(float v, float &e) {
     const float t = v * -kLog2e;
     e = __builtin_amdgcn_exp2f(t);
@@ -348,9 +348,9 @@ struct Rows {
 };
 
 // Forward: TT tokens to a stream. y NULL: the kept states and h_last alone. Bound by memory:
-// 8 x 8192 x 4096 in bf16 409 us, 2.15 GB at 5.25 TB/s; one row of 131072 x 5120 1091 us, 4.92.
-// 16 tokens in bf16 halve the chunks to join (8 tokens: 461 us); fp32 takes 8, whose values fit the
-// registers of four waves a SIMD (744 us, with 16 tokens 941), and so do resets.
+// 8 x 8192 x 4096 in bf16 405 to 417 us from run to run (figures beside one another, here and in
+// other comments, are of one run), 2.15 GB at 5.15 to 5.3 TB/s; one row of 131072 x 5120 1097 us, 4.9.
+// How many tokens a stream takes: fwd_tokens.
 template <typename T, int VEC, int TT, bool RESET>
 __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParams p) {
     typedef typename Raw<T, VEC>::type R;
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kFwdStreams * kRow, 4) void glr_fwd_kernel(GlrParam
 // registers. 4 x 2048 x 1536 in bf16 with a gate 59 us, 230 MB at 3.9 TB/s: the arithmetic of two
 // sigmoids, the decay and four gradients (80 instructions to a value, 26 us of issue at 2.4 GHz)
 // stands beside the memory. Three workgroups a CU, two where pairs of fp32 and a gate would spill
-// (training on 4 x 2048 x 1536 165 us, with three 176; without a gate 132 either way).
+// (training on 4 x 2048 x 1536 161 us, with three 177; without a gate 129 either way).
 template <typename T, int VEC, bool RESET, bool GATE>
 __global__ __launch_bounds__(kBwdStreams * kRow, sizeof(T) * VEC == 8 && GATE ? 2 : 3) void glr_bwd_kernel(GlrParams p) {
     typedef typename Raw<T, VEC>::type R;
@@ -716,8 +716,10 @@ __global__ __launch_bounds__(256) void glr_clear_kernel(uint4 *at, int64_t n) {
     if (k < n) at[k] = uint4{v, v, v, v};
 }
 
-// One token: bound by its launch and one trip to memory (256 x 5120 in bf16 with a gate 7.6 us for 24 MB).
-// A lane takes VEC channels of `rows` batch rows, so that softplus(lam) is formed once for them.
+// One token: bound by its launch and its trips to memory, one for softplus(lam) and the first row and one for
+// each further row of a lane, which waits for the stores of the one before (256 x 5120 in bf16 with a
+// gate, two rows to a lane, 7.4 us for 24 MB; after one another in a graph 6.1, fp32 7.0 to 7.2).
+// A lane takes VEC channels of `rows_per` batch rows, so that softplus(lam) is formed once for them.
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p, const float *h, float *h_out, int rows_per) {
     typedef typename Raw<T, VEC>::type R;
@@ -758,8 +760,8 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p, const float 
 // Launching
 
 // Tokens to a stream of the forward: 16 halve what joining chunks costs (8 x 8192 x 4096 bf16
-// 437 us, with 8 464), where they fit the registers: not in fp32, nor with resets (4 x 4096 x
-// 2048 bf16 160 us, with 8 98)
+// 415 us, with 8 461), where they fit the registers of four waves a SIMD: not in fp32 (8 x 8192 x 4096
+// 974 us, with 8 741), nor with resets (4 x 4096 x 2048 bf16 149 us, with 8 81; without resets 62)
 int fwd_tokens(int dtype, bool reset) { return (dtype == SSM_BF16 && !reset ? 16 : 8) * kFwdStreams; }
 int64_t chunks_of(int64_t L, int tokens) { return (L + tokens - 1) / tokens; }
 

@@ -18,8 +18,9 @@ using namespace ssm_detail;
 constexpr int64_t kMaxWidth = ((int64_t)1 << 22) - 1;   // of a row: a tile's lane offsets stay in 32 bits
 constexpr int kCus = 256, kMostSplits = 64;
 // Bytes of a 16-bit output beyond which it goes past the cache. A product and one that reads its
-// output: 65536 x 1024 -> 2048 (268 MB) 540 -> 494 us, 16384 x 2048 -> 4096 (134 MB) 463 -> 430;
-// 16384 x 2560 -> 2560 (84 MB) 405 -> 417. fp32 gains nowhere (16384 x 768 -> 2048, 134 MB, 729 -> 738).
+// output: 65536 x 1024 -> 2048 (268 MB) 530 -> 507 us, 16384 x 2048 -> 4096 (134 MB) 455 -> 449;
+// 16384 x 2560 -> 2560 (84 MB) 416 -> 421, 16384 x 1024 -> 2560 (84 MB) 166 -> 175. fp32 gains nowhere
+// (16384 x 768 -> 2048, 134 MB, 737 -> 743).
 constexpr int64_t kCached = (int64_t)100 << 20;
 
 size_t esize(int t) { return t == SSM_BF16 ? 2 : 4; }
@@ -124,13 +125,14 @@ struct Tiling {
 // The time of a product of J x I outputs over R, in us, from how many workgroups a CU
 // gets: it holds `hold` of a tile at once, and a step of 128 bytes of r takes it
 // step[k] with k + 1 of them, next to `fixed` for a workgroup's first loads and its
-// output. Splits add their sums' traffic and a launch. Measured (bf16, us, tiles of 256
-// / 128 / 64, one split): 16384 x 2048 -> 4096 233 / 263 / 355; 8192 x 768 -> 1536 28.1
-// / 29.2 / 33.3; 16384 x 64 -> 4096 43.8 / 47.5 / 49.8; 2048 x 2048 -> 2048 46 (2 splits
-// 41) / 27.4 / 27.2; 8192 x 12 groups of 128 -> 128 26.3 / 16.5 / 15.1; 2048 x 768 -> 1536
-// 23.8 / 12.6 / 10.5; 512 x 2048 -> 2048 44 / 21.7 / 12.0 (2 splits 32 / 20.6 / 16.5);
-// dweight of 8192 x 768 -> 1536 175 / 92 / 63, in 8 splits 43 / 35 / -; fp32 8192 x 768 ->
-// 1536 187 / 145 / 143.
+// output. Splits add their sums' traffic and a launch. It puts tiles in their order; the
+// times themselves come out 0.85 to 1.3 times what it says (the 12 groups below: 11.5 with 128,
+// 11.3 with 64). Measured (bf16, us, tiles of 256 / 128 / 64, one split): 16384 x 2048 -> 4096 216-234 / 264 / 361; 8192 x 768 -> 1536 27.4
+// / 29.0 / 32.9; 16384 x 64 -> 4096 41.6 / 45.0 / 48.7; 2048 x 2048 -> 2048 47 (2 splits
+// 41) / 27.4 / 27.4; 8192 x 12 groups of 128 -> 128 25.4 / 16.1 / 14.5; 2048 x 768 -> 1536
+// 24.1 / 12.8 / 10.8; 512 x 2048 -> 2048 45 / 21.9 / 12.2 (2 splits 33 / 21.0 / 16.9);
+// dweight of 8192 x 768 -> 1536 175 / 92 / 63, in 8 splits 44 / 43 / -, as planned (128, 6 splits) 35;
+// fp32 8192 x 768 -> 1536 187 / 146 / 144.
 Tiling plan_for(int64_t I, int64_t J, int64_t R, int64_t groups, int dtype) {
     struct Kind { int side, hold; double step[4], fixed; };
     static const Kind narrow[] = {{256, 1, {1.75}, 8.0}, {128, 2, {0.75, 1.0}, 4.0}, {64, 4, {0.3, 0.42, 0.58, 0.74}, 2.3}};
@@ -162,9 +164,10 @@ constexpr int kFew = 16;    // rows that the forward can take without tiles, rea
 
 // Whether it does: not where the weight's rows are so long that the waves of a workgroup are longer
 // at theirs than split tiles take. By the weight's rows in KB and workgroups a CU; measured in us
-// without tiles / with: one row 4096 -> 2048 4.3 / 8.3, 65536 -> 16 19.3 / 12.5; 8 rows 4096 -> 4096
-// 5.9 / 10.5, 8192 -> 1024 7.8 / 10.4, 16384 -> 512 13.0 / 9.3, 65536 -> 256 50 / 18.5; fp32 4096 -> 4096
-// 14.5 / 23.8, 8192 -> 512 15.0 / 11.7.
+// without tiles / with: one row 4096 -> 2048 4.2 / 9.9, 65536 -> 16 19.1 / 13.7; 8 rows 4096 -> 4096
+// 6.0 / 10.2, 8192 -> 1024 7.8 / 9.6, 8192 -> 256 7.6 / 8.8 (taken with), 16384 -> 512 13.0 / 10.4,
+// 65536 -> 256 50 / 18.5; fp32 4096 -> 4096 14.4 / 23.8, 8192 -> 512 14.7 / 12.0. The time
+// without tiles is rough: fp32 4096 -> 4096 comes out as 7.9.
 bool without_tiles(const ssm_proj_desc &d, const Tiling &pl) {
     if (d.rows > kFew) return false;
     const double kb = (double)d.in * (d.dtype == SSM_BF16 ? 2 : 4) / 1024;
@@ -247,8 +250,8 @@ int64_t span(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? (r
 // Rows of an odd number of 16-bit values begin between 4-byte words, from where nothing goes
 // straight into LDS. Such operands are first copied, their rows padded to whole pieces, where the
 // product is long enough for that: a launch and twice the bytes against its planned time again, at
-// least (gradients of 7447 x 155 -> 3200 through registers 171 us, with copies 64; 8192 x 767 -> 1535
-// 87 and 68, its gradients 98 and 105 and 58 each). Rows of less than a piece go through registers
+// least (gradients of 7447 x 155 -> 3200 through registers 93 and 77 us, with copies 34 and 32; 8192 x 767 -> 1535
+// 83 and 66, its gradients 96 and 101 and 55 each). Rows of less than a piece go through registers
 // padded or not, and are left where they are: `row` is the shorter one of a product's operands
 // (50000 x 5 -> 515 forward 47.6 us, with copies 52.4; both gradients of 200000 x 7 -> 2048 496, with 507).
 int64_t padded(int64_t width) { return ceil_div(width, 8) * 8; }

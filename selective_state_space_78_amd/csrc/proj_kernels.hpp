@@ -21,10 +21,10 @@
 // in 16-byte stores of whole lines (16384 x 2048 -> 4096 writing pre as well 239 us; stored
 // from the accumulators, 8 bytes a lane over 16 rows, 329).
 //
-// Bound by the matrix cores at the large sizes: 8192^3 in bf16 takes 753 us (1460 TFLOP/s),
-// products running in 71 % of its cycles, the rest at the steps' barriers; fp32 4096^3 930 us
-// (148 TFLOP/s). Four waves of 128 x 128 instead of eight of 128 x 64 halve what is read from
-// LDS, and read a step ahead: 841 us where this took 798; with four buffers of 64 bytes of r 832.
+// Bound by the matrix cores at the large sizes: 8192^3 in bf16 takes 758 us (1450 TFLOP/s),
+// products running in 71 % of its cycles, the rest at the steps' barriers; fp32 4096^3 930 to 944 us
+// (146 to 148 TFLOP/s). Four waves of 128 x 128 instead of eight of 128 x 64 halve what is read from
+// LDS, and read a step ahead: 8192^3 took 5 % longer so, with four buffers of 64 bytes of r 4 %.
 //
 // Where tiles are few the reduction is split over workgroups: each writes its fp32 sums,
 // and a second kernel adds them in order and finishes as the first would.
@@ -627,13 +627,13 @@ template <typename T> __global__ __launch_bounds__(256) void proj_one_row_kernel
     proj_finish<T, 1>(a, (int)g, 0, i, bias, v);
 }
 
-// Up to 16 rows: the weight is read once, straight into the matrix instructions' registers,
-// 16 bytes a lane along r at any address. A workgroup takes 16 of its rows, the waves share r
-// in runs of pairs of steps (whole lines); their sums are added in LDS in order. Lanes read four
-// to a row, next to one another, and hand over to the lane that the instruction has the piece in
-// (read there directly, neighbouring lanes in different rows, loads pass one lane at a time: 8 rows
-// 4096 -> 4096 in bf16 8.3 us, 16 rows 9.6; so 5.9 and 6.3; in tiles 10.6; 8 rows 768 -> 1536 2.9 us,
-// in tiles 5.7; fp32 4096 -> 4096 14.5 us, 2 rows read directly 12.2, 16 rows 16.8).
+// Up to 16 rows: the weight is read once, into registers, 16 bytes a lane along r at any address.
+// A workgroup takes 16 of its rows, the waves share r in runs of pairs of steps (whole lines); their
+// sums are added in LDS in order. Lanes read four to a row, next to one another, and hand over, by
+// ds_bpermute, to the lane that the matrix instruction has the piece in. Read there directly,
+// neighbouring lanes in different rows, loads pass one lane at a time: 8 rows 4096 -> 4096 in bf16
+// 8.3 us, 16 rows 9.6; so 6.0 and 6.2; in tiles 10.2 to 10.5. 8 rows 768 -> 1536 2.9 us, in tiles 5.6.
+// fp32 4096 -> 4096 14.3 to 14.6 us for 2 to 16 rows; read directly 16 rows took 16.8, but 2 rows 12.2.
 template <typename T, int W> __global__ __launch_bounds__(W * 64) void proj_few_rows_kernel(ProjParams a) {
     constexpr int E = 16 / (int)sizeof(T), kStep = 4 * E;
     __shared__ float4 sum[W][64];
