@@ -254,6 +254,19 @@ def test_workspace_of_the_size_said(env):
             backward_check(torch, dict(s, x=x), 1, None, g, show)
 
 
+@pytest.mark.parametrize("dtype,K,stride", [("float32", 512, 2 ** 22 - 1), ("bfloat16", 520, 2 ** 22 - 2), ("bfloat16", 519, 2 ** 22 - 1)])
+def test_rows_as_far_apart_as_can_be(env, dtype, K, stride):
+    """A tile's rows span more than 2^31 bytes, in memory that ends with the last row: as dense rows, bit for bit."""
+    torch, ssm = env
+    s = make(torch, 1000, 1, K, 1030, getattr(torch, dtype))
+    x = torch.empty(999 * stride + K, dtype=s["x"].dtype, device="cuda").as_strided((1000, K), (stride, 1))
+    x.copy_(s["x"])
+    y, g = ssm.ssm_proj_fwd(x, s["weight"]), ssm.ssm_proj_bwd(s["dy"], x, s["weight"])
+    want, ref = ssm.ssm_proj_fwd(s["x"], s["weight"]), ssm.ssm_proj_bwd(s["dy"], s["x"], s["weight"])
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all(torch.equal(g[n], ref[n]) for n in ("dx", "dweight"))
+
+
 # rows shorter than one 16-byte piece, of an odd number of values, in long products
 SHORT = [(20000, 1, 7, 515), (20000, 3, 5, 257), (20000, 1, 515, 7), (50000, 1, 3, 1024)]
 

@@ -308,6 +308,25 @@ def test_more_batch_rows_than_a_grid_is_high(env, B, D):
             assert k == "dlam" or v is None or torch.equal(whole[k][r], v), k
 
 
+@pytest.mark.parametrize("dtype,D,stride", [("float32", 64, 2 ** 24 - 1), ("bfloat16", 66, 2 ** 24 - 2), ("bfloat16", 33, 2 ** 24 - 1)])
+def test_rows_as_far_apart_as_can_be(env, dtype, D, stride):
+    """A wave's rows span up to 2^31 bytes, in memory that ends with the last row: as dense rows, bit for bit."""
+    torch, ssm = env
+    B, L, t = 2, 75, getattr(torch, dtype)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    dense = [torch.randn(B, L, D, generator=g, device="cuda").to(t) for _ in range(3)]
+    dy, lam = torch.randn(B, L, D, generator=g, device="cuda").to(t), torch.randn(D, generator=g, device="cuda")
+    wide = []
+    for v in dense:
+        wide.append(torch.empty((B * L - 1) * stride + D, dtype=t, device="cuda").as_strided((B, L, D), (L * stride, stride, 1)))
+        wide[-1].copy_(v)
+    (y, h), (want, last) = ssm.ssm_glr_fwd(*wide, lam), ssm.ssm_glr_fwd(*dense, lam)
+    grads, ref = ssm.ssm_glr_bwd(*wide, lam, dy), ssm.ssm_glr_bwd(*dense, lam, dy)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(h, last)
+    assert all(torch.equal(grads[n], ref[n]) for n in ("dx", "drgate", "digate", "dlam", "dh0"))
+
+
 def test_empty(env):
     torch, ssm = env
     z = lambda *s: torch.zeros(s, device="cuda")
